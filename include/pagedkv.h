@@ -84,6 +84,9 @@ typedef enum { PKV_DTYPE_BF16 = 0, PKV_DTYPE_FP8_E4M3 = 1 } pkv_dtype;
 #define PKV_DEVERR_CONTEXT 4     /* context_len outside [0, max_blocks_per_seq*block_size],
                                     or longer than the call's context bound */
 #define PKV_DEVERR_ORDER 5       /* seq_order entry outside [0, num_seqs)      */
+#define PKV_DEVERR_DRAFT 6       /* a sequence's drafts: a negative number or more than
+                                    max_draft, more than its context; an accepted list
+                                    that is too long, not increasing or out of range */
 
 /* Geometry of one layer's K and V pools (both share it). */
 typedef struct {
@@ -315,6 +318,126 @@ int pkv_paged_attention_decode_shared_prefix(
     void* workspace, size_t workspace_bytes, const int32_t* seq_order, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * paged_attention_window: decode with a sliding window and sink tokens. The
+ * query of sequence s (its last cached token, position ctx - 1) sees the last
+ * `window` tokens, its own included, and the first `sinks` tokens:
+ *     V_s = { t < min(sinks, ctx) } u { max(0, ctx - window) <= t < ctx }
+ *     z_t = scale * <q[s,j,:], K_s[t,:]>,  out[s,j,:] = sum_{t in V_s} softmax(z)_t V_s[t,:]
+ * (the pages have no counterpart). A block with no visible token is never
+ * read: its block_tables entry may be anything, so a caller can give the
+ * blocks behind the window back to its pool. Masked slots of the blocks that
+ * are read may hold anything, NaN included.
+ *
+ *   window      : >= 1; larger than the context: plain decode
+ *   sinks       : >= 0
+ *   partition_size : 0 = one pass (a thread-block cluster per sequence and KV
+ *               head, no workspace); otherwise a multiple of block_size: the
+ *               sequence's visible blocks, in order (the sinks', then the
+ *               window's), are cut into partitions of partition_size /
+ *               block_size blocks, whose partials go to `workspace` and are
+ *               merged into `out` by the same call. Any value gives the same
+ *               attention; pkv_window_partition_size returns the library's
+ *               choice.
+ *   workspace, workspace_bytes : device scratch of at least
+ *               pkv_window_workspace_bytes(...) bytes (0 when partition_size
+ *               is 0; may be NULL then). Its contents do not matter before or
+ *               after; calls whose kernels may overlap need one each.
+ *   other args  : as for pkv_paged_attention_decode. A context of 0 yields
+ *               zeros. `out` may not be `q`.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+int pkv_window_partition_size(int num_seqs, int num_kv_heads, int block_size, int max_context,
+                              int window, int sinks);
+size_t pkv_window_workspace_bytes(int num_seqs, int num_heads, int head_dim, int block_size,
+                                  int max_context, int window, int sinks, int partition_size);
+int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
+                               const void* v_cache, pkv_cache_desc cache,
+                               const float* k_scale, const float* v_scale,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* context_lens, int num_seqs, int num_heads,
+                               int max_context, float scale, int window, int sinks,
+                               int partition_size, void* workspace, size_t workspace_bytes,
+                               const int32_t* seq_order, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * paged_attention_tree: attention of several drafted tokens per sequence, a
+ * chain or a tree, over the paged cache (the pages have no counterpart; this
+ * is the verification step of speculative decoding). The drafts' K and V are
+ * in the cache already (pkv_kv_cache_write): they are the last n_s tokens of
+ * sequence s, n_s = q_start[s+1] - q_start[s], behind base_s = ctx_s - n_s
+ * committed tokens. Draft i of sequence s is row q_start[s] + i of q and out;
+ * it sees the committed tokens and the drafts its mask names:
+ *     V = { t < base_s } u { base_s + b : b < n_s and bit b of tree_mask[row] }
+ *     z_t = scale * <q[row,j,:], K_s[t,:]>, out[row,j,:] = sum_{t in V} softmax(z)_t V_s[t,:]
+ * An empty V yields zeros. Bits n_s and above are ignored.
+ *
+ *   q, out      : device bf16 [num_queries][num_heads][head_dim]; rows at or
+ *               behind q_start[num_seqs] are neither read nor written; `out`
+ *               may not be `q`
+ *   q_start     : device int32 [num_seqs + 1], not decreasing, q_start[0] >= 0,
+ *               q_start[num_seqs] <= num_queries; n_s may be 0
+ *   max_draft   : host upper bound of n_s, 1..64. A sequence with a negative
+ *               n_s or more drafts than the bound or than its context is
+ *               reported (PKV_DEVERR_DRAFT) and its rows are left as they were
+ *   tree_mask   : device uint64 [num_queries], or NULL for a chain (draft i
+ *               sees drafts 0..i)
+ *   context_lens: device int32 [num_seqs], the drafts included
+ *   workspace, workspace_bytes : device scratch of at least
+ *               pkv_tree_workspace_bytes(...) bytes; its contents do not
+ *               matter before or after; calls whose kernels may overlap need
+ *               one each.
+ *   other args  : as for pkv_paged_attention_decode
+ * Slots behind the context may hold anything, NaN included; a draft's K and V
+ * must be finite if any draft of its sequence sees it.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define PKV_MAX_DRAFT 64
+size_t pkv_tree_workspace_bytes(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
+                                int head_dim, int max_context, int max_draft);
+int pkv_paged_attention_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             pkv_cache_desc cache, const float* k_scale, const float* v_scale,
+                             const int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* q_start, int num_seqs,
+                             int num_queries, int max_draft, const uint64_t* tree_mask,
+                             int num_heads, int max_context, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * kv_cache_accept: after a verification step, move the K and V rows of the
+ * accepted drafts up behind the committed tokens, in every layer's pools (the
+ * pages have no counterpart). With base_s and n_s as for
+ * pkv_paged_attention_tree and a_k = accepted[s][k], k < m_s = num_accepted[s]:
+ *     row base_s + k  <-  row base_s + a_k   (all heads, byte for byte)
+ * as if every row were read before any is written. The sequence then has
+ * base_s + m_s tokens; what the rows behind them hold is not specified
+ * (pkv_seq_truncate gives their blocks back).
+ *
+ *   k_caches, v_caches : HOST arrays of num_layers device pointers, pools of
+ *               the geometry `cache` that share the block tables; read during
+ *               the call only. A pool may appear once.
+ *   accepted    : device int32 [num_seqs][max_accepted], strictly increasing,
+ *               0 <= a_k < n_s; entries from num_accepted[s] on are not read
+ *   num_accepted: device int32 [num_seqs], 0 <= m_s <= max_accepted
+ *   new_context_lens : NULL, or device int32 [num_seqs] that receives
+ *               base_s + m_s; it may not be context_lens
+ * A block that a moved row is written to must not be shared with another
+ * sequence (pkv_seq_append's copy-on-write sees to that when the drafts are
+ * appended). A bad list or number of drafts is reported (PKV_DEVERR_DRAFT):
+ * no row of that sequence moves and its new length is base_s (ctx_s if base_s
+ * would be negative). A context outside the table (PKV_DEVERR_CONTEXT) moves
+ * nothing and is kept. A move from or to a bad block id is skipped and
+ * reported (PKV_DEVERR_BLOCK_ID).
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * num_layers < 1 is PKV_ERR_INVALID_ARG; num_seqs == 0 is a no-op.
+ * ------------------------------------------------------------------------ */
+int pkv_kv_cache_accept(void* const* k_caches, void* const* v_caches, int num_layers,
+                        pkv_cache_desc cache, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* q_start, int num_seqs, const int32_t* accepted,
+                        int max_accepted, const int32_t* num_accepted,
+                        int32_t* new_context_lens, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * copy_blocks: copy-on-write duplication. Sequences forked from one prompt
  * share its physical blocks; a block is cloned only when a sibling is about
  * to write into it ([HowVLLM] "PagedAttention borrows from operating
@@ -459,6 +582,11 @@ int pkv_seq_append(pkv_allocator* a, int seq, int n_tokens, int64_t* slots_out,
                    int32_t* cow_pairs_out, int* n_cow);
 /* Release the sequence and its references. */
 int pkv_seq_free(pkv_allocator* a, int seq);
+/* Cut the sequence to its first new_len tokens (0 <= new_len <= its length,
+ * else PKV_ERR_INVALID_ARG) and release its references to the blocks behind
+ * them, e.g. the rejected drafts' after pkv_kv_cache_accept. The last block
+ * kept may be shared: the next append into it copies it as usual. */
+int pkv_seq_truncate(pkv_allocator* a, int seq, int new_len);
 /* Copy the sequence's block table into out[0..cap); *n_blocks = its length.
  * Returns PKV_ERR_INVALID_ARG if cap is too small (nothing written). */
 int pkv_seq_block_table(const pkv_allocator* a, int seq, int32_t* out, int cap,

@@ -14,6 +14,8 @@ Tensors (caller-owned device memory):
   context_lens     : [num_seqs] torch.int32
   slot_mapping     : [num_tokens] torch.int64 (-1 = skip)
   k_scale, v_scale : [num_kv_heads] torch.float32 (FP8 pools)
+  q_start          : [num_seqs + 1] torch.int32, the first draft row of each
+                     sequence (paged_attention_tree, kv_cache_accept)
 """
 from __future__ import annotations
 
@@ -46,6 +48,9 @@ DEVERR_SLOT = 2
 DEVERR_WAIT_TIMEOUT = 3
 DEVERR_CONTEXT = 4
 DEVERR_ORDER = 5
+DEVERR_DRAFT = 6
+
+MAX_DRAFT = 64
 
 
 class PagedKVError(RuntimeError):
@@ -83,6 +88,15 @@ SIGNATURES = {
                                                       _P, _I,
                                                       _I, _I, ctypes.c_float, _P, _I, _I, _P,
                                                       _I, _I, _P, ctypes.c_size_t, _P, _P]),
+    "pkv_window_partition_size": (_I, [_I, _I, _I, _I, _I, _I]),
+    "pkv_window_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pkv_paged_attention_window": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _I, _I,
+                                        _I, ctypes.c_float, _I, _I, _I, _P, ctypes.c_size_t, _P,
+                                        _P]),
+    "pkv_tree_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I]),
+    "pkv_paged_attention_tree": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _P, _I, _I,
+                                      _I, _P, _I, _I, ctypes.c_float, _P, ctypes.c_size_t, _P]),
+    "pkv_kv_cache_accept": (_I, [_P, _P, _I, CacheDesc, _P, _I, _P, _P, _I, _P, _I, _P, _P, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, CacheDesc, _P, _I, _P]),
     "pkv_swap_out": (_I, [_P, _P, CacheDesc, _P, _I, _P, _P, _P]),
     "pkv_swap_in": (_I, [_P, _P, CacheDesc, _P, _I, _P, _P, _P]),
@@ -96,6 +110,7 @@ SIGNATURES = {
     "pkv_seq_fork": (_I, [_P, _I, ctypes.POINTER(_I)]),
     "pkv_seq_append": (_I, [_P, _I, _I, _P, _P, ctypes.POINTER(_I)]),
     "pkv_seq_free": (_I, [_P, _I]),
+    "pkv_seq_truncate": (_I, [_P, _I, _I]),
     "pkv_seq_block_table": (_I, [_P, _I, _P, _I, ctypes.POINTER(_I)]),
     "pkv_seq_len": (_I, [_P, _I, ctypes.POINTER(_I)]),
     "pkv_block_refcount": (_I, [_P, _I, ctypes.POINTER(_I)]),
@@ -378,6 +393,223 @@ def paged_attention_shared_prefix(q, k_cache, v_cache, block_tables, context_len
     return out
 
 
+class _Launch:
+    """Where a call runs: the device of its tensors, made current for the
+    call, and its stream (by default that device's current one). Scratch and
+    results that the call allocates belong to the same stream."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("q and the caches must be CUDA tensors")
+        self.device = device
+        self.raw = None if stream is None else _stream(stream).value or 0
+        self._ctx = []
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(self.device))
+            self._ctx[-1].__enter__()
+        current = torch.cuda.current_stream().cuda_stream
+        if self.raw is None:
+            self.raw = current
+        elif self.raw != current:
+            side = (torch.cuda.ExternalStream(self.raw) if self.raw
+                    else torch.cuda.default_stream())
+            self._ctx.append(torch.cuda.stream(side))
+            self._ctx[-1].__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        while self._ctx:
+            self._ctx.pop().__exit__(*exc)
+
+
+def _ptr(t, name, device, dtype, shape=None):
+    """Address of a contiguous tensor of the given type on the call's device."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError("%s must be a tensor on %s" % (name, device))
+    if t.dtype not in dtype:
+        raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtype))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_MASK = (torch.int64,) + ((torch.uint64,) if hasattr(torch, "uint64") else ())
+_CACHE = (torch.bfloat16,) + _FP8_DTYPES
+
+
+def _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, rows, out):
+    """Checked shapes and addresses of an attention call: (desc, dict)."""
+    desc = cache_desc(k_cache)
+    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+        raise ValueError("q must be [rows, num_heads, %d]" % desc.head_dim)
+    if block_tables.dim() != 2 or tuple(context_lens.shape) != (block_tables.shape[0],):
+        raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
+    if rows is not None and q.shape[0] != rows:
+        raise ValueError("q must have one row per sequence")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must match")
+    dev = q.device
+    if out is not None and q.numel() and out.data_ptr() == q.data_ptr():
+        raise ValueError("out may not be q")
+    scales = (desc.num_kv_heads,)
+    return desc, dict(
+        out=_ptr(out, "out", dev, _BF16, tuple(q.shape)), q=_ptr(q, "q", dev, _BF16),
+        k=_ptr(k_cache, "k_cache", dev, _CACHE), v=_ptr(v_cache, "v_cache", dev, _CACHE,
+                                                       tuple(k_cache.shape)),
+        ks=_ptr(k_scale, "k_scale", dev, _F32, scales),
+        vs=_ptr(v_scale, "v_scale", dev, _F32, scales),
+        tables=_ptr(block_tables, "block_tables", dev, _I32),
+        lens=_ptr(context_lens, "context_lens", dev, _I32))
+
+
+def _scratch(workspace, need, device):
+    """(address, bytes, tensor) of a call's workspace, allocated if not given."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def window_partition_size(num_seqs, num_kv_heads, block_size, max_context, window,
+                          sinks=0) -> int:
+    """The library's choice of partition_size for paged_attention_window
+    (0 = one pass)."""
+    rc = lib().pkv_window_partition_size(int(num_seqs), int(num_kv_heads), int(block_size),
+                                         int(max_context), int(window), int(sinks))
+    if rc < 0:
+        _check(rc, "window_partition_size")
+    return int(rc)
+
+
+def window_workspace_bytes(num_seqs, num_heads, head_dim, block_size, max_context, window,
+                           sinks, partition_size) -> int:
+    return int(lib().pkv_window_workspace_bytes(num_seqs, num_heads, head_dim, block_size,
+                                                max_context, window, sinks, partition_size))
+
+
+def paged_attention_window(q, k_cache, v_cache, block_tables, context_lens, scale, max_context,
+                           window, sinks=0, partition_size=None, k_scale=None, v_scale=None,
+                           out=None, workspace=None, stream=None, seq_order=None) -> torch.Tensor:
+    """Decode attention through a sliding window: q [S, Hq, D] sees the last
+    `window` tokens of its sequence and the first `sinks` ones; blocks with no
+    visible token are not read (their table entries may be anything). Returns
+    out [S, Hq, D] bf16. partition_size: None = the library's choice
+    (window_partition_size), 0 = one pass, else a multiple of the block size.
+    out and workspace are allocated if not given."""
+    S = int(block_tables.shape[0])
+    desc, a = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
+                              S, out)
+    max_context, window, sinks = int(max_context), int(window), int(sinks)
+    order = _ptr(seq_order, "seq_order", q.device, _I32, (S,))
+    if partition_size is None:
+        partition_size = window_partition_size(S, desc.num_kv_heads, desc.block_size,
+                                               max_context, window, sinks)
+    with _Launch(q.device, stream) as at:
+        if out is None:
+            out = torch.empty_like(q)
+            a["out"] = out.data_ptr()
+        need = lib().pkv_window_workspace_bytes(S, q.shape[1], desc.head_dim, desc.block_size,
+                                                max_context, window, sinks, partition_size)
+        ws, wsb, keep = _scratch(workspace, need, q.device)
+        rc = lib().pkv_paged_attention_window(
+            a["out"], a["q"], a["k"], a["v"], desc, a["ks"], a["vs"], a["tables"],
+            block_tables.shape[1], a["lens"], S, q.shape[1], max_context, float(scale), window,
+            sinks, int(partition_size), ws, wsb, order, at.raw)
+    _check(rc, "paged_attention_window")
+    return out
+
+
+def tree_workspace_bytes(num_seqs, num_queries, num_heads, num_kv_heads, head_dim, max_context,
+                         max_draft) -> int:
+    return int(lib().pkv_tree_workspace_bytes(num_seqs, num_queries, num_heads, num_kv_heads,
+                                              head_dim, max_context, max_draft))
+
+
+def paged_attention_tree(q, k_cache, v_cache, block_tables, context_lens, q_start, scale,
+                         max_context, max_draft, tree_mask=None, k_scale=None, v_scale=None,
+                         out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over the cache (see the C header): sequence
+    s has the drafts q[q_start[s]:q_start[s + 1]], whose K/V are its last
+    tokens in the cache; each sees every committed token and the drafts whose
+    bits its tree_mask entry (int64 or uint64 [N]) has set, or with
+    tree_mask=None the drafts up to itself. context_lens counts the drafts;
+    max_draft (at most 64) bounds the drafts of a sequence. Returns out
+    [N, Hq, D] bf16; rows at or behind q_start[S] are not written. out and
+    workspace are allocated if not given."""
+    S = int(block_tables.shape[0])
+    desc, a = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
+                              None, out)
+    n, heads = int(q.shape[0]), int(q.shape[1])
+    start = _ptr(q_start, "q_start", q.device, _I32, (S + 1,))
+    mask = _ptr(tree_mask, "tree_mask", q.device, _MASK, (n,))
+    max_context, max_draft = int(max_context), int(max_draft)
+    with _Launch(q.device, stream) as at:
+        if out is None:
+            out = torch.empty_like(q)
+            a["out"] = out.data_ptr()
+        need = lib().pkv_tree_workspace_bytes(S, n, heads, desc.num_kv_heads, desc.head_dim,
+                                              max_context, max_draft)
+        ws, wsb, keep = _scratch(workspace, need, q.device)
+        rc = lib().pkv_paged_attention_tree(
+            a["out"], a["q"], a["k"], a["v"], desc, a["ks"], a["vs"], a["tables"],
+            block_tables.shape[1], a["lens"], start, S, n, max_draft, mask, heads, max_context,
+            float(scale), ws, wsb, at.raw)
+    _check(rc, "paged_attention_tree")
+    return out
+
+
+def kv_cache_accept(k_caches, v_caches, block_tables, context_lens, q_start, accepted,
+                    num_accepted, new_context_lens=None, stream=None) -> torch.Tensor:
+    """Keep the accepted drafts: row base + k <- row base + accepted[s, k] of
+    K and V for k < num_accepted[s], base = context_lens[s] - number of drafts
+    (see the C header). k_caches, v_caches: a pool each, or equally long lists
+    of them (one per layer, sharing block_tables). accepted int32 [S, M],
+    strictly increasing; num_accepted int32 [S]. Returns the new context
+    lengths, int32 [S] (in new_context_lens if given; not context_lens)."""
+    if isinstance(k_caches, torch.Tensor):
+        k_caches = [k_caches]
+    if isinstance(v_caches, torch.Tensor):
+        v_caches = [v_caches]
+    if len(k_caches) != len(v_caches) or not len(k_caches):
+        raise ValueError("k_caches and v_caches must be equally many, one at least")
+    first = k_caches[0]
+    desc, dev, shape = cache_desc(first), first.device, tuple(first.shape)
+    dt = (first.dtype,)
+    n = len(k_caches)
+    if block_tables.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks], accepted [S, M]")
+    S, M = int(block_tables.shape[0]), int(accepted.shape[1])
+    pools = (_P * n)(*[_ptr(t, "k_caches", dev, dt, shape) for t in k_caches])
+    vpools = (_P * n)(*[_ptr(t, "v_caches", dev, dt, shape) for t in v_caches])
+    args = (_ptr(block_tables, "block_tables", dev, _I32), int(block_tables.shape[1]),
+            _ptr(context_lens, "context_lens", dev, _I32, (S,)),
+            _ptr(q_start, "q_start", dev, _I32, (S + 1,)), S,
+            _ptr(accepted, "accepted", dev, _I32, (S, M)), M,
+            _ptr(num_accepted, "num_accepted", dev, _I32, (S,)))
+    if new_context_lens is not None and S and new_context_lens.data_ptr() == context_lens.data_ptr():
+        raise ValueError("new_context_lens may not be context_lens")
+    with _Launch(dev, stream) as at:
+        if new_context_lens is None:
+            new_context_lens = torch.empty_like(context_lens)
+        rc = lib().pkv_kv_cache_accept(
+            pools, vpools, n, desc, *args,
+            _ptr(new_context_lens, "new_context_lens", dev, _I32, (S,)), at.raw)
+    _check(rc, "kv_cache_accept")
+    return new_context_lens
+
+
 def copy_blocks(k_cache, v_cache, block_pairs, stream=None) -> None:
     """k_cache[dst] = k_cache[src] (same for v) for each row (src, dst) of
     block_pairs [n, 2] int32."""
@@ -509,6 +741,11 @@ class BlockAllocator:
 
     def free(self, seq: int) -> None:
         _check(lib().pkv_seq_free(self._h, int(seq)), "seq_free")
+
+    def truncate(self, seq: int, new_len: int) -> None:
+        """Cut the sequence to its first new_len tokens; the blocks behind
+        them lose its reference (pkv_seq_truncate)."""
+        _check(lib().pkv_seq_truncate(self._h, int(seq), int(new_len)), "seq_truncate")
 
     def block_table(self, seq: int) -> np.ndarray:
         n = ctypes.c_int()

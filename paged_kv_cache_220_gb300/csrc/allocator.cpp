@@ -139,7 +139,7 @@ extern "C" int pkv_seq_append(pkv_allocator* a, int seq, int n_tokens, int64_t* 
   if (cow) {
     const int32_t old = s.table.back();
     const int32_t fresh = a->pop();
-    a->fill[fresh] = a->fill[old];
+    a->fill[fresh] = static_cast<int32_t>(len % B);
     --a->refcount[old];  // still > 0: another holder keeps it
     s.table.back() = fresh;
     cow_pairs_out[0] = old;
@@ -152,7 +152,7 @@ extern "C" int pkv_seq_append(pkv_allocator* a, int seq, int n_tokens, int64_t* 
     if (bi == static_cast<int64_t>(s.table.size())) s.table.push_back(a->pop());
     const int32_t b = s.table[bi];
     slots_out[i] = static_cast<int64_t>(b) * B + pos % B;
-    ++a->fill[b];
+    a->fill[b] = static_cast<int32_t>(pos % B) + 1;
   }
   s.len = len + n_tokens;
   return PKV_OK;
@@ -166,6 +166,29 @@ extern "C" int pkv_seq_free(pkv_allocator* a, int seq) {
   const std::vector<int32_t>& t = it->second.table;
   for (auto b = t.rbegin(); b != t.rend(); ++b) a->release(*b);
   a->seqs.erase(it);
+  return PKV_OK;
+}
+
+// Blocks behind the cut lose this sequence's reference, last one first, so the
+// earliest is reused first. The last block kept may now hold fewer of this
+// sequence's tokens than `fill` says; it is lowered only if no other sequence
+// holds the block (the statistics count tokens per holder, so they stay exact
+// either way).
+extern "C" int pkv_seq_truncate(pkv_allocator* a, int seq, int new_len) {
+  if (!a) return PKV_ERR_INVALID_ARG;
+  auto it = a->seqs.find(seq);
+  if (it == a->seqs.end()) return PKV_ERR_NOT_FOUND;
+  pkv_allocator::Seq& s = it->second;
+  if (new_len < 0 || new_len > s.len) return PKV_ERR_INVALID_ARG;
+  const int B = a->block_size;
+  const size_t keep = (static_cast<size_t>(new_len) + B - 1) / B;
+  while (s.table.size() > keep) {
+    a->release(s.table.back());
+    s.table.pop_back();
+  }
+  if (keep > 0 && a->refcount[s.table.back()] == 1)
+    a->fill[s.table.back()] = static_cast<int32_t>(new_len - static_cast<int64_t>(keep - 1) * B);
+  s.len = new_len;
   return PKV_OK;
 }
 
@@ -203,9 +226,24 @@ extern "C" int pkv_alloc_stats(const pkv_allocator* a, int* free_blocks, int* us
   if (free_blocks) *free_blocks = nfree;
   if (used_blocks) *used_blocks = a->num_blocks - nfree;
   if (used_slots) {
+    // slots of a block that some holder's length covers (holders of a shared
+    // block may have been cut to different lengths)
+    const int B = a->block_size;
+    std::vector<int32_t> used;
+    try {
+      used.assign(a->num_blocks, 0);
+    } catch (...) {
+      return PKV_ERR_OUT_OF_BLOCKS;
+    }
+    for (const auto& kv : a->seqs) {
+      const pkv_allocator::Seq& q = kv.second;
+      for (size_t i = 0; i < q.table.size(); ++i) {
+        const int64_t n = std::min<int64_t>(B, q.len - static_cast<int64_t>(i) * B);
+        used[q.table[i]] = std::max(used[q.table[i]], static_cast<int32_t>(n));
+      }
+    }
     long long u = 0;
-    for (int b = 0; b < a->num_blocks; ++b)
-      if (a->refcount[b] > 0) u += a->fill[b];
+    for (int32_t n : used) u += n;
     *used_slots = u;
   }
   return PKV_OK;
