@@ -24,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
            "--expt-relaxed-constexpr", "-I" + INCLUDE]
 SOURCES = ["api.cu", "kv_cache_write.cu", "copy_blocks.cu", "swap_blocks.cu", "decode.cu", "decode_tc.cu", "decode_prefix.cu", "reduce.cu",
-           "decode_noalloc.cu", "decode_rows.cu", "kv_cache_accept.cu", "allocator.cpp", "scheduler.cpp"]
+           "decode_noalloc.cu", "decode_tree.cu", "decode_window.cu", "kv_cache_accept.cu", "allocator.cpp", "scheduler.cpp"]
 
 
 def nvcc() -> str:

@@ -39,11 +39,45 @@ struct DecodeParams {
   // 0..gridDim.z-1): the CTAs take the sequences in this order
   const int32_t* seq_order;
   float qscale;          // scale * log2(e)
+  // the windowed form only (launch_decode_window): each query sees the last
+  // `window` tokens of its context and the first `sinks` ones
+  int window, sinks;
+};
+
+// The blocks of a context that a window and its sink tokens touch, in order:
+// the first `sink_blocks` blocks, then `first` .. `first + rest` - 1. Visible
+// block v is block v if v < sink_blocks, else v - sink_blocks + first; where
+// the two ranges meet they are one. Every one of them holds a visible token.
+struct WindowBlocks {
+  int sink_end;     // tokens [0, sink_end) and [win_begin, ctx) are visible
+  int win_begin;
+  int sink_blocks;
+  int first;
+  int count;        // all visible blocks
+
+  __host__ __device__ WindowBlocks(int ctx, int window, int sinks, int block) {
+    sink_end = sinks < ctx ? sinks : ctx;
+    win_begin = ctx > window ? ctx - window : 0;
+    first = win_begin / block;
+    sink_blocks = (sink_end + block - 1) / block;
+    if (sink_blocks > first) sink_blocks = first;
+    count = sink_blocks + (ctx + block - 1) / block - first;
+  }
+  __host__ __device__ int block_of(int v) const {
+    return v < sink_blocks ? v : v - sink_blocks + first;
+  }
+  __host__ __device__ bool sees(int t, int ctx) const {
+    return t < ctx && (t < sink_end || t >= win_begin);
+  }
 };
 
 // Tensor-core decode (decode_tc.cu) for bf16 or E4M3 pools. Returns a pkv_status.
 int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_cache,
                      int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
+
+// The same for the windowed form; the partitions are runs of visible blocks.
+int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
+                         int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
 
 // Merge of split partials (reduce.cu). With prefix_blocks == NULL the slots of
 // sequence s are [0, ceil(ctx/P)); otherwise [0, npre) and [slot_split,
@@ -53,5 +87,12 @@ int launch_reduce(void* out, const float* tmp, const float* ml, const float* es,
                   const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
                   int np_max, int partition_size, const int32_t* prefix_blocks, int block_size,
                   int slot_split, int prefix_partition, cudaStream_t st);
+
+// The merge of the windowed form: a row has ceil(visible blocks /
+// (partition_size / block_size)) slots.
+int launch_reduce_window(void* out, const float* tmp, const float* ml, const float* es,
+                         const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
+                         int np_max, int partition_size, int block_size, int window, int sinks,
+                         cudaStream_t st);
 
 }  // namespace pkv

@@ -97,7 +97,14 @@ struct TcGeom {
 // BS = rows of a ring page; a pool block holds UPB such pages (UPB = 2 runs a
 // 32-token pool in 16-token pages), or a page holds BPP pool blocks (BPP = 2
 // runs a 16-token E4M3 pool in 32-row pages, split form only).
-template <int D, int BS, bool FP8, int NW, int NST, int UPB, int BPP>
+//
+// WIN: the windowed form. The blocks that the window and the sink tokens touch
+// take the place of the context's blocks (WindowBlocks: partitions and cluster
+// shares are runs of visible blocks, only they are read); rows of their pages
+// that are not visible get the logit -inf and a zero V row, as the rows behind
+// the context do. A 16-row page may then hold no visible row, so the running
+// maximum may still be -inf after it.
+template <int D, int BS, bool FP8, int NW, int NST, int UPB, int BPP, bool WIN>
 __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const DecodeParams p) {
@@ -155,8 +162,15 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
   // pool blocks [blk_begin, blk_end), BPP of them to a ring page
   int blk_begin = 0, blk_end = 0, nblk = 0;
   int tok0 = 0;  // first token of this CTA's pages
+  const WindowBlocks wb(ctx, WIN ? p.window : 1, WIN ? p.sinks : 0, PB);
   if constexpr (BPP == 1) {
-    blk_end = (ctx + BS - 1) / BS;
+    if constexpr (WIN)
+      // the last block's second page may lie behind the context
+      blk_end = wb.count > 0 ? (wb.count - 1) * UPB +
+                                   (ctx - wb.block_of(wb.count - 1) * PB + BS - 1) / BS
+                             : 0;
+    else
+      blk_end = (ctx + BS - 1) / BS;
     if (p.partition_blocks > 0) {
       blk_begin = (part * p.partition_blocks + (p.block_offset ? p.block_offset[s] : 0)) * UPB;
       if (blk_begin >= blk_end) return;  // partition past the end: nothing to store
@@ -171,7 +185,7 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
     nblk = blk_end - blk_begin;
     tok0 = blk_begin * BS;
   } else {
-    blk_end = (ctx + PB - 1) / PB;
+    blk_end = WIN ? wb.count : (ctx + PB - 1) / PB;
     blk_begin = part * p.partition_blocks + (p.block_offset ? p.block_offset[s] : 0);
     if (blk_begin >= blk_end) return;  // partition past the end: nothing to store
     blk_end = min(blk_end, blk_begin + p.partition_blocks);
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
         bool bad = false;
         if constexpr (BPP == 1) {
           const int u = blk_begin + it;  // page of the sequence
-          const int32_t pb = bt[u / UPB];
+          const int32_t pb = bt[WIN ? wb.block_of(u / UPB) : u / UPB];
           bad = pb < 0 || pb >= p.num_blocks;
           y[0] = bad ? 0 : (pb * p.num_kv_heads + h) * (BS * UPB) + (u % UPB) * BS;
           nb = 1;
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
           for (int b = 0; b < BPP; ++b) {
             const int q = blk_begin + BPP * it + b;
             if (q >= blk_end) break;
-            const int32_t pb = bt[q];
+            const int32_t pb = bt[WIN ? wb.block_of(q) : q];
             const bool ok_b = pb >= 0 && pb < p.num_blocks;
             bad = bad || !ok_b;
             y[b] = ok_b ? (pb * p.num_kv_heads + h) * PB : 0;
@@ -320,6 +334,22 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
                        : "memory");
       __syncwarp();
     };
+    // WIN: first tokens of the page's block (page, if UPB > 1) and of its
+    // second block, behind the context if there is none; tok(r): row r's token
+    int base0 = 0, base1 = 0;
+    auto tok = [&](int r) { return BPP == 1 || r < PB ? base0 + r : base1 + r - PB; };
+    // zero this warp's columns of the V rows that are not visible
+    auto zero_v_hidden = [&](uint32_t vpage) {
+      for (int r = 0; r < BS; ++r) {
+        if (wb.sees(tok(r), ctx)) continue;
+        for (int c = lane * 16; c < G::kDW * ESZ; c += 512)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                           swz_bytes<BS>(vpage, r, warp * G::kDW * ESZ + c)),
+                       "r"(0u)
+                       : "memory");
+      }
+      __syncwarp();
+    };
     bool ok = true;
     int slice = 0;  // 16-token slices so far (exchange buffer and phase)
     for (int it = 0; it < nblk && ok; ++it) {
@@ -328,12 +358,30 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
       const uint32_t kp = ring + st * G::kStage;
       const uint32_t vp = kp + PAGE;
       const int ntok = min(BS, tok_end - (tok0 + it * BS));
+      bool whole = true;  // WIN: every row of the page is visible
+      if constexpr (WIN) {
+        if constexpr (BPP == 1) {
+          const int u = blk_begin + it;
+          base0 = wb.block_of(u / UPB) * PB + (u % UPB) * BS;
+        } else {
+          const int v = blk_begin + BPP * it;
+          base0 = wb.block_of(v) * PB;
+          base1 = v + 1 < blk_end ? wb.block_of(v + 1) * PB : ctx;
+        }
+        auto run = [&](int t, int n) {
+          return t + n <= ctx && (t >= wb.win_begin || t + n <= wb.sink_end);
+        };
+        whole = BPP == 1 ? run(base0, BS) : run(base0, PB) && run(base1, PB);
+      }
       // V page of this stage waited for and its tail zeroed (with one barrier
       // pair per stage it landed with K: the tail is zeroed before the slices)
       bool vready = false;
       if constexpr (!G::kSplitKV) {
         vready = true;
-        zero_v_tail(vp, ntok);
+        if constexpr (!WIN)
+          zero_v_tail(vp, ntok);
+        else if (!whole)
+          zero_v_hidden(vp);
       }
       // one slice = kNH 16-row halves: their logits are exchanged once and
       // go through one max / rescale step of the online softmax
@@ -402,10 +450,12 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
             sv[3] += x.w;
           }
           const int t0 = r0 + 16 * hh + (lane >> 2), t1 = t0 + 8;
-          sc[hh][0] = t0 < ntok ? sv[0] * qs : -INFINITY;
-          sc[hh][1] = t0 < ntok ? sv[1] * qs : -INFINITY;
-          sc[hh][2] = t1 < ntok ? sv[2] * qs : -INFINITY;
-          sc[hh][3] = t1 < ntok ? sv[3] * qs : -INFINITY;
+          const bool see0 = WIN ? whole || wb.sees(tok(t0), ctx) : t0 < ntok;
+          const bool see1 = WIN ? whole || wb.sees(tok(t1), ctx) : t1 < ntok;
+          sc[hh][0] = see0 ? sv[0] * qs : -INFINITY;
+          sc[hh][1] = see0 ? sv[1] * qs : -INFINITY;
+          sc[hh][2] = see1 ? sv[2] * qs : -INFINITY;
+          sc[hh][3] = see1 ? sv[3] * qs : -INFINITY;
           mx0 = fmaxf(mx0, fmaxf(sc[hh][0], sc[hh][2]));
           mx1 = fmaxf(mx1, fmaxf(sc[hh][1], sc[hh][3]));
         }
@@ -416,7 +466,9 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
         }
         const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
         if (__any_sync(0xffffffffu, (mn0 > m0) || (mn1 > m1))) {
-          const float c0 = fast_exp2(m0 - mn0), c1 = fast_exp2(m1 - mn1);  // 0 when m was -inf
+          // 0 when m was -inf (WIN: 1 while it stays -inf)
+          const float c0 = WIN && !(mn0 > m0) ? 1.f : fast_exp2(m0 - mn0);
+          const float c1 = WIN && !(mn1 > m1) ? 1.f : fast_exp2(m1 - mn1);
           l0 *= c0;
           l1 *= c1;
 #pragma unroll
@@ -434,16 +486,22 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
             ok = false;
             break;
           }
-          zero_v_tail(vp, ntok);
+          if constexpr (!WIN)
+            zero_v_tail(vp, ntok);
+          else if (!whole)
+            zero_v_hidden(vp);
           vready = true;
         }
+        // every slice has a valid token in row 0 of the CTA's first page, so
+        // m is finite from the first slice on and masked logits give p = 0;
+        // WIN: a slice may have none, the reference is then any finite number
+        const float ref0 = WIN && m0 == -INFINITY ? 0.f : m0;
+        const float ref1 = WIN && m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
           const int rh = r0 + 16 * hh;  // first row of this half
-          // every slice has a valid token in row 0 of the CTA's first page, so
-          // m is finite from the first slice on and masked logits give p = 0
-          const float p00 = fast_exp2(sc[hh][0] - m0), p01 = fast_exp2(sc[hh][1] - m1);
-          const float p10 = fast_exp2(sc[hh][2] - m0), p11 = fast_exp2(sc[hh][3] - m1);
+          const float p00 = fast_exp2(sc[hh][0] - ref0), p01 = fast_exp2(sc[hh][1] - ref1);
+          const float p10 = fast_exp2(sc[hh][2] - ref0), p11 = fast_exp2(sc[hh][3] - ref1);
           l0 += p00 + p10;
           l1 += p01 + p11;
           if constexpr (!FP8) {
@@ -493,7 +551,7 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
         }
       }
       if (!ok) break;
-      if (ntok < BS) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (WIN ? !whole : ntok < BS) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(G::kSplitKV ? &vempty[st] : &empty[st]);
     }
@@ -682,7 +740,7 @@ int pool_tensor_map(CUtensorMap* out, const void* base, int64_t rows, int D, int
   return PKV_OK;
 }
 
-template <int D, int BS, bool FP8, int NW, int NST, int UPB = 1, int BPP = 1>
+template <bool WIN, int D, int BS, bool FP8, int NW, int NST, int UPB = 1, int BPP = 1>
 static int launch_tc(const DecodeParams& p_in, const void* k_cache, const void* v_cache,
                      dim3 grid, cudaStream_t st) {
   using G = TcGeom<D, BS, FP8, NW, NST>;
@@ -697,7 +755,7 @@ static int launch_tc(const DecodeParams& p_in, const void* k_cache, const void* 
   rc = pool_tensor_map(&tv, v_cache, rows, D, BPP == 1 ? BS : PB, FP8, BPP == 1);
   if (rc != PKV_OK) return rc;
   static DeviceFlags done;
-  auto kern = decode_tc_kernel<D, BS, FP8, NW, NST, UPB, BPP>;
+  auto kern = decode_tc_kernel<D, BS, FP8, NW, NST, UPB, BPP, WIN>;
   rc = ensure_smem(kern, G::kSmem, done);
   if (rc != PKV_OK) return rc;
   DecodeParams p = p_in;
@@ -757,7 +815,7 @@ static int launch_tc(const DecodeParams& p_in, const void* k_cache, const void* 
   return launch_status();
 }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 static int dispatch_tc(const DecodeParams& p, const void* k_cache, const void* v_cache,
                        int head_dim, int block_size, dim3 grid, cudaStream_t st) {
   // (consumer warps, ring stages). At d = 256 two stages and more CTAs per SM
@@ -779,31 +837,37 @@ static int dispatch_tc(const DecodeParams& p, const void* k_cache, const void* v
     // (GB300, same box: long-context shapes at B = 16 0.3338 -> 0.3227 ms per
     // decode, copy-on-write rollouts over an E4M3 cache 0.1533 -> 0.1460 ms)
     if constexpr (FP8)
-      if (p.partition_blocks > 0) return launch_tc<256, 32, FP8, 2, 2, 1, 2>(p, k_cache, v_cache, grid, st);
+      if (p.partition_blocks > 0) return launch_tc<WIN, 256, 32, FP8, 2, 2, 1, 2>(p, k_cache, v_cache, grid, st);
     if (p.partition_blocks > 0 && p.partition_blocks <= 48)
-      return launch_tc<256, 16, FP8, 2, 3>(p, k_cache, v_cache, grid, st);
-    return launch_tc<256, 16, FP8, 2, 2>(p, k_cache, v_cache, grid, st);
+      return launch_tc<WIN, 256, 16, FP8, 2, 3>(p, k_cache, v_cache, grid, st);
+    return launch_tc<WIN, 256, 16, FP8, 2, 2>(p, k_cache, v_cache, grid, st);
   }
   if (head_dim == 256 && block_size == 32) {
     if constexpr (FP8) {
-      return launch_tc<256, 32, FP8, 2, 2>(p, k_cache, v_cache, grid, st);
+      return launch_tc<WIN, 256, 32, FP8, 2, 2>(p, k_cache, v_cache, grid, st);
     } else {
       // 16-row pages, two per pool block (mixed lengths at 512-token
       // partitions, 32 pages: three stages 0.3305 -> 0.3271 ms)
       if (p.partition_blocks > 0 && 2 * p.partition_blocks <= 48)
-        return launch_tc<256, 16, FP8, 2, 3, 2>(p, k_cache, v_cache, grid, st);
-      return launch_tc<256, 16, FP8, 2, 2, 2>(p, k_cache, v_cache, grid, st);
+        return launch_tc<WIN, 256, 16, FP8, 2, 3, 2>(p, k_cache, v_cache, grid, st);
+      return launch_tc<WIN, 256, 16, FP8, 2, 2, 2>(p, k_cache, v_cache, grid, st);
     }
   }
   if (head_dim == 128 && block_size == 16)
-    return launch_tc<128, 16, FP8, 4, 8>(p, k_cache, v_cache, grid, st);
-  return launch_tc<128, 32, FP8, 4, 4>(p, k_cache, v_cache, grid, st);
+    return launch_tc<WIN, 128, 16, FP8, 4, 8>(p, k_cache, v_cache, grid, st);
+  return launch_tc<WIN, 128, 32, FP8, 4, 4>(p, k_cache, v_cache, grid, st);
 }
 
 int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_cache,
                      int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st) {
-  return fp8 ? dispatch_tc<true>(p, k_cache, v_cache, head_dim, block_size, grid, st)
-             : dispatch_tc<false>(p, k_cache, v_cache, head_dim, block_size, grid, st);
+  return fp8 ? dispatch_tc<true, false>(p, k_cache, v_cache, head_dim, block_size, grid, st)
+             : dispatch_tc<false, false>(p, k_cache, v_cache, head_dim, block_size, grid, st);
+}
+
+int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
+                         int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st) {
+  return fp8 ? dispatch_tc<true, true>(p, k_cache, v_cache, head_dim, block_size, grid, st)
+             : dispatch_tc<false, true>(p, k_cache, v_cache, head_dim, block_size, grid, st);
 }
 
 }  // namespace pkv

@@ -1,6 +1,5 @@
 // Attention of several query tokens per sequence (drafted tokens, a chain or
-// a tree) and of one query token through a sliding window with sink tokens,
-// over the paged cache.
+// a tree) over the paged cache.
 //
 // One CTA per (query row, query head); its warps take the visible tokens in
 // turn, each lane 1/32 of the head dimension, with an online softmax in fp32
@@ -23,13 +22,11 @@ struct RowsParams {
   const float* v_scale;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  const int32_t* q_start;      // NULL: one row per sequence
+  const int32_t* q_start;
   const uint64_t* tree_mask;
-  const int32_t* seq_order;    // window: the sequence of each x index, or NULL
   int* err;
   int num_seqs, num_blocks, num_kv_heads, num_heads, group, block_size, max_blocks_per_seq;
   int max_draft;
-  int64_t window, sinks;       // window 0: none
   float qscale;
 };
 
@@ -64,50 +61,36 @@ __global__ void __launch_bounds__(kRowsWarps * 32) rows_kernel(const RowsParams 
   __shared__ float sm_m[kRowsWarps], sm_l[kRowsWarps];
   __shared__ float sm_o[kRowsWarps][D];
   const int j = blockIdx.y, h = j / p.group;
-  int64_t row = blockIdx.x;
-  if (p.seq_order != nullptr) {
-    row = p.seq_order[row];
-    if (row < 0 || row >= p.num_seqs) {
-      if (threadIdx.x == 0 && j == 0) report_error(p.err, PKV_DEVERR_ORDER);
-      return;
-    }
-  }
+  const int64_t row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int s = static_cast<int>(row), i = 0, n = 1;
-  if (p.q_start != nullptr) {
-    // the sequence of this row: the last one that starts at or before it
-    int lo = 0, hi = p.num_seqs;
-    if (row < p.q_start[0] || row >= p.q_start[p.num_seqs]) return;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (p.q_start[mid] <= row) lo = mid; else hi = mid;
-    }
-    s = lo;
-    i = static_cast<int>(row) - p.q_start[s];
-    n = p.q_start[s + 1] - p.q_start[s];
+  // the sequence of this row: the last one that starts at or before it
+  if (row < p.q_start[0] || row >= p.q_start[p.num_seqs]) return;
+  int s = 0, hi = p.num_seqs;
+  while (hi - s > 1) {
+    const int mid = (s + hi) / 2;
+    if (p.q_start[mid] <= row) s = mid; else hi = mid;
   }
+  const int i = static_cast<int>(row) - p.q_start[s];
+  const int n = p.q_start[s + 1] - p.q_start[s];
   int ctx = p.context_lens[s];
   const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
   if (ctx < 0 || ctx > cap) {
     if (threadIdx.x == 0) report_error(p.err, PKV_DEVERR_CONTEXT);
     ctx = ctx < 0 ? 0 : static_cast<int>(cap);
   }
-  if (p.q_start != nullptr && (n > p.max_draft || n > ctx || i >= n)) {
+  if (n > p.max_draft || n > ctx || i >= n) {
     if (threadIdx.x == 0) report_error(p.err, PKV_DEVERR_DRAFT);
     return;
   }
-  const int base = p.q_start != nullptr ? ctx - n : ctx;
-  const uint64_t mask = p.q_start == nullptr ? 0
-                        : p.tree_mask != nullptr ? p.tree_mask[row]
-                                                 : (2ull << i) - 1;
-  const int64_t win0 = p.window > 0 ? ctx - p.window : 0;
+  const int base = ctx - n;
+  const uint64_t mask = p.tree_mask != nullptr ? p.tree_mask[row] : (2ull << i) - 1;
   float q[E], o[E], m = -INFINITY, l = 0.f;
   load_row<D, false>(reinterpret_cast<const uint8_t*>(p.q), (row * p.num_heads + j) * D, lane, q);
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   const float qs = FP8 ? p.qscale * p.k_scale[h] : p.qscale;
   for (int t = warp; t < ctx; t += kRowsWarps) {
-    const bool see = t < base ? (t < p.sinks || t >= win0) : (mask >> (t - base)) & 1;
+    const bool see = t < base || ((mask >> (t - base)) & 1);
     if (!see) continue;
     const int32_t b = p.block_tables[static_cast<int64_t>(s) * p.max_blocks_per_seq +
                                      t / p.block_size];
@@ -166,91 +149,7 @@ static int launch_rows(const RowsParams& p, int head_dim, bool fp8, int rows, cu
   return launch_status();
 }
 
-// Checks common to both calls; *group receives num_heads / num_kv_heads.
-static int check_call(const pkv_cache_desc& cache, const void* out, const void* q,
-                      const void* k_cache, const void* v_cache, const float* k_scale,
-                      const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
-                      const int32_t* context_lens, int num_seqs, int num_heads, int max_context,
-                      float scale, int* group) {
-  int rc = check_cache_desc(cache);
-  if (rc != PKV_OK) return rc;
-  if (num_seqs < 0 || num_heads <= 0 || max_context < 0 || max_blocks_per_seq <= 0)
-    return PKV_ERR_INVALID_ARG;
-  if (num_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
-  *group = num_heads / cache.num_kv_heads;
-  if (*group > 8) return PKV_ERR_UNSUPPORTED;
-  const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * cache.block_size;
-  if (max_context > cap) return PKV_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
-  if (num_seqs > 65535 || cap > INT_MAX) return PKV_ERR_UNSUPPORTED;
-  // TMA row coordinates are 32-bit
-  if (static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads * cache.block_size >=
-      (int64_t{1} << 31))
-    return PKV_ERR_UNSUPPORTED;
-  if (num_seqs == 0) return PKV_OK;
-  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || out == q)
-    return PKV_ERR_INVALID_ARG;
-  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
-    return PKV_ERR_INVALID_ARG;
-  if (cache.dtype == PKV_DTYPE_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
-  return PKV_OK;
-}
-
 }  // namespace pkv
-
-extern "C" int pkv_window_partition_size(int num_seqs, int num_kv_heads, int block_size,
-                                         int max_context, int window, int sinks) {
-  if (num_seqs < 0 || num_kv_heads <= 0 || (block_size != 16 && block_size != 32) ||
-      max_context < 0 || window <= 0 || sinks < 0)
-    return PKV_ERR_INVALID_ARG;
-  return 0;
-}
-
-extern "C" size_t pkv_window_workspace_bytes(int num_seqs, int num_heads, int head_dim,
-                                             int block_size, int max_context, int window,
-                                             int sinks, int partition_size) {
-  return 0;
-}
-
-extern "C" int pkv_paged_attention_window(
-    void* out, const void* q, const void* k_cache, const void* v_cache, pkv_cache_desc cache,
-    const float* k_scale, const float* v_scale, const int32_t* block_tables,
-    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_heads,
-    int max_context, float scale, int window, int sinks, int partition_size, void* workspace,
-    size_t workspace_bytes, const int32_t* seq_order, void* stream) {
-  using namespace pkv;
-  int g = 0;
-  int rc = check_call(cache, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                      max_blocks_per_seq, context_lens, num_seqs, num_heads, max_context, scale,
-                      &g);
-  if (rc != PKV_OK) return rc;
-  if (window <= 0 || sinks < 0 || partition_size < 0 || partition_size % cache.block_size != 0)
-    return PKV_ERR_INVALID_ARG;
-  if (num_seqs == 0) return PKV_OK;
-  RowsParams p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.out = static_cast<uint16_t*>(out);
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
-  p.v_cache = static_cast<const uint8_t*>(v_cache);
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.err = device_error_ptr();
-  p.num_seqs = num_seqs;
-  p.num_blocks = cache.num_blocks;
-  p.num_kv_heads = cache.num_kv_heads;
-  p.num_heads = num_heads;
-  p.group = g;
-  p.block_size = cache.block_size;
-  p.max_blocks_per_seq = max_blocks_per_seq;
-  p.window = window;
-  p.sinks = sinks;
-  p.seq_order = seq_order;
-  p.qscale = scale * 1.4426950408889634f;
-  return launch_rows(p, cache.head_dim, cache.dtype == PKV_DTYPE_FP8_E4M3, num_seqs,
-                     static_cast<cudaStream_t>(stream));
-}
 
 extern "C" size_t pkv_tree_workspace_bytes(int num_seqs, int num_queries, int num_heads,
                                            int num_kv_heads, int head_dim, int max_context,
@@ -266,7 +165,7 @@ extern "C" int pkv_paged_attention_tree(
     float scale, void* workspace, size_t workspace_bytes, void* stream) {
   using namespace pkv;
   int g = 0;
-  int rc = check_call(cache, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+  int rc = check_attention(cache, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                       max_blocks_per_seq, context_lens, num_queries > 0 ? num_seqs : 0, num_heads,
                       max_context, scale, &g);
   if (rc != PKV_OK) return rc;

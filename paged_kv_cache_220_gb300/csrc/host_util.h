@@ -2,6 +2,8 @@
 #pragma once
 
 #include <atomic>
+#include <climits>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -26,6 +28,36 @@ inline int check_cache_desc(const pkv_cache_desc& c) {
   if (c.block_size != 16 && c.block_size != 32) return PKV_ERR_UNSUPPORTED;
   if (c.head_dim != 128 && c.head_dim != 256) return PKV_ERR_UNSUPPORTED;
   if (c.num_kv_heads > 32) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+
+// Checks common to the window and the tree call; *group receives num_heads / num_kv_heads.
+inline int check_attention(const pkv_cache_desc& cache, const void* out, const void* q,
+                      const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* context_lens, int num_seqs, int num_heads, int max_context,
+                      float scale, int* group) {
+  int rc = check_cache_desc(cache);
+  if (rc != PKV_OK) return rc;
+  if (num_seqs < 0 || num_heads <= 0 || max_context < 0 || max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+  *group = num_heads / cache.num_kv_heads;
+  if (*group > 8) return PKV_ERR_UNSUPPORTED;
+  const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * cache.block_size;
+  if (max_context > cap) return PKV_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || cap > INT_MAX) return PKV_ERR_UNSUPPORTED;
+  // TMA row coordinates are 32-bit
+  if (static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads * cache.block_size >=
+      (int64_t{1} << 31))
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || out == q)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_ERR_INVALID_ARG;
+  if (cache.dtype == PKV_DTYPE_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
   return PKV_OK;
 }
 

@@ -44,13 +44,40 @@ __device__ __forceinline__ void row_slots(const int32_t* context_lens, const int
   }
 }
 
-template <int D, int kReduceWarps>
+// The slots of a row: of the plain and the shared-prefix form (row_slots), or
+// of the windowed one, whose slots are partitions of the visible blocks.
+struct SlotArgs {
+  const int32_t* prefix_blocks;
+  int partition_size, block_size, slot_split, prefix_partition;
+  int window, sinks;
+};
+
+template <bool WIN>
+__device__ __forceinline__ void slots_of_row(const int32_t* context_lens, const SlotArgs& a, int s,
+                                             int np_max, int* err, bool report, int& npre,
+                                             int& nsuf) {
+  if constexpr (WIN) {
+    const int ctx = min(max(0, context_lens[s]), 0x7FFFFF00);
+    const int per = a.partition_size / a.block_size;
+    npre = 0;
+    nsuf = (WindowBlocks(ctx, a.window, a.sinks, a.block_size).count + per - 1) / per;
+    if (nsuf > np_max) {
+      if (report) report_error(err, PKV_DEVERR_CONTEXT);
+      nsuf = np_max;
+    }
+  } else {
+    row_slots(context_lens, a.prefix_blocks, s, a.partition_size, a.block_size,
+              a.prefix_partition, a.slot_split, np_max, err, report, npre, nsuf);
+  }
+}
+
+template <int D, int kReduceWarps, bool WIN>
 __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
     uint16_t* __restrict__ out, const float* __restrict__ tmp_out,
     const float* __restrict__ max_logits, const float* __restrict__ exp_sums,
-    const int32_t* __restrict__ context_lens, int num_heads, int np_max, int partition_size,
-    const int32_t* __restrict__ prefix_blocks, int block_size, int slot_split,
-    int prefix_partition, int* err) {
+    const int32_t* __restrict__ context_lens, int num_heads, int np_max, const SlotArgs slots,
+    int* err) {
+  const int slot_split = slots.slot_split;
   constexpr int kReduceThreads = kReduceWarps * 32;
   // this CTA's 128 columns (blockIdx.z selects them): one float4 per lane
   const int c4 = blockIdx.z * 32;  // first float4 column
@@ -63,8 +90,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   int npre, nsuf;
-  row_slots(context_lens, prefix_blocks, s, partition_size, block_size, prefix_partition,
-            slot_split, np_max, err, tid == 0, npre, nsuf);
+  slots_of_row<WIN>(context_lens, slots, s, np_max, err, tid == 0, npre, nsuf);
   const int np = npre + nsuf;
   const int64_t row = static_cast<int64_t>(s) * num_heads + j;
   if (np == 0) {
@@ -153,13 +179,13 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
 
 constexpr int kRowWarps = 8;  // rows (warps) per CTA of the narrow merge
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
     uint16_t* __restrict__ out, const float* __restrict__ tmp_out,
     const float* __restrict__ max_logits, const float* __restrict__ exp_sums,
     const int32_t* __restrict__ context_lens, int num_rows, int num_heads, int np_max,
-    int partition_size, const int32_t* __restrict__ prefix_blocks, int block_size,
-    int slot_split, int prefix_partition, int* err) {
+    const SlotArgs slots, int* err) {
+  const int slot_split = slots.slot_split;
   constexpr int V4 = D / 128;  // float4 per lane per partition row
   constexpr int U = 4;         // partitions' loads in flight per lane
   wait_prerequisite();  // the partials come from the decode launched before
@@ -182,8 +208,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
       x[u][v] = u < np_max ? src[static_cast<int64_t>(u) * (D / 4) + lane + 32 * v]
                            : make_float4(0.f, 0.f, 0.f, 0.f);
   int npre, nsuf;
-  row_slots(context_lens, prefix_blocks, s, partition_size, block_size, prefix_partition,
-            slot_split, np_max, err, lane == 0, npre, nsuf);
+  slots_of_row<WIN>(context_lens, slots, s, np_max, err, lane == 0, npre, nsuf);
   const int np = npre + nsuf;  // <= np_max <= 32
   uint2* dst = reinterpret_cast<uint2*>(out + row * D);
   if (np == 0) {
@@ -258,46 +283,53 @@ __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
 
 namespace pkv {
 
-int launch_reduce(void* out, const float* tmp, const float* ml, const float* es,
-                  const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
-                  int np_max, int partition_size, const int32_t* prefix_blocks, int block_size,
-                  int slot_split, int prefix_partition, cudaStream_t st) {
-  const int pp = prefix_partition > 0 ? prefix_partition : partition_size;
-  uint16_t* o = static_cast<uint16_t*>(out);
+template <int D, bool WIN>
+static int launch_reduce_t(uint16_t* o, const float* tmp, const float* ml, const float* es,
+                           const int32_t* context_lens, int num_seqs, int num_heads, int np_max,
+                           const SlotArgs& slots, cudaStream_t st) {
   int* err = device_error_ptr();
   if (np_max <= 32) {
     // one warp per (sequence, query head) row
     const int rows = num_seqs * num_heads;
     const dim3 grid((rows + kRowWarps - 1) / kRowWarps);
-    if (head_dim == 128)
-      return launch_dependent(reduce_rows_kernel<128>, grid, dim3(kRowWarps * 32), 0, st, o, tmp,
-                              ml, es, context_lens, rows, num_heads, np_max, partition_size,
-                              prefix_blocks, block_size, slot_split, pp, err);
-    return launch_dependent(reduce_rows_kernel<256>, grid, dim3(kRowWarps * 32), 0, st, o, tmp, ml,
-                            es, context_lens, rows, num_heads, np_max, partition_size,
-                            prefix_blocks, block_size, slot_split, pp, err);
+    return launch_dependent(reduce_rows_kernel<D, WIN>, grid, dim3(kRowWarps * 32), 0, st, o, tmp,
+                            ml, es, context_lens, rows, num_heads, np_max, slots, err);
   }
   // one 16-warp CTA per row and 128 columns
   const size_t smem = static_cast<size_t>(np_max) * sizeof(float);
   constexpr size_t kMaxSmem = 160 * 1024;  // plus the static accumulators
   if (smem > kMaxSmem) return PKV_ERR_UNSUPPORTED;
-  const dim3 grid(num_heads, num_seqs, head_dim / 128);
-  if (head_dim == 128) {
-    static DeviceFlags done;
-    int rc = ensure_smem(reduce_kernel<128, 16>, kMaxSmem, done);
-    if (rc != PKV_OK) return rc;
-    return launch_dependent(reduce_kernel<128, 16>, grid, dim3(16 * 32), smem, st, o, tmp, ml, es,
-                            context_lens, num_heads, np_max, partition_size, prefix_blocks,
-                            block_size, slot_split, pp, err);
-  } else {
-    static DeviceFlags done;
-    int rc = ensure_smem(reduce_kernel<256, 16>, kMaxSmem, done);
-    if (rc != PKV_OK) return rc;
-    return launch_dependent(reduce_kernel<256, 16>, grid, dim3(16 * 32), smem, st, o, tmp, ml, es,
-                            context_lens, num_heads, np_max, partition_size, prefix_blocks,
-                            block_size, slot_split, pp, err);
-  }
-  return launch_status();
+  const dim3 grid(num_heads, num_seqs, D / 128);
+  static DeviceFlags done;
+  int rc = ensure_smem(reduce_kernel<D, 16, WIN>, kMaxSmem, done);
+  if (rc != PKV_OK) return rc;
+  return launch_dependent(reduce_kernel<D, 16, WIN>, grid, dim3(16 * 32), smem, st, o, tmp, ml, es,
+                          context_lens, num_heads, np_max, slots, err);
+}
+
+int launch_reduce(void* out, const float* tmp, const float* ml, const float* es,
+                  const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
+                  int np_max, int partition_size, const int32_t* prefix_blocks, int block_size,
+                  int slot_split, int prefix_partition, cudaStream_t st) {
+  const SlotArgs a{prefix_blocks, partition_size, block_size, slot_split,
+                   prefix_partition > 0 ? prefix_partition : partition_size, 0, 0};
+  uint16_t* o = static_cast<uint16_t*>(out);
+  return head_dim == 128 ? launch_reduce_t<128, false>(o, tmp, ml, es, context_lens, num_seqs,
+                                                       num_heads, np_max, a, st)
+                         : launch_reduce_t<256, false>(o, tmp, ml, es, context_lens, num_seqs,
+                                                       num_heads, np_max, a, st);
+}
+
+int launch_reduce_window(void* out, const float* tmp, const float* ml, const float* es,
+                         const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
+                         int np_max, int partition_size, int block_size, int window, int sinks,
+                         cudaStream_t st) {
+  const SlotArgs a{nullptr, partition_size, block_size, 0, partition_size, window, sinks};
+  uint16_t* o = static_cast<uint16_t*>(out);
+  return head_dim == 128 ? launch_reduce_t<128, true>(o, tmp, ml, es, context_lens, num_seqs,
+                                                      num_heads, np_max, a, st)
+                         : launch_reduce_t<256, true>(o, tmp, ml, es, context_lens, num_seqs,
+                                                      num_heads, np_max, a, st);
 }
 
 }  // namespace pkv

@@ -40,7 +40,9 @@ def test_window_refusals(lib):
                 dict(Hq=7), dict(Hq=0), dict(maxc=1025), dict(maxc=-1), dict(mb=0),
                 dict(scale=float("inf")), dict(out=None), dict(q=None), dict(k=None),
                 dict(bt=None), dict(out=FAKE), dict(q=ODD), dict(out=ODD), dict(k=ODD),
-                dict(desc=_desc(dt=1)), dict(desc=_desc(dt=2)), dict(desc=_desc(nb=0))):
+                dict(desc=_desc(dt=1)), dict(desc=_desc(dt=2)), dict(desc=_desc(nb=0)),
+                dict(P=16, ws=None), dict(P=16, ws=FAKE, wsb=16),
+                dict(P=16, ws=ODD, wsb=1 << 30)):
         assert call(**bad) == INV, bad
     for bad in (dict(Hq=18), dict(desc=_desc(bs=8)), dict(desc=_desc(d=64)), dict(S=65536),
                 dict(desc=_desc(nb=1 << 27)), dict(mb=1 << 28)):
