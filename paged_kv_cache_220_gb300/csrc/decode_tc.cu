@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
 
 // ---------------------------------------------------------------- host side
 
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -682,29 +682,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // Tensor map of one pool: 2-D with one box per 128-byte chunk of a page, or
-// 3-D with one box per whole page (declared in tc_common.cuh). Encodings are
-// cached per (pointer, shape, kind).
-int pool_tensor_map(CUtensorMap* out, const void* base, int64_t rows, int D, int BS,
-                    bool fp8, bool whole_page) {
-  struct Entry {
-    const void* base;
-    int64_t rows;
-    int d, bs;
-    bool fp8, whole_page;
-    CUtensorMap map;
-  };
-  static std::mutex mu;
-  static Entry cache[32];
-  static int used = 0, next = 0;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i)
-      if (cache[i].base == base && cache[i].rows == rows && cache[i].d == D &&
-          cache[i].bs == BS && cache[i].fp8 == fp8 && cache[i].whole_page == whole_page) {
-        *out = cache[i].map;
-        return PKV_OK;
-      }
-  }
+// 3-D with one box per whole page (declared in tc_common.cuh).
+int encode_pool_map(CUtensorMap* out, const void* base, int64_t rows, int D, int BS, bool fp8,
+                    bool whole_page) {
   auto enc = tensor_map_encoder();
   if (!enc) return PKV_ERR_CUDA;
   const int esz = fp8 ? 1 : 2;
@@ -731,6 +711,35 @@ int pool_tensor_map(CUtensorMap* out, const void* base, int64_t rows, int D, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
   if (r != CUDA_SUCCESS) return PKV_ERR_CUDA;
+  *out = m;
+  return PKV_OK;
+}
+
+// The same, cached per (pointer, shape, kind).
+int pool_tensor_map(CUtensorMap* out, const void* base, int64_t rows, int D, int BS,
+                    bool fp8, bool whole_page) {
+  struct Entry {
+    const void* base;
+    int64_t rows;
+    int d, bs;
+    bool fp8, whole_page;
+    CUtensorMap map;
+  };
+  static std::mutex mu;
+  static Entry cache[32];
+  static int used = 0, next = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+      if (cache[i].base == base && cache[i].rows == rows && cache[i].d == D &&
+          cache[i].bs == BS && cache[i].fp8 == fp8 && cache[i].whole_page == whole_page) {
+        *out = cache[i].map;
+        return PKV_OK;
+      }
+  }
+  CUtensorMap m;
+  const int rc = encode_pool_map(&m, base, rows, D, BS, fp8, whole_page);
+  if (rc != PKV_OK) return rc;
   std::lock_guard<std::mutex> lock(mu);
   Entry& e = cache[next];
   e = Entry{base, rows, D, BS, fp8, whole_page, m};
@@ -750,9 +759,10 @@ static int launch_tc(const DecodeParams& p_in, const void* k_cache, const void* 
   CUtensorMap tk, tv;
   // whole-page 3-D boxes, or (several blocks to a page) 2-D boxes of one
   // pool block and 128-byte chunk
-  int rc = pool_tensor_map(&tk, k_cache, rows, D, BPP == 1 ? BS : PB, FP8, BPP == 1);
+  constexpr auto pool_map = WIN ? encode_pool_map : pool_tensor_map;
+  int rc = pool_map(&tk, k_cache, rows, D, BPP == 1 ? BS : PB, FP8, BPP == 1);
   if (rc != PKV_OK) return rc;
-  rc = pool_tensor_map(&tv, v_cache, rows, D, BPP == 1 ? BS : PB, FP8, BPP == 1);
+  rc = pool_map(&tv, v_cache, rows, D, BPP == 1 ? BS : PB, FP8, BPP == 1);
   if (rc != PKV_OK) return rc;
   static DeviceFlags done;
   auto kern = decode_tc_kernel<D, BS, FP8, NW, NST, UPB, BPP, WIN>;

@@ -146,5 +146,10 @@ __device__ __forceinline__ uint32_t swz_bytes(uint32_t page, int row, int byte_c
 // Returns a pkv_status. (decode_tc.cu)
 int pool_tensor_map(CUtensorMap* out, const void* base, int64_t rows, int D, int BS, bool fp8,
                     bool whole_page = false);
+// The same map, encoded anew. (decode_tc.cu)
+int encode_pool_map(CUtensorMap* out, const void* base, int64_t rows, int D, int BS, bool fp8,
+                    bool whole_page);
+// cuTensorMapEncodeTiled, or NULL if the driver has none. (decode_tc.cu)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace pkv

@@ -81,7 +81,8 @@ def test_tree_refusals(lib):
     for bad in (dict(draft=0), dict(draft=65), dict(N=-1), dict(S=-1), dict(start=None),
                 dict(Hq=7), dict(maxc=1025), dict(mb=0), dict(scale=float("nan")),
                 dict(out=None), dict(q=None), dict(k=None), dict(bt=None), dict(out=FAKE),
-                dict(q=ODD), dict(out=ODD), dict(k=ODD), dict(desc=_desc(dt=1))):
+                dict(q=ODD), dict(out=ODD), dict(k=ODD), dict(desc=_desc(dt=1)),
+                dict(ws=FAKE, wsb=16), dict(ws=ODD, wsb=1 << 30), dict(ws=None)):
         assert call(**bad) == INV, bad
     for bad in (dict(Hq=18), dict(desc=_desc(bs=8)), dict(desc=_desc(d=64)), dict(S=65536),
                 dict(desc=_desc(nb=1 << 27)), dict(mb=1 << 28)):
