@@ -176,12 +176,40 @@ struct TreeWalk {
   }
 };
 
-// The ring's slot sequence numbers (the slot is number % slots): K of step t,
-// V of step t, of a CTA with `total` steps.
-template <int KS, int VS>
-__device__ __forceinline__ int64_t k_seq(int64_t t) {
-  return t == 0 ? 0 : KS + (t - 1) * (KS + VS);
+// A place in a ring of N: the producer waits for `empty` with parity ph ^ 1
+// (passes at once in the first round), the reader for `full` with parity ph.
+template <int N>
+struct RingPos {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// r / g for a row of a unit (r < 64 g, g <= 8): exact, no division.
+__device__ __forceinline__ int div_group(int r, int g) { return (r * (65536 / g + 1)) >> 16; }
+
+// 16 bytes global -> shared in the background; zeros if not `live`.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
 }
+
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// The number of V's first slot of step t in the ring's order (the slot is that
+// modulo the slots), of a CTA with `total` steps.
 template <int KS, int VS>
 __device__ __forceinline__ int64_t v_seq(int64_t t, int64_t total) {
   return KS + t * (KS + VS) + (t + 1 < total ? KS : 0);
@@ -304,7 +332,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       const int prod = warp - 5;  // takes the step's pages prod, prod + 2, ...
       const int B = p.block_size;
       const int per_v = G::kVTok / B;  // pages of a V slot
-      int64_t seq = 0;
+      RingPos<FP8 ? G::kNStage : NS> at;
       // this producer's block ids of one step, read well before they are used
       struct Step {
         int id[4];
@@ -323,11 +351,10 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       // the copies of one slot: K columns [128 part, 128 part + 128) of the
       // step's pages, or its pages of V slot `part`
       auto slot_copy = [&](const Step& x, bool is_v, int part) {
-        const int n = FP8 ? G::kNStage : NS;
-        const int i = static_cast<int>(seq % n);
+        const int i = at.i;
         uint64_t* f = FP8 ? &full8[i] : &full[i];
         uint64_t* e = FP8 ? &empty8[i] : &empty[i];
-        if (seq >= n && !mbar_wait(e, ((seq / n) - 1) & 1, p.err)) return false;
+        if (!mbar_wait(e, at.ph ^ 1, p.err)) return false;
         const int first = is_v ? part * per_v : 0;
         const int last = min(x.pages, is_v ? first + per_v : x.pages);
         const int page_bytes = B * (is_v ? D : 128) * (FP8 ? 1 : 2);
@@ -357,7 +384,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
             tma_load_2d(to, &tmk, part * 128, y, f);
           }
         }
-        issued = ++seq;
+        at.next();
+        ++issued;
         return true;
       };
       if (walk.left > 0) {
@@ -379,86 +407,97 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
     }
   } else if (warp == 4) {
-    // ---------------- the products, issued by one thread
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = FP8 ? umma_idesc_f16(128, kTreeTok, false)
-                                        : umma_idesc_bf16(128, kTreeTok, false);
-      constexpr uint32_t idesc_pv = FP8 ? umma_idesc_f16(128, D, true)
-                                        : umma_idesc_bf16(128, D, true);
-      int64_t t = 0;          // step of this CTA
-      int64_t segs = 0;       // segments whose S has begun
-      int64_t pv_segs = 0;    // segments whose P.V has begun
-      bool prev_begins = false;
-      int prev_tok = 0;       // valid tokens of the step before
-      for (;; ++t) {
-        const bool have = walk.left > 0;
-        if (have) {
-          const int b = static_cast<int>(t & 1);
-          // S of step t overwrites P of step t - 2
-          if (t >= 2 && !mbar_wait(&o_done[b], ((t - 2) >> 1) & 1, p.err)) break;
-          if (walk.begins) {
-            if (!mbar_wait(q_full, segs & 1, p.err)) break;
-            ++segs;
-          }
-          bool ok = true;
-          for (int ks = 0; ks < KS; ++ks) {
-            const int64_t seq = k_seq<KS, VS>(t) + ks;
-            const int i = static_cast<int>(seq % NS);
-            if (!(ok = mbar_wait(&full[i], (seq / NS) & 1, p.err))) break;
-            tc_fence_after();
-            const uint32_t kp = ring + i * G::kSlot;
+    // ---------------- the products: the whole warp walks, one lane issues.
+    // Operand descriptors are a constant plus the address: one addition each
+    // (built one by one they cost the issuing lane about as much as the
+    // tensor core takes for a product).
+    constexpr uint32_t idesc_qk = FP8 ? umma_idesc_f16(128, kTreeTok, false)
+                                      : umma_idesc_bf16(128, kTreeTok, false);
+    constexpr uint32_t idesc_pv = FP8 ? umma_idesc_f16(128, D, true)
+                                      : umma_idesc_bf16(128, D, true);
+    const bool lead = elect_one();
+    const uint64_t qd = umma_sdesc(sq, 16, NCH * 1024, 2);
+    const uint64_t kd0 = umma_sdesc(ring, 16, 2048, 2);
+    const uint64_t vd0 = umma_sdesc(ring, 1024, NCH * 1024, 2);
+    RingPos<NS> at;
+    uint32_t segs = 0;     // segments whose S has begun
+    uint32_t pv_segs = 0;  // segments whose P.V has begun
+    bool prev_begins = false;
+    int prev_tok = 0;      // valid tokens of the step before
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err)) != 0;
+    };
+    for (uint32_t t = 0;; ++t) {
+      const bool have = walk.left > 0;
+      if (have) {
+        const int b = t & 1;
+        // S of step t overwrites P of step t - 2
+        if (t >= 2 && !wait(&o_done[b], ((t - 2) >> 1) & 1)) break;
+        if (walk.begins && !wait(q_full, segs++ & 1)) break;
+        bool ok = true;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t a = umma_sdesc(sq + (ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32, 16,
-                                            NCH * 1024, 2);
-              const uint64_t bd = umma_sdesc(kp + (k >> 2) * 1024 + (k & 3) * 32, 16, 2048, 2);
-              umma_ss(t_s + b * kTreeTok, a, bd, idesc_qk, (ks > 0 || k > 0) ? 1u : 0u);
-            }
-            umma_commit(&empty[i]);
+        for (int ks = 0; ks < KS; ++ks) {
+          if (!(ok = wait(&full[at.i], at.ph))) break;
+          tc_fence_after();
+          if (lead) {
+            const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_ss(t_s + b * kTreeTok, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
+                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
+                      (ks > 0 || k > 0) ? 1u : 0u);
+            umma_commit(&empty[at.i]);
           }
-          if (!ok) break;
+          at.next();
+        }
+        if (!ok) break;
+        if (lead) {
           umma_commit(&s_full[b]);
           if (walk.ends()) umma_commit(q_empty);
         }
-        if (t >= 1) {
-          const int64_t j = t - 1;
-          const int b = static_cast<int>(j & 1);
-          if (!mbar_wait(&p_full[b], (j >> 1) & 1, p.err)) break;
-          if (prev_begins) {
-            // the segment before has left O
-            if (pv_segs > 0 && !mbar_wait(o_free, (pv_segs - 1) & 1, p.err)) break;
-            ++pv_segs;
-          }
-          const int ksteps = (prev_tok + 15) / 16;
-          bool ok = true;
-          // v_seq: K of step t was filled before V of step t - 1, if there is one
-          const int64_t v0 = KS + j * (KS + VS) + (have ? KS : 0);
-          for (int vs = 0; vs < VS; ++vs) {
-            const int64_t seq = v0 + vs;
-            const int i = static_cast<int>(seq % NS);
-            if (!(ok = mbar_wait(&full[i], (seq / NS) & 1, p.err))) break;
-            tc_fence_after();
-            const uint32_t vp = ring + i * G::kSlot;
-            const int k1 = min(ksteps - vs * (G::kVTok / 16), G::kVTok / 16);
-            for (int kk = 0; kk < k1; ++kk) {
-              const uint64_t vd = umma_sdesc(vp + kk * 2 * NCH * 1024, 1024, NCH * 1024, 2);
-              umma_bf16_ta(t_o, t_s + b * kTreeTok + 8 * (vs * (G::kVTok / 16) + kk), vd, idesc_pv,
-                           (!prev_begins || vs > 0 || kk > 0) ? 1u : 0u);
-            }
-            umma_commit(&empty[i]);
-          }
-          if (!ok) break;
-          umma_commit(&o_done[b]);
-        }
-        if (!have) break;
-        prev_begins = walk.begins;
-        prev_tok = min(kTreeTok, walk.q.ctx - walk.st * kTreeTok);
-        walk.next(p);
       }
-      // every product issued here has finished before tensor memory is released
-      umma_commit(drained);
-      (void)mbar_wait(drained, 0, p.err);
+      if (t >= 1) {
+        const uint32_t j = t - 1;
+        const int b = j & 1;
+        if (!wait(&p_full[b], (j >> 1) & 1)) break;
+        // the segment before has left O
+        if (prev_begins && pv_segs++ > 0 && !wait(o_free, (pv_segs - 2) & 1)) break;
+        bool ok = true;
+#pragma unroll
+        for (int vs = 0; vs < VS; ++vs) {
+          if (!(ok = wait(&full[at.i], at.ph))) break;
+          tc_fence_after();
+          if (lead) {
+            constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
+            const uint64_t vd = vd0 + ((at.i * G::kSlot) >> 4);
+            const uint32_t pa = t_s + b * kTreeTok + 8 * vs * kPer;
+            const int k1 = (prev_tok + 15) / 16 - vs * kPer;
+            const uint32_t keep = !prev_begins || vs > 0 ? 1u : 0u;
+            if (k1 >= kPer) {
+#pragma unroll
+              for (int kk = 0; kk < kPer; ++kk)
+                umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
+                             kk > 0 ? 1u : keep);
+            } else {
+              for (int kk = 0; kk < k1; ++kk)
+                umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
+                             kk > 0 ? 1u : keep);
+            }
+            umma_commit(&empty[at.i]);
+          }
+          at.next();
+        }
+        if (!ok) break;
+        if (lead) umma_commit(&o_done[b]);
+      }
+      if (!have) break;
+      prev_begins = walk.begins;
+      prev_tok = min(kTreeTok, walk.q.ctx - walk.st * kTreeTok);
+      walk.next(p);
     }
+    // every product issued here has finished before tensor memory is released
+    if (lead) umma_commit(drained);
+    (void)wait(drained, 0);
   } else if (warp < 4) {
     // ---------------- softmax: one query row per thread
     const int row = 32 * warp + lane;
@@ -477,8 +516,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       if (begins) {
         const int r = walk.tile * kTreeRows + row;
         live = r < walk.q.n * g;
-        draft = live ? r / g : 0;
-        head = walk.h * g + (live ? r % g : 0);
+        draft = live ? div_group(r, g) : 0;
+        head = walk.h * g + (live ? r - draft * g : 0);
         mask = p.tree_mask != nullptr ? p.tree_mask[walk.q.q0 + draft] : (2ull << draft) - 1;
         if (walk.q.n < 64) mask &= (1ull << walk.q.n) - 1;
         if constexpr (FP8) qs = p.qscale * p.k_scale[walk.h];
@@ -502,19 +541,25 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           else if (sh > -32) see[w] = static_cast<uint32_t>(mask << -sh) | ((1u << -sh) - 1);
         }
       }
-      float mx = -INFINITY;
       float sv[64];
+      float mx = -INFINITY;
+      {
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int hf = 1; hf >= 0; --hf) {
-        tmem_ld64(ts + 64 * hf, sv);
-        if (clean) {
+        for (int hf = 1; hf >= 0; --hf) {
+          tmem_ld64(ts + 64 * hf, sv);
+          if (clean) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) mx = fmaxf(mx, sv[i] * qs);
-        } else {
+            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i] * qs);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if ((see[2 * hf + i / 32] >> (i % 32)) & 1) mx = fmaxf(mx, sv[i] * qs);
+            for (int i = 0; i < 64; ++i) {
+              sv[i] = (see[2 * hf + i / 32] >> (i % 32)) & 1 ? sv[i] * qs : -INFINITY;
+              m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+            }
+          }
         }
+        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       }
       // O is rescaled when the maximum grows by more than 2^8 (loads and
       // stores of tensor memory are warp-collective: all lanes or none)
@@ -539,27 +584,37 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       const float ref = m == -INFINITY ? 0.f : m;
       // P over S's columns: the first half (still in registers) goes to columns
       // 0..31, then the second, read again, to columns 32..63
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         if (hf == 1) tmem_ld64(ts + 64, sv);
         uint32_t pw[32];
+        if (clean) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t word = see[2 * hf + i / 16];
-          const int bit = (2 * i) % 32;
-          float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
-          float c = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
-          if (!clean) {
-            a = (word >> bit) & 1 ? a : 0.f;
-            c = (word >> (bit + 1)) & 1 ? c : 0.f;
+          for (int i = 0; i < 32; ++i) {
+            const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
+            const float c = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
+            l4[(2 * i) & 3] += a;
+            l4[(2 * i + 1) & 3] += c;
+            pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
           }
-          l += a;
-          l += c;
-          pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t word = see[2 * hf + i / 16] >> ((2 * i) % 32);
+            // the first half was scaled and masked in place above
+            const float x = hf == 0 ? sv[2 * i] : word & 1 ? sv[2 * i] * qs : -INFINITY;
+            const float y = hf == 0 ? sv[2 * i + 1] : word & 2 ? sv[2 * i + 1] * qs : -INFINITY;
+            const float a = fast_exp2(x - ref), c = fast_exp2(y - ref);
+            l4[(2 * i) & 3] += a;
+            l4[(2 * i + 1) & 3] += c;
+            pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
+          }
         }
         tmem_st16_nowait(ts + 32 * hf, pw);
         tmem_st16_nowait(ts + 32 * hf + 16, pw + 16);
       }
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       const int valid = walk.q.ctx - tok0;
       if (valid < kTreeTok && (valid & 15) != 0) {
         // the rows behind the context that the last product of P.V covers
@@ -648,39 +703,47 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // swizzle); rows past the tile's query rows are zero
     const int i0 = threadIdx.x - 7 * 32;
     const int g = p.group;
-    int64_t seg = 0;
-    bool ok = true;
-    while (walk.left > 0 && ok) {
-      const int rows = min(kTreeRows, walk.q.n * g - walk.tile * kTreeRows);
-      if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (seg - 1) & 1, p.err));
-      if (!ok) break;
-      constexpr int U = D / 8;  // 16-byte units of a row
-      constexpr int kBatch = 16;
-      for (int x0 = i0; x0 < kTreeRows * U; x0 += kBatch * G::kQWarps * 32) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int x = x0 + e * G::kQWarps * 32, r = x / U, u = x % U;
-          v[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows) {
-            const int rr = walk.tile * kTreeRows + r;
-            v[e] = *reinterpret_cast<const uint4*>(
-                p.q + (static_cast<int64_t>(walk.q.q0 + rr / g) * p.num_heads + walk.h * g +
-                       rr % g) * D + u * 8);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int x = x0 + e * G::kQWarps * 32, r = x / U, u = x % U;
-          if constexpr (FP8) {
-            v[e].x = pack_f16(bf16lo(v[e].x), bf16hi(v[e].x));
-            v[e].y = pack_f16(bf16lo(v[e].y), bf16hi(v[e].y));
-            v[e].z = pack_f16(bf16lo(v[e].z), bf16hi(v[e].z));
-            v[e].w = pack_f16(bf16lo(v[e].w), bf16hi(v[e].w));
-          }
-          const uint32_t at = sq + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at ^ (((at >> 7) & 7u) << 4)),
-                       "r"(v[e].x), "r"(v[e].y), "r"(v[e].z), "r"(v[e].w)
+    constexpr int U = D / 8;  // 16-byte units of a row
+    constexpr int kStep = G::kQWarps * 32;
+    const int inv = 65536 / g + 1;
+    uint32_t seg = 0;
+    while (walk.left > 0) {
+      const int r0 = walk.tile * kTreeRows;
+      const int rows = min(kTreeRows, walk.q.n * g - r0);
+      const uint16_t* q0 = p.q + (static_cast<int64_t>(walk.q.q0) * p.num_heads + walk.h * g) * D;
+      // row r of the tile: draft (r0 + r) / g, group row (r0 + r) % g
+      auto row_of = [&](int r) {
+        const int dr = ((r0 + r) * inv) >> 16;
+        return q0 + (static_cast<int64_t>(dr) * p.num_heads + (r0 + r - dr * g)) * D;
+      };
+      // into L2 while the segment before is still being multiplied
+      for (int x = i0; x < rows * (D / 64); x += kStep)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(x / (D / 64)) + x % (D / 64) * 64));
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (seg & 1) ^ 1, p.err))) break;
+      auto place = [&](int r, int u) {
+        const uint32_t at = sq + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
+        return at ^ (((at >> 7) & 7u) << 4);
+      };
+#pragma unroll 4
+      for (int x = i0; x < kTreeRows * U; x += kStep) {
+        const int r = x / U, u = x % U;
+        cp_async16(place(r, u), row_of(r < rows ? r : 0) + u * 8, r < rows);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (FP8) {
+        // f16 operands: each thread converts the units it brought
+#pragma unroll 4
+        for (int x = i0; x < kTreeRows * U; x += kStep) {
+          const uint32_t at = place(x / U, x % U);
+          uint4 v;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(at));
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at),
+                       "r"(pack_f16(bf16lo(v.x), bf16hi(v.x))),
+                       "r"(pack_f16(bf16lo(v.y), bf16hi(v.y))),
+                       "r"(pack_f16(bf16lo(v.z), bf16hi(v.z))),
+                       "r"(pack_f16(bf16lo(v.w), bf16hi(v.w)))
                        : "memory");
         }
       }
@@ -693,20 +756,17 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   } else if constexpr (FP8) {
     // ---------------- converters: codes of a stage -> the f16 values of a slot
     const int ct = threadIdx.x - (7 + G::kQWarps) * 32;
-    const int64_t slots = count * (KS + VS);
     const int B = p.block_size;
-    for (int64_t seq = 0; seq < slots; ++seq) {
-      const int i8 = static_cast<int>(seq % G::kNStage), i = static_cast<int>(seq % NS);
-      if (!__all_sync(0xffffffffu, mbar_wait(&full8[i8], (seq / G::kNStage) & 1, p.err))) break;
-      if (seq >= NS &&
-          !__all_sync(0xffffffffu, mbar_wait(&empty[i], ((seq / NS) - 1) & 1, p.err)))
-        break;
-      // which slot this is: K slots of step 0, then (K of t + 1, V of t) rounds
-      bool is_v = false;
-      if (seq >= KS) {
-        const int64_t x = seq - KS, t = x / (KS + VS);
-        is_v = t + 1 >= count || x % (KS + VS) >= KS;
-      }
+    RingPos<FP8 ? G::kNStage : 1> from;
+    RingPos<NS> to;
+    // order of the slots: K(0), then K(t + 1) and V(t) for each step t
+    int64_t k_left = count * KS, v_left = count * VS;
+    int run = KS;  // slots of the kind at hand before the other kind's turn
+    bool is_v = false;
+    while (k_left + v_left > 0) {
+      const int i8 = from.i, i = to.i;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full8[i8], from.ph, p.err))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[i], to.ph ^ 1, p.err))) break;
       const uint32_t src0 = stage + i8 * G::kStage, dst0 = ring + i * G::kSlot;
       // codes per row: 128 (K; V at d = 128) or 256 (V at d = 256)
       const int nch = is_v ? NCH : 2;
@@ -737,6 +797,14 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       if (lane == 0) {
         mbar_arrive(&full[i]);
         mbar_arrive(&empty8[i8]);
+      }
+      from.next();
+      to.next();
+      (is_v ? v_left : k_left) -= 1;
+      if (--run == 0) {
+        // after K(0) comes K(1); V(t) follows K(t + 1), or stands alone at the end
+        is_v = k_left == 0 || (!is_v && k_left != (count - 1) * KS);
+        run = is_v ? VS : KS;
       }
     }
   }
