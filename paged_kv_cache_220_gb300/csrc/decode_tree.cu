@@ -29,15 +29,21 @@
 // each), V d/128 slots (64 or 128 tokens each). Slots are filled and used in
 // the order K(0), K(1), V(0), K(2), V(1), ...
 //
-// E4M3 pools: TMA stages the codes in a second ring; converter warps turn
-// them into their exact f16 values in the slots. Q is converted to f16, P is
-// f16; k_scale goes into the logits, v_scale into the output.
+// E4M3 pools: K's codes are the operand as they are (kind::f8f6f4). Q is split
+// into two E4M3 parts, q 2^e = hi + lo with a power of two per row that puts
+// the row's largest element in [128, 256): bf16 has 8 significant bits and
+// each part 4, so elements down to 2^-9 of the largest are exact and the rest
+// are off by at most 2^-17 of it. V's codes are staged by TMA and turned into
+// their exact f16 values by converter warps; P is f16. k_scale and the row's
+// 2^-e go into the logits, v_scale into the output.
 //
-// P is one bf16 part (2^-9 relative rounding of each weight, as many bits as
-// the output; a second part would double the P.V products).
+// P is one bf16 part (a rounding of each weight to as many bits as the output
+// has; a second part would double the P.V products).
 //
-// Warps: 0-3 softmax (thread t of warp w owns query row 32 w + t), 4 issues
-// the products, 5-6 load pages, 7(-8) load Q, 8-15 convert (E4M3).
+// Warps: 0-7 softmax (threads t and t + 128 own query row t, 64 of a step's
+// columns each; they exchange maxima through shared memory), 8 issues the
+// products; bf16: 9-11 load Q, 12-15 load pages; E4M3: 9-10 load pages, 11-14
+// convert V and load Q.
 #include <algorithm>
 #include <cmath>
 
@@ -72,7 +78,7 @@ struct TreeParams {
   const uint64_t* tree_mask;
   int* err;
   TreeMeta* meta;   // [ctas]
-  float* part_o;    // [ctas][2][128][d]
+  float* part_o;    // [ctas][2][d][128]: a column's rows side by side
   float* part_m;    // [ctas][2][128]
   float* part_l;
   int num_seqs, num_queries, max_draft;
@@ -83,19 +89,26 @@ struct TreeParams {
 
 template <int D, bool FP8>
 struct TreeGeom {
-  static constexpr int kSlot = 32768;
-  static constexpr int kQ = kTreeRows * D * 2;
-  static constexpr int kKS = D / 128;        // slots of a step's K
-  static constexpr int kVS = D / 128;        // slots of a step's V
+  static constexpr int kQ = kTreeRows * D * 2;  // E4M3: two parts of one byte
+  static constexpr int kSlot = 32768;           // bf16: a ring slot; E4M3: f16 values of V
+  static constexpr int kKS = FP8 ? 1 : D / 128;  // slots of a step's K
+  static constexpr int kVS = D / 128;            // slots of a step's V
   static constexpr int kVTok = kTreeTok / kVS;
-  static constexpr int kNSlot = FP8 ? 4 : (D == 256 ? 5 : 6);
-  static constexpr int kStage = kSlot / 2;   // E4M3: codes of a slot
-  static constexpr int kNStage = FP8 ? (D == 256 ? 2 : 4) : 0;
-  static constexpr int kProducers = 2;
-  static constexpr int kQWarps = FP8 ? 1 : 2;  // E4M3: 512 threads, 128 registers each
-  static constexpr int kConvWarps = FP8 ? 8 : 0;
-  static constexpr int kThreads = (4 + 1 + kProducers + kQWarps + kConvWarps) * 32;
-  static constexpr int kSmem = 2048 + kQ + kNSlot * kSlot + kNStage * kStage;
+  static constexpr int kNSlot = FP8 ? 2 : (D == 256 ? 5 : 6);
+  // E4M3: K's codes of a step, and staged codes of a V slot
+  static constexpr int kK8 = kTreeTok * D;
+  static constexpr int kNK8 = FP8 ? (D == 256 ? 2 : 4) : 0;
+  static constexpr int kV8 = kSlot / 2;
+  static constexpr int kNV8 = FP8 ? (D == 256 ? 2 : 4) : 0;
+  static constexpr int kSoftWarps = 8;
+  static constexpr int kMmaWarp = 8;
+  static constexpr int kProdWarp = FP8 ? 9 : 12, kProducers = FP8 ? 2 : 4;
+  static constexpr int kConvWarp = 11, kConvWarps = FP8 ? 4 : 0;
+  // bf16: warps of their own load Q; E4M3: the converters do
+  static constexpr int kQWarp = FP8 ? kConvWarp : 9, kQWarps = FP8 ? kConvWarps : 3;
+  static constexpr int kThreads = (FP8 ? 15 : 16) * 32;
+  static constexpr int kHead = 3072;  // barriers, exchange buffers
+  static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNK8 * kK8 + kNV8 * kV8;
   static constexpr uint32_t kColS = D;       // S of step t at kColS + 128 * (t & 1)
   static constexpr uint32_t kCols = 512;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -109,6 +122,22 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a, uint64_t b,
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// The same on E4M3 operands (32 bytes of a row each).
+__device__ __forceinline__ void umma_ss_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4 with E4M3 A and B (both K-major), fp32
+// accumulator.
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // One box of a 4-D pool map: chunk c, 8-row group y.
@@ -208,6 +237,109 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Loads a segment's Q into shared memory (K-major, 128-byte swizzle) with NW
+// warps; rows past the tile's query rows are zero.
+template <int D, bool FP8, int NW>
+struct TreeQ {
+  static constexpr int U = D / 8;     // 16-byte units of a row of q
+  static constexpr int RPW = 32 / U;  // rows a warp takes at a time
+  static constexpr int kRowStep = NW * RPW;
+  const uint16_t* q0;
+  int64_t draft_stride;  // elements from a draft's rows to the next one's
+  int r0, rows, inv, g, rl, rs, u;
+
+  __device__ __forceinline__ TreeQ(const TreeParams& p, const TreeWalk& w, int wi, int lane) {
+    g = p.group;
+    inv = 65536 / g + 1;
+    r0 = w.tile * kTreeRows;
+    rows = min(kTreeRows, w.q.n * g - r0);
+    rs = lane / U;
+    rl = wi * RPW + rs;  // first row of this lane
+    u = lane % U;
+    draft_stride = static_cast<int64_t>(p.num_heads) * D;
+    q0 = p.q + w.q.q0 * draft_stride + w.h * g * D + u * 8;
+  }
+  // this lane's unit of row r of the tile: draft (r0 + r) / g, group row (r0 + r) % g
+  __device__ __forceinline__ const uint16_t* unit_of(int r) const {
+    const int rr = r0 + (r < rows ? r : 0);
+    const int dr = (rr * inv) >> 16;
+    return q0 + dr * draft_stride + (rr - dr * g) * D;
+  }
+  // into L2 while the segment before is still being multiplied
+  __device__ __forceinline__ void prefetch() const {
+    if (u % 8 == 0)
+      for (int r = rl; r < rows; r += kRowStep)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(unit_of(r)));
+  }
+  // exps (E4M3): [128] exponents of the rows' scales
+  __device__ __forceinline__ void run(uint32_t sq, int8_t* exps) const {
+    if constexpr (!FP8) {
+      constexpr int NCH = D / 64;
+#pragma unroll 4
+      for (int r = rl; r < kTreeRows; r += kRowStep) {
+        const uint32_t at = sq + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
+        cp_async16(at ^ (((at >> 7) & 7u) << 4), unit_of(r), r < rows);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      constexpr int NC8 = D / 128;
+      constexpr int kBatch = 8;
+      for (int rb = rl; rb - rs < kTreeRows; rb += kBatch * kRowStep) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int r = rb + e * kRowStep;
+          v[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) v[e] = *reinterpret_cast<const uint4*>(unit_of(r));
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int r = rb + e * kRowStep;
+          float x[8] = {bf16lo(v[e].x), bf16hi(v[e].x), bf16lo(v[e].y), bf16hi(v[e].y),
+                        bf16lo(v[e].z), bf16hi(v[e].z), bf16lo(v[e].w), bf16hi(v[e].w)};
+          // the row's largest magnitude; as bit patterns, so NaN counts as largest
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+          for (int off = U / 2; off > 0; off >>= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+          // 2^ex puts it in [128, 256); zero and tiny rows are scaled by 2^100
+          const int ex = max(-120, min(100, 134 - static_cast<int>(top >> 23)));
+          const float up = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i] * up, c = x[2 * i + 1] * up;
+            const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE,
+                                                        __NV_E4M3);
+            const uint32_t back = e4m3x2_f16x2(h, 0);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            const uint32_t r2 = __nv_cvt_float2_to_fp8x2(make_float2(a - f.x, c - f.y),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            hi[i / 2] |= (h & 0xFFFFu) << (16 * (i & 1));
+            lo[i / 2] |= (r2 & 0xFFFFu) << (16 * (i & 1));
+          }
+          if (r < kTreeRows) {
+            // 8 codes of the row: half of a 16-byte unit
+            uint32_t at = sq + ((r / 8) * NC8 + u / 16) * 1024 + (r % 8) * 128 +
+                          ((u % 16) / 2) * 16;
+            at = (at ^ (((at >> 7) & 7u) << 4)) + (u & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
+                         : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kTreeRows * D),
+                         "r"(lo[0]), "r"(lo[1])
+                         : "memory");
+            if (u == 0)
+              exps[r] = static_cast<int8_t>(top >= 0x7F800000u ? -128 : ex);
+          }
+        }
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+};
+
 // The number of V's first slot of step t in the ring's order (the slot is that
 // modulo the slots), of a CTA with `total` steps.
 template <int KS, int VS>
@@ -220,29 +352,35 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                 const __grid_constant__ TreeParams p) {
   using G = TreeGeom<D, FP8>;
-  constexpr int NCH = D / 64;
+  constexpr int NCH = D / 64;    // 128-byte chunks of a 16-bit row
+  constexpr int NC8 = D / 128;   // of a row of codes
   constexpr int KS = G::kKS, VS = G::kVS, NS = G::kNSlot;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* sbase = smem_raw + (base - raw);
+  constexpr int NK8 = FP8 ? G::kNK8 : 1, NV8 = FP8 ? G::kNV8 : 1;
+  extern __shared__ __align__(1024) uint8_t sbase[];  // no room to align it by hand
+  const uint32_t base = smem_addr(sbase);
   uint64_t* full = reinterpret_cast<uint64_t*>(sbase);  // [NS] slot filled
   uint64_t* empty = full + 8;                            // [NS] slot read
-  uint64_t* full8 = empty + 8;                           // [NST] codes staged
-  uint64_t* empty8 = full8 + 4;                          // [NST] codes converted
+  uint64_t* kfull = empty + 8;                           // [NK8] K's codes in
+  uint64_t* kempty = kfull + 4;
+  uint64_t* full8 = kempty + 4;                          // [NV8] V's codes staged
+  uint64_t* empty8 = full8 + 4;
   uint64_t* s_full = empty8 + 4;                         // [2]
   uint64_t* p_full = s_full + 2;                         // [2]
   uint64_t* o_done = p_full + 2;                         // [2]
-  uint64_t* q_full = o_done + 2;
+  uint64_t* pair = o_done + 2;                           // [4] the two threads of a row
+  uint64_t* q_full = pair + 4;
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_free = q_empty + 1;
   uint64_t* drained = o_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 512);
-  int64_t* found = reinterpret_cast<int64_t*>(sbase + 520);    // sequence, offset in it
-  int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 544);     // [warps + 1]
-  const uint32_t sq = base + 1024;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 368);
+  int64_t* found = reinterpret_cast<int64_t*>(sbase + 376);    // sequence, offset in it
+  int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 400);     // [warps], until the share is known
+  int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 400);      // [4][128] E4M3: e of Q's rows
+  float* xch = reinterpret_cast<float*>(sbase + 1024);         // [2][2][128]
+  const uint32_t sq = base + G::kHead;
   const uint32_t ring = sq + G::kQ;
-  const uint32_t stage = ring + NS * G::kSlot;
+  const uint32_t k8 = ring + NS * G::kSlot;
+  const uint32_t v8 = k8 + G::kNK8 * G::kK8;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
@@ -251,25 +389,31 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       mbar_init(&full[i], FP8 ? G::kConvWarps : G::kProducers);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < G::kNStage; ++i) {
+    for (int i = 0; i < G::kNK8; ++i) {
+      mbar_init(&kfull[i], G::kProducers);
+      mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < G::kNV8; ++i) {
       mbar_init(&full8[i], G::kProducers);
       mbar_init(&empty8[i], G::kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], G::kSoftWarps * 32);
       mbar_init(&o_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 64);
     mbar_init(q_full, G::kQWarps * 32);
     mbar_init(q_empty, 1);
-    mbar_init(o_free, 128);
+    mbar_init(o_free, G::kSoftWarps * 32);
     mbar_init(drained, 1);
     fence_mbar_init();
     found[0] = 0;
     found[1] = 0;
   }
-  if (warp == 4) tmem_alloc(tmem_slot, G::kCols);
+  if (warp == G::kMmaWarp) tmem_alloc(tmem_slot, G::kCols);
   wait_prerequisite();
+  if ((base & 1023u) != 0 && threadIdx.x == 0) report_error(p.err, PKV_DEVERR_WAIT_TIMEOUT);
   if (threadIdx.x == 0) p.meta[cta] = TreeMeta{0, 0, 0, 0, 0, 0};
 
   // ---- this CTA's share of the line: every thread sums a run of sequences,
@@ -294,6 +438,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   int64_t before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < G::kThreads / 32; ++w) {
     if (w < warp) before += wsum[w];
     total += wsum[w];
@@ -325,17 +470,21 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   TreeWalk walk;
   walk.start(p, static_cast<int>(found[0]), found[1], count);
 
-  int64_t issued = 0;  // producers: slots (E4M3: stages) whose copies were started
-  if (warp == 5 || warp == 6) {
+  // producers: slots whose copies were started (E4M3: of K, of V)
+  int64_t issued = 0, issued_v = 0;
+  if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers) {
     // ---------------- producers: the block table walk and the TMA copies
     if (lane == 0) {
-      const int prod = warp - 5;  // takes the step's pages prod, prod + 2, ...
+      constexpr int NP = G::kProducers;
+      constexpr int NID = 8 / NP;            // ids of a step's pages per producer
+      const int prod = warp - G::kProdWarp;  // takes the step's pages prod, prod + NP, ...
       const int B = p.block_size;
       const int per_v = G::kVTok / B;  // pages of a V slot
-      RingPos<FP8 ? G::kNStage : NS> at;
+      RingPos<FP8 ? NK8 : NS> at;      // bf16: K's and V's slots are one ring
+      RingPos<NV8> at_v;
       // this producer's block ids of one step, read well before they are used
       struct Step {
-        int id[4];
+        int id[NID];
         int head, pages;
       };
       auto read = [&](const TreeWalk& w) {
@@ -345,47 +494,49 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         const int32_t* bt = p.block_tables + static_cast<int64_t>(w.s) * p.max_blocks_per_seq +
                             w.st * (kTreeTok / B);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x.id[j] = 2 * j + prod < x.pages ? bt[2 * j + prod] : 0;
+        for (int j = 0; j < NID; ++j) x.id[j] = NP * j + prod < x.pages ? bt[NP * j + prod] : 0;
         return x;
       };
-      // the copies of one slot: K columns [128 part, 128 part + 128) of the
-      // step's pages, or its pages of V slot `part`
+      // the copies of one slot: K columns [128 part, 128 part + 128) (E4M3: K
+      // as it is) of the step's pages, or its pages of V slot `part`
       auto slot_copy = [&](const Step& x, bool is_v, int part) {
-        const int i = at.i;
-        uint64_t* f = FP8 ? &full8[i] : &full[i];
-        uint64_t* e = FP8 ? &empty8[i] : &empty[i];
-        if (!mbar_wait(e, at.ph ^ 1, p.err)) return false;
+        uint64_t *f, *e;
+        uint32_t dst, ph;
+        if (!FP8) {
+          f = &full[at.i], e = &empty[at.i], dst = ring + at.i * G::kSlot, ph = at.ph;
+        } else if (is_v) {
+          f = &full8[at_v.i], e = &empty8[at_v.i], dst = v8 + at_v.i * G::kV8, ph = at_v.ph;
+        } else {
+          f = &kfull[at.i], e = &kempty[at.i], dst = k8 + at.i * G::kK8, ph = at.ph;
+        }
+        if (!mbar_wait(e, ph ^ 1, p.err)) return false;
         const int first = is_v ? part * per_v : 0;
         const int last = min(x.pages, is_v ? first + per_v : x.pages);
-        const int page_bytes = B * (is_v ? D : 128) * (FP8 ? 1 : 2);
+        const int page_bytes = FP8 ? B * D : B * (is_v ? D : 128) * 2;
         int good = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pg = 2 * j + prod;
+        for (int j = 0; j < NID; ++j) {
+          const int pg = NP * j + prod;
           if (pg < first || pg >= last) continue;
           if (x.id[j] >= 0 && x.id[j] < p.num_blocks) ++good;
           else report_error(p.err, PKV_DEVERR_BLOCK_ID);
         }
         mbar_arrive_expect_tx(f, good * page_bytes);
-        const uint32_t dst = FP8 ? stage + i * G::kStage : ring + i * G::kSlot;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pg = 2 * j + prod;
+        for (int j = 0; j < NID; ++j) {
+          const int pg = NP * j + prod;
           if (pg < first || pg >= last || x.id[j] < 0 || x.id[j] >= p.num_blocks) continue;
           const int y = (x.id[j] * p.num_kv_heads + x.head) * B;
-          const uint32_t to = dst + (pg - first) * page_bytes;
-          if constexpr (!FP8) {
-            tma_load_4d(to, is_v ? &tmv : &tmk, is_v ? 0 : 2 * part, y / 8, f);
-          } else if (is_v) {
-#pragma unroll
-            for (int c = 0; c < D / 128; ++c)
-              tma_load_2d(to + c * B * 128, &tmv, c * 128, y, f);
-          } else {
-            tma_load_2d(to, &tmk, part * 128, y, f);
-          }
+          tma_load_4d(dst + (pg - first) * page_bytes, is_v ? &tmv : &tmk,
+                      FP8 || is_v ? 0 : 2 * part, y / 8, f);
         }
-        at.next();
-        ++issued;
+        if (FP8 && is_v) {
+          at_v.next();
+          ++issued_v;
+        } else {
+          at.next();
+          ++issued;
+        }
         return true;
       };
       if (walk.left > 0) {
@@ -406,20 +557,21 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         }
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == G::kMmaWarp) {
     // ---------------- the products: the whole warp walks, one lane issues.
     // Operand descriptors are a constant plus the address: one addition each
     // (built one by one they cost the issuing lane about as much as the
     // tensor core takes for a product).
-    constexpr uint32_t idesc_qk = FP8 ? umma_idesc_f16(128, kTreeTok, false)
-                                      : umma_idesc_bf16(128, kTreeTok, false);
+    constexpr uint32_t idesc_qk =
+        FP8 ? umma_idesc_e4m3(128, kTreeTok) : umma_idesc_bf16(128, kTreeTok, false);
     constexpr uint32_t idesc_pv = FP8 ? umma_idesc_f16(128, D, true)
                                       : umma_idesc_bf16(128, D, true);
     const bool lead = elect_one();
-    const uint64_t qd = umma_sdesc(sq, 16, NCH * 1024, 2);
-    const uint64_t kd0 = umma_sdesc(ring, 16, 2048, 2);
+    const uint64_t qd = umma_sdesc(sq, 16, (FP8 ? NC8 : NCH) * 1024, 2);
+    const uint64_t kd0 = FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
     const uint64_t vd0 = umma_sdesc(ring, 1024, NCH * 1024, 2);
-    RingPos<NS> at;
+    RingPos<NS> at;        // bf16: K's and V's slots in turn; E4M3: V's
+    RingPos<NK8> at_k;     // E4M3: K's
     uint32_t segs = 0;     // segments whose S has begun
     uint32_t pv_segs = 0;  // segments whose P.V has begun
     bool prev_begins = false;
@@ -435,22 +587,41 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         if (t >= 2 && !wait(&o_done[b], ((t - 2) >> 1) & 1)) break;
         if (walk.begins && !wait(q_full, segs++ & 1)) break;
         bool ok = true;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          if (!(ok = wait(&full[at.i], at.ph))) break;
+        if constexpr (FP8) {
+          if (!wait(&kfull[at_k.i], at_k.ph)) break;
           tc_fence_after();
           if (lead) {
-            const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
+            const uint64_t kd = kd0 + ((at_k.i * G::kK8) >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ss(t_s + b * kTreeTok, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
-                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
-                      (ks > 0 || k > 0) ? 1u : 0u);
-            umma_commit(&empty[at.i]);
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                umma_ss_e4m3(t_s + b * kTreeTok,
+                             qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                             kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
+                             (part > 0 || k > 0) ? 1u : 0u);
+            umma_commit(&kempty[at_k.i]);
           }
-          at.next();
+          at_k.next();
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (!(ok = wait(&full[at.i], at.ph))) break;
+            tc_fence_after();
+            if (lead) {
+              const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                umma_ss(t_s + b * kTreeTok,
+                        qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
+                        kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
+                        (ks > 0 || k > 0) ? 1u : 0u);
+              umma_commit(&empty[at.i]);
+            }
+            at.next();
+          }
+          if (!ok) break;
         }
-        if (!ok) break;
         if (lead) {
           umma_commit(&s_full[b]);
           if (walk.ends()) umma_commit(q_empty);
@@ -498,10 +669,11 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // every product issued here has finished before tensor memory is released
     if (lead) umma_commit(drained);
     (void)wait(drained, 0);
-  } else if (warp < 4) {
-    // ---------------- softmax: one query row per thread
-    const int row = 32 * warp + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
+  } else if (warp < G::kSoftWarps) {
+    // ---------------- softmax: two threads per query row, 64 columns each
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = 32 * quad + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
     const int g = p.group;
     float m = -INFINITY, l = 0.f, qs = p.qscale;
     uint64_t mask = 0;
@@ -509,6 +681,18 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     int draft = 0, head = 0;
     int seg_st = 0;         // the segment's first step in its unit
     bool first_seg = true;  // of this share
+    uint32_t seg = 0;
+    uint32_t swaps = 0;     // exchanges with the row's other thread so far
+    // v of the row's other thread; false if it does not come
+    auto exchange = [&](float& v) {
+      float* x = xch + (swaps & 1) * 256;
+      x[half * 128 + row] = v;
+      mbar_arrive(&pair[quad]);
+      if (!__all_sync(0xffffffffu, mbar_wait(&pair[quad], swaps & 1, p.err))) return false;
+      ++swaps;
+      v = x[(half ^ 1) * 128 + row];
+      return true;
+    };
     for (int64_t t = 0; walk.left > 0; ++t) {
       const int b = static_cast<int>(t & 1);
       const int base_tok = walk.q.ctx - walk.q.n;
@@ -527,40 +711,42 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], (t >> 1) & 1, p.err))) break;
       tc_fence_after();
+      if constexpr (FP8)
+        if (begins) {
+          // infinite or NaN queries give NaN
+          const int ex = q_exp[(seg & 3) * 128 + row];
+          qs *= ex == -128 ? __uint_as_float(0x7FC00000u)
+                           : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        }
       const uint32_t ts = t_s + lane_off + b * kTreeTok;
       const int tok0 = walk.st * kTreeTok;
       const bool clean = tok0 + kTreeTok <= base_tok;  // committed tokens only
-      // visible columns of this row, 32 to a word
-      uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-      if (!clean) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int sh = tok0 + 32 * w - base_tok;  // draft of the word's first column
-          if (sh >= 64) see[w] = 0;
-          else if (sh >= 0) see[w] = static_cast<uint32_t>(mask >> sh);
-          else if (sh > -32) see[w] = static_cast<uint32_t>(mask << -sh) | ((1u << -sh) - 1);
-        }
-      }
       float sv[64];
-      float mx = -INFINITY;
-      {
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tmem_ld64(ts + 64 * half, sv);
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (!clean) {
+        // visible columns of this row: committed, or named by the mask
 #pragma unroll
-        for (int hf = 1; hf >= 0; --hf) {
-          tmem_ld64(ts + 64 * hf, sv);
-          if (clean) {
+        for (int w = 0; w < 2; ++w) {
+          const int sh = tok0 + 64 * half + 32 * w - base_tok;  // draft of the first column
+          uint32_t see = ~0u;
+          if (sh >= 64) see = 0;
+          else if (sh >= 0) see = static_cast<uint32_t>(mask >> sh);
+          else if (sh > -32) see = static_cast<uint32_t>(mask << -sh) | ((1u << -sh) - 1);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i] * qs);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              sv[i] = (see[2 * hf + i / 32] >> (i % 32)) & 1 ? sv[i] * qs : -INFINITY;
-              m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
-            }
-          }
+          for (int i = 0; i < 32; ++i)
+            sv[32 * w + i] = (see >> i) & 1 ? sv[32 * w + i] * qs : -INFINITY;
         }
-        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i] * qs);
       }
+      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      float other = mx;
+      if (!exchange(other)) break;
+      mx = fmaxf(mx, other);
       // O is rescaled when the maximum grows by more than 2^8 (loads and
       // stores of tensor memory are warp-collective: all lanes or none)
       const bool want = mx > m + 8.f;
@@ -571,7 +757,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         tc_fence_after();
         const float alpha = want ? fast_exp2(m - mx) : 1.f;  // 0 while m is -inf
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
           float ov[16];
           tmem_ld16(t_o + lane_off + c, ov);
 #pragma unroll
@@ -582,50 +768,47 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
       if (want) m = mx;
       const float ref = m == -INFINITY ? 0.f : m;
-      // P over S's columns: the first half (still in registers) goes to columns
-      // 0..31, then the second, read again, to columns 32..63
+      // P over S's columns (both threads of the row have read theirs): tokens
+      // 64 half .. go to columns 32 half ..
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t pw[32];
+      if (clean) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (hf == 1) tmem_ld64(ts + 64, sv);
-        uint32_t pw[32];
-        if (clean) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
-            const float c = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
-            l4[(2 * i) & 3] += a;
-            l4[(2 * i + 1) & 3] += c;
-            pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t word = see[2 * hf + i / 16] >> ((2 * i) % 32);
-            // the first half was scaled and masked in place above
-            const float x = hf == 0 ? sv[2 * i] : word & 1 ? sv[2 * i] * qs : -INFINITY;
-            const float y = hf == 0 ? sv[2 * i + 1] : word & 2 ? sv[2 * i + 1] * qs : -INFINITY;
-            const float a = fast_exp2(x - ref), c = fast_exp2(y - ref);
-            l4[(2 * i) & 3] += a;
-            l4[(2 * i + 1) & 3] += c;
-            pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
-          }
+        for (int i = 0; i < 32; ++i) {
+          const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
+          const float c = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
+          l4[(2 * i) & 3] += a;
+          l4[(2 * i + 1) & 3] += c;
+          pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
         }
-        tmem_st16_nowait(ts + 32 * hf, pw);
-        tmem_st16_nowait(ts + 32 * hf + 16, pw + 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float a = fast_exp2(sv[2 * i] - ref), c = fast_exp2(sv[2 * i + 1] - ref);
+          l4[(2 * i) & 3] += a;
+          l4[(2 * i + 1) & 3] += c;
+          pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
+        }
       }
+      tmem_st16_nowait(ts + 32 * half, pw);
+      tmem_st16_nowait(ts + 32 * half + 16, pw + 16);
       l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       const int valid = walk.q.ctx - tok0;
       if (valid < kTreeTok && (valid & 15) != 0) {
         // the rows behind the context that the last product of P.V covers
-        // hold whatever was there: zero them, P is zero there
-        const int64_t seq = v_seq<KS, VS>(t, count) + valid / G::kVTok;
+        // hold whatever was there: zero them, P is zero there. The step
+        // before is waited for first: its V may have been the slot's last
+        // use, and a wait must not be two phases ahead of its barrier
+        if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[(t - 1) & 1],
+                                                         ((t - 1) >> 1) & 1, p.err)))
+          break;
+        const int64_t seq = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
         const int i = static_cast<int>(seq % NS);
         if (!__all_sync(0xffffffffu, mbar_wait(&full[i], (seq / NS) & 1, p.err))) break;
         const uint32_t vp = ring + i * G::kSlot;
         const int r0 = valid % G::kVTok, r1 = (r0 + 15) & ~15;
         constexpr int U = NCH * 8;  // 16-byte units of a row
-        for (int x = threadIdx.x; x < (r1 - r0) * U; x += 128) {
+        for (int x = threadIdx.x; x < (r1 - r0) * U; x += G::kSoftWarps * 32) {
           const int r = r0 + x / U, u = x % U;
           const uint32_t at =
               vp + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
@@ -639,17 +822,22 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(&p_full[b]);
       if (walk.ends()) {
-        // ---- the segment's result
+        // ---- the segment's result, each thread d / 2 columns of its row
+        other = l;
+        if (!exchange(other)) break;
+        const float sum = half == 0 ? l + other : other + l;
         if (!__all_sync(0xffffffffu, mbar_wait(&o_done[b], (t >> 1) & 1, p.err))) break;
         tc_fence_after();
-        const float inv = l > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / l : 0.f;
+        const float inv = sum > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / sum : 0.f;
         const bool whole = seg_st == 0 && walk.st + 1 == walk.q.steps;
+        const int c0 = half * (D / 2);
         if (whole) {
-          uint16_t* dst = p.out + (static_cast<int64_t>(walk.q.q0 + draft) * p.num_heads + head) * D;
+          uint16_t* dst = p.out +
+                          (static_cast<int64_t>(walk.q.q0 + draft) * p.num_heads + head) * D + c0;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < D / 2; c += 16) {
             float ov[16];
-            tmem_ld16(t_o + lane_off + c, ov);
+            tmem_ld16(t_o + lane_off + c0 + c, ov);
             if (live) {
               uint32_t w[8];
 #pragma unroll
@@ -659,23 +847,21 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
             }
           }
         } else {
-          const int slot = first_seg ? 0 : 1;
-          const int64_t at = (static_cast<int64_t>(cta) * 2 + slot) * kTreeRows + row;
-          float* dst = p.part_o + at * D;
+          // a partial, a column's rows side by side: full lines per store
+          const int64_t part = static_cast<int64_t>(cta) * 2 + (first_seg ? 0 : 1);
+          float* dst = p.part_o + (part * D + c0) * kTreeRows + row;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < D / 2; c += 16) {
             float ov[16];
-            tmem_ld16(t_o + lane_off + c, ov);
+            tmem_ld16(t_o + lane_off + c0 + c, ov);
             if (live) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(dst + c + i) =
-                    make_float4(ov[i] * inv, ov[i + 1] * inv, ov[i + 2] * inv, ov[i + 3] * inv);
+              for (int i = 0; i < 16; ++i) dst[(c + i) * kTreeRows] = ov[i] * inv;
             }
           }
-          if (live) {
-            p.part_m[at] = m;
-            p.part_l[at] = l;
+          if (live && half == 0) {
+            p.part_m[part * kTreeRows + row] = m;
+            p.part_l[part * kTreeRows + row] = sum;
           }
         }
         tc_fence_before();
@@ -695,116 +881,89 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           p.meta[cta] = md;
         }
         first_seg = false;
+        ++seg;
       }
       walk.next(p);
     }
-  } else if (warp < 7 + G::kQWarps) {
-    // ---------------- Q of each segment into shared memory (K-major, 128-byte
-    // swizzle); rows past the tile's query rows are zero
-    const int i0 = threadIdx.x - 7 * 32;
-    const int g = p.group;
-    constexpr int U = D / 8;  // 16-byte units of a row
-    constexpr int kStep = G::kQWarps * 32;
-    const int inv = 65536 / g + 1;
-    uint32_t seg = 0;
-    while (walk.left > 0) {
-      const int r0 = walk.tile * kTreeRows;
-      const int rows = min(kTreeRows, walk.q.n * g - r0);
-      const uint16_t* q0 = p.q + (static_cast<int64_t>(walk.q.q0) * p.num_heads + walk.h * g) * D;
-      // row r of the tile: draft (r0 + r) / g, group row (r0 + r) % g
-      auto row_of = [&](int r) {
-        const int dr = ((r0 + r) * inv) >> 16;
-        return q0 + (static_cast<int64_t>(dr) * p.num_heads + (r0 + r - dr * g)) * D;
-      };
-      // into L2 while the segment before is still being multiplied
-      for (int x = i0; x < rows * (D / 64); x += kStep)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(x / (D / 64)) + x % (D / 64) * 64));
+  } else if (!FP8 && warp >= G::kQWarp && warp < G::kQWarp + G::kQWarps) {
+    // ---------------- Q of each segment
+    for (uint32_t seg = 0; walk.left > 0; ++seg) {
+      const TreeQ<D, FP8, G::kQWarps> load(p, walk, warp - G::kQWarp, lane);
+      load.prefetch();
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (seg & 1) ^ 1, p.err))) break;
-      auto place = [&](int r, int u) {
-        const uint32_t at = sq + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
-        return at ^ (((at >> 7) & 7u) << 4);
-      };
-#pragma unroll 4
-      for (int x = i0; x < kTreeRows * U; x += kStep) {
-        const int r = x / U, u = x % U;
-        cp_async16(place(r, u), row_of(r < rows ? r : 0) + u * 8, r < rows);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if constexpr (FP8) {
-        // f16 operands: each thread converts the units it brought
-#pragma unroll 4
-        for (int x = i0; x < kTreeRows * U; x += kStep) {
-          const uint32_t at = place(x / U, x % U);
-          uint4 v;
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(at));
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at),
-                       "r"(pack_f16(bf16lo(v.x), bf16hi(v.x))),
-                       "r"(pack_f16(bf16lo(v.y), bf16hi(v.y))),
-                       "r"(pack_f16(bf16lo(v.z), bf16hi(v.z))),
-                       "r"(pack_f16(bf16lo(v.w), bf16hi(v.w)))
-                       : "memory");
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      load.run(sq, nullptr);
       mbar_arrive(q_full);
-      ++seg;
       while (!walk.ends()) walk.next(p);
       walk.next(p);
     }
   } else if constexpr (FP8) {
-    // ---------------- converters: codes of a stage -> the f16 values of a slot
-    const int ct = threadIdx.x - (7 + G::kQWarps) * 32;
-    const int B = p.block_size;
-    RingPos<FP8 ? G::kNStage : 1> from;
+    // ---------------- converters: a staged V slot's codes -> their f16 values
+    const int ct = threadIdx.x - G::kConvWarp * 32;
+    constexpr int UPR = D / 16;  // 16-code units of a row
+    constexpr int kUnits = G::kV8 / 16 / (G::kConvWarps * 32);
+    RingPos<NV8> from;
     RingPos<NS> to;
-    // order of the slots: K(0), then K(t + 1) and V(t) for each step t
-    int64_t k_left = count * KS, v_left = count * VS;
-    int run = KS;  // slots of the kind at hand before the other kind's turn
-    bool is_v = false;
-    while (k_left + v_left > 0) {
-      const int i8 = from.i, i = to.i;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full8[i8], from.ph, p.err))) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[i], to.ph ^ 1, p.err))) break;
-      const uint32_t src0 = stage + i8 * G::kStage, dst0 = ring + i * G::kSlot;
-      // codes per row: 128 (K; V at d = 128) or 256 (V at d = 256)
-      const int nch = is_v ? NCH : 2;
-      const int upr = is_v ? D / 16 : 8;  // 16-code units of a row
-      for (int x = ct; x < G::kStage / 16; x += G::kConvWarps * 32) {
-        const int u = x % upr, r = x / upr;
-        // staged page: [128-code chunk][B rows][128 B]
-        const int pg = r / B, rr = r % B;
-        uint32_t src = src0 + pg * B * upr * 16 + (u >> 3) * B * 128 + rr * 128 + (u & 7) * 16;
+    // Q of a segment is loaded as soon as V of the segment before is converted
+    // and its last S is done
+    auto load_q = [&](uint32_t seg) {
+      const TreeQ<D, FP8, G::kQWarps> load(p, walk, warp - G::kConvWarp, lane);
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (seg & 1) ^ 1, p.err))) return false;
+      load.run(sq, q_exp + (seg & 3) * 128);
+      mbar_arrive(q_full);
+      return true;
+    };
+    uint32_t seg = 0;
+    bool ok = walk.left <= 0 || load_q(seg++);
+    for (int vs = 0; walk.left > 0 && ok;) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full8[from.i], from.ph, p.err)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&empty[to.i], to.ph ^ 1, p.err)))) break;
+      const uint32_t src0 = v8 + from.i * G::kV8, dst0 = ring + to.i * G::kSlot;
+      uint32_t c[kUnits][4];
+#pragma unroll
+      for (int e = 0; e < kUnits; ++e) {
+        const int x = ct + e * G::kConvWarps * 32, u = x % UPR, r = x / UPR;
+        uint32_t src = src0 + ((r / 8) * NC8 + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
         src ^= ((src >> 7) & 7u) << 4;
-        uint32_t dst = dst0 + ((r / 8) * nch + u / 4) * 1024 + (r % 8) * 128 + (u % 4) * 32;
-        const uint32_t sw = ((dst >> 7) & 7u) << 4;
-        uint32_t c0, c1, c2, c3;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(c0), "=r"(c1), "=r"(c2), "=r"(c3)
+                     : "=r"(c[e][0]), "=r"(c[e][1]), "=r"(c[e][2]), "=r"(c[e][3])
                      : "r"(src));
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst ^ sw),
-                     "r"(e4m3x2_f16x2(c0, 0)), "r"(e4m3x2_f16x2(c0, 1)), "r"(e4m3x2_f16x2(c1, 0)),
-                     "r"(e4m3x2_f16x2(c1, 1))
+      }
+#pragma unroll
+      for (int e = 0; e < kUnits; ++e) {
+        const int x = ct + e * G::kConvWarps * 32, u = x % UPR, r = x / UPR;
+        uint32_t dst = dst0 + ((r / 8) * NCH + u / 4) * 1024 + (r % 8) * 128 + (u % 4) * 32;
+        dst ^= ((dst >> 7) & 7u) << 4;
+        // odd chunks store their second half first: the two chunks of a
+        // quarter-warp then use different banks
+        const bool odd = (u >> 2) & 1;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = e4m3x2_f16x2(c[e][i], 0);
+          w[2 * i + 1] = e4m3x2_f16x2(c[e][i], 1);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(odd ? dst ^ 16 : dst),
+                     "r"(odd ? w[4] : w[0]), "r"(odd ? w[5] : w[1]), "r"(odd ? w[6] : w[2]),
+                     "r"(odd ? w[7] : w[3])
                      : "memory");
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"((dst + 16) ^ sw),
-                     "r"(e4m3x2_f16x2(c2, 0)), "r"(e4m3x2_f16x2(c2, 1)), "r"(e4m3x2_f16x2(c3, 0)),
-                     "r"(e4m3x2_f16x2(c3, 1))
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(odd ? dst : dst ^ 16),
+                     "r"(odd ? w[0] : w[4]), "r"(odd ? w[1] : w[5]), "r"(odd ? w[2] : w[6]),
+                     "r"(odd ? w[3] : w[7])
                      : "memory");
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&full[i]);
-        mbar_arrive(&empty8[i8]);
+        mbar_arrive(&full[to.i]);
+        mbar_arrive(&empty8[from.i]);
       }
       from.next();
       to.next();
-      (is_v ? v_left : k_left) -= 1;
-      if (--run == 0) {
-        // after K(0) comes K(1); V(t) follows K(t + 1), or stands alone at the end
-        is_v = k_left == 0 || (!is_v && k_left != (count - 1) * KS);
-        run = is_v ? VS : KS;
+      if (++vs == VS) {
+        vs = 0;
+        const bool last = walk.ends();
+        walk.next(p);
+        if (last && walk.left > 0) ok = load_q(seg++);
       }
     }
   }
@@ -812,86 +971,112 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   allow_dependents();  // the merge may be scheduled; it waits for this grid
   tc_fence_before();
   __syncthreads();
-  if ((warp == 5 || warp == 6) && lane == 0) {
+  if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers && lane == 0) {
     // no copy may still be writing this CTA's shared memory when it exits
-    const int n = FP8 ? G::kNStage : NS;
-    for (int64_t seq = issued > n ? issued - n : 0; seq < issued; ++seq)
-      if (!mbar_wait(FP8 ? &full8[seq % n] : &full[seq % n], (seq / n) & 1, p.err)) break;
+    const int n = FP8 ? NK8 : NS;
+    uint64_t* f = FP8 ? kfull : full;
+    for (int64_t i = issued > n ? issued - n : 0; i < issued; ++i)
+      if (!mbar_wait(&f[i % n], (i / n) & 1, p.err)) break;
+    for (int64_t i = issued_v > NV8 ? issued_v - NV8 : 0; i < issued_v; ++i)
+      if (!mbar_wait(&full8[i % NV8], (i / NV8) & 1, p.err)) break;
   }
-  if (warp == 4) {
+  if (warp == G::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, G::kCols);
   }
 }
 
-// Joins the partials of the units that were cut: CTA (c, y) takes rows
-// 8 y .. 8 y + 7 of the unit that starts in share c, one warp per row. With
-// m_i, l_i, o_i of the unit's segments in order, M = max m_i (base 2) and
-// w_i = l_i 2^(m_i - M): out = sum (w_i / sum w) o_i.
+// Joins the partials of the units that were cut: CTA (c, y) takes columns
+// 16 y .. of the unit that starts in share c, thread (i, r) of it the parts
+// i, i + 4, ... of row r. With m_i, l_i, o_i of the unit's segments, M = max m_i
+// (base 2) and w_i = l_i 2^(m_i - M): out = sum (w_i / sum w) o_i.
+constexpr int kMergeCols = 16, kMergeGroups = 4;
+
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kMergeGroups * kTreeRows)
+    tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ float sm_m[kMergeGroups][kTreeRows], sm_w[kMergeGroups][kTreeRows];
+  __shared__ float sm_o[kMergeGroups][kMergeCols][kTreeRows];
   wait_prerequisite();
   const int c = blockIdx.x;
   const TreeMeta md = p.meta[c];
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (md.parts == 0 || row >= md.rows) return;
+  if (md.parts == 0) return;
+  const int row = threadIdx.x % kTreeRows, grp = threadIdx.x / kTreeRows;
+  const int c0 = blockIdx.y * kMergeCols;
+  const bool live = row < md.rows;
   // partial i: the first is share c's, the others are slot 0 of the next shares
-  auto at = [&](int i) {
-    return (static_cast<int64_t>(c + i) * 2 + (i == 0 ? md.slot : 0)) * kTreeRows + row;
-  };
-  float M = -INFINITY;
-  for (int i = lane; i < md.parts; i += 32) M = fmaxf(M, p.part_m[at(i)]);
+  auto at = [&](int i) { return static_cast<int64_t>(c + i) * 2 + (i == 0 ? md.slot : 0); };
+  float M = -INFINITY, W = 0.f, acc[kMergeCols];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float W = 0.f;
-  for (int i = lane; i < md.parts; i += 32) W += p.part_l[at(i)] * fast_exp2(p.part_m[at(i)] - ref);
+  for (int i = 0; i < kMergeCols; ++i) acc[i] = 0.f;
+  if (live) {
+    for (int i = grp; i < md.parts; i += kMergeGroups)
+      M = fmaxf(M, p.part_m[at(i) * kTreeRows + row]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 2
+    for (int i = grp; i < md.parts; i += kMergeGroups) {
+      const float* src = p.part_o + (at(i) * D + c0) * kTreeRows + row;
+      float x[kMergeCols];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
-  const float inv = W > 0.f ? 1.f / W : 0.f;
-  constexpr int V4 = D / 128;
-  float4 acc[V4];
+      for (int e = 0; e < kMergeCols; ++e) x[e] = src[e * kTreeRows];
+      const float w = p.part_l[at(i) * kTreeRows + row] *
+                      fast_exp2(p.part_m[at(i) * kTreeRows + row] - ref);
+      W += w;
 #pragma unroll
-  for (int v = 0; v < V4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < md.parts; ++i) {
-    const float w = p.part_l[at(i)] * fast_exp2(p.part_m[at(i)] - ref) * inv;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + at(i) * D);
-#pragma unroll
-    for (int v = 0; v < V4; ++v) {
-      const float4 x = src[lane + 32 * v];
-      acc[v].x = fmaf(w, x.x, acc[v].x);
-      acc[v].y = fmaf(w, x.y, acc[v].y);
-      acc[v].z = fmaf(w, x.z, acc[v].z);
-      acc[v].w = fmaf(w, x.w, acc[v].w);
+      for (int e = 0; e < kMergeCols; ++e) acc[e] = fmaf(w, x[e], acc[e]);
     }
   }
-  const int r = md.first + row;
-  const int64_t hq = static_cast<int64_t>(md.row0 + r / p.group) * p.num_heads +
-                     md.head * p.group + r % p.group;
-  uint2* dst = reinterpret_cast<uint2*>(p.out + hq * D);
+  sm_m[grp][row] = M;
+  sm_w[grp][row] = W;
 #pragma unroll
-  for (int v = 0; v < V4; ++v)
-    dst[lane + 32 * v] = make_uint2(pack_bf16(acc[v].x, acc[v].y), pack_bf16(acc[v].z, acc[v].w));
+  for (int e = 0; e < kMergeCols; ++e) sm_o[grp][e][row] = acc[e];
+  __syncthreads();
+  if (!live) return;
+  float top = sm_m[0][row];
+#pragma unroll
+  for (int i = 1; i < kMergeGroups; ++i) top = fmaxf(top, sm_m[i][row]);
+  float f[kMergeGroups], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeGroups; ++i) {
+    f[i] = sm_m[i][row] == -INFINITY ? 0.f : fast_exp2(sm_m[i][row] - top);
+    sum = fmaf(f[i], sm_w[i][row], sum);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  constexpr int E = kMergeCols / kMergeGroups;  // this thread's columns
+  float o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeGroups; ++i) x = fmaf(f[i], sm_o[i][grp * E + e][row], x);
+    o[e] = x * inv;
+  }
+  const int r = md.first + row, draft = div_group(r, p.group);
+  const int64_t hq = static_cast<int64_t>(md.row0 + draft) * p.num_heads + md.head * p.group +
+                     (r - draft * p.group);
+  *reinterpret_cast<uint2*>(p.out + hq * D + c0 + grp * E) =
+      make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
 }
 
 // ---------------------------------------------------------------- host side
 
-// 4-D map of a bf16 pool, [8-row group][64-column chunk][8 rows][64 columns],
-// boxes of `chunks` chunks of one page.
-static int tree_pool_map(CUtensorMap* out, const void* base, int64_t rows, int D, int B,
+// 4-D map of a pool, [8-row group][128-byte chunk][8 rows][128 bytes], boxes of
+// `chunks` chunks of one page.
+static int tree_pool_map(CUtensorMap* out, const void* base, int64_t rows, int D, int B, bool fp8,
                          int chunks) {
   auto enc = tensor_map_encoder();
   if (!enc) return PKV_ERR_CUDA;
-  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
-  cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(rows / 8)};
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * (fp8 ? 1 : 2);
+  const cuuint32_t elems = fp8 ? 128 : 64;
+  cuuint64_t dims[4] = {elems, 8, row / 128, static_cast<cuuint64_t>(rows / 8)};
   cuuint64_t strides[3] = {row, 128, 8 * row};
-  cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(chunks), static_cast<cuuint32_t>(B / 8)};
+  cuuint32_t box[4] = {elems, 8, static_cast<cuuint32_t>(chunks), static_cast<cuuint32_t>(B / 8)};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r =
-      enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
-          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      enc(out, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -901,11 +1086,9 @@ static int launch_tree(const TreeParams& p, const void* k_cache, const void* v_c
   using G = TreeGeom<D, FP8>;
   const int64_t rows = static_cast<int64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   CUtensorMap tk, tv;
-  int rc = FP8 ? encode_pool_map(&tk, k_cache, rows, D, p.block_size, true, false)
-               : tree_pool_map(&tk, k_cache, rows, D, p.block_size, 2);
+  int rc = tree_pool_map(&tk, k_cache, rows, D, p.block_size, FP8, FP8 ? D / 128 : 2);
   if (rc != PKV_OK) return rc;
-  rc = FP8 ? encode_pool_map(&tv, v_cache, rows, D, p.block_size, true, false)
-           : tree_pool_map(&tv, v_cache, rows, D, p.block_size, D / 64);
+  rc = tree_pool_map(&tv, v_cache, rows, D, p.block_size, FP8, FP8 ? D / 128 : D / 64);
   if (rc != PKV_OK) return rc;
   static DeviceFlags done;
   auto kern = tree_kernel<D, FP8>;
@@ -913,7 +1096,8 @@ static int launch_tree(const TreeParams& p, const void* k_cache, const void* v_c
   if (rc != PKV_OK) return rc;
   rc = launch_dependent(kern, dim3(ctas), dim3(G::kThreads), G::kSmem, st, tk, tv, p);
   if (rc != PKV_OK) return rc;
-  return launch_dependent(tree_merge_kernel<D>, dim3(ctas, kTreeRows / 8), dim3(256), 0, st, p);
+  return launch_dependent(tree_merge_kernel<D>, dim3(ctas, D / kMergeCols),
+                          dim3(kMergeGroups * kTreeRows), 0, st, p);
 }
 
 }  // namespace pkv

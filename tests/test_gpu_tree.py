@@ -283,6 +283,24 @@ def test_repeats_streams_and_graphs(fp8, _lib):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_slow_first_loads(fp8, _lib):
+    """Fresh caches whose pages come from memory and whose last pages hold NaN
+    behind the context: what the kernel masks may not depend on when a page
+    arrives (first and second run give the same finite bits)."""
+    lens, drafts = [2000, 60, 700, 9, 1500], [8, 60, 1, 9, 3]
+    start = starts(drafts)
+    q = queries(start[-1], 8, 256, seed=21)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(60):
+        c = Cache(lens, 2, 256, 16, fp8, seed=100 + i)
+        flush.fill_(i)
+        a = call(c, q, start, drafts, None, 0.0625)
+        b = call(c, q, start, drafts, None, 0.0625)
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b), i
+    assert int(_lib.item()) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_large_pool(fp8, _lib):
     """Blocks whose element offsets pass 2^32."""
     nb = (1 << 32) // (4 * 32 * 256) + 2000
