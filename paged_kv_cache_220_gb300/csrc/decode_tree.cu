@@ -35,7 +35,7 @@
 // each part 4, so elements down to 2^-9 of the largest are exact and the rest
 // are off by at most 2^-17 of it. V's codes are staged by TMA and turned into
 // their exact f16 values by converter warps; P is f16. k_scale and the row's
-// 2^-e go into the logits, v_scale into the output.
+// 2^-e go into the logits, v_scale into the output. The ring's slots are 16 KB of codes.
 //
 // P is one bf16 part (a rounding of each weight to as many bits as the output
 // has; a second part would double the P.V products).
@@ -90,16 +90,15 @@ struct TreeParams {
 template <int D, bool FP8>
 struct TreeGeom {
   static constexpr int kQ = kTreeRows * D * 2;  // E4M3: two parts of one byte
-  static constexpr int kSlot = 32768;           // bf16: a ring slot; E4M3: f16 values of V
-  static constexpr int kKS = FP8 ? 1 : D / 128;  // slots of a step's K
-  static constexpr int kVS = D / 128;            // slots of a step's V
+  static constexpr int kKS = D / 128;           // slots of a step's K
+  static constexpr int kVS = D / 128;           // slots of a step's V
   static constexpr int kVTok = kTreeTok / kVS;
-  static constexpr int kNSlot = FP8 ? 2 : (D == 256 ? 5 : 6);
-  // E4M3: K's codes of a step, and staged codes of a V slot
-  static constexpr int kK8 = kTreeTok * D;
-  static constexpr int kNK8 = FP8 ? (D == 256 ? 2 : 4) : 0;
-  static constexpr int kV8 = kSlot / 2;
-  static constexpr int kNV8 = FP8 ? (D == 256 ? 2 : 4) : 0;
+  // the ring that TMA fills: 16-bit values, or codes
+  static constexpr int kSlot = FP8 ? 16384 : 32768;
+  static constexpr int kNSlot = FP8 ? (D == 256 ? 6 : 8) : (D == 256 ? 5 : 6);
+  // E4M3: V's f16 values, two slots
+  static constexpr int kV16 = 32768;
+  static constexpr int kNV16 = FP8 ? 2 : 0;
   static constexpr int kSoftWarps = 8;
   static constexpr int kMmaWarp = 8;
   static constexpr int kProdWarp = FP8 ? 9 : 12, kProducers = FP8 ? 2 : 4;
@@ -108,7 +107,7 @@ struct TreeGeom {
   static constexpr int kQWarp = FP8 ? kConvWarp : 9, kQWarps = FP8 ? kConvWarps : 3;
   static constexpr int kThreads = (FP8 ? 15 : 16) * 32;
   static constexpr int kHead = 3072;  // barriers, exchange buffers
-  static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNK8 * kK8 + kNV8 * kV8;
+  static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNV16 * kV16;
   static constexpr uint32_t kColS = D;       // S of step t at kColS + 128 * (t & 1)
   static constexpr uint32_t kCols = 512;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -142,11 +141,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
 
 // One box of a 4-D pool map: chunk c, 8-row group y.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c, int y,
-                                            uint64_t* bar) {
+                                            uint64_t* bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(c), "r"(y), "r"(smem_addr(bar))
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(c), "r"(y), "r"(smem_addr(bar)),
+      "l"(policy)
       : "memory");
 }
 
@@ -154,18 +154,21 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 // drafts or a context that cannot be).
 struct TreeSeq {
   int ctx, n, q0, tiles, steps;
-  __device__ __forceinline__ void load(const TreeParams& p, int s, bool report) {
-    q0 = p.q_start[s];
-    const int q1 = p.q_start[s + 1];
-    ctx = p.context_lens[s];
+  __device__ __forceinline__ void set(const TreeParams& p, int first, int next, int context,
+                                      bool report) {
+    q0 = first;
+    ctx = context;
     const bool ctx_ok =
         ctx >= 0 && ctx <= static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
-    const bool ok = ctx_ok && q0 >= 0 && q1 >= q0 && q1 <= p.num_queries &&
-                    q1 - q0 <= p.max_draft && q1 - q0 <= ctx;
+    const bool ok = ctx_ok && q0 >= 0 && next >= q0 && next <= p.num_queries &&
+                    next - q0 <= p.max_draft && next - q0 <= ctx;
     if (!ok && report) report_error(p.err, ctx_ok ? PKV_DEVERR_DRAFT : PKV_DEVERR_CONTEXT);
-    n = ok ? q1 - q0 : 0;
+    n = ok ? next - q0 : 0;
     tiles = (n * p.group + kTreeRows - 1) / kTreeRows;
     steps = ok ? (ctx + kTreeTok - 1) / kTreeTok : 0;
+  }
+  __device__ __forceinline__ void load(const TreeParams& p, int s, bool report) {
+    set(p, p.q_start[s], p.q_start[s + 1], p.context_lens[s], report);
   }
   __device__ __forceinline__ int64_t weight(const TreeParams& p) const {
     return static_cast<int64_t>(p.num_kv_heads) * tiles * steps;
@@ -178,16 +181,27 @@ struct TreeWalk {
   int s, h, tile, st;   // the current step
   int64_t left;         // steps left, this one included
   bool begins;          // first step of a segment
-  __device__ __forceinline__ void start(const TreeParams& p, int s0, int64_t off, int64_t count) {
+  int next_q0, next_q1, next_ctx;  // of sequence s + 1, read when s is entered
+  __device__ __forceinline__ void peek(const TreeParams& p) {
+    const int x = min(s + 1, p.num_seqs - 1);
+    next_q0 = p.q_start[x];
+    next_q1 = p.q_start[x + 1];
+    next_ctx = p.context_lens[x];
+  }
+  // off: the share's first step, counted from sequence s0's first
+  __device__ __forceinline__ void start(const TreeParams& p, const TreeSeq& q0, int s0,
+                                        int64_t off, int64_t count) {
+    q = q0;
     s = s0;
     left = count;
     begins = true;
+    h = tile = st = 0;
     if (count <= 0) return;
-    q.load(p, s, false);
+    peek(p);
     const int64_t unit = off / q.steps;
     st = static_cast<int>(off - unit * q.steps);
-    h = static_cast<int>(unit / q.tiles);
-    tile = static_cast<int>(unit % q.tiles);
+    h = static_cast<int>(unit) / q.tiles;
+    tile = static_cast<int>(unit) % q.tiles;
   }
   __device__ __forceinline__ bool ends() const { return left == 1 || st + 1 == q.steps; }
   __device__ __forceinline__ void next(const TreeParams& p) {
@@ -200,8 +214,10 @@ struct TreeWalk {
     tile = 0;
     if (++h < p.num_kv_heads) return;
     h = 0;
-    do q.load(p, ++s, false);
-    while (q.tiles == 0 && s + 1 < p.num_seqs);
+    q.set(p, next_q0, next_q1, next_ctx, false);
+    ++s;
+    while (q.tiles == 0 && s + 1 < p.num_seqs) q.load(p, ++s, false);
+    peek(p);
   }
 };
 
@@ -275,10 +291,17 @@ struct TreeQ {
   __device__ __forceinline__ void run(uint32_t sq, int8_t* exps) const {
     if constexpr (!FP8) {
       constexpr int NCH = D / 64;
-#pragma unroll 4
-      for (int r = rl; r < kTreeRows; r += kRowStep) {
-        const uint32_t at = sq + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
-        cp_async16(at ^ (((at >> 7) & 7u) << 4), unit_of(r), r < rows);
+      constexpr int kBatch = 11;  // rows whose addresses are worked out together
+      for (int rb = rl; rb < kTreeRows; rb += kBatch * kRowStep) {
+        const uint16_t* src[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) src[e] = unit_of(rb + e * kRowStep);
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int r = rb + e * kRowStep;
+          const uint32_t at = sq + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
+          if (r < kTreeRows) cp_async16(at ^ (((at >> 7) & 7u) << 4), src[e], r < rows);
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -355,16 +378,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   constexpr int NCH = D / 64;    // 128-byte chunks of a 16-bit row
   constexpr int NC8 = D / 128;   // of a row of codes
   constexpr int KS = G::kKS, VS = G::kVS, NS = G::kNSlot;
-  constexpr int NK8 = FP8 ? G::kNK8 : 1, NV8 = FP8 ? G::kNV8 : 1;
   extern __shared__ __align__(1024) uint8_t sbase[];  // no room to align it by hand
   const uint32_t base = smem_addr(sbase);
   uint64_t* full = reinterpret_cast<uint64_t*>(sbase);  // [NS] slot filled
   uint64_t* empty = full + 8;                            // [NS] slot read
-  uint64_t* kfull = empty + 8;                           // [NK8] K's codes in
-  uint64_t* kempty = kfull + 4;
-  uint64_t* full8 = kempty + 4;                          // [NV8] V's codes staged
-  uint64_t* empty8 = full8 + 4;
-  uint64_t* s_full = empty8 + 4;                         // [2]
+  uint64_t* vfull = empty + 8;                           // [2] E4M3: V converted
+  uint64_t* vempty = vfull + 2;                          // [2]
+  uint64_t* s_full = vempty + 2;                         // [2]
   uint64_t* p_full = s_full + 2;                         // [2]
   uint64_t* o_done = p_full + 2;                         // [2]
   uint64_t* pair = o_done + 2;                           // [4] the two threads of a row
@@ -372,30 +392,29 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_free = q_empty + 1;
   uint64_t* drained = o_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 368);
-  int64_t* found = reinterpret_cast<int64_t*>(sbase + 376);    // sequence, offset in it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 320);
+  int* found = reinterpret_cast<int*>(sbase + 328);            // sequence, its TreeSeq
+  int64_t* found_off = reinterpret_cast<int64_t*>(sbase + 352);  // the share's first step in it
   int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 400);     // [warps], until the share is known
   int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 400);      // [4][128] E4M3: e of Q's rows
+  int32_t* ids = reinterpret_cast<int32_t*>(sbase + 912);      // [3][8] block ids of three steps
   float* xch = reinterpret_cast<float*>(sbase + 1024);         // [2][2][128]
   const uint32_t sq = base + G::kHead;
   const uint32_t ring = sq + G::kQ;
-  const uint32_t k8 = ring + NS * G::kSlot;
-  const uint32_t v8 = k8 + G::kNK8 * G::kK8;
+  const uint32_t v16 = FP8 ? ring + NS * G::kSlot : ring;  // V's 16-bit values
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], FP8 ? G::kConvWarps : G::kProducers);
-      mbar_init(&empty[i], 1);
+      mbar_init(&full[i], G::kProducers);
+      // E4M3: a V slot is released by the converter warps, a K slot by the
+      // products (one arrival) and the issuing lane (the others)
+      mbar_init(&empty[i], FP8 ? G::kConvWarps : 1);
     }
-    for (int i = 0; i < G::kNK8; ++i) {
-      mbar_init(&kfull[i], G::kProducers);
-      mbar_init(&kempty[i], 1);
-    }
-    for (int i = 0; i < G::kNV8; ++i) {
-      mbar_init(&full8[i], G::kProducers);
-      mbar_init(&empty8[i], G::kConvWarps);
+    for (int i = 0; i < G::kNV16; ++i) {
+      mbar_init(&vfull[i], G::kConvWarps);
+      mbar_init(&vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -408,13 +427,11 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     mbar_init(o_free, G::kSoftWarps * 32);
     mbar_init(drained, 1);
     fence_mbar_init();
-    found[0] = 0;
-    found[1] = 0;
   }
   if (warp == G::kMmaWarp) tmem_alloc(tmem_slot, G::kCols);
   wait_prerequisite();
   if ((base & 1023u) != 0 && threadIdx.x == 0) report_error(p.err, PKV_DEVERR_WAIT_TIMEOUT);
-  if (threadIdx.x == 0) p.meta[cta] = TreeMeta{0, 0, 0, 0, 0, 0};
+  if (threadIdx.x == G::kProdWarp * 32) p.meta[cta] = TreeMeta{0, 0, 0, 0, 0, 0};
 
   // ---- this CTA's share of the line: every thread sums a run of sequences,
   // the thread whose run holds the share's first step finds its sequence
@@ -422,10 +439,10 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   const int s_lo = min(p.num_seqs, static_cast<int>(threadIdx.x) * per);
   const int s_hi = min(p.num_seqs, s_lo + per);
   int64_t mine = 0;
+  TreeSeq seq;  // the run's last sequence (its only one, for small batches)
   for (int s = s_lo; s < s_hi; ++s) {
-    TreeSeq q;
-    q.load(p, s, cta == 0);
-    mine += q.weight(p);
+    seq.load(p, s, cta == 0);
+    mine += seq.weight(p);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -451,110 +468,180 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   const int64_t count = end - begin;
   if (count > 0 && excl <= begin && begin < excl + mine) {
     int64_t at = excl;
-    for (int s = s_lo; s < s_hi; ++s) {
-      TreeSeq q;
-      q.load(p, s, false);
-      const int64_t w = q.weight(p);
-      if (begin < at + w) {
-        found[0] = s;
-        found[1] = begin - at;
-        break;
+    int s = s_lo;
+    if (per > 1) {
+      for (;; ++s) {
+        seq.load(p, s, false);
+        if (begin < at + seq.weight(p)) break;
+        at += seq.weight(p);
       }
-      at += w;
     }
+    found[0] = s;
+    found[1] = seq.ctx;
+    found[2] = seq.n;
+    found[3] = seq.q0;
+    found[4] = seq.tiles;
+    found[5] = seq.steps;
+    *found_off = begin - at;
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_o = tmem;
   const uint32_t t_s = tmem + G::kColS;
   TreeWalk walk;
-  walk.start(p, static_cast<int>(found[0]), found[1], count);
+  walk.start(p, TreeSeq{found[1], found[2], found[3], found[4], found[5]}, found[0],
+             *found_off, count);
 
-  // producers: slots whose copies were started (E4M3: of K, of V)
-  int64_t issued = 0, issued_v = 0;
+  int64_t issued = 0;  // producers: slots whose copies were started
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers) {
     // ---------------- producers: the block table walk and the TMA copies
     if (lane == 0) {
       constexpr int NP = G::kProducers;
-      constexpr int NID = 8 / NP;            // ids of a step's pages per producer
+      constexpr int NID = 8 / NP;            // pages of a step per producer, at most
       const int prod = warp - G::kProdWarp;  // takes the step's pages prod, prod + NP, ...
-      const int B = p.block_size;
-      const int per_v = G::kVTok / B;  // pages of a V slot
-      RingPos<FP8 ? NK8 : NS> at;      // bf16: K's and V's slots are one ring
-      RingPos<NV8> at_v;
-      // this producer's block ids of one step, read well before they are used
-      struct Step {
-        int id[NID];
-        int head, pages;
+      const int B = p.block_size, lgB = B == 32 ? 5 : 4;
+      const int per_v = G::kVTok >> lgB;     // pages of a V slot
+      RingPos<NS> at;
+      // pages of a single row tile are read once: they need not stay in L2
+      uint64_t once, stay;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(stay));
+      int seg_st = walk.st;    // the segment's first step in its unit
+      bool first_seg = true;   // of this share
+      // on to the walk's next step; at the share's end, what the merge needs
+      // if the unit starts here and goes on, up to the share that holds its end
+      auto advance = [&] {
+        if (walk.left == 1 && prod == 0 && seg_st == 0 && walk.st + 1 < walk.q.steps) {
+          const int64_t u_end = end + (walk.q.steps - 1 - walk.st);
+          int64_t last = cta + 1;
+          while ((last + 1) * total / ctas < u_end) ++last;
+          TreeMeta md;
+          md.row0 = walk.q.q0;
+          md.first = walk.tile * kTreeRows;
+          md.rows = min(kTreeRows, walk.q.n * p.group - md.first);
+          md.head = walk.h;
+          md.slot = first_seg ? 0 : 1;
+          md.parts = static_cast<int>(last - cta + 1);
+          p.meta[cta] = md;
+        }
+        if (walk.left <= 0) return;
+        walk.next(p);
+        if (walk.begins) {
+          seg_st = walk.st;
+          first_seg = false;
+        }
       };
-      auto read = [&](const TreeWalk& w) {
+      // What the copies of a step need. The block ids come through shared
+      // memory in the background, two steps ahead: a load into registers would
+      // be waited for as soon as the steps' registers change places.
+      struct Step {
+        int head, pages;
+        bool once;
+        int y[NID];  // first 8-row group of this producer's pages; -1 = no copy
+      };
+      int put = 0;  // ids: place of the step to be fetched
+      auto fetch = [&] {
         Step x;
-        x.head = w.h;
-        x.pages = w.left > 0 ? (min(kTreeTok, w.q.ctx - w.st * kTreeTok) + B - 1) / B : 0;
-        const int32_t* bt = p.block_tables + static_cast<int64_t>(w.s) * p.max_blocks_per_seq +
-                            w.st * (kTreeTok / B);
+        x.head = walk.h;
+        x.once = walk.q.tiles == 1;
+        x.pages = walk.left > 0
+                      ? (min(kTreeTok, walk.q.ctx - walk.st * kTreeTok) + B - 1) >> lgB : 0;
+        const int32_t* bt = p.block_tables + static_cast<int64_t>(walk.s) * p.max_blocks_per_seq +
+                            walk.st * (kTreeTok >> lgB);
 #pragma unroll
-        for (int j = 0; j < NID; ++j) x.id[j] = NP * j + prod < x.pages ? bt[NP * j + prod] : 0;
+        for (int j = 0; j < NID; ++j)
+          if (NP * j + prod < x.pages)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                             smem_addr(ids + put * 8 + NP * j + prod)),
+                         "l"(bt + NP * j + prod)
+                         : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        put = put == 2 ? 0 : put + 1;
         return x;
       };
-      // the copies of one slot: K columns [128 part, 128 part + 128) (E4M3: K
-      // as it is) of the step's pages, or its pages of V slot `part`
-      auto slot_copy = [&](const Step& x, bool is_v, int part) {
-        uint64_t *f, *e;
-        uint32_t dst, ph;
-        if (!FP8) {
-          f = &full[at.i], e = &empty[at.i], dst = ring + at.i * G::kSlot, ph = at.ph;
-        } else if (is_v) {
-          f = &full8[at_v.i], e = &empty8[at_v.i], dst = v8 + at_v.i * G::kV8, ph = at_v.ph;
-        } else {
-          f = &kfull[at.i], e = &kempty[at.i], dst = k8 + at.i * G::kK8, ph = at.ph;
-        }
-        if (!mbar_wait(e, ph ^ 1, p.err)) return false;
-        const int first = is_v ? part * per_v : 0;
-        const int last = min(x.pages, is_v ? first + per_v : x.pages);
-        const int page_bytes = FP8 ? B * D : B * (is_v ? D : 128) * 2;
-        int good = 0;
+      int get = 0;  // ids: place of the next step to be loaded
+      auto resolve = [&](Step& x) {
 #pragma unroll
         for (int j = 0; j < NID; ++j) {
           const int pg = NP * j + prod;
-          if (pg < first || pg >= last) continue;
-          if (x.id[j] >= 0 && x.id[j] < p.num_blocks) ++good;
-          else report_error(p.err, PKV_DEVERR_BLOCK_ID);
+          int id = -1;
+          if (pg < x.pages) {
+            id = ids[get * 8 + pg];
+            if (id < 0 || id >= p.num_blocks) {
+              report_error(p.err, PKV_DEVERR_BLOCK_ID);
+              id = -1;
+            }
+          }
+          x.y[j] = id >= 0 ? ((id * p.num_kv_heads + x.head) << lgB) >> 3 : -1;
         }
-        mbar_arrive_expect_tx(f, good * page_bytes);
+        get = get == 2 ? 0 : get + 1;
+      };
+      // K columns [128 ks, 128 ks + 128) of a step
+      auto copy_k = [&](const Step& x) {
 #pragma unroll
-        for (int j = 0; j < NID; ++j) {
-          const int pg = NP * j + prod;
-          if (pg < first || pg >= last || x.id[j] < 0 || x.id[j] >= p.num_blocks) continue;
-          const int y = (x.id[j] * p.num_kv_heads + x.head) * B;
-          tma_load_4d(dst + (pg - first) * page_bytes, is_v ? &tmv : &tmk,
-                      FP8 || is_v ? 0 : 2 * part, y / 8, f);
+        for (int ks = 0; ks < KS; ++ks) {
+          if (!mbar_wait(&empty[at.i], at.ph ^ 1, p.err)) return false;
+          const int bytes = 128 * (FP8 ? 1 : 2) << lgB;  // of one page
+          int good = 0;
+#pragma unroll
+          for (int j = 0; j < NID; ++j) good += x.y[j] >= 0 ? 1 : 0;
+          mbar_arrive_expect_tx(&full[at.i], good * bytes);
+          const uint32_t dst = ring + at.i * G::kSlot + prod * bytes;
+#pragma unroll
+          for (int j = 0; j < NID; ++j)
+            if (x.y[j] >= 0)
+              tma_load_4d(dst + j * NP * bytes, &tmk, FP8 ? ks : 2 * ks, x.y[j], &full[at.i],
+                          x.once ? once : stay);
+          at.next();
+          ++issued;
         }
-        if (FP8 && is_v) {
-          at_v.next();
-          ++issued_v;
-        } else {
+        return true;
+      };
+      // V of a step, kVTok tokens to a slot
+      auto copy_v = [&](const Step& x) {
+#pragma unroll
+        for (int vs = 0; vs < VS; ++vs) {
+          if (!mbar_wait(&empty[at.i], at.ph ^ 1, p.err)) return false;
+          const int bytes = D * (FP8 ? 1 : 2) << lgB;
+          const int first = vs * per_v;
+          int good = 0;
+#pragma unroll
+          for (int j = 0; j < NID; ++j) {
+            const int pg = NP * j + prod;
+            good += x.y[j] >= 0 && pg >= first && pg < first + per_v ? 1 : 0;
+          }
+          mbar_arrive_expect_tx(&full[at.i], good * bytes);
+#pragma unroll
+          for (int j = 0; j < NID; ++j) {
+            const int pg = NP * j + prod;
+            if (x.y[j] >= 0 && pg >= first && pg < first + per_v)
+              tma_load_4d(ring + at.i * G::kSlot + (pg - first) * bytes, &tmv, 0, x.y[j],
+                          &full[at.i], x.once ? once : stay);
+          }
           at.next();
           ++issued;
         }
         return true;
       };
       if (walk.left > 0) {
-        // V of step t, K of step t + 1, ids of step t + 2
-        Step now = read(walk), ahead;
-        bool ok = true;
-        for (int ks = 0; ks < KS && ok; ++ks) ok = slot_copy(now, false, ks);
-        walk.next(p);
-        ahead = read(walk);
+        // ids of step t + 2, K of step t + 1, V of step t
+        Step now = fetch();
+        advance();
+        Step ahead = fetch();
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        resolve(now);
+        bool ok = copy_k(now);
         for (int64_t t = 0; t < count && ok; ++t) {
-          if (t + 1 < count)
-            for (int ks = 0; ks < KS && ok; ++ks) ok = slot_copy(ahead, false, ks);
-          walk.next(p);
-          const Step far = read(walk);
-          for (int vs = 0; vs < VS && ok; ++vs) ok = slot_copy(now, true, vs);
+          advance();
+          Step far = fetch();
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          resolve(ahead);
+          if (t + 1 < count) ok = copy_k(ahead);
+          if (ok) ok = copy_v(now);
           now = ahead;
           ahead = far;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
     }
   } else if (warp == G::kMmaWarp) {
@@ -568,98 +655,109 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                                       : umma_idesc_bf16(128, D, true);
     const bool lead = elect_one();
     const uint64_t qd = umma_sdesc(sq, 16, (FP8 ? NC8 : NCH) * 1024, 2);
-    const uint64_t kd0 = FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
-    const uint64_t vd0 = umma_sdesc(ring, 1024, NCH * 1024, 2);
-    RingPos<NS> at;        // bf16: K's and V's slots in turn; E4M3: V's
-    RingPos<NK8> at_k;     // E4M3: K's
+    const uint64_t kd0 = umma_sdesc(ring, 16, FP8 ? 1024 : 2048, 2);
+    const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
+    RingPos<NS> at;        // the ring's slots in turn (E4M3: V's are passed over)
+    RingPos<2> at_v;       // E4M3: V's 16-bit slots
     uint32_t segs = 0;     // segments whose S has begun
     uint32_t pv_segs = 0;  // segments whose P.V has begun
-    bool prev_begins = false;
-    int prev_tok = 0;      // valid tokens of the step before
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err)) != 0;
     };
-    for (uint32_t t = 0;; ++t) {
-      const bool have = walk.left > 0;
-      if (have) {
-        const int b = t & 1;
-        // S of step t overwrites P of step t - 2
-        if (t >= 2 && !wait(&o_done[b], ((t - 2) >> 1) & 1)) break;
-        if (walk.begins && !wait(q_full, segs++ & 1)) break;
-        bool ok = true;
-        if constexpr (FP8) {
-          if (!wait(&kfull[at_k.i], at_k.ph)) break;
-          tc_fence_after();
-          if (lead) {
-            const uint64_t kd = kd0 + ((at_k.i * G::kK8) >> 4);
+    // S of step t
+    auto issue_s = [&](uint32_t t) {
+      const int b = t & 1;
+      // S of step t overwrites P of step t - 2
+      if (t >= 2 && !wait(&o_done[b], ((t - 2) >> 1) & 1)) return false;
+      if (walk.begins && !wait(q_full, segs++ & 1)) return false;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (!wait(&full[at.i], at.ph)) return false;
+        tc_fence_after();
+        if (lead) {
+          const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
+          if constexpr (FP8) {
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k)
+              for (int k = 0; k < 4; ++k)
                 umma_ss_e4m3(t_s + b * kTreeTok,
-                             qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
-                             kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
-                             (part > 0 || k > 0) ? 1u : 0u);
-            umma_commit(&kempty[at_k.i]);
-          }
-          at_k.next();
-        } else {
+                             qd + ((part * kTreeRows * D + ks * 1024 + k * 32) >> 4),
+                             kd + ((k * 32) >> 4), idesc_qk,
+                             (ks > 0 || part > 0 || k > 0) ? 1u : 0u);
+            for (int i = 1; i < G::kConvWarps; ++i) mbar_arrive(&empty[at.i]);
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            if (!(ok = wait(&full[at.i], at.ph))) break;
-            tc_fence_after();
-            if (lead) {
-              const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                umma_ss(t_s + b * kTreeTok,
-                        qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
-                        kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
-                        (ks > 0 || k > 0) ? 1u : 0u);
-              umma_commit(&empty[at.i]);
-            }
-            at.next();
+            for (int k = 0; k < 8; ++k)
+              umma_ss(t_s + b * kTreeTok, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
+                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
+                      (ks > 0 || k > 0) ? 1u : 0u);
           }
-          if (!ok) break;
+          umma_commit(&empty[at.i]);
         }
-        if (lead) {
-          umma_commit(&s_full[b]);
-          if (walk.ends()) umma_commit(q_empty);
-        }
+        at.next();
       }
-      if (t >= 1) {
-        const uint32_t j = t - 1;
-        const int b = j & 1;
-        if (!wait(&p_full[b], (j >> 1) & 1)) break;
-        // the segment before has left O
-        if (prev_begins && pv_segs++ > 0 && !wait(o_free, (pv_segs - 2) & 1)) break;
-        bool ok = true;
+      if (lead) {
+        umma_commit(&s_full[b]);
+        if (walk.ends()) umma_commit(q_empty);
+      }
+      return true;
+    };
+    // P.V of step j, the first of its segment or not, with tok valid tokens
+    auto issue_pv = [&](uint32_t j, bool first, int tok) {
+      const int b = j & 1;
+      if (!wait(&p_full[b], (j >> 1) & 1)) return false;
+      // the segment before has left O
+      if (first && pv_segs++ > 0 && !wait(o_free, (pv_segs - 2) & 1)) return false;
 #pragma unroll
-        for (int vs = 0; vs < VS; ++vs) {
-          if (!(ok = wait(&full[at.i], at.ph))) break;
-          tc_fence_after();
-          if (lead) {
-            constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
-            const uint64_t vd = vd0 + ((at.i * G::kSlot) >> 4);
-            const uint32_t pa = t_s + b * kTreeTok + 8 * vs * kPer;
-            const int k1 = (prev_tok + 15) / 16 - vs * kPer;
-            const uint32_t keep = !prev_begins || vs > 0 ? 1u : 0u;
-            if (k1 >= kPer) {
+      for (int vs = 0; vs < VS; ++vs) {
+        uint64_t* f = FP8 ? &vfull[at_v.i] : &full[at.i];
+        uint64_t* e = FP8 ? &vempty[at_v.i] : &empty[at.i];
+        if (!wait(f, FP8 ? at_v.ph : at.ph)) return false;
+        tc_fence_after();
+        if (lead) {
+          constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
+          const uint64_t vd = vd0 + (FP8 ? (at_v.i * G::kV16) >> 4 : (at.i * G::kSlot) >> 4);
+          const uint32_t pa = t_s + b * kTreeTok + 8 * vs * kPer;
+          const int k1 = (tok + 15) / 16 - vs * kPer;
+          const uint32_t keep = !first || vs > 0 ? 1u : 0u;
+          if (k1 >= kPer) {
 #pragma unroll
-              for (int kk = 0; kk < kPer; ++kk)
-                umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
-                             kk > 0 ? 1u : keep);
-            } else {
-              for (int kk = 0; kk < k1; ++kk)
-                umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
-                             kk > 0 ? 1u : keep);
-            }
-            umma_commit(&empty[at.i]);
+            for (int kk = 0; kk < kPer; ++kk)
+              umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
+                           kk > 0 ? 1u : keep);
+          } else {
+            for (int kk = 0; kk < k1; ++kk)
+              umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
+                           kk > 0 ? 1u : keep);
           }
-          at.next();
+          umma_commit(e);
         }
-        if (!ok) break;
-        if (lead) umma_commit(&o_done[b]);
+        at.next();  // E4M3: past the slot of V's codes
+        at_v.next();
+      }
+      if (lead) umma_commit(&o_done[b]);
+      return true;
+    };
+    bool prev_begins = false;
+    int prev_tok = 0;  // valid tokens of the step before
+    RingPos<NS> at_next;
+    for (uint32_t t = 0;; ++t) {
+      const bool have = walk.left > 0;
+      // a new segment's Q takes a while: P.V of the step before goes first
+      // then. The ring's order is K of step t, then V of step t - 1 all the same
+      if (have && t >= 1 && walk.begins) {
+        at_next = at;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) at.next();
+        if (!issue_pv(t - 1, prev_begins, prev_tok)) break;
+        const RingPos<NS> after = at;
+        at = at_next;
+        if (!issue_s(t)) break;
+        at = after;
+      } else {
+        if (have && !issue_s(t)) break;
+        if (t >= 1 && !issue_pv(t - 1, prev_begins, prev_tok)) break;
       }
       if (!have) break;
       prev_begins = walk.begins;
@@ -802,10 +900,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[(t - 1) & 1],
                                                          ((t - 1) >> 1) & 1, p.err)))
           break;
-        const int64_t seq = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
-        const int i = static_cast<int>(seq % NS);
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[i], (seq / NS) & 1, p.err))) break;
-        const uint32_t vp = ring + i * G::kSlot;
+        constexpr int NV = FP8 ? 2 : NS;
+        const int64_t at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
+        const int i = static_cast<int>(at_v % NV);
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(FP8 ? &vfull[i] : &full[i], (at_v / NV) & 1, p.err)))
+          break;
+        const uint32_t vp = v16 + i * (FP8 ? G::kV16 : G::kSlot);
         const int r0 = valid % G::kVTok, r1 = (r0 + 15) & ~15;
         constexpr int U = NCH * 8;  // 16-byte units of a row
         for (int x = threadIdx.x; x < (r1 - r0) * U; x += G::kSoftWarps * 32) {
@@ -866,20 +967,6 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(o_free);
-        if (threadIdx.x == 0 && !whole && seg_st == 0) {
-          // the unit starts here and goes on, up to the share that holds its end
-          const int64_t u_end = end + (walk.q.steps - 1 - walk.st);
-          int64_t last = cta + 1;
-          while ((last + 1) * total / ctas < u_end) ++last;
-          TreeMeta md;
-          md.row0 = walk.q.q0;
-          md.first = walk.tile * kTreeRows;
-          md.rows = min(kTreeRows, walk.q.n * g - md.first);
-          md.head = walk.h;
-          md.slot = first_seg ? 0 : 1;
-          md.parts = static_cast<int>(last - cta + 1);
-          p.meta[cta] = md;
-        }
         first_seg = false;
         ++seg;
       }
@@ -900,9 +987,14 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // ---------------- converters: a staged V slot's codes -> their f16 values
     const int ct = threadIdx.x - G::kConvWarp * 32;
     constexpr int UPR = D / 16;  // 16-code units of a row
-    constexpr int kUnits = G::kV8 / 16 / (G::kConvWarps * 32);
-    RingPos<NV8> from;
-    RingPos<NS> to;
+    constexpr int kUnits = G::kSlot / 16 / (G::kConvWarps * 32);
+    RingPos<NS> from;
+    RingPos<2> to;
+    // K of the first step, then K of step t + 1 (if there is one), V of step t
+    auto skip_k = [&] {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) from.next();
+    };
     // Q of a segment is loaded as soon as V of the segment before is converted
     // and its last S is done
     auto load_q = [&](uint32_t seg) {
@@ -914,10 +1006,12 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     };
     uint32_t seg = 0;
     bool ok = walk.left <= 0 || load_q(seg++);
+    skip_k();
+    if (walk.left > 1) skip_k();
     for (int vs = 0; walk.left > 0 && ok;) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full8[from.i], from.ph, p.err)))) break;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&empty[to.i], to.ph ^ 1, p.err)))) break;
-      const uint32_t src0 = v8 + from.i * G::kV8, dst0 = ring + to.i * G::kSlot;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full[from.i], from.ph, p.err)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&vempty[to.i], to.ph ^ 1, p.err)))) break;
+      const uint32_t src0 = ring + from.i * G::kSlot, dst0 = v16 + to.i * G::kV16;
       uint32_t c[kUnits][4];
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
@@ -954,8 +1048,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&full[to.i]);
-        mbar_arrive(&empty8[from.i]);
+        mbar_arrive(&vfull[to.i]);
+        mbar_arrive(&empty[from.i]);
       }
       from.next();
       to.next();
@@ -963,6 +1057,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         vs = 0;
         const bool last = walk.ends();
         walk.next(p);
+        if (walk.left > 1) skip_k();
         if (last && walk.left > 0) ok = load_q(seg++);
       }
     }
@@ -973,12 +1068,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   __syncthreads();
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers && lane == 0) {
     // no copy may still be writing this CTA's shared memory when it exits
-    const int n = FP8 ? NK8 : NS;
-    uint64_t* f = FP8 ? kfull : full;
-    for (int64_t i = issued > n ? issued - n : 0; i < issued; ++i)
-      if (!mbar_wait(&f[i % n], (i / n) & 1, p.err)) break;
-    for (int64_t i = issued_v > NV8 ? issued_v - NV8 : 0; i < issued_v; ++i)
-      if (!mbar_wait(&full8[i % NV8], (i / NV8) & 1, p.err)) break;
+    for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+      if (!mbar_wait(&full[i % NS], (i / NS) & 1, p.err)) break;
   }
   if (warp == G::kMmaWarp) {
     tc_fence_after();
@@ -1086,7 +1177,7 @@ static int launch_tree(const TreeParams& p, const void* k_cache, const void* v_c
   using G = TreeGeom<D, FP8>;
   const int64_t rows = static_cast<int64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   CUtensorMap tk, tv;
-  int rc = tree_pool_map(&tk, k_cache, rows, D, p.block_size, FP8, FP8 ? D / 128 : 2);
+  int rc = tree_pool_map(&tk, k_cache, rows, D, p.block_size, FP8, FP8 ? 1 : 2);
   if (rc != PKV_OK) return rc;
   rc = tree_pool_map(&tv, v_cache, rows, D, p.block_size, FP8, FP8 ? D / 128 : D / 64);
   if (rc != PKV_OK) return rc;
