@@ -393,23 +393,27 @@ def paged_attention_shared_prefix(q, k_cache, v_cache, block_tables, context_len
     return out
 
 
-class _Launch:
-    """Where a call runs: the device of its tensors, made current for the
-    call, and its stream (by default that device's current one). Scratch and
-    results that the call allocates belong to the same stream."""
+# The current stream's handle by device index; the plain call costs more than
+# all checks of a launch together.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("q and the caches must be CUDA tensors")
-        self.device = device
+
+class _Launch:
+    """Where a call runs when it is not the tensors' device and its current
+    stream: the device is made current for the call, and scratch and results
+    that the call allocates belong to the given stream."""
+
+    def __init__(self, index, stream):
+        self.index = index
         self.raw = None if stream is None else _stream(stream).value or 0
         self._ctx = []
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(self.device))
+        if self.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(self.index))
             self._ctx[-1].__enter__()
-        current = torch.cuda.current_stream().cuda_stream
+        current = _raw_stream(self.index)
         if self.raw is None:
             self.raw = current
         elif self.raw != current:
@@ -417,25 +421,54 @@ class _Launch:
                     else torch.cuda.default_stream())
             self._ctx.append(torch.cuda.stream(side))
             self._ctx[-1].__enter__()
-        return self
+        return self.raw
 
     def __exit__(self, *exc):
         while self._ctx:
             self._ctx.pop().__exit__(*exc)
 
 
-def _ptr(t, name, device, dtype, shape=None):
-    """Address of a contiguous tensor of the given type on the call's device."""
+class _Here:
+    """The same for the current device and its current stream."""
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _at(index, stream):
+    if index < 0:
+        raise ValueError("q and the caches must be CUDA tensors")
+    if stream is None and index == torch.cuda.current_device():
+        return _Here(_raw_stream(index))
+    return _Launch(index, stream)
+
+
+def _bad(t, name, index, dtypes, shape):
+    """Why _ptr refuses a tensor."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError("%s must be a tensor on the device of the others (%s)" % (
+            name, "cuda:%d" % index if index >= 0 else "cpu"))
+    if t.dtype not in dtypes:
+        raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _ptr(t, name, index, dtypes, shape=None):
+    """Address of a contiguous tensor of the given type and shape on device
+    `index` (-1: the host, for the refusals' sake); None for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError("%s must be a tensor on %s" % (name, device))
-    if t.dtype not in dtype:
-        raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtype))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype in dtypes
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        _bad(t, name, index, dtypes, shape)
     return t.data_ptr()
 
 
@@ -447,38 +480,43 @@ _CACHE = (torch.bfloat16,) + _FP8_DTYPES
 
 
 def _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, rows, out):
-    """Checked shapes and addresses of an attention call: (desc, dict)."""
+    """Checks of an attention call: (cache geometry, q's shape, device index,
+    number of sequences, addresses of out, q, k, v, scales, tables, lengths)."""
     desc = cache_desc(k_cache)
-    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != desc.head_dim:
         raise ValueError("q must be [rows, num_heads, %d]" % desc.head_dim)
-    if block_tables.dim() != 2 or tuple(context_lens.shape) != (block_tables.shape[0],):
-        raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
-    if rows is not None and q.shape[0] != rows:
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    S = block_tables.shape[0]
+    if rows and shape[0] != S:
         raise ValueError("q must have one row per sequence")
-    if v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must match")
-    dev = q.device
-    if out is not None and q.numel() and out.data_ptr() == q.data_ptr():
+    dev = q.get_device()
+    qp = _ptr(q, "q", dev, _BF16)
+    op = _ptr(out, "out", dev, _BF16, shape)
+    if op is not None and op == qp and q.numel():
         raise ValueError("out may not be q")
-    scales = (desc.num_kv_heads,)
-    return desc, dict(
-        out=_ptr(out, "out", dev, _BF16, tuple(q.shape)), q=_ptr(q, "q", dev, _BF16),
-        k=_ptr(k_cache, "k_cache", dev, _CACHE), v=_ptr(v_cache, "v_cache", dev, _CACHE,
-                                                       tuple(k_cache.shape)),
-        ks=_ptr(k_scale, "k_scale", dev, _F32, scales),
-        vs=_ptr(v_scale, "v_scale", dev, _F32, scales),
-        tables=_ptr(block_tables, "block_tables", dev, _I32),
-        lens=_ptr(context_lens, "context_lens", dev, _I32))
+    kdt = (k_cache.dtype,)
+    kp = _ptr(k_cache, "k_cache", dev, kdt)
+    vp = _ptr(v_cache, "v_cache", dev, kdt, k_cache.shape)
+    if k_scale is not None or v_scale is not None:
+        scales = (desc.num_kv_heads,)
+        k_scale = _ptr(k_scale, "k_scale", dev, _F32, scales)
+        v_scale = _ptr(v_scale, "v_scale", dev, _F32, scales)
+    return (desc, shape, dev, S, op, qp, kp, vp, k_scale, v_scale,
+            _ptr(block_tables, "block_tables", dev, _I32),
+            _ptr(context_lens, "context_lens", dev, _I32, (S,)))
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, q):
     """(address, bytes, tensor) of a call's workspace, allocated if not given."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        return workspace.data_ptr(), need, workspace
+    if not workspace.is_contiguous() or workspace.get_device() != q.get_device():
+        raise ValueError("workspace must be a contiguous tensor on the device of the others")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -508,26 +546,28 @@ def paged_attention_window(q, k_cache, v_cache, block_tables, context_lens, scal
     out [S, Hq, D] bf16. partition_size: None = the library's choice
     (window_partition_size), 0 = one pass, else a multiple of the block size.
     out and workspace are allocated if not given."""
-    S = int(block_tables.shape[0])
-    desc, a = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
-                              S, out)
-    max_context, window, sinks = int(max_context), int(window), int(sinks)
-    order = _ptr(seq_order, "seq_order", q.device, _I32, (S,))
+    L = _lib or lib()
+    desc, shape, dev, S, op, qp, kp, vp, ks, vs, tables, lens = _attention_args(
+        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, True, out)
+    order = _ptr(seq_order, "seq_order", dev, _I32, (S,))
     if partition_size is None:
-        partition_size = window_partition_size(S, desc.num_kv_heads, desc.block_size,
-                                               max_context, window, sinks)
-    with _Launch(q.device, stream) as at:
+        partition_size = L.pkv_window_partition_size(S, desc.num_kv_heads, desc.block_size,
+                                                     max_context, window, sinks)
+        if partition_size < 0:
+            _check(partition_size, "window_partition_size")
+    with _at(dev, stream) as raw:
         if out is None:
             out = torch.empty_like(q)
-            a["out"] = out.data_ptr()
-        need = lib().pkv_window_workspace_bytes(S, q.shape[1], desc.head_dim, desc.block_size,
-                                                max_context, window, sinks, partition_size)
-        ws, wsb, keep = _scratch(workspace, need, q.device)
-        rc = lib().pkv_paged_attention_window(
-            a["out"], a["q"], a["k"], a["v"], desc, a["ks"], a["vs"], a["tables"],
-            block_tables.shape[1], a["lens"], S, q.shape[1], max_context, float(scale), window,
-            sinks, int(partition_size), ws, wsb, order, at.raw)
-    _check(rc, "paged_attention_window")
+            op = out.data_ptr()
+        need = 0 if partition_size == 0 else L.pkv_window_workspace_bytes(
+            S, shape[1], desc.head_dim, desc.block_size, max_context, window, sinks,
+            partition_size)
+        ws, wsb, keep = _scratch(workspace, need, q)
+        rc = L.pkv_paged_attention_window(
+            op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, S, shape[1],
+            max_context, scale, window, sinks, partition_size, ws, wsb, order, raw)
+    if rc:
+        _check(rc, "paged_attention_window")
     return out
 
 
@@ -548,25 +588,24 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, context_lens, q_star
     max_draft (at most 64) bounds the drafts of a sequence. Returns out
     [N, Hq, D] bf16; rows at or behind q_start[S] are not written. out and
     workspace are allocated if not given."""
-    S = int(block_tables.shape[0])
-    desc, a = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
-                              None, out)
-    n, heads = int(q.shape[0]), int(q.shape[1])
-    start = _ptr(q_start, "q_start", q.device, _I32, (S + 1,))
-    mask = _ptr(tree_mask, "tree_mask", q.device, _MASK, (n,))
-    max_context, max_draft = int(max_context), int(max_draft)
-    with _Launch(q.device, stream) as at:
+    L = _lib or lib()
+    desc, shape, dev, S, op, qp, kp, vp, ks, vs, tables, lens = _attention_args(
+        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, False, out)
+    n = shape[0]
+    start = _ptr(q_start, "q_start", dev, _I32, (S + 1,))
+    mask = _ptr(tree_mask, "tree_mask", dev, _MASK, (n,))
+    with _at(dev, stream) as raw:
         if out is None:
             out = torch.empty_like(q)
-            a["out"] = out.data_ptr()
-        need = lib().pkv_tree_workspace_bytes(S, n, heads, desc.num_kv_heads, desc.head_dim,
-                                              max_context, max_draft)
-        ws, wsb, keep = _scratch(workspace, need, q.device)
-        rc = lib().pkv_paged_attention_tree(
-            a["out"], a["q"], a["k"], a["v"], desc, a["ks"], a["vs"], a["tables"],
-            block_tables.shape[1], a["lens"], start, S, n, max_draft, mask, heads, max_context,
-            float(scale), ws, wsb, at.raw)
-    _check(rc, "paged_attention_tree")
+            op = out.data_ptr()
+        need = L.pkv_tree_workspace_bytes(S, n, shape[1], desc.num_kv_heads, desc.head_dim,
+                                          max_context, max_draft) if workspace is None else 0
+        ws, wsb, keep = _scratch(workspace, need, q)
+        rc = L.pkv_paged_attention_tree(
+            op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, start, S, n,
+            max_draft, mask, shape[1], max_context, scale, ws, wsb, raw)
+    if rc:
+        _check(rc, "paged_attention_tree")
     return out
 
 
@@ -578,35 +617,37 @@ def kv_cache_accept(k_caches, v_caches, block_tables, context_lens, q_start, acc
     of them (one per layer, sharing block_tables). accepted int32 [S, M],
     strictly increasing; num_accepted int32 [S]. Returns the new context
     lengths, int32 [S] (in new_context_lens if given; not context_lens)."""
+    L = _lib or lib()
     if isinstance(k_caches, torch.Tensor):
-        k_caches = [k_caches]
+        k_caches = (k_caches,)
     if isinstance(v_caches, torch.Tensor):
-        v_caches = [v_caches]
-    if len(k_caches) != len(v_caches) or not len(k_caches):
+        v_caches = (v_caches,)
+    n = len(k_caches)
+    if n != len(v_caches) or not n:
         raise ValueError("k_caches and v_caches must be equally many, one at least")
     first = k_caches[0]
-    desc, dev, shape = cache_desc(first), first.device, tuple(first.shape)
-    dt = (first.dtype,)
-    n = len(k_caches)
+    desc, dev, shape, dt = cache_desc(first), first.get_device(), first.shape, (first.dtype,)
     if block_tables.dim() != 2 or accepted.dim() != 2:
         raise ValueError("block_tables must be [S, max_blocks], accepted [S, M]")
-    S, M = int(block_tables.shape[0]), int(accepted.shape[1])
+    S, M = block_tables.shape[0], accepted.shape[1]
     pools = (_P * n)(*[_ptr(t, "k_caches", dev, dt, shape) for t in k_caches])
     vpools = (_P * n)(*[_ptr(t, "v_caches", dev, dt, shape) for t in v_caches])
-    args = (_ptr(block_tables, "block_tables", dev, _I32), int(block_tables.shape[1]),
-            _ptr(context_lens, "context_lens", dev, _I32, (S,)),
-            _ptr(q_start, "q_start", dev, _I32, (S + 1,)), S,
-            _ptr(accepted, "accepted", dev, _I32, (S, M)), M,
-            _ptr(num_accepted, "num_accepted", dev, _I32, (S,)))
-    if new_context_lens is not None and S and new_context_lens.data_ptr() == context_lens.data_ptr():
+    tables = _ptr(block_tables, "block_tables", dev, _I32)
+    lens = _ptr(context_lens, "context_lens", dev, _I32, (S,))
+    start = _ptr(q_start, "q_start", dev, _I32, (S + 1,))
+    acc = _ptr(accepted, "accepted", dev, _I32, (S, M))
+    cnt = _ptr(num_accepted, "num_accepted", dev, _I32, (S,))
+    new = _ptr(new_context_lens, "new_context_lens", dev, _I32, (S,))
+    if S and new == lens:
         raise ValueError("new_context_lens may not be context_lens")
-    with _Launch(dev, stream) as at:
+    with _at(dev, stream) as raw:
         if new_context_lens is None:
             new_context_lens = torch.empty_like(context_lens)
-        rc = lib().pkv_kv_cache_accept(
-            pools, vpools, n, desc, *args,
-            _ptr(new_context_lens, "new_context_lens", dev, _I32, (S,)), at.raw)
-    _check(rc, "kv_cache_accept")
+            new = new_context_lens.data_ptr()
+        rc = L.pkv_kv_cache_accept(pools, vpools, n, desc, tables, block_tables.shape[1], lens,
+                                   start, S, acc, M, cnt, new, raw)
+    if rc:
+        _check(rc, "kv_cache_accept")
     return new_context_lens
 
 

@@ -122,8 +122,14 @@ def test_python_refusals():
         win(q, k, k, bt, n, 0.1, 16, 4, out=q)
     with pytest.raises(ValueError, match="contiguous"):
         win(q, k.transpose(2, 3).contiguous().transpose(2, 3), k, bt, n, 0.1, 16, 4)
-    with pytest.raises(ValueError, match="k_cache and v_cache"):
+    with pytest.raises(ValueError, match="v_cache has dtype"):
         win(q, k, k.float(), bt, n, 0.1, 16, 4)
+    with pytest.raises(ValueError, match="v_cache has shape"):
+        win(q, k, k[:2], bt, n, 0.1, 16, 4)
+    with pytest.raises(ValueError, match="context_lens has shape"):
+        win(q, k, k, bt, n[:1], 0.1, 16, 4)
+    with pytest.raises(ValueError, match="context_lens must be a tensor"):
+        pkv.kv_cache_accept(k, k.clone(), bt, [1, 1], start, torch.zeros(2, 3, dtype=torch.int32), n)
     with pytest.raises(ValueError, match="q must be"):
         win(q[:, :, :64], k, k, bt, n, 0.1, 16, 4)
     with pytest.raises(ValueError, match="q_start has shape"):
