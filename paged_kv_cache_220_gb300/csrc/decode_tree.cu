@@ -39,7 +39,7 @@
 // each part 4, so elements down to 2^-9 of the largest are exact and the rest
 // are off by at most 2^-17 of it. V's codes are staged by TMA and turned into
 // their exact f16 values by converter warps; P is f16. k_scale and the row's
-// 2^-e go into the logits, v_scale into the output. The ring's slots are 16 KB of codes.
+// 2^-e go into the logits, v_scale into the output. K and V have rings of their own.
 //
 // P is one bf16 part (a rounding of each weight to as many bits as the output
 // has; a second part would double the P.V products).
@@ -96,12 +96,15 @@ struct TreeParams {
 template <int D, bool FP8>
 struct TreeGeom {
   static constexpr int kQ = kTreeRows * D * 2;  // E4M3: two parts of one byte
-  static constexpr int kKS = D / 128;           // slots of a step's K
+  static constexpr int kKS = FP8 ? 1 : D / 128;  // slots of a step's K
   static constexpr int kVS = D / 128;           // slots of a step's V
   static constexpr int kVTok = kTreeTok / kVS;
-  // the ring that TMA fills: 16-bit values, or codes
+  // the ring that TMA fills: K's and V's 16-bit values; E4M3: V's codes
   static constexpr int kSlot = FP8 ? 16384 : 32768;
-  static constexpr int kNSlot = FP8 ? (D == 256 ? 6 : 8) : (D == 256 ? 5 : 6);
+  static constexpr int kNSlot = FP8 ? (D == 256 ? 2 : 4) : (D == 256 ? 5 : 6);
+  // E4M3: K's codes, a step to a slot
+  static constexpr int kK8 = kTreeTok * D;
+  static constexpr int kNK8 = FP8 ? (D == 256 ? 2 : 4) : 0;
   // E4M3: V's f16 values, two slots
   static constexpr int kV16 = 32768;
   static constexpr int kNV16 = FP8 ? 2 : 0;
@@ -113,7 +116,7 @@ struct TreeGeom {
   static constexpr int kQWarp = FP8 ? kConvWarp : 9, kQWarps = FP8 ? kConvWarps : 3;
   static constexpr int kThreads = (FP8 ? 15 : 16) * 32;
   static constexpr int kHead = 3072;  // barriers, exchange buffers
-  static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNV16 * kV16;
+  static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNK8 * kK8 + kNV16 * kV16;
   static constexpr uint32_t kColS = D;       // S of step t at kColS + 128 * (t & 1)
   static constexpr uint32_t kCols = 512;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -400,13 +403,16 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   constexpr int NCH = D / 64;    // 128-byte chunks of a 16-bit row
   constexpr int NC8 = D / 128;   // of a row of codes
   constexpr int KS = G::kKS, VS = G::kVS, NS = G::kNSlot;
+  constexpr int NK8 = FP8 ? G::kNK8 : 1;
   extern __shared__ __align__(1024) uint8_t sbase[];  // no room to align it by hand
   const uint32_t base = smem_addr(sbase);
   uint64_t* full = reinterpret_cast<uint64_t*>(sbase);  // [NS] slot filled
   uint64_t* empty = full + 8;                            // [NS] slot read
   uint64_t* vfull = empty + 8;                           // [2] E4M3: V converted
   uint64_t* vempty = vfull + 2;                          // [2]
-  uint64_t* s_full = vempty + 2;                         // [2]
+  uint64_t* kfull = vempty + 2;                          // [4] E4M3: K's codes in
+  uint64_t* kempty = kfull + 4;                          // [4]
+  uint64_t* s_full = kempty + 4;                         // [2]
   uint64_t* p_full = s_full + 2;                         // [2]
   uint64_t* o_done = p_full + 2;                         // [2]
   uint64_t* pair = o_done + 2;                           // [4] the two threads of a row
@@ -415,9 +421,9 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   uint64_t* o_free = q_empty + 1;
   uint64_t* drained = o_free + 1;
   uint64_t* q_first = drained + 1;                       // Q of the share's first segment
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 320);
-  int* found = reinterpret_cast<int*>(sbase + 328);            // sequence, its TreeSeq
-  int64_t* found_off = reinterpret_cast<int64_t*>(sbase + 352);  // the share's first step in it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 360);
+  int* found = reinterpret_cast<int*>(sbase + 364);            // sequence, its TreeSeq
+  int64_t* found_off = reinterpret_cast<int64_t*>(sbase + 392);  // the share's first step in it
   int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 400);     // [warps], until the share is known
   int* wtiles = reinterpret_cast<int*>(sbase + 560);           // [warps][2], the same
   int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 400);      // [4][128] E4M3: e of Q's rows
@@ -425,16 +431,19 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   float* xch = reinterpret_cast<float*>(sbase + 1024);         // [2][2][128]
   const uint32_t sq = base + G::kHead;
   const uint32_t ring = sq + G::kQ;
-  const uint32_t v16 = FP8 ? ring + NS * G::kSlot : ring;  // V's 16-bit values
+  const uint32_t k8 = ring + NS * G::kSlot;                   // E4M3: K's codes
+  const uint32_t v16 = FP8 ? k8 + G::kNK8 * G::kK8 : ring;     // V's 16-bit values
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], G::kProducers);
-      // E4M3: a V slot is released by the converter warps, a K slot by the
-      // products (one arrival) and the issuing lane (the others)
       mbar_init(&empty[i], FP8 ? G::kConvWarps : 1);
+    }
+    for (int i = 0; i < G::kNK8; ++i) {
+      mbar_init(&kfull[i], G::kProducers);
+      mbar_init(&kempty[i], 1);
     }
     for (int i = 0; i < G::kNV16; ++i) {
       mbar_init(&vfull[i], G::kConvWarps);
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   walk.start(p, TreeSeq{found[1], found[2], found[3], found[4], found[5]}, found[0],
              *found_off, count, T > 1 ? cta % T : -1);
 
-  int64_t issued = 0;  // producers: slots whose copies were started
+  int64_t issued = 0, issued_k = 0;  // producers: slots whose copies were started
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers) {
     // ---------------- producers: the block table walk and the TMA copies
     if (lane == 0) {
@@ -629,24 +638,32 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         }
         get = get == 2 ? 0 : get + 1;
       };
-      // K columns [128 ks, 128 ks + 128) of a step
+      RingPos<NK8> at_k;  // E4M3: K has a ring of its own
+      // K of a step: columns [128 ks, 128 ks + 128) to a slot (E4M3: all)
       auto copy_k = [&](const Step& x) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          if (!mbar_wait(&empty[at.i], at.ph ^ 1, p.err)) return false;
-          const int bytes = 128 * (FP8 ? 1 : 2) << lgB;  // of one page
+          uint64_t* f = FP8 ? &kfull[at_k.i] : &full[at.i];
+          uint64_t* e = FP8 ? &kempty[at_k.i] : &empty[at.i];
+          if (!mbar_wait(e, (FP8 ? at_k.ph : at.ph) ^ 1, p.err)) return false;
+          const int bytes = (FP8 ? D : 256) << lgB;  // of one page
           int good = 0;
 #pragma unroll
           for (int j = 0; j < NID; ++j) good += x.y[j] >= 0 ? 1 : 0;
-          mbar_arrive_expect_tx(&full[at.i], good * bytes);
-          const uint32_t dst = ring + at.i * G::kSlot + prod * bytes;
+          mbar_arrive_expect_tx(f, good * bytes);
+          const uint32_t dst = (FP8 ? k8 + at_k.i * G::kK8 : ring + at.i * G::kSlot) + prod * bytes;
 #pragma unroll
           for (int j = 0; j < NID; ++j)
             if (x.y[j] >= 0)
-              tma_load_4d(dst + j * NP * bytes, &tmk, FP8 ? ks : 2 * ks, x.y[j], &full[at.i],
+              tma_load_4d(dst + j * NP * bytes, &tmk, FP8 ? 0 : 2 * ks, x.y[j], f,
                           x.once ? once : stay);
-          at.next();
-          ++issued;
+          if constexpr (FP8) {
+            at_k.next();
+            ++issued_k;
+          } else {
+            at.next();
+            ++issued;
+          }
         }
         return true;
       };
@@ -708,9 +725,10 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                                       : umma_idesc_bf16(128, D, true);
     const bool lead = elect_one();
     const uint64_t qd = umma_sdesc(sq, 16, (FP8 ? NC8 : NCH) * 1024, 2);
-    const uint64_t kd0 = umma_sdesc(ring, 16, FP8 ? 1024 : 2048, 2);
+    const uint64_t kd0 = FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
     const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
-    RingPos<NS> at;        // the ring's slots in turn (E4M3: V's are passed over)
+    RingPos<NS> at;        // the ring's slots in turn
+    RingPos<NK8> at_k;     // E4M3: K's codes
     RingPos<2> at_v;       // E4M3: V's 16-bit slots
     uint32_t segs = 0;     // segments whose S has begun
     uint32_t pv_segs = 0;  // segments whose P.V has begun
@@ -727,32 +745,38 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         if (!in) return false;
         ++segs;
       }
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (!wait(&full[at.i], at.ph)) return false;
+      if constexpr (FP8) {
+        if (!wait(&kfull[at_k.i], at_k.ph)) return false;
         tc_fence_after();
         if (lead) {
-          const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
-          if constexpr (FP8) {
+          const uint64_t kd = kd0 + ((at_k.i * G::kK8) >> 4);
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_ss_e4m3(t_s + b * kTreeTok,
-                             qd + ((part * kTreeRows * D + ks * 1024 + k * 32) >> 4),
-                             kd + ((k * 32) >> 4), idesc_qk,
-                             (ks > 0 || part > 0 || k > 0) ? 1u : 0u);
-            for (int i = 1; i < G::kConvWarps; ++i) mbar_arrive(&empty[at.i]);
-          } else {
+            for (int k = 0; k < D / 32; ++k)
+              umma_ss_e4m3(t_s + b * kTreeTok,
+                           qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                           kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
+                           (part > 0 || k > 0) ? 1u : 0u);
+          umma_commit(&kempty[at_k.i]);
+        }
+        at_k.next();
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          if (!wait(&full[at.i], at.ph)) return false;
+          tc_fence_after();
+          if (lead) {
+            const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               umma_ss(t_s + b * kTreeTok, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
                       kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
                       (ks > 0 || k > 0) ? 1u : 0u);
+            umma_commit(&empty[at.i]);
           }
-          umma_commit(&empty[at.i]);
+          at.next();
         }
-        at.next();
       }
       if (lead) {
         umma_commit(&s_full[b]);
@@ -790,7 +814,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           }
           umma_commit(e);
         }
-        at.next();  // E4M3: past the slot of V's codes
+        at.next();
         at_v.next();
       }
       if (lead) umma_commit(&o_done[b]);
@@ -805,8 +829,10 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       // then. The ring's order is K of step t, then V of step t - 1 all the same
       if (have && t >= 1 && walk.begins) {
         at_next = at;
+        if constexpr (!FP8) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) at.next();
+          for (int ks = 0; ks < KS; ++ks) at.next();
+        }
         if (!issue_pv(t - 1, prev_begins, prev_tok)) break;
         const RingPos<NS> after = at;
         at = at_next;
@@ -1053,11 +1079,6 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     constexpr int kUnits = G::kSlot / 16 / (G::kConvWarps * 32);
     RingPos<NS> from;
     RingPos<2> to;
-    // K of the first step, then K of step t + 1 (if there is one), V of step t
-    auto skip_k = [&] {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) from.next();
-    };
     // Q of a segment is loaded as soon as V of the segment before is converted
     // and its last S is done
     auto load_q = [&](uint32_t seg) {
@@ -1069,8 +1090,6 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     };
     uint32_t seg = 1;  // the first segment's Q is not theirs
     bool ok = true;
-    skip_k();
-    if (walk.left > 1) skip_k();
     for (int vs = 0; walk.left > 0 && ok;) {
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full[from.i], from.ph, p.err)))) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&vempty[to.i], to.ph ^ 1, p.err)))) break;
@@ -1120,7 +1139,6 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         vs = 0;
         const bool last = walk.ends();
         walk.next(p);
-        if (walk.left > 1) skip_k();
         if (last && walk.left > 0) ok = load_q(seg++);
       }
     }
@@ -1133,6 +1151,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // no copy may still be writing this CTA's shared memory when it exits
     for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
       if (!mbar_wait(&full[i % NS], (i / NS) & 1, p.err)) break;
+    for (int64_t i = issued_k > NK8 ? issued_k - NK8 : 0; i < issued_k; ++i)
+      if (!mbar_wait(&kfull[i % NK8], (i / NK8) & 1, p.err)) break;
   }
   if (warp == G::kMmaWarp) {
     tc_fence_after();
@@ -1281,7 +1301,7 @@ static int launch_tree(const TreeParams& p, const void* k_cache, const void* v_c
   using G = TreeGeom<D, FP8>;
   const int64_t rows = static_cast<int64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   CUtensorMap tk, tv;
-  int rc = tree_pool_map(&tk, k_cache, rows, D, p.block_size, FP8, FP8 ? 1 : 2);
+  int rc = tree_pool_map(&tk, k_cache, rows, D, p.block_size, FP8, FP8 ? D / 128 : 2);
   if (rc != PKV_OK) return rc;
   rc = tree_pool_map(&tv, v_cache, rows, D, p.block_size, FP8, FP8 ? D / 128 : D / 64);
   if (rc != PKV_OK) return rc;
