@@ -9,7 +9,7 @@
 //     P = 2^(S scale log2e - m), masked; m the row's reference maximum
 //     O = O + P.V  8 products of 128 x d x 16, P in tensor memory over S's
 //                  columns, V in shared memory
-// with fp32 accumulators in tensor memory: O [d], S of two steps [2][128].
+// with fp32 accumulators in tensor memory: O [d], S of two or three steps [128].
 //
 // Work split. A unit is (sequence, KV head, row tile); its steps are the 128-
 // token runs of its context. All steps of all units form one line that is cut
@@ -117,8 +117,12 @@ struct TreeGeom {
   static constexpr int kThreads = (FP8 ? 15 : 16) * 32;
   static constexpr int kHead = 3072;  // barriers, exchange buffers
   static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNK8 * kK8 + kNV16 * kV16;
-  static constexpr uint32_t kColS = D;       // S of step t at kColS + 128 * (t & 1)
+  // S of step t at kColS + 128 * (t % kNB). Three buffers where they fit (d =
+  // 128): S of step t + 1 then does not wait for the end of P.V of step t - 1
+  static constexpr int kNB = D == 128 ? 3 : 2;
+  static constexpr uint32_t kColS = D;
   static constexpr uint32_t kCols = 512;
+  static_assert(kColS + kNB * kTreeTok <= kCols, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -257,6 +261,22 @@ struct RingPos {
 
 // r / g for a row of a unit (r < 64 g, g <= 8): exact, no division.
 __device__ __forceinline__ int div_group(int r, int g) { return (r * (65536 / g + 1)) >> 16; }
+
+// Two E4M3 codes (the low or the high 16 bits of w) -> their values / 256 as
+// f16x2, exact. A code's seven low bits, moved up by seven, are the f16 of the
+// same exponent field, whose bias is 8 larger; subnormal codes become f16
+// subnormals of the same weight. No conversion instruction: those share a unit
+// with 2^x, which the softmax keeps busy (E4M3 steps took twice as long in the
+// exponentials with them). Not for NaN codes (0x7F, 0xFF): e4m3x2_f16x2_256th.
+__device__ __forceinline__ uint32_t e4m3x2_shifted(uint32_t w, int hi) {
+  const uint32_t t = __byte_perm(w, 0, hi ? 0x3424 : 0x1404);  // code << 8 in each half
+  return (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u);
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_256th(uint32_t w, int hi) {
+  const uint32_t v = e4m3x2_f16x2(w, hi);
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.00390625f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // One lane of the warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -404,6 +424,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   constexpr int NC8 = D / 128;   // of a row of codes
   constexpr int KS = G::kKS, VS = G::kVS, NS = G::kNSlot;
   constexpr int NK8 = FP8 ? G::kNK8 : 1;
+  constexpr int NB = G::kNB;
   extern __shared__ __align__(1024) uint8_t sbase[];  // no room to align it by hand
   const uint32_t base = smem_addr(sbase);
   uint64_t* full = reinterpret_cast<uint64_t*>(sbase);  // [NS] slot filled
@@ -412,22 +433,22 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   uint64_t* vempty = vfull + 2;                          // [2]
   uint64_t* kfull = vempty + 2;                          // [4] E4M3: K's codes in
   uint64_t* kempty = kfull + 4;                          // [4]
-  uint64_t* s_full = kempty + 4;                         // [2]
-  uint64_t* p_full = s_full + 2;                         // [2]
-  uint64_t* o_done = p_full + 2;                         // [2]
-  uint64_t* pair = o_done + 2;                           // [4] the two threads of a row
+  uint64_t* s_full = kempty + 4;                         // [NB] S of a step is done
+  uint64_t* p_full = s_full + 3;                         // [NB] its P is written
+  uint64_t* o_done = p_full + 3;                         // [NB] its P.V is done
+  uint64_t* pair = o_done + 3;                           // [4] the two threads of a row
   uint64_t* q_full = pair + 4;
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_free = q_empty + 1;
   uint64_t* drained = o_free + 1;
   uint64_t* q_first = drained + 1;                       // Q of the share's first segment
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 360);
-  int* found = reinterpret_cast<int*>(sbase + 364);            // sequence, its TreeSeq
-  int64_t* found_off = reinterpret_cast<int64_t*>(sbase + 392);  // the share's first step in it
-  int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 400);     // [warps], until the share is known
-  int* wtiles = reinterpret_cast<int*>(sbase + 560);           // [warps][2], the same
-  int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 400);      // [4][128] E4M3: e of Q's rows
-  int32_t* ids = reinterpret_cast<int32_t*>(sbase + 912);      // [3][8] block ids of three steps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 376);
+  int* found = reinterpret_cast<int*>(sbase + 380);            // sequence, its TreeSeq
+  int64_t* found_off = reinterpret_cast<int64_t*>(sbase + 408);  // the share's first step in it
+  int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 416);     // [warps], until the share is known
+  int* wtiles = reinterpret_cast<int*>(sbase + 576);           // [warps][2], the same
+  int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 416);      // [4][128] E4M3: e of Q's rows
+  int32_t* ids = reinterpret_cast<int32_t*>(sbase + 928);      // [3][8] block ids of three steps
   float* xch = reinterpret_cast<float*>(sbase + 1024);         // [2][2][128]
   const uint32_t sq = base + G::kHead;
   const uint32_t ring = sq + G::kQ;
@@ -449,7 +470,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       mbar_init(&vfull[i], G::kConvWarps);
       mbar_init(&vempty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < G::kNB; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], G::kSoftWarps * 32);
       mbar_init(&o_done[i], 1);
@@ -715,91 +736,84 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
     }
   } else if (warp == G::kMmaWarp) {
-    // ---------------- the products: the whole warp walks, one lane issues.
-    // Operand descriptors are a constant plus the address: one addition each
-    // (built one by one they cost the issuing lane about as much as the
-    // tensor core takes for a product).
-    constexpr uint32_t idesc_qk =
-        FP8 ? umma_idesc_e4m3(128, kTreeTok) : umma_idesc_bf16(128, kTreeTok, false);
-    constexpr uint32_t idesc_pv = FP8 ? umma_idesc_f16(128, D, true)
-                                      : umma_idesc_bf16(128, D, true);
-    const bool lead = elect_one();
-    const uint64_t qd = umma_sdesc(sq, 16, (FP8 ? NC8 : NCH) * 1024, 2);
-    const uint64_t kd0 = FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
-    const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
-    RingPos<NS> at;        // the ring's slots in turn
-    RingPos<NK8> at_k;     // E4M3: K's codes
-    RingPos<2> at_v;       // E4M3: V's 16-bit slots
-    uint32_t segs = 0;     // segments whose S has begun
-    uint32_t pv_segs = 0;  // segments whose P.V has begun
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err)) != 0;
-    };
-    // S of step t
-    auto issue_s = [&](uint32_t t) {
-      const int b = t & 1;
-      // S of step t overwrites P of step t - 2
-      if (t >= 2 && !wait(&o_done[b], ((t - 2) >> 1) & 1)) return false;
-      if (walk.begins) {
-        const bool in = segs == 0 ? wait(q_first, 0) : wait(q_full, (segs - 1) & 1);
-        if (!in) return false;
-        ++segs;
-      }
-      if constexpr (FP8) {
-        if (!wait(&kfull[at_k.i], at_k.ph)) return false;
-        tc_fence_after();
-        if (lead) {
+    // ---------------- the products, issued by one lane. Operand descriptors
+    // are a constant plus the address: one addition each (built one by one
+    // they cost the issuing lane about as much as the tensor core takes for a
+    // product).
+    if (elect_one()) {
+      constexpr uint32_t idesc_qk =
+          FP8 ? umma_idesc_e4m3(128, kTreeTok) : umma_idesc_bf16(128, kTreeTok, false);
+      constexpr uint32_t idesc_pv = FP8 ? umma_idesc_f16(128, D, true)
+                                        : umma_idesc_bf16(128, D, true);
+      const uint64_t qd = umma_sdesc(sq, 16, (FP8 ? NC8 : NCH) * 1024, 2);
+      const uint64_t kd0 =
+          FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
+      const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
+      RingPos<NS> at;        // the ring's slots in turn
+      RingPos<NK8> at_k;     // E4M3: K's codes
+      RingPos<2> at_v;       // E4M3: V's 16-bit slots
+      RingPos<NB> sb, pb;    // S buffers: of the next S, of the next P.V
+      uint32_t segs = 0;     // segments whose S has begun
+      uint32_t pv_segs = 0;  // segments whose P.V has begun
+      // S of the walk's step, over P of the step NB before
+      auto issue_s = [&] {
+        if (walk.begins) {
+          const bool in = segs == 0 ? mbar_wait(q_first, 0, p.err)
+                                    : mbar_wait(q_full, (segs - 1) & 1, p.err);
+          if (!in) return false;
+          ++segs;
+        }
+        const uint32_t ts = t_s + sb.i * kTreeTok;
+        if constexpr (FP8) {
+          if (!mbar_wait(&kfull[at_k.i], at_k.ph, p.err)) return false;
+          if (!mbar_wait(&o_done[sb.i], sb.ph ^ 1, p.err)) return false;
+          tc_fence_after();
           const uint64_t kd = kd0 + ((at_k.i * G::kK8) >> 4);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              umma_ss_e4m3(t_s + b * kTreeTok,
-                           qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
+              umma_ss_e4m3(ts, qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
                            kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
                            (part > 0 || k > 0) ? 1u : 0u);
+          umma_commit(&s_full[sb.i]);
           umma_commit(&kempty[at_k.i]);
-        }
-        at_k.next();
-      } else {
+          at_k.next();
+        } else {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          if (!wait(&full[at.i], at.ph)) return false;
-          tc_fence_after();
-          if (lead) {
+          for (int ks = 0; ks < KS; ++ks) {
+            if (!mbar_wait(&full[at.i], at.ph, p.err)) return false;
+            if (ks == 0 && !mbar_wait(&o_done[sb.i], sb.ph ^ 1, p.err)) return false;
+            tc_fence_after();
             const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              umma_ss(t_s + b * kTreeTok, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
+              umma_ss(ts, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
                       kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
                       (ks > 0 || k > 0) ? 1u : 0u);
+            if (ks == KS - 1) umma_commit(&s_full[sb.i]);
             umma_commit(&empty[at.i]);
+            at.next();
           }
-          at.next();
         }
-      }
-      if (lead) {
-        umma_commit(&s_full[b]);
         if (walk.ends()) umma_commit(q_empty);
-      }
-      return true;
-    };
-    // P.V of step j, the first of its segment or not, with tok valid tokens
-    auto issue_pv = [&](uint32_t j, bool first, int tok) {
-      const int b = j & 1;
-      if (!wait(&p_full[b], (j >> 1) & 1)) return false;
-      // the segment before has left O
-      if (first && pv_segs++ > 0 && !wait(o_free, (pv_segs - 2) & 1)) return false;
+        sb.next();
+        return true;
+      };
+      // P.V of the step before, the first of its segment or not, with tok valid tokens
+      auto issue_pv = [&](bool first, int tok) {
+        // the segment before has left O
+        if (first && pv_segs++ > 0 && !mbar_wait(o_free, (pv_segs - 2) & 1, p.err)) return false;
 #pragma unroll
-      for (int vs = 0; vs < VS; ++vs) {
-        uint64_t* f = FP8 ? &vfull[at_v.i] : &full[at.i];
-        uint64_t* e = FP8 ? &vempty[at_v.i] : &empty[at.i];
-        if (!wait(f, FP8 ? at_v.ph : at.ph)) return false;
-        tc_fence_after();
-        if (lead) {
+        for (int vs = 0; vs < VS; ++vs) {
+          uint64_t* f = FP8 ? &vfull[at_v.i] : &full[at.i];
+          uint64_t* e = FP8 ? &vempty[at_v.i] : &empty[at.i];
+          if (!mbar_wait(f, FP8 ? at_v.ph : at.ph, p.err)) return false;
+          if (vs == 0 && !mbar_wait(&p_full[pb.i], pb.ph, p.err)) return false;
+          tc_fence_after();
           constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
           const uint64_t vd = vd0 + (FP8 ? (at_v.i * G::kV16) >> 4 : (at.i * G::kSlot) >> 4);
-          const uint32_t pa = t_s + b * kTreeTok + 8 * vs * kPer;
+          const uint32_t pa = t_s + pb.i * kTreeTok + 8 * vs * kPer;
           const int k1 = (tok + 15) / 16 - vs * kPer;
           const uint32_t keep = !first || vs > 0 ? 1u : 0u;
           if (k1 >= kPer) {
@@ -812,44 +826,44 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
               umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
                            kk > 0 ? 1u : keep);
           }
+          if (vs == VS - 1) umma_commit(&o_done[pb.i]);
           umma_commit(e);
+          at.next();
+          at_v.next();
         }
-        at.next();
-        at_v.next();
-      }
-      if (lead) umma_commit(&o_done[b]);
-      return true;
-    };
-    bool prev_begins = false;
-    int prev_tok = 0;  // valid tokens of the step before
-    RingPos<NS> at_next;
-    for (uint32_t t = 0;; ++t) {
-      const bool have = walk.left > 0;
-      // a new segment's Q takes a while: P.V of the step before goes first
-      // then. The ring's order is K of step t, then V of step t - 1 all the same
-      if (have && t >= 1 && walk.begins) {
-        at_next = at;
-        if constexpr (!FP8) {
+        pb.next();
+        return true;
+      };
+      bool prev_begins = false;
+      int prev_tok = 0;  // valid tokens of the step before
+      for (bool any = false;; any = true) {
+        const bool have = walk.left > 0;
+        // a new segment's Q takes a while: P.V of the step before goes first
+        // then. The ring's order is K of step t, then V of step t - 1 all the same
+        if (have && any && walk.begins) {
+          const RingPos<NS> k_at = at;
+          if constexpr (!FP8) {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) at.next();
+            for (int ks = 0; ks < KS; ++ks) at.next();
+          }
+          if (!issue_pv(prev_begins, prev_tok)) break;
+          const RingPos<NS> after = at;
+          at = k_at;
+          if (!issue_s()) break;
+          at = after;
+        } else {
+          if (have && !issue_s()) break;
+          if (any && !issue_pv(prev_begins, prev_tok)) break;
         }
-        if (!issue_pv(t - 1, prev_begins, prev_tok)) break;
-        const RingPos<NS> after = at;
-        at = at_next;
-        if (!issue_s(t)) break;
-        at = after;
-      } else {
-        if (have && !issue_s(t)) break;
-        if (t >= 1 && !issue_pv(t - 1, prev_begins, prev_tok)) break;
+        if (!have) break;
+        prev_begins = walk.begins;
+        prev_tok = min(kTreeTok, walk.q.ctx - walk.st * kTreeTok);
+        walk.next(p);
       }
-      if (!have) break;
-      prev_begins = walk.begins;
-      prev_tok = min(kTreeTok, walk.q.ctx - walk.st * kTreeTok);
-      walk.next(p);
+      // every product issued here has finished before tensor memory is released
+      umma_commit(drained);
+      (void)mbar_wait(drained, 0, p.err);
     }
-    // every product issued here has finished before tensor memory is released
-    if (lead) umma_commit(drained);
-    (void)wait(drained, 0);
   } else if (warp < G::kSoftWarps) {
     // ---------------- softmax: two threads per query row, 64 columns each
     const int quad = warp & 3, half = warp >> 2;
@@ -880,8 +894,9 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       v = x[(half ^ 1) * 128 + row];
       return true;
     };
+    RingPos<NB> sb, before_sb;  // S buffer of the step, of the step before
     for (int64_t t = 0; walk.left > 0; ++t) {
-      const int b = static_cast<int>(t & 1);
+      const int b = sb.i;
       const int base_tok = walk.q.ctx - walk.q.n;
       const bool begins = walk.begins;
       if (begins) {
@@ -896,7 +911,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         l = 0.f;
         seg_st = walk.st;
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], (t >> 1) & 1, p.err))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], sb.ph, p.err))) break;
       tc_fence_after();
       if constexpr (FP8)
         if (begins) {
@@ -939,7 +954,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       const bool want = mx > m + 8.f;
       if (__any_sync(0xffffffffu, want) && !begins) {
         if (!__all_sync(0xffffffffu,
-                        mbar_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err)))
+                        mbar_wait(&o_done[before_sb.i], before_sb.ph, p.err)))
           break;
         tc_fence_after();
         const float alpha = want ? fast_exp2(m - mx) : 1.f;  // 0 while m is -inf
@@ -986,8 +1001,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         // hold whatever was there: zero them, P is zero there. The step
         // before is waited for first: its V may have been the slot's last
         // use, and a wait must not be two phases ahead of its barrier
-        if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[(t - 1) & 1],
-                                                         ((t - 1) >> 1) & 1, p.err)))
+        if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[before_sb.i], before_sb.ph,
+                                                         p.err)))
           break;
         constexpr int NV = FP8 ? 2 : NS;
         const int64_t at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
@@ -1016,9 +1031,10 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         other = l;
         if (!exchange(other)) break;
         const float sum = half == 0 ? l + other : other + l;
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[b], (t >> 1) & 1, p.err))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[b], sb.ph, p.err))) break;
         tc_fence_after();
-        const float inv = sum > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / sum : 0.f;
+        // E4M3: V's f16 values are 1/256 of the codes'
+        const float inv = sum > 0.f ? (FP8 ? 256.f * p.v_scale[walk.h] : 1.f) / sum : 0.f;
         const bool whole = seg_st == 0 && walk.st + 1 == walk.q.steps;
         const int c0 = half * (D / 2);
         if (whole) {
@@ -1059,6 +1075,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         first_seg = false;
         ++seg;
       }
+      before_sb = sb;
+      sb.next();
       walk.next(p);
     }
   } else if (!FP8 && warp >= G::kQWarp && warp < G::kQWarp + G::kQWarps) {
@@ -1104,6 +1122,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                      : "=r"(c[e][0]), "=r"(c[e][1]), "=r"(c[e][2]), "=r"(c[e][3])
                      : "r"(src));
       }
+      // NaN codes (all seven low bits set) take the conversion instruction
+      uint32_t nan = 0;
+#pragma unroll
+      for (int e = 0; e < kUnits; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nan |= (c[e][i] & 0x7F7F7F7Fu) + 0x01010101u;
+      const bool exact = __any_sync(0xffffffffu, (nan & 0x80808080u) != 0);
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
         const int x = ct + e * G::kConvWarps * 32, u = x % UPR, r = x / UPR;
@@ -1115,8 +1140,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          w[2 * i] = e4m3x2_f16x2(c[e][i], 0);
-          w[2 * i + 1] = e4m3x2_f16x2(c[e][i], 1);
+          w[2 * i] = exact ? e4m3x2_f16x2_256th(c[e][i], 0) : e4m3x2_shifted(c[e][i], 0);
+          w[2 * i + 1] = exact ? e4m3x2_f16x2_256th(c[e][i], 1) : e4m3x2_shifted(c[e][i], 1);
         }
         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(odd ? dst ^ 16 : dst),
                      "r"(odd ? w[4] : w[0]), "r"(odd ? w[5] : w[1]), "r"(odd ? w[6] : w[2]),
