@@ -47,7 +47,7 @@
 // Warps: 0-7 softmax (threads t and t + 128 own query row t, 64 of a step's
 // columns each; they exchange maxima through shared memory), 8 issues the
 // products; bf16: 9-11 load Q, 12-15 load pages; E4M3: 9-10 load pages, 11-14
-// convert V and load Q.
+// convert V and load Q (16 warps of 128 registers; with 19 and 96 the softmax spills).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -198,7 +198,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 struct TreeWalk {
   TreeSeq q;
   int s, h, tile, st;   // the current step
-  int64_t left;         // steps left, this one included
+  int left;             // steps left, this one included
   bool begins;          // first step of a segment
   int next_q0, next_q1, next_ctx;  // of sequence s + 1, read when s is entered
   bool team;            // the tile is the CTA's for good (see tree_kernel)
@@ -211,7 +211,7 @@ struct TreeWalk {
   // off: the share's first step, counted from sequence s0's first; member: the
   // CTA's tile if it belongs to a team, else -1
   __device__ __forceinline__ void start(const TreeParams& p, const TreeSeq& q0, int s0,
-                                        int64_t off, int64_t count, int member) {
+                                        int64_t off, int count, int member) {
     q = q0;
     s = s0;
     left = count;
@@ -261,22 +261,6 @@ struct RingPos {
 
 // r / g for a row of a unit (r < 64 g, g <= 8): exact, no division.
 __device__ __forceinline__ int div_group(int r, int g) { return (r * (65536 / g + 1)) >> 16; }
-
-// Two E4M3 codes (the low or the high 16 bits of w) -> their values / 256 as
-// f16x2, exact. A code's seven low bits, moved up by seven, are the f16 of the
-// same exponent field, whose bias is 8 larger; subnormal codes become f16
-// subnormals of the same weight. No conversion instruction: those share a unit
-// with 2^x, which the softmax keeps busy (E4M3 steps took twice as long in the
-// exponentials with them). Not for NaN codes (0x7F, 0xFF): e4m3x2_f16x2_256th.
-__device__ __forceinline__ uint32_t e4m3x2_shifted(uint32_t w, int hi) {
-  const uint32_t t = __byte_perm(w, 0, hi ? 0x3424 : 0x1404);  // code << 8 in each half
-  return (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u);
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16x2_256th(uint32_t w, int hi) {
-  const uint32_t v = e4m3x2_f16x2(w, hi);
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.00390625f));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // One lane of the warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -411,7 +395,7 @@ struct TreeQ {
 // The number of V's first slot of step t in the ring's order (the slot is that
 // modulo the slots), of a CTA with `total` steps.
 template <int KS, int VS>
-__device__ __forceinline__ int64_t v_seq(int64_t t, int64_t total) {
+__device__ __forceinline__ int v_seq(int t, int total) {
   return KS + t * (KS + VS) + (t + 1 < total ? KS : 0);
 }
 
@@ -546,7 +530,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                              quotient(total + p.min_steps - 1, p.min_steps));
   const int64_t begin = share < shares ? quotient(share * total, shares) : 0;
   const int64_t end = share < shares ? quotient((share + 1) * total, shares) : 0;
-  const int64_t count = end - begin;
+  const int count = static_cast<int>(end - begin);
   if (count > 0 && excl <= begin && begin < excl + mine) {
     int64_t at = excl;
     int s = s_lo;
@@ -574,7 +558,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   walk.start(p, TreeSeq{found[1], found[2], found[3], found[4], found[5]}, found[0],
              *found_off, count, T > 1 ? cta % T : -1);
 
-  int64_t issued = 0, issued_k = 0;  // producers: slots whose copies were started
+  uint32_t issued = 0, issued_k = 0;  // producers: slots whose copies were started
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers) {
     // ---------------- producers: the block table walk and the TMA copies
     if (lane == 0) {
@@ -722,7 +706,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         resolve(now);
         bool ok = copy_k(now);
-        for (int64_t t = 0; t < count && ok; ++t) {
+        for (int t = 0; t < count && ok; ++t) {
           advance();
           Step far = fetch();
           asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -813,17 +797,19 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           tc_fence_after();
           constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
           const uint64_t vd = vd0 + (FP8 ? (at_v.i * G::kV16) >> 4 : (at.i * G::kSlot) >> 4);
-          const uint32_t pa = t_s + pb.i * kTreeTok + 8 * vs * kPer;
+          // P of tokens 16 kk of the step: 8 columns, 32 to each half of S's columns
+          const uint32_t ps = t_s + pb.i * kTreeTok;
+          auto pa = [&](int kk) { return ps + 64 * (kk / 4) + 8 * (kk % 4); };
           const int k1 = (tok + 15) / 16 - vs * kPer;
           const uint32_t keep = !first || vs > 0 ? 1u : 0u;
           if (k1 >= kPer) {
 #pragma unroll
             for (int kk = 0; kk < kPer; ++kk)
-              umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
+              umma_bf16_ta(t_o, pa(vs * kPer + kk), vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
                            kk > 0 ? 1u : keep);
           } else {
             for (int kk = 0; kk < k1; ++kk)
-              umma_bf16_ta(t_o, pa + 8 * kk, vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
+              umma_bf16_ta(t_o, pa(vs * kPer + kk), vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
                            kk > 0 ? 1u : keep);
           }
           if (vs == VS - 1) umma_commit(&o_done[pb.i]);
@@ -895,7 +881,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       return true;
     };
     RingPos<NB> sb, before_sb;  // S buffer of the step, of the step before
-    for (int64_t t = 0; walk.left > 0; ++t) {
+    for (int t = 0; walk.left > 0; ++t) {
       const int b = sb.i;
       const int base_tok = walk.q.ctx - walk.q.n;
       const bool begins = walk.begins;
@@ -923,11 +909,14 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       const uint32_t ts = t_s + lane_off + b * kTreeTok;
       const int tok0 = walk.st * kTreeTok;
       const bool clean = tok0 + kTreeTok <= base_tok;  // committed tokens only
+      // this thread's columns, 64 half .. 64 half + 63
+      const uint32_t mine = ts + 64 * half;
       float sv[64];
-      tmem_ld64(ts + 64 * half, sv);
+      tmem_ld64(mine, sv);
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (!clean) {
-        // visible columns of this row: committed, or named by the mask
+        // scaled here, columns that the row does not see -inf; it sees the
+        // committed ones and those its mask names
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int sh = tok0 + 64 * half + 32 * w - base_tok;  // draft of the first column
@@ -970,30 +959,29 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
       if (want) m = mx;
       const float ref = m == -INFINITY ? 0.f : m;
-      // P over S's columns (both threads of the row have read theirs): tokens
-      // 64 half .. go to columns 32 half ..
+      // P over this thread's own columns of S, two tokens to a column
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t pw[32];
       if (clean) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
-          const float c = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
+          const float e = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
           l4[(2 * i) & 3] += a;
-          l4[(2 * i + 1) & 3] += c;
-          pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
+          l4[(2 * i + 1) & 3] += e;
+          pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float a = fast_exp2(sv[2 * i] - ref), c = fast_exp2(sv[2 * i + 1] - ref);
+          const float a = fast_exp2(sv[2 * i] - ref), e = fast_exp2(sv[2 * i + 1] - ref);
           l4[(2 * i) & 3] += a;
-          l4[(2 * i + 1) & 3] += c;
-          pw[i] = FP8 ? pack_f16(a, c) : pack_bf16(a, c);
+          l4[(2 * i + 1) & 3] += e;
+          pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
         }
       }
-      tmem_st16_nowait(ts + 32 * half, pw);
-      tmem_st16_nowait(ts + 32 * half + 16, pw + 16);
+      tmem_st16_nowait(mine, pw);
+      tmem_st16_nowait(mine + 16, pw + 16);
       l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       const int valid = walk.q.ctx - tok0;
       if (valid < kTreeTok && (valid & 15) != 0) {
@@ -1005,8 +993,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                                                          p.err)))
           break;
         constexpr int NV = FP8 ? 2 : NS;
-        const int64_t at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
-        const int i = static_cast<int>(at_v % NV);
+        const int at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
+        const int i = at_v % NV;
         if (!__all_sync(0xffffffffu,
                         mbar_wait(FP8 ? &vfull[i] : &full[i], (at_v / NV) & 1, p.err)))
           break;
@@ -1033,8 +1021,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         const float sum = half == 0 ? l + other : other + l;
         if (!__all_sync(0xffffffffu, mbar_wait(&o_done[b], sb.ph, p.err))) break;
         tc_fence_after();
-        // E4M3: V's f16 values are 1/256 of the codes'
-        const float inv = sum > 0.f ? (FP8 ? 256.f * p.v_scale[walk.h] : 1.f) / sum : 0.f;
+        const float inv = sum > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / sum : 0.f;
         const bool whole = seg_st == 0 && walk.st + 1 == walk.q.steps;
         const int c0 = half * (D / 2);
         if (whole) {
@@ -1094,7 +1081,21 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // ---------------- converters: a staged V slot's codes -> their f16 values
     const int ct = threadIdx.x - G::kConvWarp * 32;
     constexpr int UPR = D / 16;  // 16-code units of a row
-    constexpr int kUnits = G::kSlot / 16 / (G::kConvWarps * 32);
+    constexpr int kCT = G::kConvWarps * 32;
+    constexpr int kUnits = G::kSlot / 16 / kCT;
+    // a thread's units lie kCT / UPR rows apart, a multiple of 8, at one place
+    // of their rows: one swizzled address each and constant steps
+    static_assert(kCT / UPR % 8 == 0, "row groups");
+    constexpr uint32_t kSrcStep = kCT / UPR / 8 * NC8 * 1024, kDstStep = kCT / UPR / 8 * NCH * 1024;
+    const int cu = ct % UPR, cr = ct / UPR;
+    uint32_t src_at = ((cr / 8) * NC8 + cu / 8) * 1024 + (cr % 8) * 128 +
+                      ((cu % 8) ^ (cr % 8)) * 16;
+    uint32_t dst_at = ((cr / 8) * NCH + cu / 4) * 1024 + (cr % 8) * 128 +
+                      ((2 * (cu % 4)) ^ (cr % 8)) * 16;
+    // odd chunks store their second half first: the two chunks of a
+    // quarter-warp then use different banks
+    const uint32_t second = (cu >> 2) & 1;
+    dst_at ^= second * 16;
     RingPos<NS> from;
     RingPos<2> to;
     // Q of a segment is loaded as soon as V of the segment before is converted
@@ -1115,41 +1116,28 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       uint32_t c[kUnits][4];
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
-        const int x = ct + e * G::kConvWarps * 32, u = x % UPR, r = x / UPR;
-        uint32_t src = src0 + ((r / 8) * NC8 + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
-        src ^= ((src >> 7) & 7u) << 4;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(c[e][0]), "=r"(c[e][1]), "=r"(c[e][2]), "=r"(c[e][3])
-                     : "r"(src));
+                     : "r"(src0 + src_at + e * kSrcStep));
       }
-      // NaN codes (all seven low bits set) take the conversion instruction
-      uint32_t nan = 0;
-#pragma unroll
-      for (int e = 0; e < kUnits; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) nan |= (c[e][i] & 0x7F7F7F7Fu) + 0x01010101u;
-      const bool exact = __any_sync(0xffffffffu, (nan & 0x80808080u) != 0);
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
-        const int x = ct + e * G::kConvWarps * 32, u = x % UPR, r = x / UPR;
-        uint32_t dst = dst0 + ((r / 8) * NCH + u / 4) * 1024 + (r % 8) * 128 + (u % 4) * 32;
-        dst ^= ((dst >> 7) & 7u) << 4;
-        // odd chunks store their second half first: the two chunks of a
-        // quarter-warp then use different banks
-        const bool odd = (u >> 2) & 1;
+        if (second) {
+          const uint32_t c0 = c[e][0], c1 = c[e][1];
+          c[e][0] = c[e][2];
+          c[e][1] = c[e][3];
+          c[e][2] = c0;
+          c[e][3] = c1;
+        }
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[2 * i] = exact ? e4m3x2_f16x2_256th(c[e][i], 0) : e4m3x2_shifted(c[e][i], 0);
-          w[2 * i + 1] = exact ? e4m3x2_f16x2_256th(c[e][i], 1) : e4m3x2_shifted(c[e][i], 1);
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(odd ? dst ^ 16 : dst),
-                     "r"(odd ? w[4] : w[0]), "r"(odd ? w[5] : w[1]), "r"(odd ? w[6] : w[2]),
-                     "r"(odd ? w[7] : w[3])
+        for (int i = 0; i < 8; ++i) w[i] = e4m3x2_f16x2(c[e][i / 2], i & 1);
+        const uint32_t dst = dst0 + dst_at + e * kDstStep;
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3])
                      : "memory");
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(odd ? dst : dst ^ 16),
-                     "r"(odd ? w[0] : w[4]), "r"(odd ? w[1] : w[5]), "r"(odd ? w[2] : w[6]),
-                     "r"(odd ? w[3] : w[7])
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst ^ 16), "r"(w[4]),
+                     "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1174,9 +1162,9 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   __syncthreads();
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers && lane == 0) {
     // no copy may still be writing this CTA's shared memory when it exits
-    for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+    for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
       if (!mbar_wait(&full[i % NS], (i / NS) & 1, p.err)) break;
-    for (int64_t i = issued_k > NK8 ? issued_k - NK8 : 0; i < issued_k; ++i)
+    for (uint32_t i = issued_k > NK8 ? issued_k - NK8 : 0; i < issued_k; ++i)
       if (!mbar_wait(&kfull[i % NK8], (i / NK8) & 1, p.err)) break;
   }
   if (warp == G::kMmaWarp) {
@@ -1413,6 +1401,7 @@ extern "C" int pkv_paged_attention_tree(
       num_seqs + static_cast<int64_t>(num_queries) * g / kTreeRows;
   const int64_t steps_most = tiles_most * cache.num_kv_heads *
                              ((static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok);
+  if (steps_most >= (int64_t{1} << 34)) return PKV_ERR_UNSUPPORTED;  // a CTA's share: 32 bits
   const int ctas = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(std::min(sms, kTreeMaxCtas),
                            (steps_most + p.min_steps - 1) / p.min_steps)));
