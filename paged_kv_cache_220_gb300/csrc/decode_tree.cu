@@ -62,6 +62,7 @@ namespace pkv {
 constexpr int kTreeMaxCtas = 160;  // one per SM; the workspace is sized for it
 constexpr int kTreeRows = 128;     // query rows of a tile
 constexpr int kTreeTok = 128;      // tokens of a step
+constexpr int kTreeEven = 4;
 
 struct TreeMeta {  // what the merge needs of a unit that starts in a CTA and is cut
   int row0;        // first query row (of q and out) of the sequence
@@ -89,7 +90,7 @@ struct TreeParams {
   float* part_l;
   int num_seqs, num_queries, max_draft;
   int num_blocks, num_kv_heads, num_heads, group, block_size, max_blocks_per_seq;
-  int min_steps;    // steps a CTA takes at least (fewer CTAs work on less)
+  int ctas;         // of the grid
   float qscale;
 };
 
@@ -526,8 +527,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     excl = quotient(excl, T);
   }
   const int share = T > 1 ? cta / T : cta;
-  const int64_t shares = min(static_cast<int64_t>(T > 1 ? gridDim.x / T : gridDim.x),
-                             quotient(total + p.min_steps - 1, p.min_steps));
+  // few steps to a CTA: as many CTAs as the longest share asks for, so that
+  // fewer shares begin or end inside a unit
+  const int most = static_cast<int>(T > 1 ? gridDim.x / T : gridDim.x);
+  const int64_t longest = quotient(total + most - 1, most);
+  const int64_t shares = longest > kTreeEven || longest == 0
+                             ? min(static_cast<int64_t>(most), total)
+                             : quotient(total + longest - 1, longest);
   const int64_t begin = share < shares ? quotient(share * total, shares) : 0;
   const int64_t end = share < shares ? quotient((share + 1) * total, shares) : 0;
   const int count = static_cast<int>(end - begin);
@@ -1173,19 +1179,20 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   }
 }
 
-// Joins the partials of the units that were cut: CTA (c, y) takes columns
-// 8 y .. of the unit that starts in share c, thread (i, r) of it the parts
-// i, i + GROUPS, ... of row r. With m_i, l_i, o_i of the unit's segments, M =
-// max m_i (base 2) and w_i = l_i 2^(m_i - M): out = sum (w_i / sum w) o_i.
-// GROUPS: 1 where units have few parts (all of a CTA's loads are in flight at
-// once, 16 CTAs to an SM), 4 where few units are cut into many.
-constexpr int kMergeCols = 8, kMergeParts = 4;  // parts whose loads are in flight at once
+// Joins the partials of the units that were cut: CTA (x, y) takes columns
+// 8 y .. of a unit, thread (i, r) of it the parts i, i + GROUPS, ... of row r.
+// With m_i, l_i, o_i of the unit's segments, M = max m_i (base 2) and w_i =
+// l_i 2^(m_i - M): out = sum (w_i / sum w) o_i. GROUPS = 1 where units have few
+// parts: x is the share that a unit starts in, as most have one. GROUPS = 8
+// where few units are cut into many: x counts the units that were cut (1 x
+// 8192 tokens x 4 KV heads, 38 parts each: @MERGE@).
+constexpr int kMergeCols = 8;
 
-// A load that stays where it is: left to itself the compiler moves each load
-// next to its use to save registers, one latency after the other.
+// A load that stays where it is: a plain one is moved next to its use to save
+// registers, one latency after the other (the merge of 5 parts: 9.6 us, so 4.1).
 __device__ __forceinline__ float load_now(const float* x) {
   float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(x) : "memory");
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(x) : "memory");
   return v;
 }
 
@@ -1193,12 +1200,32 @@ template <int D, int GROUPS>
 __global__ void __launch_bounds__(GROUPS * kTreeRows)
     tree_merge_kernel(const __grid_constant__ TreeParams p) {
   wait_prerequisite();
-  const int c = blockIdx.x;
+  int c = blockIdx.x;
+  if constexpr (GROUPS > 1) {
+    // the x-th share that has a unit to merge
+    __shared__ int below[kTreeMaxCtas / 32], mine;
+    static_assert(GROUPS * kTreeRows >= kTreeMaxCtas && kTreeMaxCtas % 32 == 0, "a thread each");
+    const int t = threadIdx.x;
+    const bool has = t < p.ctas && p.meta[t].parts > 0;
+    const uint32_t with = __ballot_sync(0xffffffffu, has);
+    if (t < kTreeMaxCtas && t % 32 == 0) below[t / 32] = __popc(with);
+    if (t == 0) mine = -1;
+    __syncthreads();
+    if (has) {
+      int rank = __popc(with & ((1u << (t % 32)) - 1));
+      for (int w = 0; w < t / 32; ++w) rank += below[w];
+      if (rank == c) mine = t;
+    }
+    __syncthreads();
+    c = mine;
+    if (c < 0) return;
+  }
   const TreeMeta md = p.meta[c];
   if (md.parts == 0) return;
   const int row = threadIdx.x % kTreeRows, grp = threadIdx.x / kTreeRows;
   const int c0 = blockIdx.y * kMergeCols;
   const bool live = row < md.rows;
+  constexpr int kMergeParts = GROUPS == 1 ? 4 : 5;  // parts whose loads are in flight at once
   // partial i: the first is share c's, the others are slot 0 of the next shares
   auto at = [&](int i) { return (c + i * md.stride) * 2 + (i == 0 ? md.slot : 0); };
   float M = -INFINITY, W = 0.f, acc[kMergeCols];
@@ -1276,13 +1303,15 @@ __global__ void __launch_bounds__(GROUPS * kTreeRows)
   const int r = md.first + row, draft = div_group(r, p.group);
   const int64_t hq = static_cast<int64_t>(md.row0 + draft) * p.num_heads + md.head * p.group +
                      (r - draft * p.group);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + hq * D + c0 + grp * E);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + hq * D + c0 + (E > 1 ? grp * E : 0));
   if constexpr (E == 8) {
     *reinterpret_cast<uint4*>(dst) =
         make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
                    pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
-  } else {
+  } else if constexpr (E == 2) {
     *dst = pack_bf16(o[0] * inv, o[1] * inv);
+  } else {
+    p.out[hq * D + c0 + grp] = float_to_bf16_bits(o[0] * inv);
   }
 }
 
@@ -1310,7 +1339,7 @@ static int tree_pool_map(CUtensorMap* out, const void* base, int64_t rows, int D
 
 template <int D, bool FP8>
 static int launch_tree(const TreeParams& p, const void* k_cache, const void* v_cache, int ctas,
-                       cudaStream_t st) {
+                       int64_t units, cudaStream_t st) {
   using G = TreeGeom<D, FP8>;
   const int64_t rows = static_cast<int64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   CUtensorMap tk, tv;
@@ -1326,10 +1355,13 @@ static int launch_tree(const TreeParams& p, const void* k_cache, const void* v_c
   if (rc != PKV_OK) return rc;
   // parts of a unit, if all were as long as the longest: its steps over a share's
   const int64_t pairs = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-  const bool many = ctas > 6 * pairs;
-  const dim3 grid(ctas, D / kMergeCols);
-  return many ? launch_dependent(tree_merge_kernel<D, 4>, grid, dim3(4 * kTreeRows), 0, st, p)
-              : launch_dependent(tree_merge_kernel<D, 1>, grid, dim3(kTreeRows), 0, st, p);
+  const bool many = ctas > 12 * pairs;
+  const int few = static_cast<int>(std::min<int64_t>(ctas, units));
+  constexpr int GR = 4, Y = D / kMergeCols;
+  return many ? launch_dependent(tree_merge_kernel<D, GR>, dim3(few, Y), dim3(GR * kTreeRows), 0,
+                                 st, p)
+              : launch_dependent(tree_merge_kernel<D, 1>, dim3(ctas, Y), dim3(kTreeRows), 0, st,
+                                 p);
 }
 
 }  // namespace pkv
@@ -1394,22 +1426,23 @@ extern "C" int pkv_paged_attention_tree(
   p.group = g;
   p.block_size = cache.block_size;
   p.max_blocks_per_seq = max_blocks_per_seq;
-  p.min_steps = 2;
   p.qscale = scale * 1.4426950408889634f;
   // no more CTAs than the call's bounds can give work
   const int64_t tiles_most =
       num_seqs + static_cast<int64_t>(num_queries) * g / kTreeRows;
-  const int64_t steps_most = tiles_most * cache.num_kv_heads *
+  const int64_t units = tiles_most * cache.num_kv_heads;
+  const int64_t steps_most = units *
                              ((static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok);
   if (steps_most >= (int64_t{1} << 34)) return PKV_ERR_UNSUPPORTED;  // a CTA's share: 32 bits
   const int ctas = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(std::min(sms, kTreeMaxCtas),
-                           (steps_most + p.min_steps - 1) / p.min_steps)));
+                           steps_most)));
+  p.ctas = ctas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache.dtype == PKV_DTYPE_FP8_E4M3;
   if (cache.head_dim == 128)
-    return fp8 ? launch_tree<128, true>(p, k_cache, v_cache, ctas, st)
-               : launch_tree<128, false>(p, k_cache, v_cache, ctas, st);
-  return fp8 ? launch_tree<256, true>(p, k_cache, v_cache, ctas, st)
-             : launch_tree<256, false>(p, k_cache, v_cache, ctas, st);
+    return fp8 ? launch_tree<128, true>(p, k_cache, v_cache, ctas, units, st)
+               : launch_tree<128, false>(p, k_cache, v_cache, ctas, units, st);
+  return fp8 ? launch_tree<256, true>(p, k_cache, v_cache, ctas, units, st)
+             : launch_tree<256, false>(p, k_cache, v_cache, ctas, units, st);
 }
