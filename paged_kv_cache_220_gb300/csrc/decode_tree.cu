@@ -121,6 +121,7 @@ struct TreeGeom {
   // S of step t at kColS + 128 * (t % kNB). Three buffers where they fit (d =
   // 128): S of step t + 1 then does not wait for the end of P.V of step t - 1
   static constexpr int kNB = D == 128 ? 3 : 2;
+  static constexpr int kLead = kNB - 1;  // steps that S runs ahead of P.V
   static constexpr uint32_t kColS = D;
   static constexpr uint32_t kCols = 512;
   static_assert(kColS + kNB * kTreeTok <= kCols, "tensor memory");
@@ -394,10 +395,11 @@ struct TreeQ {
 };
 
 // The number of V's first slot of step t in the ring's order (the slot is that
-// modulo the slots), of a CTA with `total` steps.
+// modulo the slots), of a CTA with `total` steps; `lead`: K of step t + lead
+// comes before V of step t.
 template <int KS, int VS>
-__device__ __forceinline__ int v_seq(int t, int total) {
-  return KS + t * (KS + VS) + (t + 1 < total ? KS : 0);
+__device__ __forceinline__ int v_seq(int t, int total, int lead) {
+  return KS * min(total, t + lead + 1) + t * VS;
 }
 
 template <int D, bool FP8>
@@ -694,10 +696,11 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         return true;
       };
       // ids of step t + 2; E4M3: K or V of step t, else K of step t and V of
-      // step t - 1
+      // step t - kLead
       Step now = fetch();
       advance();
-      Step ahead = fetch(), before = now;
+      Step ahead = fetch();
+      Step before[G::kLead];
       bool ok = true;
       for (int t = 0; t < count && ok; ++t) {
         advance();
@@ -708,13 +711,19 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           ok = loads_v ? copy_v(now) : copy_k(now);
         } else {
           ok = copy_k(now);
-          if (ok && t > 0) ok = copy_v(before);
-          before = now;
+          if (ok && t >= G::kLead) ok = copy_v(before[0]);
+#pragma unroll
+          for (int i = 0; i + 1 < G::kLead; ++i) before[i] = before[i + 1];
+          before[G::kLead - 1] = now;
         }
         now = ahead;
         ahead = far;
       }
-      if (!FP8 && ok) copy_v(before);
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int i = 0; i < G::kLead; ++i)
+          if (ok && count - G::kLead + i >= 0) ok = copy_v(before[i]);
+      }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp == G::kMmaWarp) {
@@ -731,9 +740,12 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       const uint64_t kd0 =
           FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
       const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
-      RingPos<NS> at;        // the ring's slots in turn
-      RingPos<NK8> at_k;     // E4M3: K's codes
-      RingPos<2> at_v;       // E4M3: V's 16-bit slots
+      // the slots of the next K and the next V; 16-bit pools: of one ring
+      RingPos<FP8 ? NK8 : NS> at_k;
+      RingPos<FP8 ? 2 : NS> at_v;
+      if constexpr (!FP8)
+        for (int i = v_seq<KS, VS>(0, count, G::kLead); i > 0; --i) at_v.next();
+      int s_done = 0, v_done = 0;  // steps whose S, whose P.V is issued
       RingPos<NB> sb, pb;    // S buffers: of the next S, of the next P.V
       uint32_t segs = 0;     // segments whose S has begun
       uint32_t pv_segs = 0;  // segments whose P.V has begun
@@ -764,18 +776,22 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         } else {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            if (!mbar_wait(&full[at.i], at.ph, p.err)) return false;
+            if (!mbar_wait(&full[at_k.i], at_k.ph, p.err)) return false;
             if (ks == 0 && !mbar_wait(&o_done[sb.i], sb.ph ^ 1, p.err)) return false;
             tc_fence_after();
-            const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
+            const uint64_t kd = kd0 + ((at_k.i * G::kSlot) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               umma_ss(ts, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
                       kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
                       (ks > 0 || k > 0) ? 1u : 0u);
             if (ks == KS - 1) umma_commit(&s_full[sb.i]);
-            umma_commit(&empty[at.i]);
-            at.next();
+            umma_commit(&empty[at_k.i]);
+            at_k.next();
+          }
+          if (s_done++ >= G::kLead) {  // over V of step s_done - kLead
+#pragma unroll
+            for (int vs = 0; vs < VS; ++vs) at_k.next();
           }
         }
         if (walk.ends()) umma_commit(q_empty);
@@ -788,13 +804,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         if (first && pv_segs++ > 0 && !mbar_wait(o_free, (pv_segs - 2) & 1, p.err)) return false;
 #pragma unroll
         for (int vs = 0; vs < VS; ++vs) {
-          uint64_t* f = FP8 ? &vfull[at_v.i] : &full[at.i];
-          uint64_t* e = FP8 ? &vempty[at_v.i] : &empty[at.i];
-          if (!mbar_wait(f, FP8 ? at_v.ph : at.ph, p.err)) return false;
+          uint64_t* f = FP8 ? &vfull[at_v.i] : &full[at_v.i];
+          uint64_t* e = FP8 ? &vempty[at_v.i] : &empty[at_v.i];
+          if (!mbar_wait(f, at_v.ph, p.err)) return false;
           if (vs == 0 && !mbar_wait(&p_full[pb.i], pb.ph, p.err)) return false;
           tc_fence_after();
           constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
-          const uint64_t vd = vd0 + (FP8 ? (at_v.i * G::kV16) >> 4 : (at.i * G::kSlot) >> 4);
+          const uint64_t vd = vd0 + ((at_v.i * (FP8 ? G::kV16 : G::kSlot)) >> 4);
           // P of tokens 16 kk of the step: 8 columns, 32 to each half of S's columns
           const uint32_t ps = t_s + pb.i * kTreeTok;
           auto pa = [&](int kk) { return ps + 64 * (kk / 4) + 8 * (kk % 4); };
@@ -812,44 +828,48 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           }
           if (vs == VS - 1) umma_commit(&o_done[pb.i]);
           umma_commit(e);
-          at.next();
           at_v.next();
+        }
+        if (!FP8 && ++v_done + G::kLead < count) {  // over K of step v_done + kLead
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) at_v.next();
         }
         pb.next();
         return true;
       };
-      bool prev_begins = false, any = false, ok = true;
-      int prev_tok = 0;  // valid tokens of the step before
-      while (walk.left > 0 && ok) {
-        const bool begins = walk.begins;
-        const int tok = min(kTreeTok, walk.q.ctx - walk.st * kTreeTok);
-        // a new segment's Q takes a while: P.V of the step before goes first
-        // then. The ring's order is K of step t, then V of step t - 1 all the same
-        if (any && begins) {
-          const RingPos<NS> k_at = at;
-          if constexpr (!FP8) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) at.next();
-          }
-          ok = issue_pv(prev_begins, prev_tok);
-          const RingPos<NS> after = at;
-          at = k_at;
-          ok = ok && issue_s();
-          at = after;
+      // S runs up to kLead steps ahead of P.V; a new segment's Q takes a while:
+      // every P.V before goes first then. The walk goes on where the lane has
+      // to wait anyway: for P or, with two S buffers, for the P.V just issued
+      // (the next S waits for it)
+      int pend[NB];  // steps whose P.V is to come: valid tokens, + 256 if a segment begins
+      int n = 0;
+      bool stale = false;  // the walk is still at the step whose S was issued last
+      for (;;) {
+        if (stale && n < NB) {
           walk.next(p);
-        } else {
-          // the walk goes on where the lane has to wait anyway: for P of the
-          // step before, or (two S buffers) for that P.V, which the next S waits for
-          ok = issue_s();
-          if (NB > 2) walk.next(p);
-          if (any) ok = ok && issue_pv(prev_begins, prev_tok);
-          if (NB == 2) walk.next(p);
+          stale = false;
         }
-        any = true;
-        prev_begins = begins;
-        prev_tok = tok;
+        if (!stale && walk.left > 0 && n < NB && !(walk.begins && n > 0)) {
+          const int info =
+              min(kTreeTok, walk.q.ctx - walk.st * kTreeTok) + (walk.begins ? 256 : 0);
+          if (!issue_s()) break;
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            if (i == n) pend[i] = info;
+          ++n;
+          if (NB > 2)
+            walk.next(p);
+          else
+            stale = true;
+        } else if (n > 0) {
+          if (!issue_pv(pend[0] >= 256, pend[0] & 255)) break;
+#pragma unroll
+          for (int i = 0; i + 1 < NB; ++i) pend[i] = pend[i + 1];
+          --n;
+        } else {
+          break;
+        }
       }
-      if (any && ok) (void)issue_pv(prev_begins, prev_tok);
       // every product issued here has finished before tensor memory is released
       umma_commit(drained);
       (void)mbar_wait(drained, 0, p.err);
@@ -1003,7 +1023,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                                                          p.err)))
           break;
         constexpr int NV = FP8 ? 2 : NS;
-        const int at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count)) + valid / G::kVTok;
+        const int at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count, G::kLead)) + valid / G::kVTok;
         const int i = at_v % NV;
         if (!__all_sync(0xffffffffu,
                         mbar_wait(FP8 ? &vfull[i] : &full[i], (at_v / NV) & 1, p.err)))
