@@ -110,12 +110,12 @@ struct TreeGeom {
   static constexpr int kV16 = 32768;
   static constexpr int kNV16 = FP8 ? 2 : 0;
   static constexpr int kSoftWarps = 8;
-  static constexpr int kMmaWarp = 8;
-  static constexpr int kProdWarp = FP8 ? 9 : 12, kProducers = FP8 ? 2 : 4;
-  static constexpr int kConvWarp = 11, kConvWarps = FP8 ? 4 : 0;
+  static constexpr int kSWarp = 8, kPvWarp = 9;
+  static constexpr int kProdWarp = FP8 ? 10 : 14, kProducers = 2;
+  static constexpr int kConvWarp = 12, kConvWarps = FP8 ? 4 : 0;
   // bf16: warps of their own load Q; E4M3: the converters do
-  static constexpr int kQWarp = FP8 ? kConvWarp : 9, kQWarps = FP8 ? kConvWarps : 3;
-  static constexpr int kThreads = (FP8 ? 15 : 16) * 32;
+  static constexpr int kQWarp = FP8 ? kConvWarp : 10, kQWarps = 4;
+  static constexpr int kThreads = 16 * 32;
   static constexpr int kHead = 3072;  // barriers, exchange buffers
   static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNK8 * kK8 + kNV16 * kV16;
   // S of step t at kColS + 128 * (t % kNB). Three buffers where they fit (d =
@@ -228,6 +228,13 @@ struct TreeWalk {
     tile = team ? member : unit - h * q.tiles;
   }
   __device__ __forceinline__ bool ends() const { return left == 1 || st + 1 == q.steps; }
+  // steps of the segment from this one on, and over them
+  __device__ __forceinline__ int run() const { return min(left, q.steps - st); }
+  __device__ __forceinline__ void skip(const TreeParams& p, int n) {
+    left -= n - 1;
+    st += n - 1;
+    next(p);
+  }
   __device__ __forceinline__ void next(const TreeParams& p) {
     begins = false;
     if (--left <= 0) return;
@@ -466,11 +473,11 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     mbar_init(q_full, G::kQWarps * 32);
     mbar_init(q_empty, 1);
     mbar_init(o_free, G::kSoftWarps * 32);
-    mbar_init(drained, 1);
+    mbar_init(drained, 2);
     mbar_init(q_first, G::kSoftWarps * 32);
     fence_mbar_init();
   }
-  if (warp == G::kMmaWarp) tmem_alloc(tmem_slot, G::kCols);
+  if (warp == G::kSWarp) tmem_alloc(tmem_slot, G::kCols);
   if (threadIdx.x == G::kProdWarp * 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
@@ -726,151 +733,135 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  } else if (warp == G::kMmaWarp) {
-    // ---------------- the products, issued by one lane. Operand descriptors
-    // are a constant plus the address: one addition each (built one by one
-    // they cost the issuing lane about as much as the tensor core takes for a
-    // product).
+  } else if (warp == G::kSWarp) {
+    // ---------------- the products S = Q.K^T, issued by one lane (P.V by a
+    // lane of another warp: waits, commits and loops of both in one lane took
+    // longer than the products). Operand descriptors are a constant plus the
+    // address: one addition each.
     if (elect_one()) {
-      constexpr uint32_t idesc_qk =
+      constexpr uint32_t idesc =
           FP8 ? umma_idesc_e4m3(128, kTreeTok) : umma_idesc_bf16(128, kTreeTok, false);
-      constexpr uint32_t idesc_pv = FP8 ? umma_idesc_f16(128, D, true)
-                                        : umma_idesc_bf16(128, D, true);
       const uint64_t qd = umma_sdesc(sq, 16, (FP8 ? NC8 : NCH) * 1024, 2);
       const uint64_t kd0 =
           FP8 ? umma_sdesc(k8, 16, NC8 * 1024, 2) : umma_sdesc(ring, 16, 2048, 2);
-      const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
-      // the slots of the next K and the next V; 16-bit pools: of one ring
-      RingPos<FP8 ? NK8 : NS> at_k;
-      RingPos<FP8 ? 2 : NS> at_v;
-      if constexpr (!FP8)
-        for (int i = v_seq<KS, VS>(0, count, G::kLead); i > 0; --i) at_v.next();
-      int s_done = 0, v_done = 0;  // steps whose S, whose P.V is issued
-      RingPos<NB> sb, pb;    // S buffers: of the next S, of the next P.V
-      uint32_t segs = 0;     // segments whose S has begun
-      uint32_t pv_segs = 0;  // segments whose P.V has begun
-      // S of the walk's step, over P of the step NB before
-      auto issue_s = [&] {
-        if (walk.begins) {
-          const bool in = segs == 0 ? mbar_wait(q_first, 0, p.err)
-                                    : mbar_wait(q_full, (segs - 1) & 1, p.err);
-          if (!in) return false;
-          ++segs;
-        }
-        const uint32_t ts = t_s + sb.i * kTreeTok;
-        if constexpr (FP8) {
-          if (!mbar_wait(&kfull[at_k.i], at_k.ph, p.err)) return false;
-          if (!mbar_wait(&o_done[sb.i], sb.ph ^ 1, p.err)) return false;
-          tc_fence_after();
-          const uint64_t kd = kd0 + ((at_k.i * G::kK8) >> 4);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              umma_ss_e4m3(ts, qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
-                           kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
-                           (part > 0 || k > 0) ? 1u : 0u);
-          umma_commit(&s_full[sb.i]);
-          umma_commit(&kempty[at_k.i]);
-          at_k.next();
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            if (!mbar_wait(&full[at_k.i], at_k.ph, p.err)) return false;
-            if (ks == 0 && !mbar_wait(&o_done[sb.i], sb.ph ^ 1, p.err)) return false;
+      RingPos<FP8 ? NK8 : NS> at;  // the next K's slot
+      RingPos<NB> sb;
+      int t = 0;
+      bool ok = true;
+      for (uint32_t seg = 0; walk.left > 0; ++seg) {
+        ok = seg == 0 ? mbar_wait(q_first, 0, p.err) : mbar_wait(q_full, (seg - 1) & 1, p.err);
+        const int n = walk.run();
+        for (int i = 0; i < n && ok; ++i, ++t) {
+          // over P of the step NB before. Its V is in then, so no wait for a
+          // slot of the ring is two phases ahead of its barrier
+          ok = mbar_wait(&o_done[sb.i], sb.ph ^ 1, p.err);
+          const uint32_t ts = t_s + sb.i * kTreeTok;
+          if constexpr (FP8) {
+            ok = ok && mbar_wait(&kfull[at.i], at.ph, p.err);
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t kd = kd0 + ((at_k.i * G::kSlot) >> 4);
+            const uint64_t kd = kd0 + ((at.i * G::kK8) >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ss(ts, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
-                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk,
-                      (ks > 0 || k > 0) ? 1u : 0u);
-            if (ks == KS - 1) umma_commit(&s_full[sb.i]);
-            umma_commit(&empty[at_k.i]);
-            at_k.next();
-          }
-          if (s_done++ >= G::kLead) {  // over V of step s_done - kLead
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int vs = 0; vs < VS; ++vs) at_k.next();
-          }
-        }
-        if (walk.ends()) umma_commit(q_empty);
-        sb.next();
-        return true;
-      };
-      // P.V of the step before, the first of its segment or not, with tok valid tokens
-      auto issue_pv = [&](bool first, int tok) {
-        // the segment before has left O
-        if (first && pv_segs++ > 0 && !mbar_wait(o_free, (pv_segs - 2) & 1, p.err)) return false;
-#pragma unroll
-        for (int vs = 0; vs < VS; ++vs) {
-          uint64_t* f = FP8 ? &vfull[at_v.i] : &full[at_v.i];
-          uint64_t* e = FP8 ? &vempty[at_v.i] : &empty[at_v.i];
-          if (!mbar_wait(f, at_v.ph, p.err)) return false;
-          if (vs == 0 && !mbar_wait(&p_full[pb.i], pb.ph, p.err)) return false;
-          tc_fence_after();
-          constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
-          const uint64_t vd = vd0 + ((at_v.i * (FP8 ? G::kV16 : G::kSlot)) >> 4);
-          // P of tokens 16 kk of the step: 8 columns, 32 to each half of S's columns
-          const uint32_t ps = t_s + pb.i * kTreeTok;
-          auto pa = [&](int kk) { return ps + 64 * (kk / 4) + 8 * (kk % 4); };
-          const int k1 = (tok + 15) / 16 - vs * kPer;
-          const uint32_t keep = !first || vs > 0 ? 1u : 0u;
-          if (k1 >= kPer) {
-#pragma unroll
-            for (int kk = 0; kk < kPer; ++kk)
-              umma_bf16_ta(t_o, pa(vs * kPer + kk), vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
-                           kk > 0 ? 1u : keep);
+              for (int k = 0; k < D / 32; ++k)
+                umma_ss_e4m3(ts,
+                             qd + ((part * kTreeRows * D + (k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                             kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc,
+                             (part > 0 || k > 0) ? 1u : 0u);
+            umma_commit(&s_full[sb.i]);
+            umma_commit(&kempty[at.i]);
+            at.next();
           } else {
-            for (int kk = 0; kk < k1; ++kk)
-              umma_bf16_ta(t_o, pa(vs * kPer + kk), vd + ((kk * 2 * NCH * 1024) >> 4), idesc_pv,
-                           kk > 0 ? 1u : keep);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              ok = ok && mbar_wait(&full[at.i], at.ph, p.err);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t kd = kd0 + ((at.i * G::kSlot) >> 4);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                umma_ss(ts, qd + (((ks * 2 + (k >> 2)) * 1024 + (k & 3) * 32) >> 4),
+                        kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc,
+                        (ks > 0 || k > 0) ? 1u : 0u);
+              if (ks == KS - 1) umma_commit(&s_full[sb.i]);
+              umma_commit(&empty[at.i]);
+              at.next();
+            }
+            if (t >= G::kLead) {  // over V of step t - kLead
+#pragma unroll
+              for (int vs = 0; vs < VS; ++vs) at.next();
+            }
           }
-          if (vs == VS - 1) umma_commit(&o_done[pb.i]);
-          umma_commit(e);
-          at_v.next();
+          sb.next();
         }
-        if (!FP8 && ++v_done + G::kLead < count) {  // over K of step v_done + kLead
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) at_v.next();
-        }
-        pb.next();
-        return true;
-      };
-      // S runs up to kLead steps ahead of P.V; a new segment's Q takes a while:
-      // every P.V before goes first then. The walk goes on where the lane has
-      // to wait anyway: for P or, with two S buffers, for the P.V just issued
-      // (the next S waits for it)
-      int pend[NB];  // steps whose P.V is to come: valid tokens, + 256 if a segment begins
-      int n = 0;
-      bool stale = false;  // the walk is still at the step whose S was issued last
-      for (;;) {
-        if (stale && n < NB) {
-          walk.next(p);
-          stale = false;
-        }
-        if (!stale && walk.left > 0 && n < NB && !(walk.begins && n > 0)) {
-          const int info =
-              min(kTreeTok, walk.q.ctx - walk.st * kTreeTok) + (walk.begins ? 256 : 0);
-          if (!issue_s()) break;
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
-            if (i == n) pend[i] = info;
-          ++n;
-          if (NB > 2)
-            walk.next(p);
-          else
-            stale = true;
-        } else if (n > 0) {
-          if (!issue_pv(pend[0] >= 256, pend[0] & 255)) break;
-#pragma unroll
-          for (int i = 0; i + 1 < NB; ++i) pend[i] = pend[i + 1];
-          --n;
-        } else {
-          break;
-        }
+        if (!ok) break;
+        umma_commit(q_empty);
+        walk.skip(p, n);
       }
       // every product issued here has finished before tensor memory is released
+      umma_commit(drained);
+      (void)mbar_wait(drained, 0, p.err);
+    }
+  } else if (warp == G::kPvWarp) {
+    // ---------------- the products O += P.V, issued by one lane
+    if (elect_one()) {
+      constexpr uint32_t idesc = FP8 ? umma_idesc_f16(128, D, true)
+                                     : umma_idesc_bf16(128, D, true);
+      const uint64_t vd0 = umma_sdesc(v16, 1024, NCH * 1024, 2);
+      RingPos<FP8 ? 2 : NS> at;  // the next V's slot
+      RingPos<NB> pb;
+      if constexpr (!FP8)
+        for (int i = v_seq<KS, VS>(0, count, G::kLead); i > 0; --i) at.next();
+      int t = 0;
+      bool ok = true;
+      for (uint32_t seg = 0; walk.left > 0; ++seg) {
+        // the segment before has left O
+        if (seg > 0) ok = mbar_wait(o_free, (seg - 1) & 1, p.err);
+        const int n = walk.run();
+        const int tail = walk.q.ctx - (walk.st + n - 1) * kTreeTok;  // tokens of the last step
+        for (int i = 0; i < n && ok; ++i, ++t) {
+          // P first: S of the step is done then, so no wait for a slot of the
+          // ring is two phases ahead of its barrier
+          ok = mbar_wait(&p_full[pb.i], pb.ph, p.err);
+          const uint32_t ps = t_s + pb.i * kTreeTok;
+          // P of tokens 16 kk of the step: 8 columns, 32 to each half of S's columns
+          auto pa = [&](int kk) { return ps + 64 * (kk / 4) + 8 * (kk % 4); };
+          const int tok = i + 1 < n ? kTreeTok : tail;
+#pragma unroll
+          for (int vs = 0; vs < VS; ++vs) {
+            uint64_t* f = FP8 ? &vfull[at.i] : &full[at.i];
+            uint64_t* e = FP8 ? &vempty[at.i] : &empty[at.i];
+            ok = ok && mbar_wait(f, at.ph, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            constexpr int kPer = G::kVTok / 16;  // k-steps of a slot
+            const uint64_t vd = vd0 + ((at.i * (FP8 ? G::kV16 : G::kSlot)) >> 4);
+            const uint32_t keep = i > 0 || vs > 0 ? 1u : 0u;
+            if (tok >= kTreeTok) {
+#pragma unroll
+              for (int kk = 0; kk < kPer; ++kk)
+                umma_bf16_ta(t_o, pa(vs * kPer + kk), vd + ((kk * 2 * NCH * 1024) >> 4), idesc,
+                             kk > 0 ? 1u : keep);
+            } else {
+              const int k1 = min(kPer, (tok + 15) / 16 - vs * kPer);
+              for (int kk = 0; kk < k1; ++kk)
+                umma_bf16_ta(t_o, pa(vs * kPer + kk), vd + ((kk * 2 * NCH * 1024) >> 4), idesc,
+                             kk > 0 ? 1u : keep);
+            }
+            if (vs == VS - 1) umma_commit(&o_done[pb.i]);
+            umma_commit(e);
+            at.next();
+          }
+          if (!FP8 && t + 1 + G::kLead < count) {  // over K of step t + 1 + kLead
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) at.next();
+          }
+          pb.next();
+        }
+        if (!ok) break;
+        walk.skip(p, n);
+      }
       umma_commit(drained);
       (void)mbar_wait(drained, 0, p.err);
     }
@@ -880,11 +871,6 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     const int row = 32 * quad + lane;
     const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
     const int g = p.group;
-    float m = -INFINITY, l = 0.f, qs = p.qscale;
-    uint64_t mask = 0;
-    bool live = false;
-    int draft = 0, head = 0;
-    int seg_st = 0;         // the segment's first step in its unit
     bool first_seg = true;  // of this share
     uint32_t seg = 0;
     uint32_t swaps = 0;     // exchanges with the row's other thread so far
@@ -905,196 +891,203 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       return true;
     };
     RingPos<NB> sb, before_sb;  // S buffer of the step, of the step before
-    for (int t = 0; walk.left > 0; ++t) {
-      const int b = sb.i;
+    bool ok = true;
+    for (int t = 0; walk.left > 0 && ok;) {
+      const int steps = walk.run();
       const int base_tok = walk.q.ctx - walk.q.n;
-      const bool begins = walk.begins;
-      if (begins) {
-        const int r = walk.tile * kTreeRows + row;
-        live = r < walk.q.n * g;
-        draft = live ? div_group(r, g) : 0;
-        head = walk.h * g + (live ? r - draft * g : 0);
-        mask = p.tree_mask != nullptr ? p.tree_mask[walk.q.q0 + draft] : (2ull << draft) - 1;
-        if (walk.q.n < 64) mask &= (1ull << walk.q.n) - 1;
-        if constexpr (FP8) qs = p.qscale * p.k_scale[walk.h];
-        m = -INFINITY;
-        l = 0.f;
-        seg_st = walk.st;
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], sb.ph, p.err))) break;
-      tc_fence_after();
-      if constexpr (FP8)
-        if (begins) {
-          // infinite or NaN queries give NaN
-          const int ex = q_exp[seg % 3 * 128 + row];
-          qs *= ex == -128 ? __uint_as_float(0x7FC00000u)
-                           : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        }
-      const uint32_t ts = t_s + lane_off + b * kTreeTok;
-      const int tok0 = walk.st * kTreeTok;
-      const bool clean = tok0 + kTreeTok <= base_tok;  // committed tokens only
-      // this thread's columns, 64 half .. 64 half + 63
-      const uint32_t mine = ts + 64 * half;
-      float sv[64];
-      tmem_ld64(mine, sv);
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (!clean) {
-        // scaled here, columns that the row does not see -inf; it sees the
-        // committed ones and those its mask names
+      const int r = walk.tile * kTreeRows + row;
+      const bool live = r < walk.q.n * g;
+      const int draft = live ? div_group(r, g) : 0;
+      const int head = walk.h * g + (live ? r - draft * g : 0);
+      uint64_t mask = p.tree_mask != nullptr ? p.tree_mask[walk.q.q0 + draft] : (2ull << draft) - 1;
+      if (walk.q.n < 64) mask &= (1ull << walk.q.n) - 1;
+      float m = -INFINITY, l = 0.f, qs = p.qscale;
+      if constexpr (FP8) qs *= p.k_scale[walk.h];
+      const int seg_st = walk.st;  // the segment's first step in its unit
+      ok = false;  // until the segment is through
+      int tok0 = seg_st * kTreeTok;
+      for (int i = 0;; ++i, ++t, tok0 += kTreeTok) {
+        const int b = sb.i;
+        const bool begins = i == 0;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[b], sb.ph, p.err))) break;
+        tc_fence_after();
+        if constexpr (FP8)
+          if (begins) {
+            // infinite or NaN queries give NaN
+            const int ex = q_exp[seg % 3 * 128 + row];
+            qs *= ex == -128 ? __uint_as_float(0x7FC00000u)
+                             : __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          }
+        const uint32_t ts = t_s + lane_off + b * kTreeTok;
+        const bool clean = tok0 + kTreeTok <= base_tok;  // committed tokens only
+        // this thread's columns, 64 half .. 64 half + 63
+        const uint32_t mine = ts + 64 * half;
+        float sv[64];
+        tmem_ld64(mine, sv);
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (!clean) {
+          // scaled here, columns that the row does not see -inf; it sees the
+          // committed ones and those its mask names
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int sh = tok0 + 64 * half + 32 * w - base_tok;  // draft of the first column
-          uint32_t see = ~0u;
-          if (sh >= 64) see = 0;
-          else if (sh >= 0) see = static_cast<uint32_t>(mask >> sh);
-          else if (sh > -32) see = static_cast<uint32_t>(mask << -sh) | ((1u << -sh) - 1);
+          for (int w = 0; w < 2; ++w) {
+            const int sh = tok0 + 64 * half + 32 * w - base_tok;  // draft of the first column
+            uint32_t see = ~0u;
+            if (sh >= 64) see = 0;
+            else if (sh >= 0) see = static_cast<uint32_t>(mask >> sh);
+            else if (sh > -32) see = static_cast<uint32_t>(mask << -sh) | ((1u << -sh) - 1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            sv[32 * w + i] = (see >> i) & 1 ? sv[32 * w + i] * qs : -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
-      } else {
-        if (qs >= 0.f) {
+            for (int i = 0; i < 32; ++i)
+              sv[32 * w + i] = (see >> i) & 1 ? sv[32 * w + i] * qs : -INFINITY;
+          }
 #pragma unroll
           for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
         } else {
+          if (qs >= 0.f) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], -sv[i]);
-        }
-      }
-      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      if (clean) mx *= fabsf(qs);
-      float other = mx;
-      if (!exchange(other)) break;
-      mx = fmaxf(mx, other);
-      // O is rescaled when the maximum grows by more than 2^8 (loads and
-      // stores of tensor memory are warp-collective: all lanes or none)
-      const bool want = mx > m + 8.f;
-      if (__any_sync(0xffffffffu, want) && !begins) {
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&o_done[before_sb.i], before_sb.ph, p.err)))
-          break;
-        tc_fence_after();
-        const float alpha = want ? fast_exp2(m - mx) : 1.f;  // 0 while m is -inf
-#pragma unroll 1
-        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-          float ov[16];
-          tmem_ld16(t_o + lane_off + c, ov);
+            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ov[i] *= alpha;
-          tmem_st16(t_o + lane_off + c, ov);
+            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], -sv[i]);
+          }
         }
-        if (want) l *= alpha;
-      }
-      if (want) m = mx;
-      const float ref = m == -INFINITY ? 0.f : m;
-      // P over this thread's own columns of S, two tokens to a column
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t pw[32];
-      if (clean) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
-          const float e = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
-          l4[(2 * i) & 3] += a;
-          l4[(2 * i + 1) & 3] += e;
-          pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = fast_exp2(sv[2 * i] - ref), e = fast_exp2(sv[2 * i + 1] - ref);
-          l4[(2 * i) & 3] += a;
-          l4[(2 * i + 1) & 3] += e;
-          pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
-        }
-      }
-      tmem_st16_nowait(mine, pw);
-      tmem_st16_nowait(mine + 16, pw + 16);
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      const int valid = walk.q.ctx - tok0;
-      if (valid < kTreeTok && (valid & 15) != 0) {
-        // the rows behind the context that the last product of P.V covers
-        // hold whatever was there: zero them, P is zero there. The step
-        // before is waited for first: its V may have been the slot's last
-        // use, and a wait must not be two phases ahead of its barrier
-        if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[before_sb.i], before_sb.ph,
-                                                         p.err)))
-          break;
-        constexpr int NV = FP8 ? 2 : NS;
-        const int at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count, G::kLead)) + valid / G::kVTok;
-        const int i = at_v % NV;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(FP8 ? &vfull[i] : &full[i], (at_v / NV) & 1, p.err)))
-          break;
-        const uint32_t vp = v16 + i * (FP8 ? G::kV16 : G::kSlot);
-        const int r0 = valid % G::kVTok, r1 = (r0 + 15) & ~15;
-        constexpr int U = NCH * 8;  // 16-byte units of a row
-        for (int x = threadIdx.x; x < (r1 - r0) * U; x += G::kSoftWarps * 32) {
-          const int r = r0 + x / U, u = x % U;
-          const uint32_t at =
-              vp + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at ^ (((at >> 7) & 7u) << 4)),
-                       "r"(0u)
-                       : "memory");
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[b]);
-      if (walk.ends()) {
-        // ---- the segment's result, each thread d / 2 columns of its row
-        other = l;
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        if (clean) mx *= fabsf(qs);
+        float other = mx;
         if (!exchange(other)) break;
-        const float sum = half == 0 ? l + other : other + l;
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[b], sb.ph, p.err))) break;
-        tc_fence_after();
-        const float inv = sum > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / sum : 0.f;
-        const bool whole = seg_st == 0 && walk.st + 1 == walk.q.steps;
-        const int c0 = half * (D / 2);
-        if (whole) {
-          uint16_t* dst = p.out +
-                          (static_cast<int64_t>(walk.q.q0 + draft) * p.num_heads + head) * D + c0;
+        mx = fmaxf(mx, other);
+        // O is rescaled when the maximum grows by more than 2^8 (loads and
+        // stores of tensor memory are warp-collective: all lanes or none)
+        const bool want = mx > m + 8.f;
+        if (__any_sync(0xffffffffu, want) && !begins) {
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait(&o_done[before_sb.i], before_sb.ph, p.err)))
+            break;
+          tc_fence_after();
+          const float alpha = want ? fast_exp2(m - mx) : 1.f;  // 0 while m is -inf
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
+          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
             float ov[16];
-            tmem_ld16(t_o + lane_off + c0 + c, ov);
-            if (live) {
-              uint32_t w[8];
+            tmem_ld16(t_o + lane_off + c, ov);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = pack_bf16(ov[2 * i] * inv, ov[2 * i + 1] * inv);
-              reinterpret_cast<uint4*>(dst + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(dst + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+            for (int i = 0; i < 16; ++i) ov[i] *= alpha;
+            tmem_st16(t_o + lane_off + c, ov);
+          }
+          if (want) l *= alpha;
+        }
+        if (want) m = mx;
+        const float ref = m == -INFINITY ? 0.f : m;
+        // P over this thread's own columns of S, two tokens to a column
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pw[32];
+        if (clean) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
+            const float e = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
+            l4[(2 * i) & 3] += a;
+            l4[(2 * i + 1) & 3] += e;
+            pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
           }
         } else {
-          // a partial, a column's rows side by side: full lines per store
-          const int64_t part = static_cast<int64_t>(cta) * 2 + (first_seg ? 0 : 1);
-          float* dst = p.part_o + (part * D + c0) * kTreeRows + row;
-#pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
-            float ov[16];
-            tmem_ld16(t_o + lane_off + c0 + c, ov);
-            if (live) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) dst[(c + i) * kTreeRows] = ov[i] * inv;
-            }
-          }
-          if (live && half == 0) {
-            p.part_m[part * kTreeRows + row] = m;
-            p.part_l[part * kTreeRows + row] = sum;
+          for (int i = 0; i < 32; ++i) {
+            const float a = fast_exp2(sv[2 * i] - ref), e = fast_exp2(sv[2 * i + 1] - ref);
+            l4[(2 * i) & 3] += a;
+            l4[(2 * i + 1) & 3] += e;
+            pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
           }
         }
+        tmem_st16_nowait(mine, pw);
+        tmem_st16_nowait(mine + 16, pw + 16);
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        const int valid = walk.q.ctx - tok0;
+        if (valid < kTreeTok && (valid & 15) != 0) {
+          // the rows behind the context that the last product of P.V covers
+          // hold whatever was there: zero them, P is zero there. The step
+          // before is waited for first: its V may have been the slot's last
+          // use, and a wait must not be two phases ahead of its barrier
+          if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[before_sb.i], before_sb.ph,
+                                                           p.err)))
+            break;
+          constexpr int NV = FP8 ? 2 : NS;
+          const int at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count, G::kLead)) + valid / G::kVTok;
+          const int i = at_v % NV;
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait(FP8 ? &vfull[i] : &full[i], (at_v / NV) & 1, p.err)))
+            break;
+          const uint32_t vp = v16 + i * (FP8 ? G::kV16 : G::kSlot);
+          const int r0 = valid % G::kVTok, r1 = (r0 + 15) & ~15;
+          constexpr int U = NCH * 8;  // 16-byte units of a row
+          for (int x = threadIdx.x; x < (r1 - r0) * U; x += G::kSoftWarps * 32) {
+            const int r = r0 + x / U, u = x % U;
+            const uint32_t at =
+                vp + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at ^ (((at >> 7) & 7u) << 4)),
+                         "r"(0u)
+                         : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(o_free);
-        first_seg = false;
-        ++seg;
+        mbar_arrive(&p_full[b]);
+        if (i + 1 == steps) {
+          // ---- the segment's result, each thread d / 2 columns of its row
+          other = l;
+          if (!exchange(other)) break;
+          const float sum = half == 0 ? l + other : other + l;
+          if (!__all_sync(0xffffffffu, mbar_wait(&o_done[b], sb.ph, p.err))) break;
+          tc_fence_after();
+          const float inv = sum > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / sum : 0.f;
+          const bool whole = seg_st == 0 && steps == walk.q.steps;
+          const int c0 = half * (D / 2);
+          if (whole) {
+            uint16_t* dst = p.out +
+                            (static_cast<int64_t>(walk.q.q0 + draft) * p.num_heads + head) * D + c0;
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 16) {
+              float ov[16];
+              tmem_ld16(t_o + lane_off + c0 + c, ov);
+              if (live) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(ov[2 * i] * inv, ov[2 * i + 1] * inv);
+                reinterpret_cast<uint4*>(dst + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          } else {
+            // a partial, a column's rows side by side: full lines per store
+            const int64_t part = static_cast<int64_t>(cta) * 2 + (first_seg ? 0 : 1);
+            float* dst = p.part_o + (part * D + c0) * kTreeRows + row;
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 16) {
+              float ov[16];
+              tmem_ld16(t_o + lane_off + c0 + c, ov);
+              if (live) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) dst[(c + i) * kTreeRows] = ov[i] * inv;
+              }
+            }
+            if (live && half == 0) {
+              p.part_m[part * kTreeRows + row] = m;
+              p.part_l[part * kTreeRows + row] = sum;
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(o_free);
+          first_seg = false;
+          ++seg;
+          ok = true;
+        }
+        before_sb = sb;
+        sb.next();
+        if (ok) {
+          ++t;
+          break;
+        }
       }
-      before_sb = sb;
-      sb.next();
-      walk.next(p);
+      walk.skip(p, steps);
     }
   } else if (!FP8 && warp >= G::kQWarp && warp < G::kQWarp + G::kQWarps) {
     // ---------------- Q of each segment but the first
@@ -1198,7 +1191,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     for (uint32_t i = issued_k > NK8 ? issued_k - NK8 : 0; i < issued_k; ++i)
       if (!mbar_wait(&kfull[i % NK8], (i / NK8) & 1, p.err)) break;
   }
-  if (warp == G::kMmaWarp) {
+  if (warp == G::kSWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, G::kCols);
   }
