@@ -63,6 +63,7 @@ constexpr int kTreeMaxCtas = 160;  // one per SM; the workspace is sized for it
 constexpr int kTreeRows = 128;     // query rows of a tile
 constexpr int kTreeTok = 128;      // tokens of a step
 constexpr int kTreeEven = 4;       // shares of at most so many steps are cut evenly
+constexpr int kTreeStart = 3;      // steps that a unit's start counts for in longer ones
 
 struct TreeMeta {  // what the merge needs of a unit that starts in a CTA and is cut
   int row0;        // first query row (of q and out) of the sequence
@@ -88,7 +89,7 @@ struct TreeParams {
   float* part_o;    // [ctas][2][d][128]: a column's rows side by side
   float* part_m;    // [ctas][2][128]
   float* part_l;
-  int num_seqs, num_queries, max_draft;
+  int num_seqs, num_queries, max_draft, max_context;
   int num_blocks, num_kv_heads, num_heads, group, block_size, max_blocks_per_seq;
   int ctas;         // of the grid
   float qscale;
@@ -174,7 +175,8 @@ struct TreeSeq {
     q0 = first;
     ctx = context;
     const bool ctx_ok =
-        ctx >= 0 && ctx <= static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+        ctx >= 0 && ctx <= p.max_context &&
+        ctx <= static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
     const bool ok = ctx_ok && q0 >= 0 && next >= q0 && next <= p.num_queries &&
                     next - q0 <= p.max_draft && next - q0 <= ctx;
     if (!ok && report) report_error(p.err, ctx_ok ? PKV_DEVERR_DRAFT : PKV_DEVERR_CONTEXT);
@@ -185,8 +187,8 @@ struct TreeSeq {
   __device__ __forceinline__ void load(const TreeParams& p, int s, bool report) {
     set(p, p.q_start[s], p.q_start[s + 1], p.context_lens[s], report);
   }
-  __device__ __forceinline__ int64_t weight(const TreeParams& p) const {
-    return static_cast<int64_t>(p.num_kv_heads) * tiles * steps;
+  __device__ __forceinline__ int units(const TreeParams& p) const {
+    return p.num_kv_heads * tiles;
   }
 };
 
@@ -210,10 +212,10 @@ struct TreeWalk {
     next_q1 = p.q_start[x + 1];
     next_ctx = p.context_lens[x];
   }
-  // off: the share's first step, counted from sequence s0's first; member: the
+  // at: the share's first step in unit `unit` of sequence s0; member: the
   // CTA's tile if it belongs to a team, else -1
-  __device__ __forceinline__ void start(const TreeParams& p, const TreeSeq& q0, int s0,
-                                        int64_t off, int count, int member) {
+  __device__ __forceinline__ void start(const TreeParams& p, const TreeSeq& q0, int s0, int unit,
+                                        int at, int count, int member) {
     q = q0;
     s = s0;
     left = count;
@@ -222,8 +224,7 @@ struct TreeWalk {
     h = tile = st = 0;
     if (count <= 0) return;
     peek(p);
-    const int unit = static_cast<int>(quotient(off, q.steps));
-    st = static_cast<int>(off - static_cast<int64_t>(unit) * q.steps);
+    st = at;
     h = team ? unit : unit / q.tiles;
     tile = team ? member : unit - h * q.tiles;
   }
@@ -437,10 +438,9 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   uint64_t* drained = o_free + 1;
   uint64_t* q_first = drained + 1;                       // Q of the share's first segment
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 376);
-  int* found = reinterpret_cast<int*>(sbase + 380);            // sequence, its TreeSeq
-  int64_t* found_off = reinterpret_cast<int64_t*>(sbase + 408);  // the share's first step in it
-  int64_t* wsum = reinterpret_cast<int64_t*>(sbase + 416);     // [warps], until the share is known
-  int* wtiles = reinterpret_cast<int*>(sbase + 576);           // [warps][2], the same
+  int* found = reinterpret_cast<int*>(sbase + 380);  // sequence, its TreeSeq, unit, step
+  int* cut = reinterpret_cast<int*>(sbase + 992);              // steps before the share, its end
+  int4* wsum = reinterpret_cast<int4*>(sbase + 416);           // [warps], until the share is known
   int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 416);      // [3][128] E4M3: e of Q's rows
   int32_t* ids = reinterpret_cast<int32_t*>(sbase + 800);      // [2][3][8] block ids of three steps
   float* xch = reinterpret_cast<float*>(sbase + 1024);         // [2][2][128]
@@ -491,12 +491,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   const int per = (p.num_seqs + G::kThreads - 1) / G::kThreads;
   const int s_lo = min(p.num_seqs, static_cast<int>(threadIdx.x) * per);
   const int s_hi = min(p.num_seqs, s_lo + per);
-  int64_t mine = 0;
+  int mine = 0, units = 0;  // steps, units
   int tiles_lo = INT_MAX, tiles_hi = 0;  // of sequences that have drafts
   TreeSeq seq;  // the run's last sequence (its only one, for small batches)
   for (int s = s_lo; s < s_hi; ++s) {
     seq.load(p, s, cta == 0);
-    mine += seq.weight(p);
+    units += seq.units(p);
+    mine += seq.units(p) * seq.steps;
     if (seq.tiles > 0) {
       tiles_lo = min(tiles_lo, seq.tiles);
       tiles_hi = max(tiles_hi, seq.tiles);
@@ -504,74 +505,102 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   }
   tiles_lo = __reduce_min_sync(0xffffffffu, tiles_lo);
   tiles_hi = __reduce_max_sync(0xffffffffu, tiles_hi);
-  int64_t incl = mine;
+  int before = mine, before_u = units;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += x;
+    const int x = __shfl_up_sync(0xffffffffu, before, off);
+    const int y = __shfl_up_sync(0xffffffffu, before_u, off);
+    if (lane >= off) {
+      before += x;
+      before_u += y;
+    }
   }
-  if (lane == 31) {
-    wsum[warp] = incl;
-    wtiles[2 * warp] = tiles_lo;
-    wtiles[2 * warp + 1] = tiles_hi;
-  }
+  if (lane == 31) wsum[warp] = make_int4(before, before_u, tiles_lo, tiles_hi);
+  before -= mine;
+  before_u -= units;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t before = 0, total = 0;
+  int total = 0, total_u = 0;
 #pragma unroll
   for (int w = 0; w < G::kThreads / 32; ++w) {
-    if (w < warp) before += wsum[w];
-    total += wsum[w];
-    tiles_lo = min(tiles_lo, wtiles[2 * w]);
-    tiles_hi = max(tiles_hi, wtiles[2 * w + 1]);
+    const int4 x = wsum[w];
+    if (w < warp) {
+      before += x.x;
+      before_u += x.y;
+    }
+    total += x.x;
+    total_u += x.y;
+    tiles_lo = min(tiles_lo, x.z);
+    tiles_hi = max(tiles_hi, x.w);
   }
   // teams: shares in steps of (sequence, KV head), T CTAs to a share
   const int T = tiles_lo == tiles_hi && tiles_hi > 1 &&
                         tiles_hi <= static_cast<int>(gridDim.x) ? tiles_hi : 1;
-  int64_t excl = before + incl - mine;
   if (T > 1) {
-    total = quotient(total, T);
-    mine = quotient(mine, T);
-    excl = quotient(excl, T);
+    total /= T;
+    before /= T;
+    mine /= T;
+    total_u /= T;
+    before_u /= T;
+    units /= T;
   }
   const int share = T > 1 ? cta / T : cta;
   // few steps to a CTA: as many CTAs as the longest share asks for, so that
   // fewer shares begin or end inside a unit
   const int most = static_cast<int>(T > 1 ? gridDim.x / T : gridDim.x);
-  const int64_t longest = quotient(total + most - 1, most);
-  const int64_t shares = longest > kTreeEven || longest == 0
-                             ? min(static_cast<int64_t>(most), total)
-                             : quotient(total + longest - 1, longest);
-  const int64_t begin = share < shares ? quotient(share * total, shares) : 0;
-  const int64_t end = share < shares ? quotient((share + 1) * total, shares) : 0;
-  const int count = static_cast<int>(end - begin);
-  if (count > 0 && excl <= begin && begin < excl + mine) {
-    int64_t at = excl;
-    int s = s_lo;
-    if (per > 1) {
+  const int longest = (total + most - 1) / most;
+  const int shares = longest > kTreeEven ? most
+                     : longest > 0       ? (total + longest - 1) / longest
+                                         : 0;
+  // many: a unit's start counts as W steps (its Q, its result)
+  const int W = longest > kTreeEven ? kTreeStart : 0;
+  total += W * total_u;
+  auto bound = [&](int x) {  // where share x of the line begins
+    return static_cast<int>(quotient(static_cast<int64_t>(x) * total, shares));
+  };
+  int begin = 0, end = 0;
+  if (share < shares) {
+    begin = bound(share);
+    end = bound(share + 1);
+    // where it begins and ends: found in the runs that hold these places
+    const int lo = before + W * before_u, hi = lo + mine + W * units;
+    if (threadIdx.x == 0 && end == total) cut[1] = total - W * total_u;
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      const int x = e == 0 ? begin : end;
+      if (x < lo || x >= hi) continue;
+      int at = lo, steps = before, s = s_lo;
       for (;; ++s) {
-        seq.load(p, s, false);
-        const int64_t w = quotient(seq.weight(p), T);
-        if (begin < at + w) break;
-        at += w;
+        if (per > 1) seq.load(p, s, false);
+        const int n = T > 1 ? p.num_kv_heads : seq.units(p);
+        if (per == 1 || x < at + n * (seq.steps + W)) break;
+        at += n * (seq.steps + W);
+        steps += n * seq.steps;
+      }
+      const int unit = (x - at) / (seq.steps + W);
+      const int st = max(0, x - at - unit * (seq.steps + W) - W);
+      cut[e] = steps + unit * seq.steps + st;
+      if (e == 0) {
+        found[0] = s;
+        found[1] = seq.ctx;
+        found[2] = seq.n;
+        found[3] = seq.q0;
+        found[4] = seq.tiles;
+        found[5] = seq.steps;
+        found[6] = unit;
+        found[7] = st;
       }
     }
-    found[0] = s;
-    found[1] = seq.ctx;
-    found[2] = seq.n;
-    found[3] = seq.q0;
-    found[4] = seq.tiles;
-    found[5] = seq.steps;
-    *found_off = begin - at;
   }
   __syncthreads();
+  const int count = begin < end ? cut[1] - cut[0] : 0;
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_o = tmem;
   const uint32_t t_s = tmem + G::kColS;
   TreeWalk walk;
-  walk.start(p, TreeSeq{found[1], found[2], found[3], found[4], found[5]}, found[0],
-             *found_off, count, T > 1 ? cta % T : -1);
+  walk.start(p, TreeSeq{found[1], found[2], found[3], found[4], found[5]}, found[0], found[6],
+             found[7], count, T > 1 ? cta % T : -1);
 
   uint32_t issued = 0, issued_k = 0;  // producers: slots whose copies were started
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers) {
@@ -601,16 +630,16 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       auto advance = [&] {
         if (walk.left == 1 && warp == G::kProdWarp && lane == 0 && seg_st == 0 &&
             walk.st + 1 < walk.q.steps) {
-          const int64_t u_end = end + (walk.q.steps - 1 - walk.st);
-          int64_t last = share + 1;
-          while (quotient((last + 1) * total, shares) < u_end) ++last;
+          const int u_end = end + (walk.q.steps - 1 - walk.st);
+          int last = share + 1;
+          while (bound(last + 1) < u_end) ++last;
           TreeMeta md;
           md.row0 = walk.q.q0;
           md.first = walk.tile * kTreeRows;
           md.rows = min(kTreeRows, walk.q.n * p.group - md.first);
           md.head = walk.h;
           md.slot = first_seg ? 0 : 1;
-          md.parts = static_cast<int>(last - share + 1);
+          md.parts = last - share + 1;
           md.stride = T;
           p.meta[cta] = md;
         }
@@ -638,7 +667,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         x.pages = walk.left > 0
                       ? (min(kTreeTok, walk.q.ctx - walk.st * kTreeTok) + B - 1) >> lgB : 0;
         if (page < x.pages)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(my_ids + put * 8)),
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                           smem_addr(my_ids + put * 8)),
                        "l"(p.block_tables +
                            static_cast<int64_t>(walk.s) * p.max_blocks_per_seq +
                            walk.st * (kTreeTok >> lgB) + page)
@@ -1020,11 +1050,9 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           constexpr int U = NCH * 8;  // 16-byte units of a row
           for (int x = threadIdx.x; x < (r1 - r0) * U; x += G::kSoftWarps * 32) {
             const int r = r0 + x / U, u = x % U;
-            const uint32_t at =
-                vp + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 + (u % 8) * 16;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at ^ (((at >> 7) & 7u) << 4)),
-                         "r"(0u)
-                         : "memory");
+            const uint32_t at = vp + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 +
+                                ((u % 8) ^ (r % 8)) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
@@ -1439,6 +1467,7 @@ extern "C" int pkv_paged_attention_tree(
   p.num_seqs = num_seqs;
   p.num_queries = num_queries;
   p.max_draft = max_draft;
+  p.max_context = max_context;
   p.num_blocks = cache.num_blocks;
   p.num_kv_heads = cache.num_kv_heads;
   p.num_heads = num_heads;
@@ -1450,12 +1479,12 @@ extern "C" int pkv_paged_attention_tree(
   const int64_t tiles_most =
       num_seqs + static_cast<int64_t>(num_queries) * g / kTreeRows;
   const int64_t units = tiles_most * cache.num_kv_heads;
-  const int64_t steps_most = units *
-                             ((static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok);
-  if (steps_most >= (int64_t{1} << 34)) return PKV_ERR_UNSUPPORTED;  // a CTA's share: 32 bits
+  const int64_t longest = (static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok;
+  // places of the line are 32-bit numbers (a q_start that is not ascending
+  // may ask for up to twice the work)
+  if (units * (longest + kTreeStart) >= (1 << 29)) return PKV_ERR_UNSUPPORTED;
   const int ctas = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>(std::min(sms, kTreeMaxCtas),
-                           steps_most)));
+      1, std::min<int64_t>(std::min(sms, kTreeMaxCtas), units * longest)));
   p.ctas = ctas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache.dtype == PKV_DTYPE_FP8_E4M3;
