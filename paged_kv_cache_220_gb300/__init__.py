@@ -20,6 +20,7 @@ Tensors (caller-owned device memory):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -472,6 +473,20 @@ def _ptr(t, name, index, dtypes, shape=None):
     return t.data_ptr()
 
 
+def _pool_ptrs(pools, name, index, like):
+    """The addresses of contiguous pools of `like`'s type and shape, as a C array."""
+    dt, shape = like.dtype, like.shape
+    # one comprehension: a pool is checked in 0.2 us, by _ptr in 0.3
+    found = [t.data_ptr() for t in pools if isinstance(t, torch.Tensor)
+             and t.get_device() == index and t.dtype is dt and t.shape == shape
+             and t.is_contiguous()]
+    if len(found) != len(pools):
+        for t in pools:
+            if t is None or _ptr(t, name, index, (dt,), shape) is None:
+                raise ValueError("%s must be tensors" % name)
+    return (_P * len(found))(*found)
+
+
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
@@ -508,16 +523,38 @@ def _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_
             _ptr(context_lens, "context_lens", dev, _I32, (S,)))
 
 
-def _scratch(workspace, need, q):
-    """(address, bytes, tensor) of a call's workspace, allocated if not given."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        return workspace.data_ptr(), need, workspace
-    if not workspace.is_contiguous() or workspace.get_device() != q.get_device():
-        raise ValueError("workspace must be a contiguous tensor on the device of the others")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+if _raw_alloc is None or _raw_free is None:
+    _raw_alloc = lambda n, raw: torch.cuda.caching_allocator_alloc(n, stream=raw)  # noqa: E731
+    _raw_free = torch.cuda.caching_allocator_delete
+
+
+class _Scratch:
+    """A call's workspace, as `with ... as (address, bytes)`: the given tensor
+    or, of the current device's caching allocator, memory of the stream `raw`
+    that goes back when the work is enqueued (what comes next in the stream may
+    use it then). As a tensor it would cost 4 us more per call."""
+
+    __slots__ = ("own", "got")
+
+    def __init__(self, workspace, need, dev, raw):
+        self.own = None
+        if workspace is None:
+            self.own = _raw_alloc(need, raw) if need else None
+            self.got = self.own, need
+            return
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError(
+                "workspace must be a contiguous tensor on the device of the others")
+        self.got = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+    def __enter__(self):
+        return self.got
+
+    def __exit__(self, *exc):
+        if self.own is not None:
+            _raw_free(self.own)
 
 
 def window_partition_size(num_seqs, num_kv_heads, block_size, max_context, window,
@@ -551,24 +588,32 @@ def paged_attention_window(q, k_cache, v_cache, block_tables, context_lens, scal
         q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, True, out)
     order = _ptr(seq_order, "seq_order", dev, _I32, (S,))
     if partition_size is None:
-        partition_size = L.pkv_window_partition_size(S, desc.num_kv_heads, desc.block_size,
-                                                     max_context, window, sinks)
+        partition_size = _window_partition(S, desc.num_kv_heads, desc.block_size, max_context,
+                                           window, sinks)
         if partition_size < 0:
             _check(partition_size, "window_partition_size")
     with _at(dev, stream) as raw:
         if out is None:
             out = torch.empty_like(q)
             op = out.data_ptr()
-        need = 0 if partition_size == 0 else L.pkv_window_workspace_bytes(
+        need = 0 if partition_size == 0 or workspace is not None else _window_need(
             S, shape[1], desc.head_dim, desc.block_size, max_context, window, sinks,
             partition_size)
-        ws, wsb, keep = _scratch(workspace, need, q)
-        rc = L.pkv_paged_attention_window(
-            op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, S, shape[1],
-            max_context, scale, window, sinks, partition_size, ws, wsb, order, raw)
+        with _Scratch(workspace, need, dev, raw) as (ws, wsb):
+            rc = L.pkv_paged_attention_window(
+                op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, S, shape[1],
+                max_context, scale, window, sinks, partition_size, ws, wsb, order, raw)
     if rc:
         _check(rc, "paged_attention_window")
     return out
+
+
+# Functions of their sizes alone, asked for at every call (a call into the
+# library is 1 us).
+_window_partition = functools.lru_cache(1024)(
+    lambda *sizes: lib().pkv_window_partition_size(*sizes))
+_window_need = functools.lru_cache(1024)(lambda *sizes: lib().pkv_window_workspace_bytes(*sizes))
+_tree_need = functools.lru_cache(1024)(lambda *sizes: lib().pkv_tree_workspace_bytes(*sizes))
 
 
 def tree_workspace_bytes(num_seqs, num_queries, num_heads, num_kv_heads, head_dim, max_context,
@@ -598,12 +643,12 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, context_lens, q_star
         if out is None:
             out = torch.empty_like(q)
             op = out.data_ptr()
-        need = L.pkv_tree_workspace_bytes(S, n, shape[1], desc.num_kv_heads, desc.head_dim,
-                                          max_context, max_draft) if workspace is None else 0
-        ws, wsb, keep = _scratch(workspace, need, q)
-        rc = L.pkv_paged_attention_tree(
-            op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, start, S, n,
-            max_draft, mask, shape[1], max_context, scale, ws, wsb, raw)
+        need = _tree_need(S, n, shape[1], desc.num_kv_heads, desc.head_dim, max_context,
+                          max_draft) if workspace is None else 0
+        with _Scratch(workspace, need, dev, raw) as (ws, wsb):
+            rc = L.pkv_paged_attention_tree(
+                op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, start, S, n,
+                max_draft, mask, shape[1], max_context, scale, ws, wsb, raw)
     if rc:
         _check(rc, "paged_attention_tree")
     return out
@@ -626,12 +671,12 @@ def kv_cache_accept(k_caches, v_caches, block_tables, context_lens, q_start, acc
     if n != len(v_caches) or not n:
         raise ValueError("k_caches and v_caches must be equally many, one at least")
     first = k_caches[0]
-    desc, dev, shape, dt = cache_desc(first), first.get_device(), first.shape, (first.dtype,)
+    desc, dev = cache_desc(first), first.get_device()
     if block_tables.dim() != 2 or accepted.dim() != 2:
         raise ValueError("block_tables must be [S, max_blocks], accepted [S, M]")
     S, M = block_tables.shape[0], accepted.shape[1]
-    pools = (_P * n)(*[_ptr(t, "k_caches", dev, dt, shape) for t in k_caches])
-    vpools = (_P * n)(*[_ptr(t, "v_caches", dev, dt, shape) for t in v_caches])
+    pools = _pool_ptrs(k_caches, "k_caches", dev, first)
+    vpools = _pool_ptrs(v_caches, "v_caches", dev, first)
     tables = _ptr(block_tables, "block_tables", dev, _I32)
     lens = _ptr(context_lens, "context_lens", dev, _I32, (S,))
     start = _ptr(q_start, "q_start", dev, _I32, (S + 1,))
