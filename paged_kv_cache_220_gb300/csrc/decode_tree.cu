@@ -1069,6 +1069,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           const float inv = sum > 0.f ? (FP8 ? p.v_scale[walk.h] : 1.f) / sum : 0.f;
           const bool whole = seg_st == 0 && steps == walk.q.steps;
           const int c0 = half * (D / 2);
+          const int64_t part = static_cast<int64_t>(cta) * 2 + (first_seg ? 0 : 1);
           if (whole) {
             uint16_t* dst = p.out +
                             (static_cast<int64_t>(walk.q.q0 + draft) * p.num_heads + head) * D + c0;
@@ -1076,6 +1077,10 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
             for (int c = 0; c < D / 2; c += 16) {
               float ov[16];
               tmem_ld16(t_o + lane_off + c0 + c, ov);
+              if (c + 16 == D / 2) {  // O is free; what is left are stores
+                tc_fence_before();
+                mbar_arrive(o_free);
+              }
               if (live) {
                 uint32_t w[8];
 #pragma unroll
@@ -1086,24 +1091,25 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
             }
           } else {
             // a partial, a column's rows side by side: full lines per store
-            const int64_t part = static_cast<int64_t>(cta) * 2 + (first_seg ? 0 : 1);
             float* dst = p.part_o + (part * D + c0) * kTreeRows + row;
 #pragma unroll 1
             for (int c = 0; c < D / 2; c += 16) {
               float ov[16];
               tmem_ld16(t_o + lane_off + c0 + c, ov);
+              if (c + 16 == D / 2) {
+                tc_fence_before();
+                mbar_arrive(o_free);
+              }
               if (live) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) dst[(c + i) * kTreeRows] = ov[i] * inv;
               }
             }
-            if (live && half == 0) {
-              p.part_m[part * kTreeRows + row] = m;
-              p.part_l[part * kTreeRows + row] = sum;
-            }
           }
-          tc_fence_before();
-          mbar_arrive(o_free);
+          if (!whole && live && half == 0) {
+            p.part_m[part * kTreeRows + row] = m;
+            p.part_l[part * kTreeRows + row] = sum;
+          }
           first_seg = false;
           ++seg;
           ok = true;
@@ -1279,25 +1285,27 @@ __global__ void __launch_bounds__(GROUPS * kTreeRows)
 #pragma unroll
   for (int i = 0; i < kMergeCols; ++i) acc[i] = 0.f;
   if (live) {
-    // several parts at a time (the last one again in place of those behind
-    // it, with weight zero), with a running maximum
+    // several parts at a time, with a running maximum
     for (int i = grp; i < md.parts; i += kMergeParts * GROUPS) {
       float x[kMergeParts][kMergeCols], m[kMergeParts], l[kMergeParts];
 #pragma unroll
       for (int k = 0; k < kMergeParts; ++k) {
-        const int64_t a = at(min(i + k * GROUPS, md.parts - 1));
-        m[k] = load_now(p.part_m + a * kTreeRows + row);
-        l[k] = load_now(p.part_l + a * kTreeRows + row);
+        m[k] = -INFINITY;
+        l[k] = 0.f;
 #pragma unroll
-        for (int e = 0; e < kMergeCols; ++e)
-          x[k][e] = load_now(p.part_o + (a * D + c0 + e) * kTreeRows + row);
+        for (int e = 0; e < kMergeCols; ++e) x[k][e] = 0.f;
+        if (i + k * GROUPS < md.parts) {
+          const int64_t a = at(i + k * GROUPS);
+          m[k] = load_now(p.part_m + a * kTreeRows + row);
+          l[k] = load_now(p.part_l + a * kTreeRows + row);
+#pragma unroll
+          for (int e = 0; e < kMergeCols; ++e)
+            x[k][e] = load_now(p.part_o + (a * D + c0 + e) * kTreeRows + row);
+        }
       }
       float top = M;
 #pragma unroll
-      for (int k = 0; k < kMergeParts; ++k) {
-        if (i + k * GROUPS >= md.parts) m[k] = -INFINITY;
-        top = fmaxf(top, m[k]);
-      }
+      for (int k = 0; k < kMergeParts; ++k) top = fmaxf(top, m[k]);
       const float ref = top == -INFINITY ? 0.f : top;
       const float f = fast_exp2(M - ref);
       M = top;
