@@ -377,19 +377,29 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
  *   q_start     : device int32 [num_seqs + 1], not decreasing, q_start[0] >= 0,
  *               q_start[num_seqs] <= num_queries; n_s may be 0
  *   max_draft   : host upper bound of n_s, 1..64. A sequence with a negative
- *               n_s or more drafts than the bound or than its context is
- *               reported (PKV_DEVERR_DRAFT) and its rows are left as they were
+ *               n_s, drafts outside q, or more of them than the bound or than
+ *               its context is reported (PKV_DEVERR_DRAFT) and its rows are
+ *               left as they were
  *   tree_mask   : device uint64 [num_queries], or NULL for a chain (draft i
  *               sees drafts 0..i)
- *   context_lens: device int32 [num_seqs], the drafts included
+ *   context_lens: device int32 [num_seqs], the drafts included. A sequence
+ *               whose context is outside its table or above max_context is
+ *               reported (PKV_DEVERR_CONTEXT) and its rows are left as they
+ *               were
  *   workspace, workspace_bytes : device scratch of at least
  *               pkv_tree_workspace_bytes(...) bytes; its contents do not
  *               matter before or after; calls whose kernels may overlap need
  *               one each.
  *   other args  : as for pkv_paged_attention_decode
  * Slots behind the context may hold anything, NaN included; a draft's K and V
- * must be finite if any draft of its sequence sees it.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * must be finite if any draft of its sequence sees it. Softmax weights are
+ * rounded to bf16 (E4M3 pools: f16) before they meet V, sums are fp32. E4M3
+ * pools: an element of q below 2^-9 of its row's largest is rounded by at most
+ * 2^-17 of that largest.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA; PKV_ERR_UNSUPPORTED also where
+ * the bounds allow more work than the kernel numbers: (num_seqs + num_queries
+ * g / 128) num_kv_heads (max_context / 128 + 3) of 2^29 or more, g = num_heads
+ * / num_kv_heads.
  * ------------------------------------------------------------------------ */
 #define PKV_MAX_DRAFT 64
 size_t pkv_tree_workspace_bytes(int num_seqs, int num_queries, int num_heads, int num_kv_heads,
@@ -414,7 +424,7 @@ int pkv_paged_attention_tree(void* out, const void* q, const void* k_cache, cons
  *
  *   k_caches, v_caches : HOST arrays of num_layers device pointers, pools of
  *               the geometry `cache` that share the block tables; read during
- *               the call only. A pool may appear once.
+ *               the call only. No pool may appear twice (PKV_ERR_INVALID_ARG).
  *   accepted    : device int32 [num_seqs][max_accepted], strictly increasing,
  *               0 <= a_k < n_s; entries from num_accepted[s] on are not read
  *   num_accepted: device int32 [num_seqs], 0 <= m_s <= max_accepted

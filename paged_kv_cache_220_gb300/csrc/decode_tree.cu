@@ -14,15 +14,18 @@
 // Work split. A unit is (sequence, KV head, row tile); its steps are the 128-
 // token runs of its context. All steps of all units form one line that is cut
 // into equal shares, one per CTA, one CTA per SM: no tail whatever the lengths
-// are. A CTA's share is a row of segments (runs of steps of one unit). A unit
-// inside one share is finished there; a unit that is cut leaves a partial
-// (normalised fp32 output, maximum, sum) per segment, at most two per CTA, and
-// tree_merge_kernel joins them by log-sum-exp. The pipeline below runs on
-// across segments, so the loads never pause. Where every sequence has the same
-// number T > 1 of row tiles, the CTAs work in teams of T: a team takes a share
-// of the line of (sequence, KV head) steps, each member one row tile of it, so
-// that the tiles' reads of a page fall together and all but the first find it
-// in L2 (16 sequences x 4096 tokens x 64 drafts, d = 256: 161 -> 133 us).
+// are. A unit's start counts as three steps more (its Q has to come, its result
+// to go: without that, 96 sequences of 16 .. 16384 tokens take 227 us instead
+// of 150, because a few CTAs get all the short ones). A CTA's share is a row of
+// segments (runs of steps of one unit). A unit inside one share is finished
+// there; a unit that is cut leaves a partial (normalised fp32 output, maximum,
+// sum) per segment, at most two per CTA, and tree_merge_kernel joins them by
+// log-sum-exp. The pipeline below runs on across segments, so the loads never
+// pause. Where every sequence has the same number T > 1 of row tiles, the CTAs
+// work in teams of T: a team takes a share of the line of (sequence, KV head)
+// steps, each member one row tile of it, so that the tiles' reads of a page
+// fall together and all but the first find it in L2 (16 sequences x 4096
+// tokens x 64 drafts, d = 256: 161 -> 133 us when it was introduced).
 //
 // Shared memory: the row tile's Q and a ring of 32 KB slots that TMA fills
 // (cp.async.bulk.tensor, whole pages, 128-byte swizzle). A slot is [8-row
@@ -30,8 +33,8 @@
 // columns, 8 rows, chunks, row groups), so pages land one behind the other in
 // what is both K's operand layout (N = tokens, row groups at one stride) and
 // V's (N = columns, MN-major). K of a step takes d/128 slots (128 columns
-// each), V d/128 slots (64 or 128 tokens each). Slots are filled and used in
-// the order K(0), K(1), V(0), K(2), V(1), ...
+// each), V d/128 slots (64 or 128 tokens each). Slots are filled in the order
+// K(0) .. K(lead), V(0), K(lead + 1), V(1), ...; lead is 1 (d = 256) or 2.
 //
 // E4M3 pools: K's codes are the operand as they are (kind::f8f6f4). Q is split
 // into two E4M3 parts, q 2^e = hi + lo with a power of two per row that puts
@@ -39,15 +42,30 @@
 // each part 4, so elements down to 2^-9 of the largest are exact and the rest
 // are off by at most 2^-17 of it. V's codes are staged by TMA and turned into
 // their exact f16 values by converter warps; P is f16. k_scale and the row's
-// 2^-e go into the logits, v_scale into the output. K and V have rings of their own.
+// 2^-e go into the logits, v_scale into the output. K and V have rings of their
+// own.
 //
 // P is one bf16 part (a rounding of each weight to as many bits as the output
 // has; a second part would double the P.V products).
 //
 // Warps: 0-7 softmax (threads t and t + 128 own query row t, 64 of a step's
-// columns each; they exchange maxima through shared memory), 8 issues the
-// products; bf16: 9-11 load Q, 12-15 load pages; E4M3: 9-10 load pages, 11-14
-// convert V and load Q (16 warps of 128 registers; with 19 and 96 the softmax spills).
+// columns each; they exchange maxima through shared memory), 8 issues Q.K^T, 9
+// P.V; bf16: 10-13 load Q, 14-15 load pages; E4M3: 10 loads K, 11 V, 12-15
+// convert V and load Q. 512 threads of 128 registers, all the SM has.
+//
+// What bounds it on GB300 (of 6788 GB/s copy, 1943 TFLOP/s bf16):
+//   few rows, bf16: HBM. 32 x 8192 tokens x 16 drafts, d = 256: 174 us, 92 %;
+//     64 x 8192 x 1: 317 us, 100 %; 96 sequences of 16 .. 16384: 151 us, 93 %
+//   many rows: a step at d = 128 costs the softmax 2000 clocks (1024 of them
+//     the 128 x 128 exponentials at 16 a clock) and the tensor core 1040; at
+//     d = 256 P, S's buffers and the reads of K and V by all tiles of a team
+//     (13 TB/s out of L2 of the 14.7 that TMA reaches) leave 2800 clocks to a
+//     step of 2100 on the tensor core. 16 x 4096 x 64, d = 256: 95 us, 56 % of
+//     the products' floor; 32 x 4096 x 64, d = 128: 242 us, 58 %
+//   E4M3: the same softmax against half the bytes. 8 x 65536 x 8, d = 256:
+//     192 us, 83 % of HBM; 32 x 8192 x 4, d = 128: 124 us, 64 %
+//   one short sequence: latency. 1033 tokens x 5 drafts 11.2 us, 4 of them the
+//     merge
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -119,8 +137,8 @@ struct TreeGeom {
   static constexpr int kThreads = 16 * 32;
   static constexpr int kHead = 3072;  // barriers, exchange buffers
   static constexpr int kSmem = kHead + kQ + kNSlot * kSlot + kNK8 * kK8 + kNV16 * kV16;
-  // S of step t at kColS + 128 * (t % kNB). Three buffers where they fit (d =
-  // 128): S of step t + 1 then does not wait for the end of P.V of step t - 1
+  // S of step t at kColS + 128 * (t % kNB); three buffers where they fit (d =
+  // 128: 32 x 4096 tokens x 64 drafts 294 -> 272 us when it was introduced)
   static constexpr int kNB = D == 128 ? 3 : 2;
   static constexpr int kLead = kNB - 1;  // steps that S runs ahead of P.V
   static constexpr uint32_t kColS = D;
@@ -605,8 +623,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   uint32_t issued = 0, issued_k = 0;  // producers: slots whose copies were started
   if (warp >= G::kProdWarp && warp < G::kProdWarp + G::kProducers) {
     // ---------------- producers: the block table walk and the TMA copies, a
-    // page to a lane (one lane for all pages: about 3000 clocks a step, more
-    // than the rest of a step of E4M3 pools took). E4M3: the first warp loads
+    // page to a lane (one lane for all pages took about 3000 clocks a step: 8 x
+    // 65536 tokens E4M3 267 us instead of 212). E4M3: the first warp loads
     // K, the second V; 16-bit pools: each warp its pages of both, in the order
     // of the one ring
     if (walk.left > 0) {
@@ -764,10 +782,11 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp == G::kSWarp) {
-    // ---------------- the products S = Q.K^T, issued by one lane (P.V by a
-    // lane of another warp: waits, commits and loops of both in one lane took
-    // longer than the products). Operand descriptors are a constant plus the
-    // address: one addition each.
+    // ---------------- the products S = Q.K^T, issued by one lane. P.V comes
+    // from a lane of another warp: waits, commits and loops of both in one
+    // lane took longer than the products (64 x 4096 x 21 drafts E4M3 180 us
+    // instead of 164). Operand descriptors are a constant plus the address:
+    // one addition each.
     if (elect_one()) {
       constexpr uint32_t idesc =
           FP8 ? umma_idesc_e4m3(128, kTreeTok) : umma_idesc_bf16(128, kTreeTok, false);
@@ -1453,6 +1472,14 @@ extern "C" int pkv_paged_attention_tree(
                                                std::max(1, max_context), max_draft);
   if (!q_start || !workspace || !aligned16(workspace) || workspace_bytes < need)
     return PKV_ERR_INVALID_ARG;
+  // the most that the call's bounds allow
+  const int64_t tiles_most =
+      num_seqs + static_cast<int64_t>(num_queries) * g / kTreeRows;
+  const int64_t units = tiles_most * cache.num_kv_heads;
+  const int64_t longest = (static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok;
+  // places of the line are 32-bit numbers (a q_start that is not ascending
+  // may ask for up to twice the work)
+  if (units * (longest + kTreeStart) >= (1 << 29)) return PKV_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -1484,13 +1511,6 @@ extern "C" int pkv_paged_attention_tree(
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.qscale = scale * 1.4426950408889634f;
   // no more CTAs than the call's bounds can give work
-  const int64_t tiles_most =
-      num_seqs + static_cast<int64_t>(num_queries) * g / kTreeRows;
-  const int64_t units = tiles_most * cache.num_kv_heads;
-  const int64_t longest = (static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok;
-  // places of the line are 32-bit numbers (a q_start that is not ascending
-  // may ask for up to twice the work)
-  if (units * (longest + kTreeStart) >= (1 << 29)) return PKV_ERR_UNSUPPORTED;
   const int ctas = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(std::min(sms, kTreeMaxCtas), units * longest)));
   p.ctas = ctas;

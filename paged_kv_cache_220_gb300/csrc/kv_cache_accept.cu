@@ -10,6 +10,7 @@
 // no later move (base + a_m, m > k, lies behind it), and reading early is
 // always safe.
 #include <algorithm>
+#include <functional>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -127,6 +128,20 @@ extern "C" int pkv_kv_cache_accept(void* const* k_caches, void* const* v_caches,
   for (int l = 0; l < num_layers; ++l)
     if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
       return PKV_ERR_INVALID_ARG;
+  // the same pool twice would be moved twice, by CTAs that do not wait for
+  // each other
+  const int pools = 2 * num_layers;
+  auto pool_at = [&](int i) { return i < num_layers ? k_caches[i] : v_caches[i - num_layers]; };
+  const void* sorted[4 * kAcceptLayers];
+  if (pools <= 4 * kAcceptLayers) {
+    for (int i = 0; i < pools; ++i) sorted[i] = pool_at(i);
+    std::sort(sorted, sorted + pools, std::less<const void*>());
+    if (std::adjacent_find(sorted, sorted + pools) != sorted + pools) return PKV_ERR_INVALID_ARG;
+  } else {
+    for (int i = 0; i < pools; ++i)
+      for (int j = 0; j < i; ++j)
+        if (pool_at(i) == pool_at(j)) return PKV_ERR_INVALID_ARG;
+  }
   AcceptParams p{};
   p.block_tables = block_tables;
   p.context_lens = context_lens;
