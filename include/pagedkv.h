@@ -346,8 +346,8 @@ int pkv_paged_attention_decode_shared_prefix(
  *               zeros. `out` may not be `q`.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  * ------------------------------------------------------------------------ */
-int pkv_window_partition_size(int num_seqs, int num_kv_heads, int block_size, int max_context,
-                              int window, int sinks);
+int pkv_window_partition_size(int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                              int max_context, int window, int sinks);
 size_t pkv_window_workspace_bytes(int num_seqs, int num_heads, int head_dim, int block_size,
                                   int max_context, int window, int sinks, int partition_size);
 int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,

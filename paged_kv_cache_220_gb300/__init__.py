@@ -89,7 +89,7 @@ SIGNATURES = {
                                                       _P, _I,
                                                       _I, _I, ctypes.c_float, _P, _I, _I, _P,
                                                       _I, _I, _P, ctypes.c_size_t, _P, _P]),
-    "pkv_window_partition_size": (_I, [_I, _I, _I, _I, _I, _I]),
+    "pkv_window_partition_size": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "pkv_window_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "pkv_paged_attention_window": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _I, _I,
                                         _I, ctypes.c_float, _I, _I, _I, _P, ctypes.c_size_t, _P,
@@ -557,12 +557,13 @@ class _Scratch:
             _raw_free(self.own)
 
 
-def window_partition_size(num_seqs, num_kv_heads, block_size, max_context, window,
+def window_partition_size(num_seqs, num_kv_heads, head_dim, block_size, max_context, window,
                           sinks=0) -> int:
     """The library's choice of partition_size for paged_attention_window
     (0 = one pass)."""
-    rc = lib().pkv_window_partition_size(int(num_seqs), int(num_kv_heads), int(block_size),
-                                         int(max_context), int(window), int(sinks))
+    rc = lib().pkv_window_partition_size(int(num_seqs), int(num_kv_heads), int(head_dim),
+                                         int(block_size), int(max_context), int(window),
+                                         int(sinks))
     if rc < 0:
         _check(rc, "window_partition_size")
     return int(rc)
@@ -588,8 +589,8 @@ def paged_attention_window(q, k_cache, v_cache, block_tables, context_lens, scal
         q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, True, out)
     order = _ptr(seq_order, "seq_order", dev, _I32, (S,))
     if partition_size is None:
-        partition_size = _window_partition(S, desc.num_kv_heads, desc.block_size, max_context,
-                                           window, sinks)
+        partition_size = _window_partition(S, desc.num_kv_heads, desc.head_dim, desc.block_size,
+                                           max_context, window, sinks)
         if partition_size < 0:
             _check(partition_size, "window_partition_size")
     with _at(dev, stream) as raw:

@@ -25,23 +25,46 @@ static int64_t window_partitions(int block_size, int max_context, int window, in
   return (window_blocks_bound(block_size, max_context, window, sinks) + per - 1) / per;
 }
 
+// CTAs that run at once: four to an SM at d = 256, three at d = 128.
+static int64_t window_wave(int head_dim) { return head_dim == 256 ? 600 : 440; }
+
+// CTAs of a pair's cluster in one pass: up to 8, two blocks or more each,
+// while one wave holds them.
+static int64_t window_cluster(int64_t pairs, int64_t blocks, int64_t wave) {
+  int64_t c = 1;
+  while (c < 8 && 2 * c < blocks && 2 * c * pairs <= wave) c <<= 1;
+  return c;
+}
+
 }  // namespace pkv
 
-extern "C" int pkv_window_partition_size(int num_seqs, int num_kv_heads, int block_size,
-                                         int max_context, int window, int sinks) {
+extern "C" int pkv_window_partition_size(int num_seqs, int num_kv_heads, int head_dim,
+                                         int block_size, int max_context, int window, int sinks) {
   using namespace pkv;
+  if (head_dim != 128 && head_dim != 256) return PKV_ERR_UNSUPPORTED;
   if (num_seqs < 0 || num_kv_heads <= 0 || (block_size != 16 && block_size != 32) ||
       max_context < 0 || window <= 0 || sinks < 0)
     return PKV_ERR_INVALID_ARG;
   const int64_t blocks = window_blocks_bound(block_size, max_context, window, sinks);
   const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
-  // One wave of CTAs: five fit an SM at d = 256, 760 on the chip, and a few
-  // more than that would run a whole partition on their own at the end
-  // (64 sequences x 4 KV heads, 4096-token windows, bf16: 2 partitions 160 us,
-  // 3 (768 CTAs) 187, 8 (2048 CTAs) 163; floor 159). Few short windows: one
-  // pass over a cluster saves the merge (2 x 516 tokens 9.8 against 10.8 us).
-  const int64_t np = std::min<int64_t>(pairs > 0 ? 740 / pairs : 1, blocks / 4);
-  if (np <= 1 || (blocks <= 40 && pairs <= 32)) return 0;
+  if (pairs == 0) return 0;
+  // One pass, a cluster of CTAs to a pair, saves the merge (64 pairs of 40
+  // blocks, bf16, d = 256, B = 16: 12.3 us against 16.6 in 8 partitions), as
+  // long as its CTAs have little to do each or fill most of a wave (64 pairs of
+  // 520 blocks: 85 against 90). Few pairs of many blocks are cut into as many
+  // partitions as a wave holds (4 pairs of 520 blocks: 17 us in 130, 46 in one
+  // pass; 8: 20 us in 58, 29 in 87, which do not fit one wave). Where one CTA
+  // to a pair leaves much of a wave empty or spills into the next one, about
+  // three waves even it out (256 pairs of 160 blocks, d = 128: 85 us in 5
+  // partitions, 101 in one pass; 512 pairs, 1.2 waves: 161 in 4, 225; but
+  // 1024 pairs of up to 34 blocks, d = 256, 1.7 waves: 103 in 2, 99).
+  const int64_t wave = window_wave(head_dim), c = window_cluster(pairs, blocks, wave);
+  const int64_t waves = (pairs * c + wave - 1) / wave;
+  if (blocks <= 12 * c || 10 * pairs * c >= (waves == 1 ? 6 : 7 * waves) * wave) return 0;
+  const int64_t np = 2 * pairs <= wave
+                         ? std::min(wave / pairs, blocks / 2)
+                         : std::min((3 * wave + pairs / 2) / pairs, blocks / 4);
+  if (np <= 1) return 0;
   const int64_t per = (blocks + np - 1) / np;
   return static_cast<int>(std::min<int64_t>(per, (INT32_MAX - 64) / block_size) * block_size);
 }
@@ -96,12 +119,8 @@ extern "C" int pkv_paged_attention_window(
   dim3 grid(1, cache.num_kv_heads, num_seqs);
   const int64_t blocks = window_blocks_bound(cache.block_size, max_context, window, sinks);
   if (partition_size == 0) {
-    // one pass: a cluster of up to 8 CTAs, four blocks or more each, while one
-    // wave holds them
-    int c = 1;
-    while (c < 8 && int64_t{c} * 4 < blocks) c <<= 1;
-    while (c > 1 && static_cast<int64_t>(num_seqs) * cache.num_kv_heads * c > 740) c >>= 1;
-    p.cluster = c;
+    p.cluster = static_cast<int>(window_cluster(
+        static_cast<int64_t>(num_seqs) * cache.num_kv_heads, blocks, window_wave(cache.head_dim)));
     return launch_decode_window(p, k_cache, v_cache, cache.head_dim, cache.block_size, fp8, grid,
                                 st);
   }

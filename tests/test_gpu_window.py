@@ -147,7 +147,7 @@ def test_repeats_streams_and_graphs(fp8, partition, _lib):
     c = Cache([2000, 64, 700, 9], 2, 256, 16, fp8, seed=21)
     q = queries(4, 8, 256, seed=21)
     if partition is None:
-        partition = pkv.window_partition_size(4, 2, 16, 2000, 600, 4)
+        partition = pkv.window_partition_size(4, 2, 256, 16, 2000, 600, 4)
     n = pkv.window_workspace_bytes(4, 8, 256, 16, 2000, 600, 4, partition)
     ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda").fill_(0xFF)
     out = torch.empty_like(q)

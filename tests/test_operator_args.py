@@ -51,14 +51,15 @@ def test_window_refusals(lib):
 
 def test_window_sizes(lib):
     f = lib.pkv_window_partition_size
-    assert f(4, 2, 16, 1024, 0, 0) == INV and f(4, 2, 8, 1024, 10, 0) == INV
-    assert f(4, 2, 16, 1024, 10, -1) == INV and f(-1, 2, 16, 1024, 10, 0) == INV
+    assert f(4, 2, 128, 16, 1024, 0, 0) == INV and f(4, 2, 128, 8, 1024, 10, 0) == INV
+    assert f(4, 2, 128, 16, 1024, 10, -1) == INV and f(-1, 2, 128, 16, 1024, 10, 0) == INV
+    assert f(4, 2, 64, 16, 1024, 10, 0) == UNS
     for S in (1, 7, 64, 300):
         for hk in (1, 4, 8):
             for b in (16, 32):
                 for maxc in (0, 1, 700, 8192, 131072, 1 << 20):
                     for win, sinks in ((1, 0), (512, 4), (4096, 4), (1 << 30, 1 << 30)):
-                        p = f(S, hk, b, maxc, win, sinks)
+                        p = f(S, hk, 128, b, maxc, win, sinks)
                         assert p >= 0 and p % b == 0
                         n = lib.pkv_window_workspace_bytes(S, 4 * hk, 128, b, maxc, win, sinks, p)
                         assert (n == 0) if p == 0 else (n % (130 * 4) == 0)
