@@ -55,15 +55,16 @@
 //
 // What bounds it on GB300 (of 6788 GB/s copy, 1943 TFLOP/s bf16):
 //   few rows, bf16: HBM. 32 x 8192 tokens x 16 drafts, d = 256: 174 us, 92 %;
-//     64 x 8192 x 1: 317 us, 100 %; 96 sequences of 16 .. 16384: 151 us, 93 %
+//     64 x 8192 x 1: 317 us, 100 %; 96 sequences of 16 .. 16384: 155 us, 90 %
 //   many rows: a step at d = 128 costs the softmax 2000 clocks (1024 of them
 //     the 128 x 128 exponentials at 16 a clock) and the tensor core 1040; at
 //     d = 256 P, S's buffers and the reads of K and V by all tiles of a team
 //     (13 TB/s out of L2 of the 14.7 that TMA reaches) leave 2800 clocks to a
-//     step of 2100 on the tensor core. 16 x 4096 x 64, d = 256: 95 us, 56 % of
+//     step of 2100 on the tensor core. 16 x 4096 x 64, d = 256: 98 us, 54 % of
 //     the products' floor; 32 x 4096 x 64, d = 128: 242 us, 58 %
 //   E4M3: the same softmax against half the bytes. 8 x 65536 x 8, d = 256:
-//     192 us, 83 % of HBM; 32 x 8192 x 4, d = 128: 124 us, 64 %
+//     210 us, 75 % of HBM; 32 x 8192 x 4, d = 128: 124 us, 64 % (half the
+//     exponentials would take 6 and 20 % off)
 //   one short sequence: latency. 1033 tokens x 5 drafts 11.2 us, 4 of them the
 //     merge
 #include <algorithm>
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       int at = lo, steps = before, s = s_lo;
       for (;; ++s) {
         if (per > 1) seq.load(p, s, false);
-        const int n = T > 1 ? p.num_kv_heads : seq.units(p);
+        const int n = seq.units(p) / T;
         if (per == 1 || x < at + n * (seq.steps + W)) break;
         at += n * (seq.steps + W);
         steps += n * seq.steps;

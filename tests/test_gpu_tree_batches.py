@@ -99,6 +99,26 @@ def test_teams_of_many_sequences(n, g, fp8, _lib):
     verify(c, q, start, drafts, out, 128 ** -0.5, set(rng.sample(range(150), 30)))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,g", [(40, 8), (3, 2)])
+def test_teams_among_idle_sequences(n, g, fp8, _lib):
+    """More sequences than threads look for a share's place, most of them
+    without a draft, the others all with the same number of row tiles."""
+    rng = random.Random(4)
+    lens = [rng.randint(n, 300) for _ in range(1300)]
+    drafts = [n if s % 7 == 3 else 0 for s in range(1300)]
+    c = Cache(lens, 2, 128, 16, fp8, seed=33)
+    start = starts(drafts)
+    q = queries(start[-1], 2 * g, 128, seed=33)
+    out = torch.full_like(q, float("nan"))
+    call(c, q, start, drafts, 128 ** -0.5, out=out)
+    torch.cuda.synchronize()
+    assert int(_lib.item()) == 0
+    assert torch.isfinite(out.float()).all()
+    verify(c, q, start, drafts, out, 128 ** -0.5,
+           set(rng.sample([s for s in range(1300) if drafts[s]], 40)))
+
+
 def test_context_above_the_bound_is_reported(_lib):
     c = Cache([100, 300, 90], 2, 128, 16, False, seed=5)
     drafts, start = [3, 3, 3], [0, 3, 6, 9]
