@@ -152,6 +152,38 @@ def test_queries_that_are_not_finite(bad, d, fp8, _lib):
     assert torch.equal(out[keep], want[keep])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1e-30])
+def test_scales(scale, d, fp8, _lib):
+    """Negative, zero and tiny scales, over committed tokens (no mask in their
+    steps) and drafts."""
+    c = Cache([900, 130, 64], 2, d, 16, fp8, seed=9)
+    drafts, start = [4, 9, 64], [0, 4, 13, 77]
+    q = queries(77, 8, d, seed=9)
+    out = call(c, q, start, drafts, scale)
+    torch.cuda.synchronize()
+    assert int(_lib.item()) == 0
+    verify(c, q, start, drafts, out, scale)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_unsigned_masks_and_padded_queries(fp8, _lib):
+    """uint64 masks, more rows of q than drafts, a larger bound of drafts."""
+    c = Cache([300, 77], 2, 128, 32, fp8, seed=10)
+    drafts, start = [5, 7], [0, 5, 12]
+    q = queries(40, 8, 128, seed=10)
+    chain = torch.tensor([(2 << i) - 1 for n in drafts for i in range(n)] + [0] * 28,
+                         dtype=torch.int64, device="cuda")
+    out = torch.full_like(q, 3.0)
+    pkv.paged_attention_tree(q, c.k, c.v, c.tables, c.context_lens, int32(start), 0.09, 300, 64,
+                             chain.view(torch.uint64), out=out, **c.kw())
+    torch.cuda.synchronize()
+    assert int(_lib.item()) == 0
+    assert bool((out[12:] == 3).all())
+    verify(c, q, start, drafts, out, 0.09)
+
+
 def test_calls_beside_each_other(_lib):
     """Calls on two streams at once, their workspaces allocated by the calls,
     between them memory that other work takes and gives back."""
