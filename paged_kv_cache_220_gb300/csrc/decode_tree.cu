@@ -1197,9 +1197,6 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
                      : "r"(src0 + src_at + e * kSrcStep)
                      : "memory");
       }
-      // the codes are in registers: the next ones may come
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[from.i]);
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&vempty[to.i], to.ph ^ 1, p.err)))) break;
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
@@ -1223,7 +1220,13 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&vfull[to.i]);
+      // the codes' slot is given back only now that they have been used: an
+      // arrival does not wait for loads that are merely issued, and the next
+      // codes would overwrite what they are still to read
+      if (lane == 0) {
+        mbar_arrive(&vfull[to.i]);
+        mbar_arrive(&empty[from.i]);
+      }
       from.next();
       to.next();
       if (++vs == VS) {

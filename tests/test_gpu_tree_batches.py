@@ -184,6 +184,26 @@ def test_unsigned_masks_and_padded_queries(fp8, _lib):
     verify(c, q, start, drafts, out, 0.09)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,lens,drafts,hk,g", [(256, [70001], [5], 2, 4),
+                                                (256, [33333, 70000, 5], [17, 30, 5], 2, 6),
+                                                (128, [8192] * 32, [4] * 32, 8, 4)])
+def test_long_repeats(d, lens, drafts, hk, g, fp8, _lib):
+    """The same bits every time, from HBM and from L2: no slot of a ring is
+    filled anew while it is still being read."""
+    c = Cache(lens, hk, d, 32, fp8, seed=7)
+    start = starts(drafts)
+    q = queries(start[-1], hk * g, d, seed=7)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    first = call(c, q, start, drafts, d ** -0.5)
+    verify(c, q, start, drafts, first, d ** -0.5, {0, len(lens) - 1})
+    for i in range(60):
+        if i % 3 == 0:
+            flush.fill_(i)
+        assert torch.equal(call(c, q, start, drafts, d ** -0.5), first), i
+    assert int(_lib.item()) == 0
+
+
 def test_calls_beside_each_other(_lib):
     """Calls on two streams at once, their workspaces allocated by the calls,
     between them memory that other work takes and gives back."""
