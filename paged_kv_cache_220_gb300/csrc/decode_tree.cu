@@ -61,10 +61,11 @@
 //     d = 256 P, S's buffers and the reads of K and V by all tiles of a team
 //     (13 TB/s out of L2 of the 14.7 that TMA reaches) leave 2800 clocks to a
 //     step of 2100 on the tensor core. 16 x 4096 x 64, d = 256: 98 us, 54 % of
-//     the products' floor; 32 x 4096 x 64, d = 128: 242 us, 58 %
+//     the products' floor; 32 x 4096 x 64, d = 128: 243 us, 58 %
 //   E4M3: the same softmax against half the bytes. 8 x 65536 x 8, d = 256:
-//     210 us, 75 % of HBM; 32 x 8192 x 4, d = 128: 124 us, 64 % (half the
-//     exponentials would take 6 and 20 % off)
+//     210 us, 75 % of HBM; 32 x 8192 x 4, d = 128: 127 us, 63 % (half the
+//     columns of the softmax would take 6 and 20 % off; its instructions, not
+//     the exponentials, are what counts)
 //   one short sequence: latency. 1033 tokens x 5 drafts 11.2 us, 4 of them the
 //     merge
 #include <algorithm>
@@ -916,7 +917,12 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       (void)mbar_wait(drained, 0, p.err);
     }
   } else if (warp < G::kSoftWarps) {
-    // ---------------- softmax: two threads per query row, 64 columns each
+    // ---------------- softmax: two threads per query row, 64 columns each, in
+    // chunks of NC. d = 256: two, read twice, in loops that are not unrolled:
+    // half the code and no spilled registers (64 x 4096 tokens x 21 drafts E4M3
+    // 164 -> 148 us, 16 x 4096 x 64 94 -> 92); d = 128: one (in two 32 x 4096 x 64 drafts take 264 us
+    // instead of 249)
+    constexpr int NC = D == 256 ? 32 : 64;
     const int quad = warp & 3, half = warp >> 2;
     const int row = 32 * quad + lane;
     const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
@@ -972,15 +978,18 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         const bool clean = tok0 + kTreeTok <= base_tok;  // committed tokens only
         // this thread's columns, 64 half .. 64 half + 63
         const uint32_t mine = ts + 64 * half;
-        float sv[64];
-        tmem_ld64(mine, sv);
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (!clean) {
-          // scaled here, columns that the row does not see -inf; it sees the
-          // committed ones and those its mask names
+        float sv[NC];
+        // the logits of chunk c: raw, or (not clean) scaled and -inf where the
+        // row does not see; it sees the committed tokens and those its mask names
+        auto chunk = [&](int c) {
+          if constexpr (NC == 64)
+            tmem_ld64(mine, sv);
+          else
+            tmem_ld32(mine + NC * c, sv);
+          if (clean) return;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int sh = tok0 + 64 * half + 32 * w - base_tok;  // draft of the first column
+          for (int w = 0; w < NC / 32; ++w) {
+            const int sh = tok0 + 64 * half + NC * c + 32 * w - base_tok;  // first column's draft
             uint32_t see = ~0u;
             if (sh >= 64) see = 0;
             else if (sh >= 0) see = static_cast<uint32_t>(mask >> sh);
@@ -989,15 +998,17 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
             for (int i = 0; i < 32; ++i)
               sv[32 * w + i] = (see >> i) & 1 ? sv[32 * w + i] * qs : -INFINITY;
           }
+        };
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < 64 / NC; ++c) {
+          chunk(c);
+          if (!clean || qs >= 0.f) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
-        } else {
-          if (qs >= 0.f) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+            for (int i = 0; i < NC; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], -sv[i]);
+            for (int i = 0; i < NC; ++i) m4[i & 3] = fmaxf(m4[i & 3], -sv[i]);
           }
         }
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
@@ -1026,29 +1037,26 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         }
         if (want) m = mx;
         const float ref = m == -INFINITY ? 0.f : m;
-        // P over this thread's own columns of S, two tokens to a column
+        // P over this thread's own columns of S, two tokens to a column (over
+        // chunks that have been read)
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pw[32];
-        if (clean) {
+        const float by = clean ? qs : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < 64 / NC; ++c) {
+          if (NC < 64) chunk(c);
+          uint32_t pw[NC / 2];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = fast_exp2(fmaf(sv[2 * i], qs, -ref));
-            const float e = fast_exp2(fmaf(sv[2 * i + 1], qs, -ref));
+          for (int i = 0; i < NC / 2; ++i) {
+            const float a = fast_exp2(fmaf(sv[2 * i], by, -ref));
+            const float e = fast_exp2(fmaf(sv[2 * i + 1], by, -ref));
             l4[(2 * i) & 3] += a;
             l4[(2 * i + 1) & 3] += e;
             pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
           }
-        } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = fast_exp2(sv[2 * i] - ref), e = fast_exp2(sv[2 * i + 1] - ref);
-            l4[(2 * i) & 3] += a;
-            l4[(2 * i + 1) & 3] += e;
-            pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
-          }
+          for (int w = 0; w < NC / 32; ++w)
+            tmem_st16_nowait(mine + NC / 2 * c + 16 * w, pw + 16 * w);
         }
-        tmem_st16_nowait(mine, pw);
-        tmem_st16_nowait(mine + 16, pw + 16);
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         const int valid = walk.q.ctx - tok0;
         if (valid < kTreeTok && (valid & 15) != 0) {
