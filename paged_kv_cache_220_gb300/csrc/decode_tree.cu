@@ -51,7 +51,7 @@
 // Warps: 0-7 softmax (threads t and t + 128 own query row t, 64 of a step's
 // columns each; they exchange maxima through shared memory), 8 issues Q.K^T, 9
 // P.V; bf16: 10-13 load Q, 14-15 load pages; E4M3: 10 loads K, 11 V, 12-15
-// convert V and load Q. 512 threads of 128 registers, all the SM has.
+// convert V and load Q. 512 threads of up to 128 registers, all the SM has.
 //
 // What bounds it on GB300 (of 6788 GB/s copy, 1943 TFLOP/s bf16):
 //   few rows, bf16: HBM. 32 x 8192 tokens x 16 drafts, d = 256: 174 us, 92 %;
@@ -920,8 +920,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // ---------------- softmax: two threads per query row, 64 columns each, in
     // chunks of NC. d = 256: two, read twice, in loops that are not unrolled:
     // half the code and no spilled registers (64 x 4096 tokens x 21 drafts E4M3
-    // 164 -> 148 us, 16 x 4096 x 64 94 -> 92); d = 128: one (in two 32 x 4096 x 64 drafts take 264 us
-    // instead of 249)
+    // 164 -> 148 us, 16 x 4096 x 64 94 -> 92); d = 128: one (in two 32 x 4096 x
+    // 64 drafts take 264 us instead of 249)
     constexpr int NC = D == 256 ? 32 : 64;
     const int quad = warp & 3, half = warp >> 2;
     const int row = 32 * quad + lane;
