@@ -391,8 +391,10 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
  *               matter before or after; calls whose kernels may overlap need
  *               one each.
  *   other args  : as for pkv_paged_attention_decode
- * Slots behind the context may hold anything, NaN included; a draft's K and V
- * must be finite if any draft of its sequence sees it. Softmax weights are
+ * Slots behind the context and of drafts that no row of their sequence sees
+ * (padding whose bits are clear everywhere) may hold anything, NaN included; a
+ * draft's K and V must be finite if any draft of its sequence sees it: what it
+ * holds would reach the rows that do not see it too. Softmax weights are
  * rounded to bf16 (E4M3 pools: f16) before they meet V, sums are fp32. E4M3
  * pools: an element of q below 2^-9 of its row's largest is rounded by at most
  * 2^-17 of that largest.

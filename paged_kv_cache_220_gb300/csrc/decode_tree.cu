@@ -289,6 +289,17 @@ struct RingPos {
   }
 };
 
+// The drafts that some row of the sequence sees, by all lanes of a warp (given
+// masks).
+__device__ __forceinline__ uint64_t drafts_seen(const TreeParams& p, const TreeSeq& q, int lane) {
+  uint64_t any = lane < q.n ? p.tree_mask[q.q0 + lane] : 0ull;
+  any |= lane + 32 < q.n ? p.tree_mask[q.q0 + lane + 32] : 0ull;
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
+  __syncwarp();
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
 // r / g for a row of a unit (r < 64 g, g <= 8): exact, no division.
 __device__ __forceinline__ int div_group(int r, int g) { return (r * (65536 / g + 1)) >> 16; }
 
@@ -459,10 +470,11 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
   uint64_t* q_first = drained + 1;                       // Q of the share's first segment
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sbase + 376);
   int* found = reinterpret_cast<int*>(sbase + 380);  // sequence, its TreeSeq, unit, step
-  int* cut = reinterpret_cast<int*>(sbase + 992);              // steps before the share, its end
+  int* cut = reinterpret_cast<int*>(sbase + 368);              // steps before the share, its end
   int4* wsum = reinterpret_cast<int4*>(sbase + 416);           // [warps], until the share is known
   int8_t* q_exp = reinterpret_cast<int8_t*>(sbase + 416);      // [3][128] E4M3: e of Q's rows
   int32_t* ids = reinterpret_cast<int32_t*>(sbase + 800);      // [2][3][8] block ids of three steps
+  uint64_t* seen = reinterpret_cast<uint64_t*>(sbase + 992);   // [4] bf16: drafts_seen
   float* xch = reinterpret_cast<float*>(sbase + 1024);         // [2][2][128]
   const uint32_t sq = base + G::kHead;
   const uint32_t ring = sq + G::kQ;
@@ -960,6 +972,14 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
       float m = -INFINITY, l = 0.f, qs = p.qscale;
       if constexpr (FP8) qs *= p.k_scale[walk.h];
       const int seg_st = walk.st;  // the segment's first step in its unit
+      if (!FP8 && half == 0 && p.tree_mask != nullptr &&
+          (seg_st + steps) * kTreeTok > base_tok) {
+        // a segment with drafts. The exchange of its first step hands this to
+        // the row's other thread, that of its sums keeps it until both have
+        // read it
+        const uint64_t any = drafts_seen(p, walk.q, lane);
+        if (lane == 0) seen[quad] = any;
+      }
       ok = false;  // until the segment is through
       int tok0 = seg_st * kTreeTok;
       for (int i = 0;; ++i, ++t, tok0 += kTreeTok) {
@@ -1058,31 +1078,48 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
             tmem_st16_nowait(mine + NC / 2 * c + 16 * w, pw + 16 * w);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        const int valid = walk.q.ctx - tok0;
-        if (valid < kTreeTok && (valid & 15) != 0) {
-          // the rows behind the context that the last product of P.V covers
-          // hold whatever was there: zero them, P is zero there. The step
-          // before is waited for first: its V may have been the slot's last
-          // use, and a wait must not be two phases ahead of its barrier
-          if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[before_sb.i], before_sb.ph,
-                                                           p.err)))
-            break;
-          constexpr int NV = FP8 ? 2 : NS;
-          const int at_v = (FP8 ? t * VS : v_seq<KS, VS>(t, count, G::kLead)) + valid / G::kVTok;
-          const int i = at_v % NV;
-          if (!__all_sync(0xffffffffu,
-                          mbar_wait(FP8 ? &vfull[i] : &full[i], (at_v / NV) & 1, p.err)))
-            break;
-          const uint32_t vp = v16 + i * (FP8 ? G::kV16 : G::kSlot);
-          const int r0 = valid % G::kVTok, r1 = (r0 + 15) & ~15;
-          constexpr int U = NCH * 8;  // 16-byte units of a row
-          for (int x = threadIdx.x; x < (r1 - r0) * U; x += G::kSoftWarps * 32) {
-            const int r = r0 + x / U, u = x % U;
-            const uint32_t at = vp + ((r / 8) * NCH + u / 8) * 1024 + (r % 8) * 128 +
-                                ((u % 8) ^ (r % 8)) * 16;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
+        if constexpr (!FP8) {
+          // P is zero for the rows behind the context that the last product of
+          // P.V covers and for the drafts that no row sees, but these rows
+          // hold whatever was there, NaN included: zero them (E4M3: the
+          // converters write zeros)
+          const int valid = walk.q.ctx - tok0;
+          const bool tail = valid < kTreeTok && (valid & 15) != 0;
+          uint64_t hidden = 0;  // drafts of this step that no row sees
+          if (!clean && p.tree_mask != nullptr) {
+            const int b0 = max(0, tok0 - base_tok), b1 = min(walk.q.n, tok0 + kTreeTok - base_tok);
+            hidden = ~seen[quad] & (~0ull << b0) & (~0ull >> (64 - b1));
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (tail || hidden != 0) {
+            // the step before is waited for first: its V may have been the
+            // slot's last use, and a wait must not be two phases ahead of its
+            // barrier
+            if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[before_sb.i], before_sb.ph,
+                                                             p.err)))
+              break;
+            const int v0 = v_seq<KS, VS>(t, count, G::kLead);
+            // row r of the step, one warp to a row in turn
+            int turn = 0;
+            bool came = true;
+            auto zero = [&](int r) {
+              if (turn++ % G::kSoftWarps != warp || !came) return;
+              const int at_v = v0 + r / G::kVTok, i = at_v % NS;
+              came = __all_sync(0xffffffffu, mbar_wait(&full[i], (at_v / NS) & 1, p.err));
+              if (!came || lane >= NCH * 8) return;  // 16-byte units of a row
+              r %= G::kVTok;
+              const uint32_t at = ring + i * G::kSlot + ((r / 8) * NCH + lane / 8) * 1024 +
+                                  (r % 8) * 128 + ((lane % 8) ^ (r % 8)) * 16;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u)
+                           : "memory");
+            };
+            if (tail)
+#pragma unroll 1
+              for (int r = valid; r & 15; ++r) zero(r);
+#pragma unroll 1
+            for (uint64_t u = hidden; u != 0; u &= u - 1) zero(base_tok - tok0 + __ffsll(u) - 1);
+            if (!came) break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1225,6 +1262,27 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst ^ 16), "r"(w[4]),
                      "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
+      }
+      // the rows of drafts that no row sees and those behind the context that
+      // the last product of P.V covers may hold anything, NaN included, and P =
+      // 0 does not hide it: zeros. A rolled loop, each thread over its own
+      // units: in registers before the conversion 64 x 4096 tokens x 21 drafts
+      // take 157 us instead of 151
+      const int draft0 = walk.q.ctx - walk.q.n - walk.st * kTreeTok;  // the first draft's row
+      if (draft0 < kTreeTok) {
+        const int valid = draft0 + walk.q.n;
+        const uint64_t seen = p.tree_mask ? drafts_seen(p, walk.q, lane) : ~0ull;
+#pragma unroll 1
+        for (int e = 0; e < kUnits; ++e) {
+          const int r = vs * G::kVTok + cr + e * (kCT / UPR);
+          if (r >= valid ? r < ((valid + 15) & ~15) : r >= draft0 && !(seen >> (r - draft0) & 1)) {
+            const uint32_t dst = dst0 + dst_at + e * kDstStep;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst ^ 16), "r"(0u)
+                         : "memory");
+          }
+        }
+        __syncwarp();
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
