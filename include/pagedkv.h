@@ -395,7 +395,8 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
  * (padding whose bits are clear everywhere) may hold anything, NaN included; a
  * draft's K and V must be finite if any draft of its sequence sees it: what it
  * holds would reach the rows that do not see it too. Softmax weights are
- * rounded to bf16 (E4M3 pools: f16) before they meet V, sums are fp32. E4M3
+ * rounded to bf16 (E4M3 pools: f16, with at most 2^-32 of the largest weight
+ * lost to underflow each) before they meet V, sums are fp32. E4M3
  * pools: an element of q below 2^-9 of its row's largest is rounded by at most
  * 2^-17 of that largest.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA; PKV_ERR_UNSUPPORTED also where

@@ -84,6 +84,12 @@ constexpr int kTreeRows = 128;     // query rows of a tile
 constexpr int kTreeTok = 128;      // tokens of a step
 constexpr int kTreeEven = 4;       // shares of at most so many steps are cut evenly
 constexpr int kTreeStart = 3;      // steps that a unit's start counts for in longer ones
+// E4M3 pools: P is 2^(z - m + kTreeUp) in f16, which holds 2^-24 to 2^16. The
+// reference m may lie 8 below the maximum, so 2^15 is P's largest value, and
+// what rounds to zero is below 2^-32 of 2^m: without the shift it was 2^-25,
+// and of 65536 such weights 0.2 % of the row's sum were lost. All partials of
+// a row have the shift in their sums, so it cancels.
+constexpr float kTreeUp = 7.f;
 
 struct TreeMeta {  // what the merge needs of a unit that starts in a CTA and is cut
   int row0;        // first query row (of q and out) of the sequence
@@ -1056,7 +1062,7 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           if (want) l *= alpha;
         }
         if (want) m = mx;
-        const float ref = m == -INFINITY ? 0.f : m;
+        const float shift = (FP8 ? kTreeUp : 0.f) - (m == -INFINITY ? 0.f : m);
         // P over this thread's own columns of S, two tokens to a column (over
         // chunks that have been read)
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1067,8 +1073,8 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
           uint32_t pw[NC / 2];
 #pragma unroll
           for (int i = 0; i < NC / 2; ++i) {
-            const float a = fast_exp2(fmaf(sv[2 * i], by, -ref));
-            const float e = fast_exp2(fmaf(sv[2 * i + 1], by, -ref));
+            const float a = fast_exp2(fmaf(sv[2 * i], by, shift));
+            const float e = fast_exp2(fmaf(sv[2 * i + 1], by, shift));
             l4[(2 * i) & 3] += a;
             l4[(2 * i + 1) & 3] += e;
             pw[i] = FP8 ? pack_f16(a, e) : pack_bf16(a, e);
