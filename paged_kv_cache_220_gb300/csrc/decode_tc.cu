@@ -494,9 +494,14 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
         }
         // every slice has a valid token in row 0 of the CTA's first page, so
         // m is finite from the first slice on and masked logits give p = 0;
-        // WIN: a slice may have none, the reference is then any finite number
-        const float ref0 = WIN && m0 == -INFINITY ? 0.f : m0;
-        const float ref1 = WIN && m1 == -INFINITY ? 0.f : m1;
+        // WIN: a slice may have none, the reference is then any finite number.
+        // WIN on E4M3 pools: weights are 2^15 times as large, so that f16
+        // loses what is below 2^-40 of the largest and not 2^-25; the sums
+        // have the same factor, which cancels (of 60000 weights of 2^-25.6
+        // beside one of 1 nothing was left without it)
+        constexpr float kUp = WIN && FP8 ? 15.f : 0.f;
+        const float ref0 = (WIN && m0 == -INFINITY ? 0.f : m0) - kUp;
+        const float ref1 = (WIN && m1 == -INFINITY ? 0.f : m1) - kUp;
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
           const int rh = r0 + 16 * hh;  // first row of this half

@@ -70,3 +70,22 @@ def test_tree_counts_a_tail_of_small_weights(d, fp8, extra, _lib):
     torch.cuda.synchronize()
     assert int(_lib.item()) == 0
     verify(out, T, "tree")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,block", [(128, 32), (256, 32)])
+@pytest.mark.parametrize("partition", [0, 32768])
+def test_window_counts_a_tail_of_small_weights(d, block, fp8, partition, _lib):
+    """The sink through `sinks`, the tail through the window, one CTA to a
+    sequence (partition 0) or two partitions."""
+    k, v, blocks, one = sink_cache(d, fp8)
+    S = 400
+    window = T - 5000
+    q = torch.zeros(S, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1
+    out = pkv.paged_attention_window(
+        q, k, v, blocks.repeat(S, 1), torch.full((S,), T, dtype=torch.int32, device="cuda"),
+        LOGIT / 16, T, window, 1, partition, k_scale=one, v_scale=one)
+    torch.cuda.synchronize()
+    assert int(_lib.item()) == 0
+    verify(out, window + 1, "window")
