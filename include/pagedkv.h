@@ -387,9 +387,10 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
  *               reported (PKV_DEVERR_CONTEXT) and its rows are left as they
  *               were
  *   workspace, workspace_bytes : device scratch of at least
- *               pkv_tree_workspace_bytes(...) bytes; its contents do not
- *               matter before or after; calls whose kernels may overlap need
- *               one each.
+ *               pkv_tree_workspace_bytes(...) bytes, also where every context
+ *               is empty (the size goes by head_dim alone: 42 MB at 256, 21 MB
+ *               at 128); its contents do not matter before or after; calls
+ *               whose kernels may overlap need one each.
  *   other args  : as for pkv_paged_attention_decode
  * Slots behind the context and of drafts that no row of their sequence sees
  * (padding whose bits are clear everywhere) may hold anything, NaN included; a

@@ -1521,7 +1521,7 @@ extern "C" size_t pkv_tree_workspace_bytes(int num_seqs, int num_queries, int nu
                                            int max_draft) {
   using namespace pkv;
   if (num_seqs <= 0 || num_queries <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
-      max_context <= 0 || max_draft <= 0)
+      max_context < 0 || max_draft <= 0)
     return 0;
   // per CTA: what the merge needs, two partial tiles
   return static_cast<size_t>(kTreeMaxCtas) *
@@ -1545,7 +1545,7 @@ extern "C" int pkv_paged_attention_tree(
   if (num_seqs == 0 || num_queries == 0) return PKV_OK;
   const size_t need = pkv_tree_workspace_bytes(num_seqs, num_queries, num_heads,
                                                cache.num_kv_heads, cache.head_dim,
-                                               std::max(1, max_context), max_draft);
+                                               max_context, max_draft);
   if (!q_start || !workspace || !aligned16(workspace) || workspace_bytes < need)
     return PKV_ERR_INVALID_ARG;
   // the most that the call's bounds allow
