@@ -343,7 +343,7 @@ int pkv_paged_attention_decode_shared_prefix(
  *               is 0; may be NULL then). Its contents do not matter before or
  *               after; calls whose kernels may overlap need one each.
  *   other args  : as for pkv_paged_attention_decode. A context of 0 yields
- *               zeros. `out` may not be `q`.
+ *               zeros. `out` may not overlap `q`.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  * ------------------------------------------------------------------------ */
 int pkv_window_partition_size(int num_seqs, int num_kv_heads, int head_dim, int block_size,
@@ -373,7 +373,7 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
  *
  *   q, out      : device bf16 [num_queries][num_heads][head_dim]; rows at or
  *               behind q_start[num_seqs] are neither read nor written; `out`
- *               may not be `q`
+ *               may not overlap `q`
  *   q_start     : device int32 [num_seqs + 1], not decreasing, q_start[0] >= 0,
  *               q_start[num_seqs] <= num_queries; n_s may be 0
  *   max_draft   : host upper bound of n_s, 1..64. A sequence with a negative
@@ -428,17 +428,19 @@ int pkv_paged_attention_tree(void* out, const void* q, const void* k_cache, cons
  *
  *   k_caches, v_caches : HOST arrays of num_layers device pointers, pools of
  *               the geometry `cache` that share the block tables; read during
- *               the call only. No pool may appear twice (PKV_ERR_INVALID_ARG).
+ *               the call only. No pools may overlap, nor one appear twice
+ *               (PKV_ERR_INVALID_ARG).
  *   accepted    : device int32 [num_seqs][max_accepted], strictly increasing,
  *               0 <= a_k < n_s; entries from num_accepted[s] on are not read
  *   num_accepted: device int32 [num_seqs], 0 <= m_s <= max_accepted
  *   new_context_lens : NULL, or device int32 [num_seqs] that receives
- *               base_s + m_s; it may not be context_lens
+ *               base_s + m_s; it may not overlap context_lens, q_start,
+ *               accepted, num_accepted or block_tables (PKV_ERR_INVALID_ARG)
  * A block that a moved row is written to must not be shared with another
  * sequence (pkv_seq_append's copy-on-write sees to that when the drafts are
  * appended). A bad list or number of drafts is reported (PKV_DEVERR_DRAFT):
- * no row of that sequence moves and its new length is base_s (ctx_s if base_s
- * would be negative). A context outside the table (PKV_DEVERR_CONTEXT) moves
+ * no row of that sequence moves and its new length is base_s (ctx_s if its
+ * number of drafts is negative or above its context). A context outside the table (PKV_DEVERR_CONTEXT) moves
  * nothing and is kept. A move from or to a bad block id is skipped and
  * reported (PKV_DEVERR_BLOCK_ID).
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.

@@ -662,7 +662,8 @@ def kv_cache_accept(k_caches, v_caches, block_tables, context_lens, q_start, acc
     (see the C header). k_caches, v_caches: a pool each, or equally long lists
     of them (one per layer, sharing block_tables). accepted int32 [S, M],
     strictly increasing; num_accepted int32 [S]. Returns the new context
-    lengths, int32 [S] (in new_context_lens if given; not context_lens)."""
+    lengths, int32 [S] (in new_context_lens if given, which may overlap none
+    of the other arguments; neither may the pools each other)."""
     L = _lib or lib()
     if isinstance(k_caches, torch.Tensor):
         k_caches = (k_caches,)

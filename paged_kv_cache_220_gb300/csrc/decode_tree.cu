@@ -1556,6 +1556,8 @@ extern "C" int pkv_paged_attention_tree(
   // places of the line are 32-bit numbers (a q_start that is not ascending
   // may ask for up to twice the work)
   if (units * (longest + kTreeStart) >= (1 << 29)) return PKV_ERR_UNSUPPORTED;
+  const size_t q_bytes = static_cast<size_t>(num_queries) * num_heads * cache.head_dim * 2;
+  if (overlap(out, q_bytes, q, q_bytes)) return PKV_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

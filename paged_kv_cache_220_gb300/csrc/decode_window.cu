@@ -95,6 +95,8 @@ extern "C" int pkv_paged_attention_window(
   if (window <= 0 || sinks < 0 || partition_size < 0 || partition_size % cache.block_size != 0)
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;
+  const size_t q_bytes = static_cast<size_t>(num_seqs) * num_heads * cache.head_dim * 2;
+  if (overlap(out, q_bytes, q, q_bytes)) return PKV_ERR_INVALID_ARG;
   DecodeParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.k_cache = static_cast<const uint8_t*>(k_cache);

@@ -18,6 +18,12 @@ int* device_error_ptr();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (a_bytes == 0 || b_bytes == 0) return false;
+  return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
+
 inline int elem_bytes(int dtype) { return dtype == PKV_DTYPE_FP8_E4M3 ? 1 : 2; }
 
 // Shape checks common to every call that touches a pool.

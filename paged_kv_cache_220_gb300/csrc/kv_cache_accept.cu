@@ -123,24 +123,42 @@ extern "C" int pkv_kv_cache_accept(void* const* k_caches, void* const* v_caches,
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;
   if (!k_caches || !v_caches || !block_tables || !context_lens || !q_start || !num_accepted ||
-      (max_accepted > 0 && !accepted) || new_context_lens == context_lens)
+      (max_accepted > 0 && !accepted))
     return PKV_ERR_INVALID_ARG;
   for (int l = 0; l < num_layers; ++l)
     if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
       return PKV_ERR_INVALID_ARG;
-  // the same pool twice would be moved twice, by CTAs that do not wait for
-  // each other
+  // the new lengths are written by one CTA of a sequence while others read
+  if (new_context_lens) {
+    const size_t n = static_cast<size_t>(num_seqs), w = sizeof(int32_t);
+    if (overlap(new_context_lens, n * w, context_lens, n * w) ||
+        overlap(new_context_lens, n * w, q_start, (n + 1) * w) ||
+        overlap(new_context_lens, n * w, num_accepted, n * w) ||
+        overlap(new_context_lens, n * w, accepted, n * max_accepted * w) ||
+        overlap(new_context_lens, n * w, block_tables, n * max_blocks_per_seq * w))
+      return PKV_ERR_INVALID_ARG;
+  }
+  // rows of pools that overlap, the same pool twice among them, would be moved
+  // by CTAs that do not wait for each other
   const int pools = 2 * num_layers;
-  auto pool_at = [&](int i) { return i < num_layers ? k_caches[i] : v_caches[i - num_layers]; };
+  const size_t pool_bytes = static_cast<size_t>(cache.num_blocks) * cache.num_kv_heads *
+                            cache.block_size * cache.head_dim * elem_bytes(cache.dtype);
+  auto pool_at = [&](int i) -> const void* {
+    return i < num_layers ? k_caches[i] : v_caches[i - num_layers];
+  };
+  auto clash = [&](const void* a, const void* b) {
+    return overlap(a, pool_bytes, b, pool_bytes);
+  };
   const void* sorted[4 * kAcceptLayers];
   if (pools <= 4 * kAcceptLayers) {
     for (int i = 0; i < pools; ++i) sorted[i] = pool_at(i);
     std::sort(sorted, sorted + pools, std::less<const void*>());
-    if (std::adjacent_find(sorted, sorted + pools) != sorted + pools) return PKV_ERR_INVALID_ARG;
+    if (std::adjacent_find(sorted, sorted + pools, clash) != sorted + pools)
+      return PKV_ERR_INVALID_ARG;
   } else {
     for (int i = 0; i < pools; ++i)
       for (int j = 0; j < i; ++j)
-        if (pool_at(i) == pool_at(j)) return PKV_ERR_INVALID_ARG;
+        if (clash(pool_at(i), pool_at(j))) return PKV_ERR_INVALID_ARG;
   }
   AcceptParams p{};
   p.block_tables = block_tables;
