@@ -227,23 +227,27 @@ extern "C" int pkv_alloc_stats(const pkv_allocator* a, int* free_blocks, int* us
   if (used_blocks) *used_blocks = a->num_blocks - nfree;
   if (used_slots) {
     // slots of a block that some holder's length covers (holders of a shared
-    // block may have been cut to different lengths)
+    // block may have been cut to different lengths): all of them, unless it
+    // is the last block of every holder. One look at each sequence and block
     const int B = a->block_size;
-    std::vector<int32_t> used;
+    std::vector<int32_t> last, most;  // holders whose last block it is, their most slots
     try {
-      used.assign(a->num_blocks, 0);
+      last.assign(a->num_blocks, 0);
+      most.assign(a->num_blocks, 0);
     } catch (...) {
       return PKV_ERR_OUT_OF_BLOCKS;
     }
     for (const auto& kv : a->seqs) {
       const pkv_allocator::Seq& q = kv.second;
-      for (size_t i = 0; i < q.table.size(); ++i) {
-        const int64_t n = std::min<int64_t>(B, q.len - static_cast<int64_t>(i) * B);
-        used[q.table[i]] = std::max(used[q.table[i]], static_cast<int32_t>(n));
-      }
+      if (q.table.empty()) continue;
+      const int32_t b = q.table.back();
+      const int64_t n = q.len - static_cast<int64_t>(q.table.size() - 1) * B;
+      ++last[b];
+      most[b] = std::max(most[b], static_cast<int32_t>(n));
     }
     long long u = 0;
-    for (int32_t n : used) u += n;
+    for (int b = 0; b < a->num_blocks; ++b)
+      if (a->refcount[b] > 0) u += last[b] < a->refcount[b] ? B : most[b];
     *used_slots = u;
   }
   return PKV_OK;
