@@ -337,6 +337,7 @@ extern "C" int pkv_alloc_load(const void* buf, size_t n, pkv_allocator** out) {
     a->num_blocks = static_cast<int>(nb);
     a->block_size = static_cast<int>(bs);
     a->next_id = static_cast<int>(next_id);
+    a->free_list.reserve(nb);  // giving blocks back then needs no memory
     a->free_list.resize(nfree);
     a->refcount.resize(nb);
     a->fill.resize(nb);
