@@ -344,7 +344,8 @@ int pkv_paged_attention_decode_shared_prefix(
  *               after; calls whose kernels may overlap need one each.
  *   other args  : as for pkv_paged_attention_decode. A context of 0 yields
  *               zeros. `out` may not overlap `q`.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA; PKV_ERR_UNSUPPORTED also for
+ * tables of more than 2^30 tokens a sequence.
  * ------------------------------------------------------------------------ */
 int pkv_window_partition_size(int num_seqs, int num_kv_heads, int head_dim, int block_size,
                               int max_context, int window, int sinks);
@@ -400,10 +401,10 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
  * lost to underflow each) before they meet V, sums are fp32. E4M3
  * pools: an element of q below 2^-9 of its row's largest is rounded by at most
  * 2^-17 of that largest.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA; PKV_ERR_UNSUPPORTED also where
- * the bounds allow more work than the kernel numbers: (num_seqs + num_queries
- * g / 128) num_kv_heads (max_context / 128 + 3) of 2^29 or more, g = num_heads
- * / num_kv_heads.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA; PKV_ERR_UNSUPPORTED also for
+ * tables of more than 2^30 tokens a sequence and where the bounds allow more
+ * work than the kernel numbers: (num_seqs + num_queries g / 128) num_kv_heads
+ * (max_context / 128 + 3) of 2^29 or more, g = num_heads / num_kv_heads.
  * ------------------------------------------------------------------------ */
 #define PKV_MAX_DRAFT 64
 size_t pkv_tree_workspace_bytes(int num_seqs, int num_queries, int num_heads, int num_kv_heads,

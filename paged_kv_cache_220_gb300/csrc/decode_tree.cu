@@ -1553,8 +1553,8 @@ extern "C" int pkv_paged_attention_tree(
       num_seqs + static_cast<int64_t>(num_queries) * g / kTreeRows;
   const int64_t units = tiles_most * cache.num_kv_heads;
   const int64_t longest = (static_cast<int64_t>(max_context) + kTreeTok - 1) / kTreeTok;
-  // places of the line are 32-bit numbers (a q_start that is not ascending
-  // may ask for up to twice the work)
+  // places of the line are 32-bit numbers (a q_start that is not ascending may
+  // ask for up to four times the work: a sequence has at most four row tiles)
   if (units * (longest + kTreeStart) >= (1 << 29)) return PKV_ERR_UNSUPPORTED;
   const size_t q_bytes = static_cast<size_t>(num_queries) * num_heads * cache.head_dim * 2;
   if (overlap(out, q_bytes, q, q_bytes)) return PKV_ERR_INVALID_ARG;

@@ -2,7 +2,6 @@
 #pragma once
 
 #include <atomic>
-#include <climits>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -53,7 +52,8 @@ inline int check_attention(const pkv_cache_desc& cache, const void* out, const v
   const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * cache.block_size;
   if (max_context > cap) return PKV_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
-  if (num_seqs > 65535 || cap > INT_MAX) return PKV_ERR_UNSUPPORTED;
+  // positions of a step or page behind the context are 32-bit numbers too
+  if (num_seqs > 65535 || cap > (1 << 30)) return PKV_ERR_UNSUPPORTED;
   // TMA row coordinates are 32-bit
   if (static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads * cache.block_size >=
       (int64_t{1} << 31))
