@@ -325,8 +325,9 @@ int pkv_paged_attention_decode_shared_prefix(
  *     z_t = scale * <q[s,j,:], K_s[t,:]>,  out[s,j,:] = sum_{t in V_s} softmax(z)_t V_s[t,:]
  * (the pages have no counterpart). A block with no visible token is never
  * read: its block_tables entry may be anything, so a caller can give the
- * blocks behind the window back to its pool. Masked slots of the blocks that
- * are read may hold anything, NaN included.
+ * blocks behind the window back to a pool of its own (pkv_allocator keeps a
+ * sequence's blocks until it is freed or cut at its end). Masked slots of the
+ * blocks that are read may hold anything, NaN included.
  *
  *   window      : >= 1; larger than the context: plain decode
  *   sinks       : >= 0

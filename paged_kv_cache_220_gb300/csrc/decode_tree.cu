@@ -45,27 +45,45 @@
 // 2^-e go into the logits, v_scale into the output. K and V have rings of their
 // own.
 //
-// P is one bf16 part (a rounding of each weight to as many bits as the output
-// has; a second part would double the P.V products).
+// What V holds behind the context and in drafts that no row sees never counts:
+// its weight is 0, and the row is zeroed in shared memory before P.V reads it,
+// since 0 x NaN is NaN (16-bit pools: by the softmax warps, in place; E4M3: by
+// the converters).
+//
+// P is one bf16 part, a rounding of each weight to as many bits as the output
+// has. The one-token decode holds P in two parts. Here a second part (the
+// remainders over the other half of S's columns, one more product each) takes
+// the error against 64 bits from 0.0023 to 0.0017 of the output (the output's
+// own rounding is 0.0017) and costs 1 % where HBM bounds the call (32 x 8192
+// tokens x 16 drafts, d = 256: 171 -> 173 us), 7 % at d = 128 (96 ragged
+// sequences 153 -> 164), 4 to 8 % of small calls and 17 to 26 % of calls with
+// several row tiles (16 x 4096 x 64, d = 256: 94 -> 118): the softmax's
+// instructions more than the products.
 //
 // Warps: 0-7 softmax (threads t and t + 128 own query row t, 64 of a step's
 // columns each; they exchange maxima through shared memory), 8 issues Q.K^T, 9
 // P.V; bf16: 10-13 load Q, 14-15 load pages; E4M3: 10 loads K, 11 V, 12-15
 // convert V and load Q. 512 threads of up to 128 registers, all the SM has.
 //
-// What bounds it on GB300 (of 6788 GB/s copy, 1943 TFLOP/s bf16):
-//   few rows, bf16: HBM. 32 x 8192 tokens x 16 drafts, d = 256: 174 us, 92 %;
-//     64 x 8192 x 1: 317 us, 100 %; 96 sequences of 16 .. 16384: 155 us, 90 %
-//   many rows: a step at d = 128 costs the softmax 2000 clocks (1024 of them
-//     the 128 x 128 exponentials at 16 a clock) and the tensor core 1040; at
-//     d = 256 P, S's buffers and the reads of K and V by all tiles of a team
-//     (13 TB/s out of L2 of the 14.7 that TMA reaches) leave 2800 clocks to a
-//     step of 2100 on the tensor core. 16 x 4096 x 64, d = 256: 98 us, 54 % of
-//     the products' floor; 32 x 4096 x 64, d = 128: 243 us, 58 %
-//   E4M3: the same softmax against half the bytes. 8 x 65536 x 8, d = 256:
-//     210 us, 75 % of HBM; 32 x 8192 x 4, d = 128: 127 us, 63 % (half the
-//     columns of the softmax would take 6 and 20 % off; its instructions, not
-//     the exponentials, are what counts)
+// What bounds it on GB300 (of 6788 GB/s copy, 1943 TFLOP/s bf16; calls in a
+// graph; clocks of a step from calls of two lengths, at 2070 MHz):
+//   few rows, bf16: HBM. 32 x 8192 tokens x 16 drafts, d = 256: 173 us, 92 %;
+//     64 x 8192 x 1: 317 us, 100 %; 96 sequences of 16 .. 16384: 153 us, 91 %
+//   many rows: at d = 128 a step takes 2000 clocks, the softmax's chain of one
+//     row tile (load S, maximum, exchange with the row's other thread,
+//     exponentials, P) on two warps a scheduler; 1040 of them are the tensor
+//     core's and 512 the 128 x 128 exponentials at 32 a clock. 32 x 4096 x 64:
+//     248 us, 57 % of the products' floor; 42 us are the starts and ends of
+//     seven units per CTA and the merge. At d = 256 a step takes 3300 clocks,
+//     2100 of them the tensor core's: P, S's two buffers and the reads of K and
+//     V by all tiles of a team out of L2. 16 x 4096 x 64: 93 us, 57 %, 27 of
+//     them starts, ends and the merge
+//   E4M3: HBM leaves a step 3040 clocks at d = 256 and 1520 at d = 128; the
+//     kernel takes 3400 and 2000. 8 x 65536 x 8, d = 256: 197 us, 80 % of HBM;
+//     32 x 8192 x 4, d = 128: 127 us, 63 %; 64 x 4096 x 21, d = 256: 154 us, 55 %
+//     (half the exponentials and loads of S would take 6 to 20 % off; every
+//     instruction that the softmax's or the converters' loop gains or loses
+//     shows)
 //   one short sequence: latency. 1033 tokens x 5 drafts 11.2 us, 4 of them the
 //     merge
 #include <algorithm>
@@ -938,8 +956,9 @@ __global__ void __launch_bounds__(TreeGeom<D, FP8>::kThreads, 1)
     // ---------------- softmax: two threads per query row, 64 columns each, in
     // chunks of NC. d = 256: two, read twice, in loops that are not unrolled:
     // half the code and no spilled registers (64 x 4096 tokens x 21 drafts E4M3
-    // 164 -> 148 us, 16 x 4096 x 64 94 -> 92); d = 128: one (in two 32 x 4096 x
-    // 64 drafts take 264 us instead of 249)
+    // 164 -> 148 us, 16 x 4096 x 64 94 -> 92 when it was introduced); d = 128:
+    // one (in two 32 x 4096 x 64 drafts take 264 us instead of 249), at the
+    // price of 12 bytes of spills (E4M3: 4)
     constexpr int NC = D == 256 ? 32 : 64;
     const int quad = warp & 3, half = warp >> 2;
     const int row = 32 * quad + lane;

@@ -28,8 +28,12 @@ static int64_t window_partitions(int block_size, int max_context, int window, in
 // CTAs that run at once: four to an SM at d = 256, three at d = 128.
 static int64_t window_wave(int head_dim) { return head_dim == 256 ? 600 : 440; }
 
-// CTAs of a pair's cluster in one pass: up to 8, two blocks or more each,
-// while one wave holds them.
+// CTAs of a pair's cluster in one pass: the smallest power of two, 8 at most,
+// with two blocks or fewer for each, while one wave holds them. The shares are
+// equal runs of pages rounded up, so some CTAs may get none; the longest share
+// is what counts. Half as many CTAs where they would get less than two blocks
+// each: 5 to 7 blocks 8.3 -> 10.7 .. 11.4 us (4 pairs, d = 256, B = 16), 11 to
+// 15 blocks 7.8 -> 9.0 .. 9.6; 3 blocks 10.2 -> 7.7.
 static int64_t window_cluster(int64_t pairs, int64_t blocks, int64_t wave) {
   int64_t c = 1;
   while (c < 8 && 2 * c < blocks && 2 * c * pairs <= wave) c <<= 1;
