@@ -630,7 +630,8 @@ def paged_attention_tree(q, k_cache, v_cache, block_tables, context_lens, q_star
     s has the drafts q[q_start[s]:q_start[s + 1]], whose K/V are its last
     tokens in the cache; each sees every committed token and the drafts whose
     bits its tree_mask entry (int64 or uint64 [N]) has set, or with
-    tree_mask=None the drafts up to itself. context_lens counts the drafts;
+    tree_mask=None the drafts up to itself. Drafts that no row sees (padding)
+    may hold anything in the cache. context_lens counts the drafts;
     max_draft (at most 64) bounds the drafts of a sequence. Returns out
     [N, Hq, D] bf16; rows at or behind q_start[S] are not written. out and
     workspace are allocated if not given."""

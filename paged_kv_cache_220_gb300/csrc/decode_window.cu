@@ -25,7 +25,8 @@ static int64_t window_partitions(int block_size, int max_context, int window, in
   return (window_blocks_bound(block_size, max_context, window, sinks) + per - 1) / per;
 }
 
-// CTAs that run at once: four to an SM at d = 256, three at d = 128.
+// CTAs that run at once on GB300's 152 SMs: four to an SM at d = 256, three at
+// d = 128, a few short of that.
 static int64_t window_wave(int head_dim) { return head_dim == 256 ? 600 : 440; }
 
 // CTAs of a pair's cluster in one pass: the smallest power of two, 8 at most,
