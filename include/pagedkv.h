@@ -24,6 +24,14 @@
  *                      row-major; element type bf16 (2 bytes) or OCP FP8 E4M3
  *                      (1 byte). One (block, head) page is one contiguous run
  *                      of block_size*head_dim elements.
+ *                      4-bit pools (PKV_DTYPE_FP4_E2M1) hold OCP E2M1 codes
+ *                      (+-0, .5, 1, 1.5, 2, 3, 4, 6) with an E4M3 scale for
+ *                      every 16 channels of a token. A page is a run of
+ *                      block_size*head_dim*9/16 bytes in lines of 144: the 128
+ *                      code bytes of 256/head_dim consecutive tokens (channel
+ *                      2i of a token in the low half of its byte i, channel
+ *                      2i + 1 in the high half), then their 16 scales, token
+ *                      after token.
  *   q, out           : [num_seqs][num_heads][head_dim] bf16.
  *                      Query head j reads KV head j / (num_heads/num_kv_heads).
  *   block_tables     : int32 [num_seqs][max_blocks_per_seq]; entries past
@@ -74,7 +82,14 @@ typedef enum {
   PKV_ERR_DEVICE_CHECK = -6   /* a kernel reported a bad id or a timed-out wait */
 } pkv_status;
 
-typedef enum { PKV_DTYPE_BF16 = 0, PKV_DTYPE_FP8_E4M3 = 1 } pkv_dtype;
+typedef enum {
+  PKV_DTYPE_BF16 = 0,
+  PKV_DTYPE_FP8_E4M3 = 1,
+  /* 4-bit pools: kv_cache_write, kv_cache_read, paged_attention_decode (and the
+   * calls made of it), paged_attention_sparse, block_bounds, copy_blocks and
+   * the swaps take them; every other call returns PKV_ERR_INVALID_ARG. */
+  PKV_DTYPE_FP4_E2M1 = 2
+} pkv_dtype;
 
 /* Device error codes written into the registered error word (first error wins). */
 #define PKV_DEVERR_NONE 0
@@ -87,6 +102,8 @@ typedef enum { PKV_DTYPE_BF16 = 0, PKV_DTYPE_FP8_E4M3 = 1 } pkv_dtype;
 #define PKV_DEVERR_DRAFT 6       /* a sequence's drafts: a negative number or more than
                                     max_draft, more than its context; an accepted list
                                     that is too long, not increasing or out of range */
+#define PKV_DEVERR_SELECT 7      /* a listed block that is none of its context's, a list
+                                    that is longer than the call's bound */
 
 /* Geometry of one layer's K and V pools (both share it). */
 typedef struct {
@@ -111,9 +128,18 @@ typedef struct {
  *   k, v         : device bf16 [num_tokens][num_kv_heads][head_dim]
  *   slot_mapping : device int64 [num_tokens]; -1 skips the token
  *   k_cache, v_cache : device pools described by `cache`
- *   k_scale, v_scale : device fp32 [num_kv_heads], FP8 pools only (else NULL).
+ *   k_scale, v_scale : device fp32 [num_kv_heads], FP8 and 4-bit pools only
+ *     (else NULL).
  *     FP8 code = round-to-nearest-even, saturating to +-448, of the fp32
  *     quotient x / scale[h] (IEEE division), OCP E4M3.
+ *     4-bit pools: with y = x / scale[h] and a = the largest |y| of the 16
+ *     channels, their scale is s = E4M3(a / 6) (nearest even, saturating) and
+ *     a code is E2M1(y / s) (nearest, ties to the even code, saturating; all
+ *     three quotients are IEEE fp32 divisions); it stands for code * s *
+ *     scale[h]. Where s is zero (a / 6 <= 2^-10) the codes are +0; a NaN among
+ *     the 16 makes s NaN and the codes +0. Nothing saturates with a scale[h] of
+ *     1/2688 of the head's largest |x| or more; s has its full precision where
+ *     a >= 6 * 2^-6.
  * For bf16 pools the copy is bit-exact.
  * Errors: PKV_ERR_INVALID_ARG (null pointers, num_tokens < 0, misaligned),
  * PKV_ERR_UNSUPPORTED (shape), PKV_ERR_CUDA. num_tokens == 0 is a no-op.
@@ -124,6 +150,26 @@ int pkv_kv_cache_write(const void* k, const void* v, const int64_t* slot_mapping
                        const float* v_scale, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * kv_cache_read: the rows that the given slots hold, as bf16 (the pages have
+ * no counterpart). A prefill attends to what later steps will read from the
+ * cache, not to the K and V it wrote there; rows may also be moved to a cache
+ * of another type (read, then pkv_kv_cache_write).
+ *
+ *   k, v         : device bf16 [num_tokens][num_kv_heads][head_dim], written:
+ *     bf16 pools bit for bit; FP8 code * scale[h] and 4-bit code * s * scale[h]
+ *     (one fp32 product; code * s is exact) rounded to nearest even. They may
+ *     not overlap each other, the pools or slot_mapping.
+ *   slot_mapping : device int64 [num_tokens]; -1 (or any negative number): the
+ *     row is zeros; a slot outside the pool is reported (PKV_DEVERR_SLOT), its
+ *     row is zeros
+ *   other args   : as for pkv_kv_cache_write
+ * Errors: as for pkv_kv_cache_write.
+ * ------------------------------------------------------------------------ */
+int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tokens,
+                      const void* k_cache, const void* v_cache, pkv_cache_desc cache,
+                      const float* k_scale, const float* v_scale, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * paged_attention_decode: one query token per sequence, grouped-query
  * attention over the paged cache ([Dissect] "PagedAttention: Virtual Memory
  * for KV Cache"; decode as the bandwidth-bound phase: [HowVLLM] "Decode is a
@@ -132,7 +178,9 @@ int pkv_kv_cache_write(const void* k, const void* v, const int64_t* slot_mapping
  * For sequence s and query head j (KV head h = j / g, g = num_heads /
  * num_kv_heads), with K_s, V_s the sequence's logical rows 0..ctx-1:
  *     z_t = scale * <q[s,j,:], K_s[t,:]>,  out[s,j,:] = sum_t softmax(z)_t V_s[t,:]
- * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]).
+ * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]), 4-bit pools as
+ * code * s * k_scale[h] (tables of at most 2^30 tokens a sequence; an element
+ * of q below 2^-14 of its row's largest is rounded by at most 2^-25 of it).
  * The softmax is the max-subtracted one, accumulated online in fp32.
  *
  *   out       : device bf16 [num_seqs][num_heads][head_dim] (written when
@@ -182,6 +230,12 @@ size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int head_dim,
  * block_size <= 0 or partition_size is not a positive multiple of it. (The
  * pages leave the split size open; this is a load-balancing choice.) */
 int pkv_split_partition_size(int max_context, int block_size, int partition_size);
+
+/* Host helper: the library's choice of partition_size for a decode of num_seqs
+ * sequences of at most max_context tokens (0 = one pass). Any other valid value
+ * gives the same attention. PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED for a bad
+ * geometry. */
+int pkv_decode_partition_size(pkv_cache_desc cache, int num_seqs, int max_context);
 
 /* Host helper: order[0..n) = the indices 0..n-1 sorted by lengths[i], longest
  * first, equal lengths in index order (a stable sort), for the seq_order
@@ -362,6 +416,116 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
                                const int32_t* seq_order, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * block_bounds: for blocks of a K pool, the lowest and the highest cached value
+ * of each channel, as whole multiples of a step per head (the pages have no
+ * counterpart; pkv_select_blocks reads them). With K the dequantised rows of
+ * the block's cached tokens (those below the context; a NaN counts as 0):
+ *     lo = min_t clamp(floor(K[t] / step[h])), hi = max_t clamp(ceil(K[t] / step[h]))
+ * (IEEE fp32 quotients, FP8 and 4-bit values rounded to fp32 once before; clamped to
+ * -127..127). A step of 1/127 of the head's largest |K| loses nothing.
+ *
+ *   bounds      : device int8 [num_blocks][num_kv_heads][2][head_dim], lo then
+ *               hi; blocks that no sequence names are left as they were
+ *   k_cache, cache, k_scale : the K pool, any type (k_scale: FP8 and 4-bit)
+ *   step        : device fp32 [num_kv_heads], positive and finite
+ *   max_new, num_new : the blocks that hold the last num_new[s] tokens of
+ *               sequence s (device int32 [num_seqs]; NULL: the last max_new
+ *               ones) are done, whole: tokens written earlier count. More
+ *               tokens than the context has mean all of it. A number that is
+ *               negative or above max_new, or a context outside the table, is
+ *               reported (PKV_DEVERR_CONTEXT) and nothing of the sequence is
+ *               done; a bad block id is reported and skipped.
+ * After a step that wrote one token per sequence max_new is 1; after
+ * pkv_copy_blocks or a swap into other blocks the copies need their bounds too.
+ * Sequences that share a block write the same bounds to it if both have it full
+ * or end at the same token in it.
+ * Errors: PKV_ERR_INVALID_ARG (max_new < 0 among them), PKV_ERR_UNSUPPORTED,
+ * PKV_ERR_CUDA. num_seqs == 0 and max_new == 0 are no-ops.
+ * ------------------------------------------------------------------------ */
+int pkv_block_bounds(int8_t* bounds, const void* k_cache, pkv_cache_desc cache,
+                     const float* k_scale, const float* step, const int32_t* block_tables,
+                     int max_blocks_per_seq, const int32_t* context_lens, const int32_t* num_new,
+                     int max_new, int num_seqs, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * select_blocks: for each sequence and KV head, the blocks of the context whose
+ * logits may be the highest (the pages have no counterpart). With q_j, j < g,
+ * the query heads of KV head h, M the largest |element| of all of them, and lo,
+ * hi the bounds of block b (pkv_block_bounds):
+ *     c_j = round(127 q_j / M)  (nearest even; 0 where M is 0)
+ *     score(b) = sum_j sum_d max(c_j[d] lo[d], c_j[d] hi[d])
+ * an upper bound of the sum of the block's highest logits, up to a factor that
+ * all blocks of the head share and the rounding of q. Scores are whole numbers
+ * without rounding, so the choice does not depend on the order of any sum.
+ *
+ *   blocks      : device int32 [num_seqs][num_kv_heads][max_selected]: the
+ *               chosen logical blocks, ascending; -1 behind the last
+ *   counts      : device int32 [num_seqs][num_kv_heads]: how many; n =
+ *               ceil(ctx / block_size) if that is at most max_selected, else
+ *               max_selected
+ *   first, last : that many blocks at the front and at the end of the context
+ *               are always chosen (first + last <= max_selected); the others
+ *               go by their score, equal ones by the lower index
+ *   q           : device bf16 [num_seqs][num_heads][head_dim], finite and below
+ *               2^120 (other values give some choice)
+ *   bounds      : device int8, as pkv_block_bounds writes it, values -127..127
+ *   cache       : geometry of the pool the bounds belong to
+ *   max_context : host upper bound of context_lens (a longer context is
+ *               reported, PKV_DEVERR_CONTEXT, and cut)
+ *   workspace   : device scratch of at least pkv_select_workspace_bytes(...)
+ *               bytes, 16-byte aligned; its contents do not matter before or
+ *               after; calls whose kernels may overlap need one each
+ * A bad block id is reported (PKV_DEVERR_BLOCK_ID); the block then comes after
+ * all others. blocks, counts and workspace may not overlap each other or an
+ * input. Errors: PKV_ERR_INVALID_ARG (max_selected < 1 among them),
+ * PKV_ERR_UNSUPPORTED (tables of more than 2^30 tokens a sequence among them),
+ * PKV_ERR_CUDA. num_seqs == 0 is a no-op.
+ * ------------------------------------------------------------------------ */
+size_t pkv_select_workspace_bytes(int num_seqs, int num_kv_heads, int block_size,
+                                  int max_context);
+int pkv_select_blocks(int32_t* blocks, int32_t* counts, const void* q, const int8_t* bounds,
+                      pkv_cache_desc cache, const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* context_lens, int num_seqs, int num_heads, int max_context,
+                      int max_selected, int first, int last, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * paged_attention_sparse: decode attention over chosen blocks of the context,
+ * for each sequence and KV head its own (the pages have no counterpart;
+ * pkv_select_blocks makes such lists). With L = blocks[s][h][0 .. counts[s][h]):
+ *     out[s,j,:] = sum_t softmax(z)_t V_s[t,:] over the tokens t < ctx of the
+ *     blocks in L, z_t = scale * <q[s,j,:], K_s[t,:]>
+ * No other block is read, nor its block_tables entry. A block listed twice
+ * counts twice. Lists may be in any order; every order gives the same attention
+ * up to the rounding of its sums. No token: zeros.
+ *
+ *   blocks      : device int32 [num_seqs][num_kv_heads][max_selected], logical
+ *               blocks 0 .. ceil(ctx / block_size) - 1; entries behind the
+ *               count may hold anything. An entry that is none of these is
+ *               reported (PKV_DEVERR_SELECT) and adds nothing
+ *   counts      : device int32 [num_seqs][num_kv_heads], 0 .. max_selected;
+ *               others are reported (PKV_DEVERR_SELECT) and cut to the range
+ *   workspace, workspace_bytes : device scratch of at least
+ *               pkv_sparse_workspace_bytes(...) bytes (which may be 0; may be
+ *               NULL then), 16-byte aligned; its contents do not matter before
+ *               or after; calls whose kernels may overlap need one each
+ *   other args  : as for pkv_paged_attention_decode; bf16, FP8 and 4-bit pools.
+ *               `out` may not overlap `q`.
+ * Errors: PKV_ERR_INVALID_ARG (max_selected < 1 among them), PKV_ERR_CUDA;
+ * PKV_ERR_UNSUPPORTED also for tables of more than 2^30 tokens a sequence and
+ * max_selected above 2^20. num_seqs == 0 is a no-op.
+ * ------------------------------------------------------------------------ */
+size_t pkv_sparse_workspace_bytes(pkv_cache_desc cache, int num_seqs, int num_heads,
+                                  int max_selected);
+int pkv_paged_attention_sparse(void* out, const void* q, const void* k_cache,
+                               const void* v_cache, pkv_cache_desc cache, const float* k_scale,
+                               const float* v_scale, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* blocks, const int32_t* counts, int max_selected,
+                               int num_seqs, int num_heads, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * paged_attention_tree: attention of several drafted tokens per sequence, a
  * chain or a tree, over the paged cache (the pages have no counterpart; this
  * is the verification step of speculative decoding). The drafts' K and V are
@@ -523,8 +687,8 @@ int pkv_paged_attention_decode_noalloc(void* out, const void* q, const void* k_c
  *
  *   blocks  : int32 [n] block ids, readable by the device (device memory or
  *             pinned host memory)
- *   k_buf, v_buf : [n][num_kv_heads*block_size*head_dim*esz] bytes, block i of
- *             the list at row i; device memory or pinned host memory the device
+ *   k_buf, v_buf : [n][num_kv_heads*page bytes] (a page is block_size*head_dim
+ *             elements of 2, 1 or 9/16 bytes), block i of the list at row i; device memory or pinned host memory the device
  *             can address (the kernel reads/writes it directly)
  * swap_out: buf[i] = pool[blocks[i]]; swap_in: pool[blocks[i]] = buf[i]
  * (byte for byte). The allocator side (freeing a sequence, re-creating it

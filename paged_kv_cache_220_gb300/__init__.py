@@ -8,12 +8,14 @@ fallback: without the built library or a CUDA device the calls raise.
 Tensors (caller-owned device memory):
   k_cache, v_cache : [num_blocks, num_kv_heads, block_size, head_dim],
                      torch.bfloat16, or torch.uint8 / torch.float8_e4m3fn
-                     holding OCP E4M3 codes
+                     holding OCP E4M3 codes; or a 4-bit pool, torch.uint8
+                     [num_blocks, num_kv_heads, block_size, 9 * head_dim / 16]
+                     (fp4_cache, its layout in include/pagedkv.h)
   q, out           : [num_seqs, num_heads, head_dim] torch.bfloat16
   block_tables     : [num_seqs, max_blocks_per_seq] torch.int32
   context_lens     : [num_seqs] torch.int32
   slot_mapping     : [num_tokens] torch.int64 (-1 = skip)
-  k_scale, v_scale : [num_kv_heads] torch.float32 (FP8 pools)
+  k_scale, v_scale : [num_kv_heads] torch.float32 (FP8 and 4-bit pools)
   q_start          : [num_seqs + 1] torch.int32, the first draft row of each
                      sequence (paged_attention_tree, kv_cache_accept)
 """
@@ -38,6 +40,7 @@ PKV_ERR_NOT_FOUND = -5
 PKV_ERR_DEVICE_CHECK = -6
 PKV_DTYPE_BF16 = 0
 PKV_DTYPE_FP8_E4M3 = 1
+PKV_DTYPE_FP4_E2M1 = 2
 PKV_PREEMPT_RECOMPUTE = 0
 PKV_PREEMPT_SWAP = 1
 PKV_BATCH_ADMISSION = 0
@@ -50,6 +53,7 @@ DEVERR_WAIT_TIMEOUT = 3
 DEVERR_CONTEXT = 4
 DEVERR_ORDER = 5
 DEVERR_DRAFT = 6
+DEVERR_SELECT = 7
 
 MAX_DRAFT = 64
 
@@ -73,8 +77,10 @@ _lib = None
 # name -> (restype, argtypes); mirrors include/pagedkv.h
 SIGNATURES = {
     "pkv_kv_cache_write": (_I, [_P, _P, _P, _I, _P, _P, CacheDesc, _P, _P, _P]),
+    "pkv_kv_cache_read": (_I, [_P, _P, _P, _I, _P, _P, CacheDesc, _P, _P, _P]),
     "pkv_decode_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "pkv_split_partition_size": (_I, [_I, _I, _I]),
+    "pkv_decode_partition_size": (_I, [CacheDesc, _I, _I]),
     "pkv_longest_first_order": (_I, [_P, _I, _P]),
     "pkv_paged_attention_decode": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _I, _I,
                                         _I, ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
@@ -94,6 +100,13 @@ SIGNATURES = {
     "pkv_paged_attention_window": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _I, _I,
                                         _I, ctypes.c_float, _I, _I, _I, _P, ctypes.c_size_t, _P,
                                         _P]),
+    "pkv_block_bounds": (_I, [_P, _P, CacheDesc, _P, _P, _P, _I, _P, _P, _I, _I, _P]),
+    "pkv_select_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "pkv_select_blocks": (_I, [_P, _P, _P, _P, CacheDesc, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P,
+                               ctypes.c_size_t, _P]),
+    "pkv_sparse_workspace_bytes": (ctypes.c_size_t, [CacheDesc, _I, _I, _I]),
+    "pkv_paged_attention_sparse": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _P, _P, _I,
+                                        _I, _I, ctypes.c_float, _P, ctypes.c_size_t, _P]),
     "pkv_tree_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I]),
     "pkv_paged_attention_tree": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _P, _I, _I,
                                       _I, _P, _I, _I, ctypes.c_float, _P, ctypes.c_size_t, _P]),
@@ -186,13 +199,20 @@ def _stream(stream):
 _FP8_DTYPES = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
 
 
+# head_dim of a 4-bit pool by its last extent, 9 * head_dim / 16 bytes
+_FP4_HEAD_DIM = {72: 128, 144: 256}
+
+
 def cache_desc(k_cache: torch.Tensor) -> CacheDesc:
-    """Geometry of a [num_blocks, Hk, B, D] pool tensor."""
+    """Geometry of a [num_blocks, Hk, B, D] pool tensor, or of a 4-bit one
+    (uint8 [num_blocks, Hk, B, 9 D / 16])."""
     if k_cache.dim() != 4:
         raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
     nb, hk, bs, d = k_cache.shape
     if k_cache.dtype == torch.bfloat16:
         dt = PKV_DTYPE_BF16
+    elif k_cache.dtype == torch.uint8 and d in _FP4_HEAD_DIM:
+        dt, d = PKV_DTYPE_FP4_E2M1, _FP4_HEAD_DIM[d]
     elif k_cache.dtype in _FP8_DTYPES:
         dt = PKV_DTYPE_FP8_E4M3
     else:
@@ -200,11 +220,28 @@ def cache_desc(k_cache: torch.Tensor) -> CacheDesc:
     return CacheDesc(nb, bs, hk, d, dt)
 
 
+def fp4_cache(num_blocks, num_kv_heads, block_size, head_dim, device=None) -> torch.Tensor:
+    """An empty (zeroed) 4-bit pool: K and V take one each."""
+    if head_dim not in _FP4_HEAD_DIM.values():
+        raise ValueError("head_dim must be 128 or 256")
+    return torch.zeros((num_blocks, num_kv_heads, block_size, head_dim // 16 * 9),
+                       dtype=torch.uint8, device=device or "cuda")
+
+
 def kv_cache_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None,
                    stream=None) -> None:
     """Scatter k, v [T, Hk, D] bf16 into their slots (bit-exact for bf16;
-    E4M3 round-to-nearest-even with saturation of x / scale[h] for FP8)."""
+    E4M3 round-to-nearest-even with saturation of x / scale[h] for FP8; E2M1
+    with an E4M3 scale for every 16 channels of x / scale[h] for 4-bit pools)."""
     desc = cache_desc(k_cache)
+    if desc.dtype == PKV_DTYPE_FP4_E2M1:
+        dev, n, kp, vp, slots, kc, vc, ks, vs = _row_args(k, v, slot_mapping, k_cache, v_cache,
+                                                          k_scale, v_scale, desc)
+        with _at(dev, stream) as raw:
+            rc = lib().pkv_kv_cache_write(kp, vp, slots, n, kc, vc, desc, ks, vs, raw)
+        if rc:
+            _check(rc, "kv_cache_write")
+        return
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must match")
     n = int(slot_mapping.shape[0])
@@ -217,6 +254,43 @@ def kv_cache_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=N
         _dev_ptr(k_scale, "k_scale", torch.float32), _dev_ptr(v_scale, "v_scale", torch.float32),
         _stream(stream))
     _check(rc, "kv_cache_write")
+
+
+def _row_args(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, desc):
+    """Checks of a call that moves rows in or out of a cache: (device index,
+    number of rows, addresses of k, v, slots, pools, scales)."""
+    dev = k_cache.get_device()
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    n = slot_mapping.shape[0]
+    rows, scales, pool = (n, desc.num_kv_heads, desc.head_dim), (desc.num_kv_heads,), k_cache.shape
+    dt = (k_cache.dtype,)
+    return (dev, n, _ptr(k, "k", dev, _BF16, rows), _ptr(v, "v", dev, _BF16, rows),
+            _ptr(slot_mapping, "slot_mapping", dev, _I64), _ptr(k_cache, "k_cache", dev, dt),
+            _ptr(v_cache, "v_cache", dev, dt, pool),
+            _ptr(k_scale, "k_scale", dev, _F32, scales),
+            _ptr(v_scale, "v_scale", dev, _F32, scales))
+
+
+def kv_cache_read(slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, k=None, v=None,
+                  stream=None):
+    """The rows that the slots hold, as bf16: (k, v) [T, Hk, D], zeros for a
+    slot of -1 (see the C header). k and v are allocated if not given."""
+    desc = cache_desc(k_cache)
+    dev, n, kp, vp, slots, kc, vc, ks, vs = _row_args(k, v, slot_mapping, k_cache, v_cache,
+                                                      k_scale, v_scale, desc)
+    with _at(dev, stream) as raw:
+        shape = (n, desc.num_kv_heads, desc.head_dim)
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+            kp = k.data_ptr()
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+            vp = v.data_ptr()
+        rc = lib().pkv_kv_cache_read(kp, vp, slots, n, kc, vc, desc, ks, vs, raw)
+    if rc:
+        _check(rc, "kv_cache_read")
+    return k, v
 
 
 def decode_workspace_bytes(num_seqs, num_heads, head_dim, max_context, partition_size) -> int:
@@ -299,8 +373,18 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, scale, max_
                     stream=None, seq_order=None) -> torch.Tensor:
     """Decode attention in one C call: the one-pass decode, or the split
     decode followed by the merge of its partitions. Returns out [S, Hq, D]
-    bf16. seq_order as for paged_attention_decode."""
+    bf16. partition_size: 0 = one pass, None = the library's choice
+    (decode_partition_size). seq_order as for paged_attention_decode."""
     desc = cache_desc(k_cache)
+    if partition_size is None:
+        partition_size = _decode_partition(desc.num_blocks, desc.num_kv_heads, desc.head_dim,
+                                           desc.block_size, desc.dtype, q.shape[0], max_context)
+        if partition_size < 0:
+            _check(partition_size, "decode_partition_size")
+    if desc.dtype == PKV_DTYPE_FP4_E2M1:
+        return _paged_attention_fp4(q, k_cache, v_cache, block_tables, context_lens, scale,
+                                    max_context, partition_size, k_scale, v_scale, out, workspace,
+                                    stream, seq_order)
     S, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -490,6 +574,8 @@ def _pool_ptrs(pools, name, index, like):
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_I8 = (torch.int8,)
 _MASK = (torch.int64,) + ((torch.uint64,) if hasattr(torch, "uint64") else ())
 _CACHE = (torch.bfloat16,) + _FP8_DTYPES
 
@@ -609,8 +695,164 @@ def paged_attention_window(q, k_cache, v_cache, block_tables, context_lens, scal
     return out
 
 
+def decode_partition_size(num_seqs, num_kv_heads, head_dim, block_size, max_context,
+                          dtype=PKV_DTYPE_BF16) -> int:
+    """The library's choice of partition_size for paged_attention over a pool
+    of the given PKV_DTYPE_* (0 = one pass)."""
+    rc = lib().pkv_decode_partition_size(
+        CacheDesc(1, int(block_size), int(num_kv_heads), int(head_dim), int(dtype)),
+        int(num_seqs), int(max_context))
+    if rc < 0:
+        _check(rc, "decode_partition_size")
+    return int(rc)
+
+
+def _paged_attention_fp4(q, k_cache, v_cache, block_tables, context_lens, scale, max_context,
+                         partition_size, k_scale, v_scale, out, workspace, stream, seq_order):
+    """paged_attention over 4-bit pools."""
+    L = _lib or lib()
+    desc, shape, dev, S, op, qp, kp, vp, ks, vs, tables, lens = _attention_args(
+        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, True, out)
+    order = _ptr(seq_order, "seq_order", dev, _I32, (S,))
+    with _at(dev, stream) as raw:
+        if out is None:
+            out = torch.empty_like(q)
+            op = out.data_ptr()
+        need = 0 if partition_size == 0 or workspace is not None else _decode_need(
+            S, shape[1], desc.head_dim, max_context, partition_size)
+        with _Scratch(workspace, need, dev, raw) as (ws, wsb):
+            rc = L.pkv_paged_attention(
+                op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, S, shape[1],
+                max_context, scale, partition_size, ws, wsb, order, raw)
+    if rc:
+        _check(rc, "paged_attention")
+    return out
+
+
+def block_bounds(bounds, k_cache, block_tables, context_lens, step, max_new=1, num_new=None,
+                 k_scale=None, stream=None) -> None:
+    """The lowest and the highest cached K of every channel of the blocks that
+    hold each sequence's last max_new tokens (num_new[s] of them, int32 [S], if
+    given), into bounds int8 [num_blocks, Hk, 2, D] in whole steps of step[h]
+    (float32 [Hk]); see the C header. select_blocks reads them."""
+    L = _lib or lib()
+    desc, dev = cache_desc(k_cache), k_cache.get_device()
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    S, heads = block_tables.shape[0], (desc.num_kv_heads,)
+    bp = _ptr(bounds, "bounds", dev, _I8,
+              (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim))
+    kp = _ptr(k_cache, "k_cache", dev, (k_cache.dtype,))
+    ks = _ptr(k_scale, "k_scale", dev, _F32, heads)
+    st = _ptr(step, "step", dev, _F32, heads)
+    tables = _ptr(block_tables, "block_tables", dev, _I32)
+    lens = _ptr(context_lens, "context_lens", dev, _I32, (S,))
+    new = _ptr(num_new, "num_new", dev, _I32, (S,))
+    with _at(dev, stream) as raw:
+        rc = L.pkv_block_bounds(bp, kp, desc, ks, st, tables, block_tables.shape[1], lens, new,
+                                max_new, S, raw)
+    if rc:
+        _check(rc, "block_bounds")
+
+
+def select_blocks(q, bounds, block_tables, context_lens, block_size, max_context, max_selected,
+                  first=1, last=1, blocks=None, counts=None, workspace=None, stream=None):
+    """For each sequence and KV head the max_selected blocks of its context with
+    the highest bounds of the logits of q [S, Hq, D], the first `first` and the
+    last `last` ones always among them (see the C header); bounds as block_bounds
+    leaves them. Returns (blocks int32 [S, Hk, max_selected], ascending, -1 behind
+    the last; counts int32 [S, Hk]), allocated if not given, for
+    paged_attention_sparse."""
+    L = _lib or lib()
+    if bounds.dim() != 4 or bounds.shape[2] != 2:
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_dim]")
+    nb, hk, _, d = bounds.shape
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError("q must be [rows, num_heads, %d]" % d)
+    if block_tables.dim() != 2 or block_tables.shape[0] != shape[0]:
+        raise ValueError("block_tables must be [S, max_blocks], q [S, num_heads, head_dim]")
+    S, dev = shape[0], q.get_device()
+    qp = _ptr(q, "q", dev, _BF16)
+    bp = _ptr(bounds, "bounds", dev, _I8)
+    tables = _ptr(block_tables, "block_tables", dev, _I32)
+    lens = _ptr(context_lens, "context_lens", dev, _I32, (S,))
+    lp = _ptr(blocks, "blocks", dev, _I32, (S, hk, max_selected))
+    cp = _ptr(counts, "counts", dev, _I32, (S, hk))
+    desc = CacheDesc(nb, block_size, hk, d, PKV_DTYPE_BF16)
+    with _at(dev, stream) as raw:
+        if blocks is None:
+            if max_selected < 1:
+                _check(PKV_ERR_INVALID_ARG, "select_blocks")
+            blocks = torch.empty((S, hk, max_selected), dtype=torch.int32, device=q.device)
+            lp = blocks.data_ptr()
+        if counts is None:
+            counts = torch.empty((S, hk), dtype=torch.int32, device=q.device)
+            cp = counts.data_ptr()
+        need = _select_need(S, hk, block_size, max_context) if workspace is None else 0
+        with _Scratch(workspace, need, dev, raw) as (ws, wsb):
+            rc = L.pkv_select_blocks(lp, cp, qp, bp, desc, tables, block_tables.shape[1], lens, S,
+                                     shape[1], max_context, max_selected, first, last, ws, wsb,
+                                     raw)
+    if rc:
+        _check(rc, "select_blocks")
+    return blocks, counts
+
+
+def select_workspace_bytes(num_seqs, num_kv_heads, block_size, max_context) -> int:
+    return int(lib().pkv_select_workspace_bytes(num_seqs, num_kv_heads, block_size, max_context))
+
+
+def sparse_workspace_bytes(k_cache, num_seqs, num_heads, max_selected) -> int:
+    return int(lib().pkv_sparse_workspace_bytes(cache_desc(k_cache), num_seqs, num_heads,
+                                                max_selected))
+
+
+def paged_attention_sparse(q, k_cache, v_cache, block_tables, context_lens, blocks, counts, scale,
+                           k_scale=None, v_scale=None, out=None, workspace=None,
+                           stream=None) -> torch.Tensor:
+    """Decode attention over listed blocks (see the C header): query head j of
+    sequence s, KV head h, sees the cached tokens of the logical blocks
+    blocks[s, h, :counts[s, h]] (int32 [S, Hk, M] and [S, Hk], from
+    select_blocks or any other source; a block listed twice counts twice).
+    bf16, FP8 and 4-bit pools. Returns out [S, Hq, D] bf16; out and workspace
+    are allocated if not given."""
+    L = _lib or lib()
+    desc, shape, dev, S, op, qp, kp, vp, ks, vs, tables, lens = _attention_args(
+        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, True, out)
+    hk = desc.num_kv_heads
+    if blocks.dim() != 3:
+        raise ValueError("blocks must be [S, num_kv_heads, max_selected]")
+    M = blocks.shape[2]
+    lp = _ptr(blocks, "blocks", dev, _I32, (S, hk, M))
+    cp = _ptr(counts, "counts", dev, _I32, (S, hk))
+    with _at(dev, stream) as raw:
+        if out is None:
+            out = torch.empty_like(q)
+            op = out.data_ptr()
+        need = _sparse_need(desc.num_blocks, hk, desc.head_dim, desc.block_size, desc.dtype, S,
+                            shape[1], M) if workspace is None else 0
+        with _Scratch(workspace, need, dev, raw) as (ws, wsb):
+            rc = L.pkv_paged_attention_sparse(
+                op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, lp, cp, M, S,
+                shape[1], scale, ws, wsb, raw)
+    if rc:
+        _check(rc, "paged_attention_sparse")
+    return out
+
+
 # Functions of their sizes alone, asked for at every call (a call into the
 # library is 1 us).
+_decode_partition = functools.lru_cache(1024)(
+    lambda nb, hk, d, b, dtype, *rest: lib().pkv_decode_partition_size(
+        CacheDesc(nb, b, hk, d, dtype), *rest))
+_decode_need = functools.lru_cache(1024)(
+    lambda *sizes: lib().pkv_decode_workspace_bytes(*sizes))
+_select_need = functools.lru_cache(1024)(
+    lambda *sizes: lib().pkv_select_workspace_bytes(*sizes))
+_sparse_need = functools.lru_cache(1024)(
+    lambda nb, hk, d, b, dtype, *rest: lib().pkv_sparse_workspace_bytes(
+        CacheDesc(nb, b, hk, d, dtype), *rest))
 _window_partition = functools.lru_cache(1024)(
     lambda *sizes: lib().pkv_window_partition_size(*sizes))
 _window_need = functools.lru_cache(1024)(lambda *sizes: lib().pkv_window_workspace_bytes(*sizes))

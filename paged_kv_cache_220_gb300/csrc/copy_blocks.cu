@@ -52,14 +52,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(
 extern "C" int pkv_copy_blocks(void* k_cache, void* v_cache, pkv_cache_desc cache,
                                const int32_t* block_pairs, int num_pairs, void* stream) {
   using namespace pkv;
-  int rc = check_cache_desc(cache);
+  int rc = check_cache_desc(cache, true);
   if (rc != PKV_OK) return rc;
   if (num_pairs < 0) return PKV_ERR_INVALID_ARG;
   if (num_pairs == 0) return PKV_OK;
   if (!k_cache || !v_cache || !block_pairs) return PKV_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
-  const int64_t block_bytes = static_cast<int64_t>(cache.num_kv_heads) * cache.block_size *
-                              cache.head_dim * elem_bytes(cache.dtype);
+  const int64_t block_bytes = cache.num_kv_heads * page_bytes(cache);
   const int64_t block_vecs = block_bytes / 16;
   const int chunks = static_cast<int>((block_vecs + kCopyChunkVec - 1) / kCopyChunkVec);
   dim3 grid(num_pairs, 2, chunks);

@@ -33,6 +33,15 @@ extern "C" size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int he
   return static_cast<size_t>(num_seqs) * num_heads * np * (head_dim + 2) * sizeof(float);
 }
 
+extern "C" int pkv_decode_partition_size(pkv_cache_desc cache, int num_seqs, int max_context) {
+  using namespace pkv;
+  const int rc = check_cache_desc(cache, true);
+  if (rc != PKV_OK) return rc;
+  // a window as wide as the context
+  return pkv_window_partition_size(num_seqs, cache.num_kv_heads, cache.head_dim,
+                                   cache.block_size, max_context, std::max(1, max_context), 0);
+}
+
 extern "C" int pkv_split_partition_size(int max_context, int block_size, int partition_size) {
   if (block_size <= 0 || partition_size <= 0 || partition_size % block_size != 0)
     return PKV_ERR_INVALID_ARG;
@@ -66,7 +75,7 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
                                           size_t workspace_bytes, const int32_t* seq_order,
                                           void* stream) {
   using namespace pkv;
-  int rc = check_cache_desc(cache);
+  int rc = check_cache_desc(cache, true);
   if (rc != PKV_OK) return rc;
   if (num_seqs < 0 || num_heads <= 0 || max_context < 0 || max_blocks_per_seq <= 0 ||
       partition_size < 0)
@@ -81,7 +90,11 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
   if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
   const bool fp8 = cache.dtype == PKV_DTYPE_FP8_E4M3;
-  if (fp8 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+  const bool fp4 = cache.dtype == PKV_DTYPE_FP4_E2M1;
+  if ((fp8 || fp4) && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+  // positions are 32-bit numbers in the 4-bit kernel
+  if (fp4 && static_cast<int64_t>(max_blocks_per_seq) * cache.block_size > (1 << 30))
+    return PKV_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
 
   DecodeParams p{};
@@ -130,6 +143,7 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
     grid.x = np;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (fp4) return launch_attention_simple(p, cache, grid, st);
   if (static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads * cache.block_size >=
       (int64_t{1} << 31))
     return PKV_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit

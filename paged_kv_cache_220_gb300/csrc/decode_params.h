@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/pagedkv.h"
+
 namespace pkv {
 
 struct DecodeParams {
@@ -42,6 +44,11 @@ struct DecodeParams {
   // the windowed form only (launch_decode_window): each query sees the last
   // `window` tokens of its context and the first `sinks` ones
   int window, sinks;
+  // the forms over listed blocks only: [S][Hk][max_selected] logical blocks and
+  // [S][Hk] how many of them
+  const int32_t* list;
+  const int32_t* counts;
+  int max_selected;
 };
 
 // The blocks of a context that a window and its sink tokens touch, in order:
@@ -78,6 +85,9 @@ int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_c
 // The same for the windowed form; the partitions are runs of visible blocks.
 int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
                          int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
+
+int launch_attention_simple(const DecodeParams& p, const pkv_cache_desc& cache, dim3 grid,
+                            cudaStream_t st);
 
 // Merge of split partials (reduce.cu). With prefix_blocks == NULL the slots of
 // sequence s are [0, ceil(ctx/P)); otherwise [0, npre) and [slot_split,

@@ -25,24 +25,33 @@ inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes
 
 inline int elem_bytes(int dtype) { return dtype == PKV_DTYPE_FP8_E4M3 ? 1 : 2; }
 
-// Shape checks common to every call that touches a pool.
-inline int check_cache_desc(const pkv_cache_desc& c) {
+// Bytes of one (block, head) page: 2, 1 or 9/16 an element.
+inline int64_t page_bytes(const pkv_cache_desc& c) {
+  const int64_t n = static_cast<int64_t>(c.block_size) * c.head_dim;
+  return c.dtype == PKV_DTYPE_FP4_E2M1 ? n / 16 * 9 : c.dtype == PKV_DTYPE_FP8_E4M3 ? n : 2 * n;
+}
+
+// Shape checks common to every call that touches a pool; fp4: the call takes
+// 4-bit pools too.
+inline int check_cache_desc(const pkv_cache_desc& c, bool fp4 = false) {
   if (c.num_blocks <= 0 || c.num_kv_heads <= 0 || c.block_size <= 0 || c.head_dim <= 0)
     return PKV_ERR_INVALID_ARG;
-  if (c.dtype != PKV_DTYPE_BF16 && c.dtype != PKV_DTYPE_FP8_E4M3) return PKV_ERR_INVALID_ARG;
+  if (c.dtype != PKV_DTYPE_BF16 && c.dtype != PKV_DTYPE_FP8_E4M3 &&
+      !(fp4 && c.dtype == PKV_DTYPE_FP4_E2M1))
+    return PKV_ERR_INVALID_ARG;
   if (c.block_size != 16 && c.block_size != 32) return PKV_ERR_UNSUPPORTED;
   if (c.head_dim != 128 && c.head_dim != 256) return PKV_ERR_UNSUPPORTED;
   if (c.num_kv_heads > 32) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
 
-// Checks common to the window and the tree call; *group receives num_heads / num_kv_heads.
+// Checks common to the window, tree and sparse calls; *group receives num_heads / num_kv_heads.
 inline int check_attention(const pkv_cache_desc& cache, const void* out, const void* q,
                       const void* k_cache, const void* v_cache, const float* k_scale,
                       const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
                       const int32_t* context_lens, int num_seqs, int num_heads, int max_context,
-                      float scale, int* group) {
-  int rc = check_cache_desc(cache);
+                      float scale, int* group, bool fp4 = false) {
+  int rc = check_cache_desc(cache, fp4);
   if (rc != PKV_OK) return rc;
   if (num_seqs < 0 || num_heads <= 0 || max_context < 0 || max_blocks_per_seq <= 0)
     return PKV_ERR_INVALID_ARG;
@@ -63,7 +72,7 @@ inline int check_attention(const pkv_cache_desc& cache, const void* out, const v
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
     return PKV_ERR_INVALID_ARG;
-  if (cache.dtype == PKV_DTYPE_FP8_E4M3 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+  if (cache.dtype != PKV_DTYPE_BF16 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
   return PKV_OK;
 }
 

@@ -11,6 +11,7 @@
 // (fp8) store each, so a token's row of a head is a coalesced 256/512-byte
 // access. The work is a few hundred kilobytes per step; it is latency-bound.
 #include "common.cuh"
+#include "fp4.cuh"
 #include "host_util.h"
 
 namespace pkv {
@@ -69,6 +70,79 @@ __global__ void __launch_bounds__(1024) kv_cache_write_kernel(
   }
 }
 
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Eight channels of a row -> their codes (a word) and the scale of their 16; the
+// lane next to this one has the group's other eight.
+__device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, uint8_t& s_code) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float y[8];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = __fdiv_rn((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale);
+    a = max_nan(a, fabsf(y[i]));
+  }
+  a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  s_code = static_cast<uint8_t>(
+      __nv_cvt_float_to_fp8(__fdiv_rn(a, 6.f), __NV_SATFINITE, __NV_E4M3));
+  const float s = e4m3_f32(s_code);
+  if (!(s > 0.f)) return 0;  // zero or NaN
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    codes |= e2m1x2_of(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * i);
+  return codes;
+}
+
+// 4-bit pools: thread (h, c8) has channels [8*c8, 8*c8+8) of a row; two threads
+// share a scale. Every warp has a whole row of a head (D = 256) or two (128).
+template <int D>
+__global__ void __launch_bounds__(1024) kv_cache_write_fp4_kernel(
+    const uint4* __restrict__ k, const uint4* __restrict__ v,
+    const int64_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_cache,
+    uint8_t* __restrict__ v_cache, int num_blocks, int block_size, int num_kv_heads,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale, int* err) {
+  allow_dependents();
+  const int token = blockIdx.x;
+  const int64_t slot = slot_mapping[token];
+  if (slot < 0) return;
+  if (slot >= static_cast<int64_t>(num_blocks) * block_size) {
+    if (threadIdx.x == 0) report_error(err, PKV_DEVERR_SLOT);
+    return;
+  }
+  // blockDim.x is a multiple of a row's threads; whole rows fall out, so the
+  // two lanes of a group stay together (a warp's idle half at D = 128 takes
+  // part in the shuffle with zeros)
+  const int h = threadIdx.x / (D / 8);
+  const int c8 = threadIdx.x % (D / 8);
+  const bool live = h < num_kv_heads;
+  const int64_t blk = slot / block_size;
+  const int off = static_cast<int>(slot % block_size);
+  const int64_t page = (blk * num_kv_heads + h) * (block_size * (D / 16 * 9));
+  const int64_t src = (static_cast<int64_t>(token) * num_kv_heads + h) * (D / 8) + c8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 kv = live ? k[src] : zero;
+  const uint4 vv = live ? v[src] : zero;
+  uint8_t ks, vs;
+  const uint32_t kc = quantize_fp4(kv, live ? k_scale[h] : 1.f, ks);
+  const uint32_t vc = quantize_fp4(vv, live ? v_scale[h] : 1.f, vs);
+  if (!live) return;
+  const int64_t codes = page + fp4_codes_at<D>(off) + 4 * c8;
+  *reinterpret_cast<uint32_t*>(k_cache + codes) = kc;
+  *reinterpret_cast<uint32_t*>(v_cache + codes) = vc;
+  if ((c8 & 1) == 0) {
+    const int64_t scales = page + fp4_scales_at<D>(off) + c8 / 2;
+    k_cache[scales] = ks;
+    v_cache[scales] = vs;
+  }
+}
+
 }  // namespace pkv
 
 extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* slot_mapping,
@@ -76,7 +150,7 @@ extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* s
                                   pkv_cache_desc cache, const float* k_scale,
                                   const float* v_scale, void* stream) {
   using namespace pkv;
-  int rc = check_cache_desc(cache);
+  int rc = check_cache_desc(cache, true);
   if (rc != PKV_OK) return rc;
   if (num_tokens < 0) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;
@@ -84,7 +158,8 @@ extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* s
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
     return PKV_ERR_INVALID_ARG;
   const bool fp8 = cache.dtype == PKV_DTYPE_FP8_E4M3;
-  if (fp8 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+  const bool fp4 = cache.dtype == PKV_DTYPE_FP4_E2M1;
+  if ((fp8 || fp4) && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
   const int threads = cache.num_kv_heads * (cache.head_dim / 8);
   if (threads > 1024) return PKV_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -92,7 +167,12 @@ extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* s
             hd = cache.head_dim;
   auto* kc = static_cast<uint8_t*>(k_cache);
   auto* vc = static_cast<uint8_t*>(v_cache);
-  if (fp8)
+  if (fp4) {
+    auto kern = hd == 256 ? kv_cache_write_fp4_kernel<256> : kv_cache_write_fp4_kernel<128>;
+    kern<<<num_tokens, (threads + 31) / 32 * 32, 0, st>>>(
+        static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, kc, vc, nb, bs,
+        hk, k_scale, v_scale, device_error_ptr());
+  } else if (fp8)
     kv_cache_write_kernel<true><<<num_tokens, threads, 0, st>>>(
         static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, kc, vc, nb,
         bs, hk, hd, k_scale, v_scale, device_error_ptr());

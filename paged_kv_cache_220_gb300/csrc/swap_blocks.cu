@@ -58,15 +58,14 @@ __global__ void __launch_bounds__(kSwapThreads) swap_blocks_kernel(
 template <bool OUT>
 int launch_swap(void* k_cache, void* v_cache, const pkv_cache_desc& cache, const int32_t* blocks,
                 int n, void* k_buf, void* v_buf, void* stream) {
-  int rc = check_cache_desc(cache);
+  int rc = check_cache_desc(cache, true);
   if (rc != PKV_OK) return rc;
   if (n < 0) return PKV_ERR_INVALID_ARG;
   if (n == 0) return PKV_OK;
   if (!k_cache || !v_cache || !blocks || !k_buf || !v_buf) return PKV_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_buf) || !aligned16(v_buf))
     return PKV_ERR_INVALID_ARG;
-  const int64_t block_bytes = static_cast<int64_t>(cache.num_kv_heads) * cache.block_size *
-                              cache.head_dim * elem_bytes(cache.dtype);
+  const int64_t block_bytes = cache.num_kv_heads * page_bytes(cache);
   const int64_t block_vecs = block_bytes / 16;
   const int chunks = static_cast<int>((block_vecs + kSwapChunkVec - 1) / kSwapChunkVec);
   dim3 grid(n, 2, chunks);
