@@ -143,7 +143,7 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
     grid.x = np;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (fp4) return launch_attention_simple(p, cache, grid, st);
+  if (fp4) return launch_decode_fp4(p, cache.head_dim, cache.block_size, grid, st);
   if (static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads * cache.block_size >=
       (int64_t{1} << 31))
     return PKV_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit

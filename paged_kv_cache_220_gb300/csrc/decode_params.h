@@ -86,6 +86,10 @@ int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_c
 int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
                          int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
 
+// 4-bit pools (decode_fp4.cu), the listed form too.
+int launch_decode_fp4(const DecodeParams& p, int head_dim, int block_size, dim3 grid,
+                      cudaStream_t st);
+
 int launch_attention_simple(const DecodeParams& p, const pkv_cache_desc& cache, dim3 grid,
                             cudaStream_t st);
 

@@ -51,5 +51,11 @@ extern "C" int pkv_paged_attention_sparse(
   p.list = blocks;
   p.counts = counts;
   p.max_selected = max_selected;
+  if (cache.dtype == PKV_DTYPE_FP4_E2M1) {
+    p.cluster = 8;
+    return launch_decode_fp4(p, cache.head_dim, cache.block_size,
+                             dim3(1, cache.num_kv_heads, num_seqs),
+                             static_cast<cudaStream_t>(stream));
+  }
   return launch_attention_simple(p, cache, dim3(1, 1, num_seqs), static_cast<cudaStream_t>(stream));
 }
