@@ -1,11 +1,13 @@
 // Attention of one query token per sequence over a 4-bit cache: over the whole
-// context (paged_attention_decode) or over listed blocks (paged_attention_sparse).
+// context (paged_attention_fp4) or over listed blocks (paged_attention_sparse).
 //
-// Every warp works alone on units of 32 tokens (one block, or two of 16 tokens):
-// lane 0 keeps a ring of their K and V in flight with bulk copies, one per block
-// and pool, a page's codes and scales being one contiguous run; the warps of a
-// CTA, and the CTAs of a cluster, are merged once at the end. Nothing is
-// exchanged per unit.
+// The batch's work is one line of units of tokens (TU = 64, 32 at D = 256), pair
+// (sequence, KV head) after pair, cut into equal shares, one per resident warp.
+// Every warp works alone: lane 0 keeps a ring of K and V of its next units in
+// flight with bulk copies, one per block and pool (a page's codes and scales are
+// one contiguous run), through the ends of pairs too. A pair inside a share is
+// written to the result; of a pair that is cut each warp leaves (maxima, sums,
+// output) in its slots, at most two, and a second kernel joins them.
 //
 // Arithmetic, with mma.m16n8k16 (f16 in, fp32 out): tokens are the M side of
 // S^T = K Q^T and the head's channels that of O^T = V^T P^T; the padded query
@@ -39,31 +41,55 @@
 
 namespace pkv {
 
-constexpr int kUnit = 32;               // tokens of a unit
-constexpr int kNoToken = 0x7F000000;    // first "token" of a block that is not there
-constexpr float kUpFp4 = 15.f;          // log2 of the factor on the weights
+constexpr float kUpFp4 = 15.f;    // log2 of the factor on the weights
+constexpr int kFp4Warps = 4;      // warps of a CTA
+constexpr int kFp4Ctas = 3;       // CTAs to an SM
+constexpr int kFp4Stages = 2;     // units in a warp's ring
+constexpr int kFp4MaxCtas = 456;  // of a launch: the residents of 152 SMs
 
-template <int D, int W, int NST>
+template <int D>
 struct Fp4Geom {
-  static constexpr int kBytes = kUnit * D / 16 * 9;  // K (or V) of a unit
+  static constexpr int TU = D == 256 ? 32 : 64;       // tokens of a unit
+  static constexpr int kBytes = TU * D / 16 * 9;      // K (or V) of a unit
   static constexpr int kStage = 2 * kBytes;
-  static constexpr int kRing = W * NST * kStage;
-  // merge: the warps' O, padded against bank conflicts, then the CTA's
-  static constexpr int kRow8 = D / 8 + 4;        // channels of one fragment row
-  static constexpr int kRowQ = 8 * kRow8 + 8;    // of one query
-  static constexpr int kMerge = (W * 8 * kRowQ + 8 * D) * 4;
-  static constexpr int kHead = 1024;  // barriers, units' blocks, maxima and sums
-  static constexpr int kSmem = kHead + (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kThreads = W * 32;
-  static_assert(W * NST * (16 + 16) + W * 64 + 64 <= kHead, "head of the shared memory");
+  static constexpr int kThreads = kFp4Warps * 32;
+  // barriers, the rows' first units by thread, the look-up cursors
+  static constexpr int kHead = kFp4Warps * kFp4Stages * 16 + (kThreads + 4) * 4 + kFp4Warps * 16;
+  static constexpr int kRingAt = (kHead + 127) / 128 * 128;
+  static constexpr int kSmem = kRingAt + kFp4Warps * kFp4Stages * kStage;
+  // a slot: O as the lanes hold it, [D/16][32] float4, then 8 maxima (base 2) and 8 sums
+  static constexpr int kSlot = 8 * D + 16;            // floats
 };
+
+struct Fp4Params {
+  const uint16_t* q;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* list;     // the listed form: [S][Hk][max_selected], [S][Hk]
+  const int32_t* counts;
+  uint16_t* out;
+  int32_t* first;          // first unit of every row (sequence, or pair if listed), and the end
+  float* slots;            // [workers][2][kSlot]
+  int* err;
+  int num_seqs, num_blocks, num_kv_heads, group, max_blocks_per_seq;
+  int max_context, max_selected;
+  int workers;             // warps of the launch
+  float qscale;            // scale * log2(e)
+};
+
+// First unit of worker w of n, T units in all.
+__device__ __forceinline__ int share_begin(int w, int n, int T) {
+  return static_cast<int>(static_cast<int64_t>(w) * T / n);
+}
 
 // One contiguous run of global memory into shared memory; evict-first in L2, a
 // page is read once.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  uint64_t policy;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+                                          uint64_t* bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
@@ -99,211 +125,268 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
-// (x.lo, x.lo) and (x.hi, x.hi)
-__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, 0, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, 0, 0x3232); }
+// Two E4M3 codes (the low or the high 16 bits of w) as f16x2
+__device__ __forceinline__ __half2 scales_of(uint32_t w, int hi) {
+  const uint32_t d = e4m3x2_f16x2(w, hi);
+  return *reinterpret_cast<const __half2*>(&d);
+}
 
-template <int D, int BS, bool LIST, int W, int NST>
-__global__ void __launch_bounds__(W * 32, (D == 256 ? 12 : 16) / W)
-    decode_fp4_kernel(const DecodeParams p) {
-  using G = Fp4Geom<D, W, NST>;
-  constexpr int UB = kUnit / BS;          // blocks of a unit
+template <int D, int BS, bool LIST>
+__global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
+    decode_fp4_kernel(const Fp4Params p) {
+  using G = Fp4Geom<D>;
+  constexpr int TU = G::TU, W = kFp4Warps, NST = kFp4Stages, THREADS = G::kThreads;
+  constexpr int UB = TU / BS;             // blocks of a unit
+  constexpr int NT = TU / 16;             // 16-token tiles of a unit
   constexpr int PAGE = BS * D / 16 * 9;   // bytes of a block's page
   constexpr int KW = D / 16;              // k-steps of S, row tiles of O
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem_raw);       // [W][NST]
-  uint64_t* vfull = kfull + W * NST;                             // [W][NST]
-  int4* meta = reinterpret_cast<int4*>(vfull + W * NST);         // [W][NST] block, first token; twice
-  float* sm_m = reinterpret_cast<float*>(meta + W * NST);        // [W][8]
-  float* sm_l = sm_m + W * 8;                                    // [W][8]
-  uint8_t* ring_p = smem_raw + G::kHead;
-  const uint32_t ring = smem_addr(ring_p);
-
-  const int part = blockIdx.x;
-  const int h = blockIdx.y;
+  uint64_t* my_k = reinterpret_cast<uint64_t*>(smem_raw) + (threadIdx.x >> 5) * NST;
+  uint64_t* my_v = my_k + W * NST;
+  int* pre = reinterpret_cast<int*>(smem_raw + W * NST * 16);  // [THREADS + 4]
+  int4* my_cursor = reinterpret_cast<int4*>(pre + THREADS + 4) + (threadIdx.x >> 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   if (lane == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&kfull[warp * NST + i], 1);
-      mbar_init(&vfull[warp * NST + i], 1);
+      mbar_init(&my_k[i], 1);
+      mbar_init(&my_v[i], 1);
     }
     fence_mbar_init();
   }
-  __syncwarp();
   wait_prerequisite();
-  int s = static_cast<int>(blockIdx.z);
-  if (p.seq_order != nullptr) {
-    s = p.seq_order[blockIdx.z];
-    if (s < 0 || s >= static_cast<int>(gridDim.z)) {
-      if (threadIdx.x == 0 && part == 0 && h == 0) report_error(p.err, PKV_DEVERR_ORDER);
-      return;
-    }
-  }
-  const int g = p.group;
-  int ctx = p.context_lens[s];
-  const int cap = p.max_blocks_per_seq * BS;
-  if (ctx < 0 || ctx > cap) {
-    if (threadIdx.x == 0 && part == 0 && h == 0) report_error(p.err, PKV_DEVERR_CONTEXT);
-    ctx = ctx < 0 ? 0 : cap;
-  }
-  // the run [b0, b1) of the context's blocks, or of the list's entries
-  const int nctx = (ctx + BS - 1) / BS;
-  int b0 = 0, b1 = nctx;
-  const int32_t* list = nullptr;
-  if constexpr (LIST) {
-    const int64_t row = static_cast<int64_t>(s) * p.num_kv_heads + h;
-    list = p.list + row * p.max_selected;
-    b1 = p.counts[row];
-    if (b1 < 0 || b1 > p.max_selected) {
-      if (threadIdx.x == 0 && part == 0) report_error(p.err, PKV_DEVERR_SELECT);
-      b1 = b1 < 0 ? 0 : p.max_selected;
-    }
-  }
-  if (p.partition_blocks > 0) {
-    b0 = part * p.partition_blocks;
-    if (b0 >= b1) return;  // a partition past the end: nothing to store
-    b1 = min(b1, b0 + p.partition_blocks);
-  } else if (p.cluster > 1) {
-    const int share = (b1 + p.cluster - 1) / p.cluster;
-    b0 = min(b1, part * share);
-    b1 = min(b1, b0 + share);
-  }
-  const int units = (b1 - b0 + UB - 1) / UB;
-  const int mine = units > warp ? (units - warp + W - 1) / W : 0;  // units of this warp
-  const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
+  const int Hk = p.num_kv_heads, g = p.group;
 
-  // ---- lanes look up the blocks of the warp's next 32 / UB units together
-  constexpr int kBatch = 32 / UB;
-  auto look_up = [&](int batch, int& pb, int& tok) {
-    const int i = batch * kBatch + lane / UB;
-    const int v = b0 + UB * (warp + W * i) + lane % UB;
-    pb = -1;
-    tok = kNoToken;
-    if (i >= mine || v >= b1) return;
-    const int b = LIST ? list[v] : v;
-    if (LIST && (b < 0 || b >= nctx)) {
-      report_error(p.err, PKV_DEVERR_SELECT);
-      return;
-    }
-    const int32_t x = table[b];
-    if (x < 0 || x >= p.num_blocks) {
-      report_error(p.err, PKV_DEVERR_BLOCK_ID);
-      return;
-    }
-    pb = x;
-    tok = b * BS;
+  // ---- the line of units: rows are sequences (all heads alike) or, listed, pairs
+  auto context = [&](int s) {
+    const int ctx = p.context_lens[s];
+    if (ctx >= 0 && ctx <= p.max_context) return ctx;
+    report_error(p.err, PKV_DEVERR_CONTEXT);
+    return ctx < 0 ? 0 : p.max_context;
   };
-  int pb_now, tok_now, pb_next = -1, tok_next = kNoToken;
-  look_up(0, pb_now, tok_now);
-  if (mine > kBatch) look_up(1, pb_next, tok_next);
-  uint64_t* my_k = kfull + warp * NST;
-  uint64_t* my_v = vfull + warp * NST;
-  int4* my_meta = meta + warp * NST;
-  const uint32_t my_ring = ring + warp * NST * G::kStage;
-  auto load = [&](uint32_t dst, const uint8_t* pool, const int4& m, uint64_t* bar) {
-    const int n = (m.x >= 0 ? 1 : 0) + (UB == 2 && m.z >= 0 ? 1 : 0);
-    if (n == 0) {
-      mbar_arrive(bar);
-      return;
-    }
-    mbar_arrive_expect_tx(bar, n * PAGE);
-    if (m.x >= 0)
-      bulk_load(dst, pool + (static_cast<int64_t>(m.x) * p.num_kv_heads + h) * PAGE, PAGE, bar);
-    if (UB == 2 && m.z >= 0)
-      bulk_load(dst + PAGE, pool + (static_cast<int64_t>(m.z) * p.num_kv_heads + h) * PAGE, PAGE,
-                bar);
+  // blocks of a pair of the row: the context's or the list's
+  auto blocks_of = [&](int row) {
+    if (!LIST) return (context(row) + BS - 1) / BS;
+    const int n = p.counts[row];
+    if (n >= 0 && n <= p.max_selected) return n;
+    report_error(p.err, PKV_DEVERR_SELECT);
+    return n < 0 ? 0 : p.max_selected;
   };
-  // K of unit i into its slot, and what the unit is; all lanes
-  auto load_k = [&](int i) {
-    if (i >= mine) return;
-    const int at = i % kBatch * UB;
-    if (at == 0 && i > 0) {
-      pb_now = pb_next;
-      tok_now = tok_next;
-      if (i + kBatch < mine) look_up(i / kBatch + 1, pb_next, tok_next);
-    }
-    int4 m;
-    m.x = __shfl_sync(0xffffffffu, pb_now, at);
-    m.y = __shfl_sync(0xffffffffu, tok_now, at);
-    m.z = UB == 2 ? __shfl_sync(0xffffffffu, pb_now, at + UB - 1) : -1;
-    m.w = UB == 2 ? __shfl_sync(0xffffffffu, tok_now, at + UB - 1) : kNoToken;
-    if (lane == 0) {
-      my_meta[i % NST] = m;
-      load(my_ring + i % NST * G::kStage, p.k_cache, m, &my_k[i % NST]);
-    }
-  };
-  // its V; after load_k of the same unit
-  auto load_v = [&](int i) {
-    if (i < mine && lane == 0)
-      load(my_ring + i % NST * G::kStage + G::kBytes, p.v_cache, my_meta[i % NST], &my_v[i % NST]);
-  };
-  for (int i = 0; i < NST; ++i) {
-    load_k(i);
-    load_v(i);
-  }
-
-  // ---- Q^T fragments: lane (n = r, c) has channels D/4 c + 4 j + {0, 1} and {2, 3}
-  // of query n for k-step j, as f16, in units of a power of two of its row
-  uint32_t bq[KW][2];
-  float f0, f1;  // logit factors of queries 2c, 2c + 1 (base 2)
+  const int rows = LIST ? p.num_seqs * Hk : p.num_seqs;
+  const int per_row = LIST ? 1 : Hk;                       // pairs of a row
+  const int chunk = (rows + THREADS - 1) / THREADS;        // rows of a thread
+  int T = 0;
   {
-    const uint2* qrow = reinterpret_cast<const uint2*>(
-        p.q + (static_cast<int64_t>(s) * p.num_heads + h * g + r) * D + D / 4 * c);
-    float top = 0.f;
+    const int row0 = min(rows, static_cast<int>(threadIdx.x) * chunk);
+    const int row1 = min(rows, row0 + chunk);
+    int sum = 0;
+    for (int row = row0; row < row1; ++row) sum += per_row * ((blocks_of(row) + UB - 1) / UB);
+    int incl = sum;
 #pragma unroll
-    for (int j = 0; j < KW; ++j) {
-      const uint2 w = r < g ? __ldg(qrow + j) : make_uint2(0, 0);
-      bq[j][0] = w.x;
-      bq[j][1] = w.y;
-      top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x))),
-                             fmaxf(fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y)))));
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
     }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
-    const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-    const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+    if (lane == 31) pre[THREADS + warp] = incl;
+    __syncthreads();
+    int before = 0;
 #pragma unroll
-    for (int j = 0; j < KW; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        bq[j][i] = pack_f16(bf16lo(bq[j][i]) * down, bf16hi(bq[j][i]) * down);
-    const float qs = p.qscale * p.k_scale[h];
-    f0 = qs * __shfl_sync(0xffffffffu, up, 8 * c);
-    f1 = qs * __shfl_sync(0xffffffffu, up, 8 * c + 4);
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) before += pre[THREADS + w];
+      T += pre[THREADS + w];
+    }
+    int at = before + incl - sum;
+    pre[threadIdx.x] = at;
+    if (blockIdx.x == 0) {
+      for (int row = row0; row < row1; ++row) {
+        p.first[row] = at;
+        at += per_row * ((blocks_of(row) + UB - 1) / UB);
+      }
+      if (threadIdx.x == 0) p.first[rows] = T;
+    }
+    __syncthreads();
   }
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  float o[KW][4];
+  // the merge launched next may be scheduled; it waits for this grid's end
+  allow_dependents();
+  const int n_workers = min(p.workers, T);
+  const int me = blockIdx.x + gridDim.x * warp;  // neighbours on different SMs
+  if (me >= n_workers) return;
+  const int u0 = share_begin(me, n_workers, T);
+  const int mine = share_begin(me + 1, n_workers, T) - u0;  // units of this warp, one at least
+  // the pair and unit that u0 is
+  int pair, unit, units;
+  {
+    int t = 0;
 #pragma unroll
-  for (int k = 0; k < KW; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+    for (int k = 0; k < W; ++k)
+      t += __popc(__ballot_sync(0xffffffffu, pre[k * 32 + lane] <= u0));
+    int row = (t - 1) * chunk;
+    int left = u0 - pre[t - 1];
+    for (;; ++row) {
+      units = (blocks_of(row) + UB - 1) / UB;
+      if (left < per_row * units) break;
+      left -= per_row * units;
+    }
+    pair = row * per_row + left / units;
+    unit = left % units;
+  }
+
+  // ---- look-ups: lanes look up the blocks of the next units of one pair, 32 / UB at
+  // most, together: lane l block l % UB of unit l / UB. pb: the block, -1 if there
+  // is none; vis: how many tokens of each of the unit's blocks are visible, a byte
+  // each. The cursor: pair, its next unit, its units, units left for this warp
+  constexpr int kBatch = 32 / UB;
+  constexpr uint32_t kWhole = BS * (UB == 1 ? 1u : UB == 2 ? 0x0101u : 0x01010101u);
+  if (lane == 0) *my_cursor = make_int4(pair, unit, units, mine);
+  __syncwarp();
+  auto look_up = [&](int& pb, uint32_t& vis) {  // -> units looked up
+    int4 u = *my_cursor;
+    pb = -1;
+    vis = 0;
+    if (u.w == 0) return 0;
+    while (u.y == u.z) {  // the next pair that has a unit
+      ++u.x;
+      u.y = 0;
+      u.z = (blocks_of(LIST ? u.x : u.x / Hk) + UB - 1) / UB;
+    }
+    const int n = min(min(kBatch, u.z - u.y), u.w);
+    const int s = u.x / Hk;
+    const int ctx = context(s);
+    const int v = UB * (u.y + lane / UB) + lane % UB;
+    if (lane / UB < n && v < (LIST ? blocks_of(u.x) : (ctx + BS - 1) / BS)) {
+      const int b = LIST ? p.list[static_cast<int64_t>(u.x) * p.max_selected + v] : v;
+      if (LIST && (b < 0 || b >= (ctx + BS - 1) / BS)) {
+        report_error(p.err, PKV_DEVERR_SELECT);
+      } else {
+        const int32_t x = p.block_tables[static_cast<int64_t>(s) * p.max_blocks_per_seq + b];
+        if (x < 0 || x >= p.num_blocks) {
+          report_error(p.err, PKV_DEVERR_BLOCK_ID);
+        } else {
+          pb = x * Hk + u.x % Hk;  // the page
+          vis = static_cast<uint32_t>(min(BS, ctx - b * BS)) << (8 * (lane % UB));
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) *my_cursor = make_int4(u.x, u.y + n, u.z, u.w - n);
+    __syncwarp();
+#pragma unroll
+    for (int off = 1; off < UB; off <<= 1) vis |= __shfl_xor_sync(0xffffffffu, vis, off);
+    return n;
+  };
+  int pb_now, pb_next;
+  uint32_t vis_now, vis_next;
+  int n_now = look_up(pb_now, vis_now);
+  int n_next = look_up(pb_next, vis_next);
+  int at = 0;  // units of the current batch that are loaded
+  const uint32_t my_ring = smem_addr(smem_raw) + G::kRingAt + warp * NST * G::kStage;
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  // the unit whose K was loaded last (its V comes next)
+  int ids[UB];
+  uint32_t vis[NST] = {};  // of the units in the ring, the oldest first
+  auto load = [&](uint32_t dst, const uint8_t* pool, uint64_t* bar) {
+    if (lane != 0) return;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int b = 0; b < UB; ++b) bytes += ids[b] >= 0 ? PAGE : 0;
+    mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int b = 0; b < UB; ++b)
+      if (ids[b] >= 0)
+        bulk_load(dst + b * PAGE, pool + static_cast<uint64_t>(ids[b]) * PAGE, PAGE, bar, policy);
+  };
+  // K of the next unit into slot st
+  auto load_k = [&](int st) {
+    if (at == n_now) {
+      pb_now = pb_next;
+      vis_now = vis_next;
+      n_now = n_next;
+      n_next = look_up(pb_next, vis_next);
+      at = 0;
+    }
+#pragma unroll
+    for (int b = 0; b < UB; ++b) ids[b] = __shfl_sync(0xffffffffu, pb_now, at * UB + b);
+    vis[NST - 1] = __shfl_sync(0xffffffffu, vis_now, at * UB);
+    ++at;
+    load(my_ring + st * G::kStage, p.k_cache, &my_k[st]);
+  };
+  auto load_v = [&](int st) { load(my_ring + st * G::kStage + G::kBytes, p.v_cache, &my_v[st]); };
+#pragma unroll
+  for (int i = 0; i < NST; ++i) {
+#pragma unroll
+    for (int k = 0; k + 1 < NST; ++k) vis[k] = vis[k + 1];
+    if (i < mine) load_k(i);
+    if (i < mine && i + 1 < NST) load_v(i);
+  }
+
+  // ---- the pair at hand: units of it that are left, whether it is this warp's alone
+  int seg = min(units - unit, mine);
+  bool alone = unit == 0 && seg == units;
+  int slot = 0;
+  bool fresh = true;
+  uint32_t bq[KW][2];
+  float f0 = 0.f, f1 = 0.f;  // logit factors of queries 2c, 2c + 1 (base 2), not negative
+  // running maxima of the products before their factor, sums, outputs
+  float m0, m1, l0, l1;
+  float o[KW][4];
   // token of the unit that row x of tile t stands for
   auto token = [](int t, int x) {
     return 16 * t + (D == 256 ? x : ((x & 7) >> 1) * 4 + (x & 1) + (x >= 8 ? 2 : 0));
   };
-
   int done = 0;          // units done
   bool v_late = false;  // the wait that ran out, if one did, was V's
+  int st = 0;
+  uint32_t parity = 0;
   for (; done < mine; ++done) {
-    const int i = done, st = i % NST;
-    const uint32_t parity = (i / NST) & 1;
+    if (fresh) {
+      fresh = false;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+      // Q^T fragments: lane (n = r, c) has channels D/4 c + 4 j + {0, 1} and {2, 3} of
+      // query n for k-step j, as f16, in units of a power of two of its row, with
+      // the logit factor's sign
+      const uint2* qrow = reinterpret_cast<const uint2*>(
+          p.q + (static_cast<int64_t>(pair) * g + r) * D + D / 4 * c);
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {
+        const uint2 w = r < g ? __ldg(qrow + j) : make_uint2(0, 0);
+        bq[j][0] = w.x;
+        bq[j][1] = w.y;
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x))),
+                               fmaxf(fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y)))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float qs = p.qscale * p.k_scale[pair % Hk];
+      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+      const float down = copysignf(__uint_as_float(static_cast<uint32_t>(254 - e) << 23), qs);
+      const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+      for (int j = 0; j < KW; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          bq[j][i] = pack_f16(bf16lo(bq[j][i]) * down, bf16hi(bq[j][i]) * down);
+      f0 = fabsf(qs) * __shfl_sync(0xffffffffu, up, 8 * c);
+      f1 = fabsf(qs) * __shfl_sync(0xffffffffu, up, 8 * c + 4);
+    }
     if (!__all_sync(0xffffffffu, mbar_wait(&my_k[st], parity, p.err))) break;
-    const int4 m = my_meta[st];
     const uint32_t kp = my_ring + st * G::kStage, vp = kp + G::kBytes;
-    // visible tokens of the unit's blocks
-    const int n0 = ctx - m.y, n1 = UB == 2 ? ctx - m.w : 0;
-    const bool whole = n0 >= BS && (UB == 1 || n1 >= BS);
-    auto sees = [&](int t) { return UB == 1 || t < BS ? t < n0 : t - BS < n1; };
+    const uint32_t seen = vis[0];
+    const bool whole = seen == kWhole;
+    auto sees = [&](int t) { return t % BS < static_cast<int>(seen >> (8 * (t / BS)) & 0xFFu); };
 
     // ---- S^T = K Q^T
-    float sc[2][4];
+    float sc[NT][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NT; ++t) {
       constexpr int NW = D / 32;  // words of codes of a lane and row
       uint32_t wa[NW], wb[NW], sa, sb;
       const int ta = token(t, r), tb = token(t, r + 8);
@@ -325,50 +408,55 @@ __global__ void __launch_bounds__(W * 32, (D == 256 ? 12 : 16) / W)
         sa = lds16(kp + fp4_scales_at<D>(ta) + 2 * c);
         sb = lds16(kp + fp4_scales_at<D>(tb) + 2 * c);
       }
-      float u[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+      sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
         // two words (16 channels) to a scale
         const int gr = x / 2;
-        const uint32_t pa = e4m3x2_f16x2(sa, gr / 2), pb = e4m3x2_f16x2(sb, gr / 2);
-        const uint32_t fa = gr & 1 ? dup_hi(pa) : dup_lo(pa);
-        const uint32_t fb = gr & 1 ? dup_hi(pb) : dup_lo(pb);
+        const __half2 pa = scales_of(sa, gr / 2), pb = scales_of(sb, gr / 2);
+        const __half2 fa = gr & 1 ? __high2half2(pa) : __low2half2(pa);
+        const __half2 fb = gr & 1 ? __high2half2(pb) : __low2half2(pb);
         uint32_t a[4], b[4];
         e2m1x8_f16x2(wa[x], a);
         e2m1x8_f16x2(wb[x], b);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          a[y] = mul_f16x2(a[y], fa);
-          b[y] = mul_f16x2(b[y], fb);
-        }
-        mma_f16(u, a[0], b[0], a[1], b[1], bq[2 * x][0], bq[2 * x][1]);
-        mma_f16(v, a[2], b[2], a[3], b[3], bq[2 * x + 1][0], bq[2 * x + 1][1]);
+        for (int y = 0; y < 2; ++y)
+          mma_f16(sc[t], mul_f16x2(a[2 * y], fa), mul_f16x2(b[2 * y], fb),
+                  mul_f16x2(a[2 * y + 1], fa), mul_f16x2(b[2 * y + 1], fb), bq[2 * x + y][0],
+                  bq[2 * x + y][1]);
       }
-      const bool see_a = whole || sees(ta), see_b = whole || sees(tb);
-      sc[t][0] = see_a ? (u[0] + v[0]) * f0 : -INFINITY;
-      sc[t][1] = see_a ? (u[1] + v[1]) * f1 : -INFINITY;
-      sc[t][2] = see_b ? (u[2] + v[2]) * f0 : -INFINITY;
-      sc[t][3] = see_b ? (u[3] + v[3]) * f1 : -INFINITY;
+    }
+    if (!whole) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (!sees(token(t, r))) sc[t][0] = sc[t][1] = -INFINITY;
+        if (!sees(token(t, r + 8))) sc[t][2] = sc[t][3] = -INFINITY;
+      }
     }
     // ---- online softmax: rows are tokens, columns queries
-    float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
-    float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+    float x0 = m0, x1 = m1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      x0 = fmaxf(x0, fmaxf(sc[t][0], sc[t][2]));
+      x1 = fmaxf(x1, fmaxf(sc[t][1], sc[t][3]));
+    }
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
       x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
     }
-    // Every lane's logits have met in the shuffles, so every lane has read this
+    // Every lane's products have met in the shuffles, so every lane has read this
     // unit's K, and (loads of a warp return in order) the unit before's V: both
-    // slots take the next unit's
+    // slots can take their next unit's
     __syncwarp();
-    load_k(i + NST);
-    if (i > 0) load_v(i - 1 + NST);
-    const float y0 = fmaxf(m0, x0), y1 = fmaxf(m1, x1);
-    if (__any_sync(0xffffffffu, y0 > m0 || y1 > m1)) {
-      // 0 where the maximum was -inf, 1 where it stays that
-      const float c0 = y0 > m0 ? fast_exp2(m0 - y0) : 1.f;
-      const float c1 = y1 > m1 ? fast_exp2(m1 - y1) : 1.f;
+    if (done + NST - 1 < mine) load_v(st == 0 ? NST - 1 : st - 1);
+#pragma unroll
+    for (int k = 0; k + 1 < NST; ++k) vis[k] = vis[k + 1];
+    if (done + NST < mine) load_k(st);
+    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+      // nothing has been summed where the maximum was -inf
+      const float c0 = m0 == -INFINITY ? 0.f : fast_exp2((m0 - x0) * f0);
+      const float c1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - x1) * f1);
       l0 *= c0;
       l1 *= c1;
 #pragma unroll
@@ -378,23 +466,37 @@ __global__ void __launch_bounds__(W * 32, (D == 256 ? 12 : 16) / W)
         o[k][2] *= c0;
         o[k][3] *= c1;
       }
-      m0 = y0;
-      m1 = y1;
+      m0 = x0;
+      m1 = x1;
     }
-    const float ref0 = (m0 == -INFINITY ? 0.f : m0) - kUpFp4;
-    const float ref1 = (m1 == -INFINITY ? 0.f : m1) - kUpFp4;
+    const float ref0 = kUpFp4 - (m0 == -INFINITY ? 0.f : m0 * f0);
+    const float ref1 = kUpFp4 - (m1 == -INFINITY ? 0.f : m1 * f1);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      sc[t][0] = fast_exp2(fmaf(sc[t][0], f0, ref0));
+      sc[t][1] = fast_exp2(fmaf(sc[t][1], f1, ref1));
+      sc[t][2] = fast_exp2(fmaf(sc[t][2], f0, ref0));
+      sc[t][3] = fast_exp2(fmaf(sc[t][3], f1, ref1));
+    }
+    if (!whole) {
+      // (a factor of 0 makes the -inf a NaN)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (!sees(token(t, r))) sc[t][0] = sc[t][1] = 0.f;
+        if (!sees(token(t, r + 8))) sc[t][2] = sc[t][3] = 0.f;
+      }
+    }
     if (!__all_sync(0xffffffffu, mbar_wait(&my_v[st], parity, p.err))) {
       v_late = true;
       break;
     }
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float p00 = fast_exp2(sc[t][0] - ref0), p01 = fast_exp2(sc[t][1] - ref1);
-      const float p10 = fast_exp2(sc[t][2] - ref0), p11 = fast_exp2(sc[t][3] - ref1);
-      l0 += p00 + p10;
-      l1 += p01 + p11;
-      const uint32_t q0 = movm_t(pack_f16(p00, p01)), q1 = movm_t(pack_f16(p10, p11));
+    for (int t = 0; t < NT; ++t) {
+      l0 += sc[t][0] + sc[t][2];
+      l1 += sc[t][1] + sc[t][3];
+      const uint32_t q0 = movm_t(pack_f16(sc[t][0], sc[t][1]));
+      const uint32_t q1 = movm_t(pack_f16(sc[t][2], sc[t][3]));
       constexpr int NW = D / 64;  // words of codes of a lane and token
       uint32_t w[4][NW], e8[4];
 #pragma unroll
@@ -409,14 +511,18 @@ __global__ void __launch_bounds__(W * 32, (D == 256 ? 12 : 16) / W)
           w[k][0] = a.x, w[k][1] = a.y;
           e8[k] = lds8(vp + fp4_scales_at<D>(tk) + r);
         }
-        if (!whole && !sees(tk)) e8[k] = 0;
+      }
+      if (!whole) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (!sees(token(t, 2 * c + (k & 1) + (k >= 2 ? 8 : 0)))) e8[k] = 0;
       }
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
         // the word's scale: byte x / 2 of each token's
         const uint32_t sel = x / 2 ? 0x51 : 0x40;
-        const uint32_t s01 = e4m3x2_f16x2(__byte_perm(e8[0], e8[1], sel), 0);
-        const uint32_t s23 = e4m3x2_f16x2(__byte_perm(e8[2], e8[3], sel), 0);
+        const __half2 s01 = scales_of(__byte_perm(e8[0], e8[1], sel), 0);
+        const __half2 s23 = scales_of(__byte_perm(e8[2], e8[3], sel), 0);
         constexpr uint32_t kLow = 0x0F0F0F0Fu;
         uint32_t ev01[4], od01[4], ev23[4], od23[4];
         e2m1x8_f16x2((w[0][x] & kLow) | ((w[1][x] << 4) & ~kLow), ev01);
@@ -429,166 +535,328 @@ __global__ void __launch_bounds__(W * 32, (D == 256 ? 12 : 16) / W)
                   mul_f16x2(ev23[y], s23), mul_f16x2(od23[y], s23), q0, q1);
       }
     }
+    if (++st == NST) {
+      st = 0;
+      parity ^= 1;
+    }
+    if (--seg > 0) continue;
+    // ---- the pair's end, or the share's
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    if (alone) {
+      const float vsc = p.v_scale[pair % Hk];
+      const float i0 = l0 != 0.f ? vsc / l0 : 0.f, i1 = l1 != 0.f ? vsc / l1 : 0.f;
+      uint16_t* dst = p.out + (static_cast<int64_t>(pair) * g + 2 * c) * D + D / 8 * r;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        if (2 * c < g)
+          *reinterpret_cast<uint32_t*>(dst + 2 * k) =
+              pack_bf16(o[k][0] * i0, o[k][2] * i0);
+        if (2 * c + 1 < g)
+          *reinterpret_cast<uint32_t*>(dst + D + 2 * k) =
+              pack_bf16(o[k][1] * i1, o[k][3] * i1);
+      }
+    } else {
+      float* dst = p.slots + (static_cast<int64_t>(me) * 2 + slot) * G::kSlot;
+      if (2 * c < g) {
+#pragma unroll
+        for (int k = 0; k < KW; ++k)
+          reinterpret_cast<float4*>(dst)[k * 32 + lane] =
+              make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+      }
+      if (lane < 4) {
+        // the maxima as base-2 logits
+        *reinterpret_cast<float2*>(dst + 8 * D + 2 * c) =
+            make_float2(m0 == -INFINITY ? m0 : m0 * f0, m1 == -INFINITY ? m1 : m1 * f1);
+        *reinterpret_cast<float2*>(dst + 8 * D + 8 + 2 * c) = make_float2(l0, l1);
+      }
+    }
+    fresh = true;
+    slot = 1;
+    if (done + 1 < mine) {
+      do {
+        ++pair;
+        units = (blocks_of(LIST ? pair : pair / Hk) + UB - 1) / UB;
+      } while (units == 0);
+      seg = min(units, mine - done - 1);
+      alone = seg == units;
+    }
   }
   if (done < mine && lane == 0) {
-    // a wait ran out: what is in flight has to land before the ring is used again
+    // a wait ran out: what is in flight has to land before the CTA's memory goes
     const int nk = min(mine, done + NST + (v_late ? 1 : 0));
-    const int nv = min(mine, done + NST - (v_late || done == 0 ? 0 : 1));
+    const int nv = min(mine, done + NST - (v_late ? 0 : 1));
     for (int i = max(done, nk - NST); i < nk; ++i)
       (void)mbar_wait(&my_k[i % NST], (i / NST) & 1, p.err);
     for (int i = max(done, nv - NST); i < nv; ++i)
       (void)mbar_wait(&my_v[i % NST], (i / NST) & 1, p.err);
   }
-#pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-  }
-  if (lane < 4) {
-    sm_m[warp * 8 + 2 * c] = m0;
-    sm_m[warp * 8 + 2 * c + 1] = m1;
-    sm_l[warp * 8 + 2 * c] = l0;
-    sm_l[warp * 8 + 2 * c + 1] = l1;
-  }
-  __syncthreads();
-  // the merge launched next may be scheduled; it waits for this grid's end
-  allow_dependents();
+}
 
-  // ---- the warps' states become the CTA's: sums over the warps in their order
-  float* os = reinterpret_cast<float*>(ring_p);       // [W][8][kRowQ]
-  float* cs_o = os + W * 8 * G::kRowQ;                // [8][D]
-  {
-    float t0 = sm_m[2 * c], t1 = sm_m[2 * c + 1];
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-      t0 = fmaxf(t0, sm_m[w * 8 + 2 * c]);
-      t1 = fmaxf(t1, sm_m[w * 8 + 2 * c + 1]);
+// The pairs that several warps had parts of: out = sum_i e_i O_i / sum_i e_i l_i with e_i
+// = 2^(m_i - max m). A CTA of 16 warps has 16 / SPLIT of the slots' D/16 pieces of a
+// pair, SPLIT warps to a piece: all pieces in one CTA where there are many pairs,
+// one piece (SPLIT = 16) where few pairs have many parts.
+constexpr int kMergeWarps = 16;
+
+template <int D, int SPLIT, bool LIST>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    merge_fp4_kernel(uint16_t* __restrict__ out, const int32_t* __restrict__ first,
+                     const float* __restrict__ slots, const float* __restrict__ v_scale,
+                     int num_rows, int Hk, int g, int workers) {
+  using G = Fp4Geom<D>;
+  constexpr int U = 8;  // parts of a warp whose loads are in flight together
+  extern __shared__ float weights[];  // [n][8]
+  __shared__ float4 acc_sh[kMergeWarps][32];
+  __shared__ float inv_sum[8];
+  wait_prerequisite();
+  const int pair = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const int piece = (blockIdx.y * kMergeWarps + warp) / SPLIT, split = warp % SPLIT;
+  const int T = first[num_rows];
+  int u, units;
+  if (LIST) {
+    u = first[pair];
+    units = first[pair + 1] - u;
+  } else {
+    const int s = pair / Hk;
+    u = first[s];
+    units = (first[s + 1] - u) / Hk;
+    u += pair % Hk * units;
+  }
+  uint16_t* dst = out + (static_cast<int64_t>(pair) * g + 2 * c) * D + D / 8 * r + 2 * piece;
+  if (units == 0) {
+    if (split == 0) {
+      if (2 * c < g) *reinterpret_cast<uint32_t*>(dst) = 0u;
+      if (2 * c + 1 < g) *reinterpret_cast<uint32_t*>(dst + D) = 0u;
     }
-    const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - t0);
-    const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - t1);
-    float* d0 = os + (warp * 8 + 2 * c) * G::kRowQ + r * G::kRow8;
-    float* d1 = d0 + G::kRowQ;
+    return;
+  }
+  const int nw = min(workers, T);
+  // the worker that has unit x: the last whose first one is not behind it
+  auto worker_of = [&](int x) {
+    return static_cast<int>((static_cast<int64_t>(x + 1) * nw - 1) / T);
+  };
+  const int w0 = worker_of(u), n = worker_of(u + units - 1) - w0 + 1;
+  if (n == 1) return;  // written already
+  const int slot0 = share_begin(w0, nw, T) != u ? 1 : 0;  // of the first; the others' is 0
+  auto part = [&](int i) {
+    return slots + (static_cast<int64_t>(w0 + i) * 2 + (i == 0 ? slot0 : 0)) * G::kSlot;
+  };
+  if (warp < 8) {
+    // query `warp`'s weights, lane i the parts i, i + 32, ..
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[8 * D + warp]);
 #pragma unroll
-    for (int k = 0; k < KW; ++k) {
-      *reinterpret_cast<float2*>(d0 + 2 * k) = make_float2(o[k][0] * a0, o[k][2] * a0);
-      *reinterpret_cast<float2*>(d1 + 2 * k) = make_float2(o[k][1] * a1, o[k][3] * a1);
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float* x = part(i);
+      const float m = x[8 * D + warp];
+      const float e = m == -INFINITY ? 0.f : fast_exp2(m - M);
+      weights[i * 8 + warp] = e;
+      L = fmaf(e, x[8 * D + 8 + warp], L);
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (lane == 0) inv_sum[warp] = L != 0.f ? v_scale[pair % Hk] / L : 0.f;
   }
   __syncthreads();
-  const float vsc = p.v_scale[h];
-  const int64_t hq0 = static_cast<int64_t>(s) * p.num_heads + h * g;
-  // query j's maximum and sum over the warps
-  auto state = [&](int j, float& M, float& L) {
-    M = sm_m[j];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool live = 2 * c < g;
+  for (int i0 = split; i0 < n; i0 += U * SPLIT) {
+    float4 x[U];
 #pragma unroll
-    for (int w = 1; w < W; ++w) M = fmaxf(M, sm_m[w * 8 + j]);
-    L = 0.f;
-    if (M != -INFINITY)
+    for (int k = 0; k < U; ++k)
+      x[k] = live && i0 + k * SPLIT < n
+                 ? reinterpret_cast<const float4*>(part(i0 + k * SPLIT))[piece * 32 + lane]
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) L = fmaf(sm_l[w * 8 + j], fast_exp2(sm_m[w * 8 + j] - M), L);
-  };
-  for (int idx = threadIdx.x; idx < g * (D / 2); idx += G::kThreads) {
-    const int j = idx / (D / 2), col = idx % (D / 2) * 2;
-    const int at = j * G::kRowQ + col / (D / 8) * G::kRow8 + col % (D / 8);
-    float2 sum = *reinterpret_cast<const float2*>(os + at);
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-      const float2 x = *reinterpret_cast<const float2*>(os + w * 8 * G::kRowQ + at);
-      sum.x += x.x;
-      sum.y += x.y;
-    }
-    if (p.cluster > 1) {
-      *reinterpret_cast<float2*>(cs_o + j * D + col) = sum;
-      continue;
-    }
-    float M, L;
-    state(j, M, L);
-    const float ox = L > 0.f ? sum.x / L * vsc : 0.f, oy = L > 0.f ? sum.y / L * vsc : 0.f;
-    if (p.partition_blocks == 0) {
-      *reinterpret_cast<uint32_t*>(p.out + (hq0 + j) * D + col) = pack_bf16(ox, oy);
-    } else {
-      const int64_t slot = (hq0 + j) * p.np_max + part;
-      *reinterpret_cast<float2*>(p.tmp_out + slot * D + col) = make_float2(ox, oy);
-      if (col == 0) {
-        // the sums have the weights' factor; the merge only compares them
-        p.max_logits[slot] = M * kLn2Tc;
-        p.exp_sums[slot] = L;
-      }
+    for (int k = 0; k < U; ++k) {
+      if (i0 + k * SPLIT >= n) continue;
+      const float2 e = *reinterpret_cast<const float2*>(&weights[(i0 + k * SPLIT) * 8 + 2 * c]);
+      acc.x = fmaf(e.x, x[k].x, acc.x);
+      acc.y = fmaf(e.y, x[k].y, acc.y);
+      acc.z = fmaf(e.x, x[k].z, acc.z);
+      acc.w = fmaf(e.y, x[k].w, acc.w);
     }
   }
-  if (p.cluster <= 1) return;
-  // ---- the CTAs of the cluster: rank k has channels [k D/C, (k + 1) D/C) of the
-  // result, from every rank's state in rank order
-  float* cs_m = sm_m + 2 * W * 8;  // [8]
-  float* cs_l = cs_m + 8;          // [8]
-  if (threadIdx.x < 8) state(threadIdx.x, cs_m[threadIdx.x], cs_l[threadIdx.x]);
-  cluster_sync_all();
-  const int C = p.cluster, SL = D / C;
-  const uint32_t o_addr = smem_addr(cs_o), m_addr = smem_addr(cs_m), l_addr = smem_addr(cs_l);
-  for (int idx = threadIdx.x; idx < g * SL; idx += G::kThreads) {
-    const int j = idx / SL, col = part * SL + idx % SL;
-    float M = -INFINITY;
-    for (int k = 0; k < C; ++k) M = fmaxf(M, ld_dsmem(m_addr + 4 * j, k));
-    float L = 0.f, O = 0.f;
-    if (M != -INFINITY) {
-      for (int k = 0; k < C; ++k) {
-        const float a = fast_exp2(ld_dsmem(m_addr + 4 * j, k) - M);
-        L = fmaf(ld_dsmem(l_addr + 4 * j, k), a, L);
-        O = fmaf(ld_dsmem(o_addr + 4 * (j * D + col), k), a, O);
-      }
+  if constexpr (SPLIT > 1) {
+    acc_sh[warp][lane] = acc;
+    __syncthreads();
+    if (split != 0) return;
+#pragma unroll
+    for (int k = 1; k < SPLIT; ++k) {
+      const float4 x = acc_sh[warp + k][lane];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
     }
-    p.out[(hq0 + j) * D + col] = float_to_bf16_bits(L > 0.f ? O / L * vsc : 0.f);
   }
-  cluster_sync_all();  // this CTA's state lives until every rank has read it
+  const float i0 = inv_sum[2 * c], i1 = inv_sum[2 * c + 1];
+  if (2 * c < g) *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc.x * i0, acc.z * i0);
+  if (2 * c + 1 < g) *reinterpret_cast<uint32_t*>(dst + D) = pack_bf16(acc.y * i1, acc.w * i1);
+}
+
+// CTAs of a launch over at most `bound` units: residents of 152 SMs, no more
+// than one to a unit.
+static int fp4_ctas(int64_t bound) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(bound, kFp4MaxCtas)));
+}
+
+// Units of all pairs at most.
+static int64_t fp4_units(const pkv_cache_desc& cache, int64_t pairs, int64_t blocks) {
+  const int64_t ub = (cache.head_dim == 256 ? 32 : 64) / cache.block_size;
+  return pairs * ((blocks + ub - 1) / ub);
+}
+
+size_t fp4_workspace_bytes(const pkv_cache_desc& cache, int num_seqs, int64_t blocks,
+                           bool listed) {
+  const int64_t pairs = static_cast<int64_t>(num_seqs) * cache.num_kv_heads;
+  const int64_t rows = listed ? pairs : num_seqs;
+  const int64_t workers =
+      static_cast<int64_t>(fp4_ctas(fp4_units(cache, pairs, blocks))) * kFp4Warps;
+  // first units (padded to 16 bytes), then the slots
+  return static_cast<size_t>((rows + 1 + 3) / 4 * 16 +
+                             workers * 2 * (8 * cache.head_dim + 16) * 4);
 }
 
 template <int D, int BS, bool LIST>
-static int launch_fp4(const DecodeParams& p_in, dim3 grid, cudaStream_t st) {
-  constexpr int W = 4, NST = D == 256 ? 2 : 3;
-  using G = Fp4Geom<D, W, NST>;
-  auto kern = decode_fp4_kernel<D, BS, LIST, W, NST>;
-  static DeviceFlags done;
+static int launch_fp4(Fp4Params p, int64_t bound, void* workspace, cudaStream_t st) {
+  using G = Fp4Geom<D>;
+  const int ctas = fp4_ctas(bound);
+  const int rows = LIST ? p.num_seqs * p.num_kv_heads : p.num_seqs;
+  const int pairs = p.num_seqs * p.num_kv_heads;
+  p.workers = ctas * kFp4Warps;
+  p.first = static_cast<int32_t*>(workspace);
+  p.slots = reinterpret_cast<float*>(p.first + (rows + 1 + 3) / 4 * 4);
+  static DeviceFlags done, done_merge;
+  auto kern = decode_fp4_kernel<D, BS, LIST>;
   int rc = ensure_smem(kern, G::kSmem, done);
   if (rc != PKV_OK) return rc;
-  DecodeParams p = p_in;
-  if (p.partition_blocks > 0 || p.cluster <= 1) {
-    p.cluster = 1;
-    return launch_dependent(kern, grid, dim3(G::kThreads), G::kSmem, st, p);
+  rc = launch_dependent(kern, dim3(ctas), dim3(G::kThreads), G::kSmem, st, p);
+  if (rc != PKV_OK) return rc;
+  // a pair has at most all workers' parts
+  const size_t smem = static_cast<size_t>(p.workers) * 8 * sizeof(float);
+  constexpr size_t kMaxSmem = static_cast<size_t>(kFp4MaxCtas) * kFp4Warps * 8 * sizeof(float);
+  if (pairs < 152) {
+    auto wide = merge_fp4_kernel<D, kMergeWarps, LIST>;
+    static DeviceFlags done_wide;
+    rc = ensure_smem(wide, kMaxSmem, done_wide);
+    if (rc != PKV_OK) return rc;
+    return launch_dependent(wide, dim3(pairs, D / 16), dim3(kMergeWarps * 32), smem, st, p.out,
+                            static_cast<const int32_t*>(p.first),
+                            static_cast<const float*>(p.slots), p.v_scale, rows, p.num_kv_heads,
+                            p.group, p.workers);
   }
-  grid.x = p.cluster;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(G::kThreads);
-  cfg.dynamicSmemBytes = G::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  // clusters of up to 8 CTAs are portable
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_status();
+  auto merge = merge_fp4_kernel<D, kMergeWarps * 16 / D, LIST>;
+  rc = ensure_smem(merge, kMaxSmem, done_merge);
+  if (rc != PKV_OK) return rc;
+  return launch_dependent(merge, dim3(pairs), dim3(kMergeWarps * 32), smem, st, p.out,
+                          static_cast<const int32_t*>(p.first),
+                          static_cast<const float*>(p.slots), p.v_scale, rows, p.num_kv_heads,
+                          p.group, p.workers);
 }
 
-int launch_decode_fp4(const DecodeParams& p, int head_dim, int block_size, dim3 grid,
-                      cudaStream_t st) {
-  if (p.list != nullptr) {
-    if (head_dim == 256)
-      return block_size == 16 ? launch_fp4<256, 16, true>(p, grid, st)
-                              : launch_fp4<256, 32, true>(p, grid, st);
-    return block_size == 16 ? launch_fp4<128, 16, true>(p, grid, st)
-                            : launch_fp4<128, 32, true>(p, grid, st);
+int launch_decode_fp4(const DecodeParams& d, const pkv_cache_desc& cache, int num_seqs,
+                      int max_context, void* workspace, cudaStream_t st) {
+  Fp4Params p{};
+  p.q = d.q;
+  p.k_cache = d.k_cache;
+  p.v_cache = d.v_cache;
+  p.k_scale = d.k_scale;
+  p.v_scale = d.v_scale;
+  p.block_tables = d.block_tables;
+  p.context_lens = d.context_lens;
+  p.list = d.list;
+  p.counts = d.counts;
+  p.out = d.out;
+  p.err = d.err;
+  p.num_seqs = num_seqs;
+  p.num_blocks = d.num_blocks;
+  p.num_kv_heads = d.num_kv_heads;
+  p.group = d.group;
+  p.max_blocks_per_seq = d.max_blocks_per_seq;
+  p.max_context = max_context;
+  p.max_selected = d.max_selected;
+  p.qscale = d.qscale;
+  const bool listed = d.list != nullptr;
+  const int64_t blocks = listed ? d.max_selected
+                                : (static_cast<int64_t>(max_context) + cache.block_size - 1) /
+                                      cache.block_size;
+  const int64_t pairs = static_cast<int64_t>(num_seqs) * cache.num_kv_heads;
+  const int64_t bound = fp4_units(cache, pairs, blocks);
+  if (bound > INT32_MAX ||
+      static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
+  auto go = [&](auto one, auto two) { return cache.block_size == 16 ? one() : two(); };
+  if (listed) {
+    if (cache.head_dim == 256)
+      return go([&] { return launch_fp4<256, 16, true>(p, bound, workspace, st); },
+                [&] { return launch_fp4<256, 32, true>(p, bound, workspace, st); });
+    return go([&] { return launch_fp4<128, 16, true>(p, bound, workspace, st); },
+              [&] { return launch_fp4<128, 32, true>(p, bound, workspace, st); });
   }
-  if (head_dim == 256)
-    return block_size == 16 ? launch_fp4<256, 16, false>(p, grid, st)
-                            : launch_fp4<256, 32, false>(p, grid, st);
-  return block_size == 16 ? launch_fp4<128, 16, false>(p, grid, st)
-                          : launch_fp4<128, 32, false>(p, grid, st);
+  if (cache.head_dim == 256)
+    return go([&] { return launch_fp4<256, 16, false>(p, bound, workspace, st); },
+              [&] { return launch_fp4<256, 32, false>(p, bound, workspace, st); });
+  return go([&] { return launch_fp4<128, 16, false>(p, bound, workspace, st); },
+            [&] { return launch_fp4<128, 32, false>(p, bound, workspace, st); });
 }
 
 }  // namespace pkv
+
+extern "C" size_t pkv_fp4_workspace_bytes(pkv_cache_desc cache, int num_seqs, int max_context) {
+  using namespace pkv;
+  if (check_cache_desc(cache, true) != PKV_OK || cache.dtype != PKV_DTYPE_FP4_E2M1 ||
+      num_seqs <= 0 || max_context < 0)
+    return 0;
+  return fp4_workspace_bytes(
+      cache, num_seqs, (static_cast<int64_t>(max_context) + cache.block_size - 1) / cache.block_size,
+      false);
+}
+
+extern "C" int pkv_paged_attention_fp4(void* out, const void* q, const void* k_cache,
+                                       const void* v_cache, pkv_cache_desc cache,
+                                       const float* k_scale, const float* v_scale,
+                                       const int32_t* block_tables, int max_blocks_per_seq,
+                                       const int32_t* context_lens, int num_seqs, int num_heads,
+                                       int max_context, float scale, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  using namespace pkv;
+  if (cache.dtype != PKV_DTYPE_FP4_E2M1) return PKV_ERR_INVALID_ARG;
+  int g = 0;
+  const int rc = check_attention(cache, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                 max_blocks_per_seq, context_lens, num_seqs, num_heads,
+                                 max_context, scale, &g, true);
+  if (rc != PKV_OK) return rc;
+  if (num_seqs == 0) return PKV_OK;
+  const size_t q_bytes = static_cast<size_t>(num_seqs) * num_heads * cache.head_dim * 2;
+  if (overlap(out, q_bytes, q, q_bytes)) return PKV_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < pkv_fp4_workspace_bytes(cache, num_seqs, max_context))
+    return PKV_ERR_INVALID_ARG;
+  DecodeParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = static_cast<uint16_t*>(out);
+  p.err = device_error_ptr();
+  p.num_blocks = cache.num_blocks;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.num_heads = num_heads;
+  p.group = g;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.qscale = scale * 1.4426950408889634f;
+  return launch_decode_fp4(p, cache, num_seqs, max_context, workspace,
+                           static_cast<cudaStream_t>(stream));
+}

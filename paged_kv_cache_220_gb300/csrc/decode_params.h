@@ -86,9 +86,12 @@ int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_c
 int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
                          int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
 
-// 4-bit pools (decode_fp4.cu), the listed form too.
-int launch_decode_fp4(const DecodeParams& p, int head_dim, int block_size, dim3 grid,
-                      cudaStream_t st);
+// 4-bit pools (decode_fp4.cu), the listed form (p.list) too; the result goes to p.out.
+// fp4_workspace_bytes: `blocks` the most blocks of a (sequence, KV head) pair.
+int launch_decode_fp4(const DecodeParams& p, const pkv_cache_desc& cache, int num_seqs,
+                      int max_context, void* workspace, cudaStream_t st);
+size_t fp4_workspace_bytes(const pkv_cache_desc& cache, int num_seqs, int64_t blocks,
+                           bool listed);
 
 int launch_attention_simple(const DecodeParams& p, const pkv_cache_desc& cache, dim3 grid,
                             cudaStream_t st);

@@ -8,6 +8,12 @@
 
 extern "C" size_t pkv_sparse_workspace_bytes(pkv_cache_desc cache, int num_seqs, int num_heads,
                                              int max_selected) {
+  using namespace pkv;
+  if (check_cache_desc(cache, true) != PKV_OK || num_seqs <= 0 || num_heads <= 0 ||
+      max_selected <= 0)
+    return 0;
+  if (cache.dtype == PKV_DTYPE_FP4_E2M1)
+    return fp4_workspace_bytes(cache, num_seqs, max_selected, true);
   return 0;
 }
 
@@ -51,11 +57,8 @@ extern "C" int pkv_paged_attention_sparse(
   p.list = blocks;
   p.counts = counts;
   p.max_selected = max_selected;
-  if (cache.dtype == PKV_DTYPE_FP4_E2M1) {
-    p.cluster = 8;
-    return launch_decode_fp4(p, cache.head_dim, cache.block_size,
-                             dim3(1, cache.num_kv_heads, num_seqs),
+  if (cache.dtype == PKV_DTYPE_FP4_E2M1)
+    return launch_decode_fp4(p, cache, num_seqs, max_blocks_per_seq * cache.block_size, workspace,
                              static_cast<cudaStream_t>(stream));
-  }
   return launch_attention_simple(p, cache, dim3(1, 1, num_seqs), static_cast<cudaStream_t>(stream));
 }
