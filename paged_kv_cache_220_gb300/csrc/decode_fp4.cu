@@ -53,8 +53,9 @@ struct Fp4Geom {
   static constexpr int kBytes = TU * D / 16 * 9;      // K (or V) of a unit
   static constexpr int kStage = 2 * kBytes;
   static constexpr int kThreads = kFp4Warps * 32;
-  // barriers, the rows' first units by thread, the look-up cursors
-  static constexpr int kHead = kFp4Warps * kFp4Stages * 16 + (kThreads + 4) * 4 + kFp4Warps * 16;
+  // barriers, the rows' first units by thread, the look-up cursors, the ends' states
+  static constexpr int kHead = kFp4Warps * kFp4Stages * 16 + (kThreads + 4) * 4 +
+                               kFp4Warps * (16 + 64 + 4);
   static constexpr int kRingAt = (kHead + 127) / 128 * 128;
   static constexpr int kSmem = kRingAt + kFp4Warps * kFp4Stages * kStage;
   // a slot: O as the lanes hold it, [D/16][32] float4, then 8 maxima (base 2) and 8 sums
@@ -149,6 +150,9 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
   uint64_t* my_v = my_k + W * NST;
   int* pre = reinterpret_cast<int*>(smem_raw + W * NST * 16);  // [THREADS + 4]
   int4* my_cursor = reinterpret_cast<int4*>(pre + THREADS + 4) + (threadIdx.x >> 5);
+  float* ends_m = reinterpret_cast<float*>(pre + THREADS + 4) + W * 4;  // [W][8]
+  float* ends_l = ends_m + W * 8;                                       // [W][8]
+  int* ends_pair = reinterpret_cast<int*>(ends_l + W * 8);              // [W]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   if (lane == 0) {
@@ -213,13 +217,14 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
   // the merge launched next may be scheduled; it waits for this grid's end
   allow_dependents();
   const int n_workers = min(p.workers, T);
-  const int me = blockIdx.x + gridDim.x * warp;  // neighbours on different SMs
-  if (me >= n_workers) return;
-  const int u0 = share_begin(me, n_workers, T);
-  const int mine = share_begin(me + 1, n_workers, T) - u0;  // units of this warp, one at least
+  const int me = blockIdx.x * W + warp;
+  if (blockIdx.x * W >= n_workers) return;
+  const int u0 = me < n_workers ? share_begin(me, n_workers, T) : T;
+  // units of this warp, one at least if it is one of the workers
+  const int mine = me < n_workers ? share_begin(me + 1, n_workers, T) - u0 : 0;
   // the pair and unit that u0 is
-  int pair, unit, units;
-  {
+  int pair = -1, unit = 0, units = 0;
+  if (mine > 0) {
     int t = 0;
 #pragma unroll
     for (int k = 0; k < W; ++k)
@@ -280,8 +285,7 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
   };
   int pb_now, pb_next;
   uint32_t vis_now, vis_next;
-  int n_now = look_up(pb_now, vis_now);
-  int n_next = look_up(pb_next, vis_next);
+  int n_now = look_up(pb_now, vis_now), n_next = 0;
   int at = 0;  // units of the current batch that are loaded
   const uint32_t my_ring = smem_addr(smem_raw) + G::kRingAt + warp * NST * G::kStage;
   uint64_t policy;
@@ -322,18 +326,29 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
     for (int k = 0; k + 1 < NST; ++k) vis[k] = vis[k + 1];
     if (i < mine) load_k(i);
     if (i < mine && i + 1 < NST) load_v(i);
+    // the second batch's look-up behind the first unit's loads
+    if (i == 0) n_next = look_up(pb_next, vis_next);
   }
 
   // ---- the pair at hand: units of it that are left, whether it is this warp's alone
   int seg = min(units - unit, mine);
   bool alone = unit == 0 && seg == units;
-  int slot = 0;
   bool fresh = true;
   uint32_t bq[KW][2];
   float f0 = 0.f, f1 = 0.f;  // logit factors of queries 2c, 2c + 1 (base 2), not negative
   // running maxima of the products before their factor, sums, outputs
-  float m0, m1, l0, l1;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   float o[KW][4];
+  // the sums over the eight lanes that share a query pair
+  auto sum_rows = [&] {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+  };
+  // a maximum as a base-2 logit
+  auto log2_max = [](float m, float f) { return m == -INFINITY ? m : m * f; };
   // token of the unit that row x of tile t stands for
   auto token = [](int t, int x) {
     return 16 * t + (D == 256 ? x : ((x & 7) >> 1) * 4 + (x & 1) + (x >= 8 ? 2 : 0));
@@ -539,13 +554,10 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
       st = 0;
       parity ^= 1;
     }
-    if (--seg > 0) continue;
-    // ---- the pair's end, or the share's
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-    }
+    --seg;
+    if (seg > 0 || (done + 1 == mine && !alone)) continue;
+    // ---- the pair's end before the share's, or a pair of this warp alone
+    sum_rows();
     if (alone) {
       const float vsc = p.v_scale[pair % Hk];
       const float i0 = l0 != 0.f ? vsc / l0 : 0.f, i1 = l1 != 0.f ? vsc / l1 : 0.f;
@@ -553,14 +565,12 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
         if (2 * c < g)
-          *reinterpret_cast<uint32_t*>(dst + 2 * k) =
-              pack_bf16(o[k][0] * i0, o[k][2] * i0);
+          *reinterpret_cast<uint32_t*>(dst + 2 * k) = pack_bf16(o[k][0] * i0, o[k][2] * i0);
         if (2 * c + 1 < g)
-          *reinterpret_cast<uint32_t*>(dst + D + 2 * k) =
-              pack_bf16(o[k][1] * i1, o[k][3] * i1);
+          *reinterpret_cast<uint32_t*>(dst + D + 2 * k) = pack_bf16(o[k][1] * i1, o[k][3] * i1);
       }
     } else {
-      float* dst = p.slots + (static_cast<int64_t>(me) * 2 + slot) * G::kSlot;
+      float* dst = p.slots + static_cast<int64_t>(me) * 2 * G::kSlot;
       if (2 * c < g) {
 #pragma unroll
         for (int k = 0; k < KW; ++k)
@@ -568,14 +578,11 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
               make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
       }
       if (lane < 4) {
-        // the maxima as base-2 logits
-        *reinterpret_cast<float2*>(dst + 8 * D + 2 * c) =
-            make_float2(m0 == -INFINITY ? m0 : m0 * f0, m1 == -INFINITY ? m1 : m1 * f1);
+        *reinterpret_cast<float2*>(dst + 8 * D + 2 * c) = make_float2(log2_max(m0, f0), log2_max(m1, f1));
         *reinterpret_cast<float2*>(dst + 8 * D + 8 + 2 * c) = make_float2(l0, l1);
       }
     }
     fresh = true;
-    slot = 1;
     if (done + 1 < mine) {
       do {
         ++pair;
@@ -594,6 +601,67 @@ __global__ void __launch_bounds__(Fp4Geom<D>::kThreads, kFp4Ctas)
     for (int i = max(done, nv - NST); i < nv; ++i)
       (void)mbar_wait(&my_v[i % NST], (i / NST) & 1, p.err);
   }
+  // ---- what the warps' shares end with, unless a warp has written it: warps of
+  // one pair are neighbours; their states are summed in their order
+  const bool open = mine > 0 && !fresh;
+  if (open) sum_rows();
+  if (lane < 4) {
+    ends_m[warp * 8 + 2 * c] = log2_max(m0, f0);
+    ends_m[warp * 8 + 2 * c + 1] = log2_max(m1, f1);
+    ends_l[warp * 8 + 2 * c] = l0;
+    ends_l[warp * 8 + 2 * c + 1] = l1;
+  }
+  if (lane == 0) ends_pair[warp] = open ? pair : -1 - warp;
+  __syncthreads();  // every warp's copies have landed and are read: the rings are free
+  float4* ends_o = reinterpret_cast<float4*>(smem_raw + G::kRingAt);  // [W][KW][32]
+  if (open) {
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (ends_pair[w] != pair) continue;
+      t0 = fmaxf(t0, ends_m[w * 8 + 2 * c]);
+      t1 = fmaxf(t1, ends_m[w * 8 + 2 * c + 1]);
+    }
+    const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 * f0 - t0);
+    const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 * f1 - t1);
+#pragma unroll
+    for (int k = 0; k < KW; ++k)
+      ends_o[(warp * KW + k) * 32 + lane] =
+          make_float4(o[k][0] * a0, o[k][1] * a1, o[k][2] * a0, o[k][3] * a1);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int w = 0; w < W; ++w) {
+    const int of = ends_pair[w];
+    if (of < 0 || (w > 0 && ends_pair[w - 1] == of)) continue;  // not the first that has it
+    int last = w;
+    while (last + 1 < W && ends_pair[last + 1] == of) ++last;
+    float* dst = p.slots + (static_cast<int64_t>(blockIdx.x * W + w) * 2 + 1) * G::kSlot;
+    if (2 * c < g) {
+      for (int k = warp; k < KW; k += W) {
+        float4 sum = ends_o[(w * KW + k) * 32 + lane];
+        for (int x = w + 1; x <= last; ++x) {
+          const float4 y = ends_o[(x * KW + k) * 32 + lane];
+          sum.x += y.x;
+          sum.y += y.y;
+          sum.z += y.z;
+          sum.w += y.w;
+        }
+        reinterpret_cast<float4*>(dst)[k * 32 + lane] = sum;
+      }
+    }
+    if (threadIdx.x < 8) {
+      const int j = threadIdx.x;
+      float M = -INFINITY, L = 0.f;
+      for (int x = w; x <= last; ++x) M = fmaxf(M, ends_m[x * 8 + j]);
+      for (int x = w; x <= last; ++x) {
+        const float m = ends_m[x * 8 + j];
+        L = fmaf(ends_l[x * 8 + j], m == -INFINITY ? 0.f : fast_exp2(m - M), L);
+      }
+      dst[8 * D + j] = M;
+      dst[8 * D + 8 + j] = L;
+    }
+  }
 }
 
 // The pairs that several warps had parts of: out = sum_i e_i O_i / sum_i e_i l_i with e_i
@@ -609,7 +677,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
                      int num_rows, int Hk, int g, int workers) {
   using G = Fp4Geom<D>;
   constexpr int U = 8;  // parts of a warp whose loads are in flight together
-  extern __shared__ float weights[];  // [n][8]
+  extern __shared__ float weights[];  // [n][8], and the parts' sums [n][8]
   __shared__ float4 acc_sh[kMergeWarps][32];
   __shared__ float inv_sum[8];
   wait_prerequisite();
@@ -641,25 +709,47 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   auto worker_of = [&](int x) {
     return static_cast<int>((static_cast<int64_t>(x + 1) * nw - 1) / T);
   };
-  const int w0 = worker_of(u), n = worker_of(u + units - 1) - w0 + 1;
-  if (n == 1) return;  // written already
-  const int slot0 = share_begin(w0, nw, T) != u ? 1 : 0;  // of the first; the others' is 0
+  const int w0 = worker_of(u), w1 = worker_of(u + units - 1);
+  if (w0 == w1) return;  // written already
+  // slot 1 of w0 and of the first warps of the CTAs behind it, as long as shares
+  // end with this pair; then slot 0 of w1 if its share ends with another one
+  const bool more = share_begin(w1 + 1, nw, T) > u + units;
+  const int c0 = w0 / kFp4Warps, ends = (more ? w1 - 1 : w1) / kFp4Warps - c0 + 1;
+  const int n = ends + (more ? 1 : 0);
   auto part = [&](int i) {
-    return slots + (static_cast<int64_t>(w0 + i) * 2 + (i == 0 ? slot0 : 0)) * G::kSlot;
+    const int64_t at = i == ends ? 2 * static_cast<int64_t>(w1)
+                       : 2 * static_cast<int64_t>(i == 0 ? w0 : (c0 + i) * kFp4Warps) + 1;
+    return slots + at * G::kSlot;
   };
+  const bool live = 2 * c < g;
+  auto piece_of = [&](int i) {
+    return live && i < n ? reinterpret_cast<const float4*>(part(i))[piece * 32 + lane]
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  // the first parts are on their way while the weights are made
+  float4 x[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) x[k] = piece_of(split + k * SPLIT);
+  // weights[i][0..8): the maxima, then the weights; sums[i][8]
+  float* sums = weights + 8 * n;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < 16 * n; i += kMergeWarps * 32) {
+    const float y = part(i / 16)[8 * D + i % 16];
+    (i % 16 < 8 ? weights : sums)[i / 16 * 8 + i % 8] = y;
+  }
+  __syncthreads();
   if (warp < 8) {
-    // query `warp`'s weights, lane i the parts i, i + 32, ..
+    // query `warp`, lane i the parts i, i + 32, ..
     float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[8 * D + warp]);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, weights[i * 8 + warp]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f;
     for (int i = lane; i < n; i += 32) {
-      const float* x = part(i);
-      const float m = x[8 * D + warp];
+      const float m = weights[i * 8 + warp];
       const float e = m == -INFINITY ? 0.f : fast_exp2(m - M);
       weights[i * 8 + warp] = e;
-      L = fmaf(e, x[8 * D + 8 + warp], L);
+      L = fmaf(e, sums[i * 8 + warp], L);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
@@ -667,14 +757,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const bool live = 2 * c < g;
   for (int i0 = split; i0 < n; i0 += U * SPLIT) {
-    float4 x[U];
+    if (i0 != split) {
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      x[k] = live && i0 + k * SPLIT < n
-                 ? reinterpret_cast<const float4*>(part(i0 + k * SPLIT))[piece * 32 + lane]
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < U; ++k) x[k] = piece_of(i0 + k * SPLIT);
+    }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (i0 + k * SPLIT >= n) continue;
@@ -741,9 +828,9 @@ static int launch_fp4(Fp4Params p, int64_t bound, void* workspace, cudaStream_t 
   if (rc != PKV_OK) return rc;
   rc = launch_dependent(kern, dim3(ctas), dim3(G::kThreads), G::kSmem, st, p);
   if (rc != PKV_OK) return rc;
-  // a pair has at most all workers' parts
-  const size_t smem = static_cast<size_t>(p.workers) * 8 * sizeof(float);
-  constexpr size_t kMaxSmem = static_cast<size_t>(kFp4MaxCtas) * kFp4Warps * 8 * sizeof(float);
+  // a pair has at most a part of every CTA and one more
+  const size_t smem = static_cast<size_t>(ctas + 1) * 16 * sizeof(float);
+  constexpr size_t kMaxSmem = static_cast<size_t>(kFp4MaxCtas + 1) * 16 * sizeof(float);
   if (pairs < 152) {
     auto wide = merge_fp4_kernel<D, kMergeWarps, LIST>;
     static DeviceFlags done_wide;
