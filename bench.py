@@ -39,6 +39,7 @@ METRIC = "paged decode-attention HBM GB/s (% of GB300 peak) and decode tokens/s 
 L2_BYTES = 129 * 1024 * 1024
 DECODE_SOURCES = ["paged_kv_cache_220_gb300/csrc/decode.cu",
                   "paged_kv_cache_220_gb300/csrc/decode_tc.cu",
+                  "paged_kv_cache_220_gb300/csrc/decode_tc_kernel.cuh",
                   "paged_kv_cache_220_gb300/csrc/decode_params.h",
                   "paged_kv_cache_220_gb300/csrc/common.cuh",
                   "paged_kv_cache_220_gb300/csrc/tc_common.cuh"]

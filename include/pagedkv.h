@@ -85,9 +85,9 @@ typedef enum {
 typedef enum {
   PKV_DTYPE_BF16 = 0,
   PKV_DTYPE_FP8_E4M3 = 1,
-  /* 4-bit pools: kv_cache_write, kv_cache_read, paged_attention_fp4,
-   * paged_attention_sparse, block_bounds, copy_blocks and the swaps take them;
-   * every other call returns PKV_ERR_INVALID_ARG. */
+  /* 4-bit pools: kv_cache_write, kv_cache_read, paged_attention_decode (and the
+   * calls made of it), paged_attention_sparse, block_bounds, copy_blocks and
+   * the swaps take them; every other call returns PKV_ERR_INVALID_ARG. */
   PKV_DTYPE_FP4_E2M1 = 2
 } pkv_dtype;
 
@@ -178,7 +178,9 @@ int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tok
  * For sequence s and query head j (KV head h = j / g, g = num_heads /
  * num_kv_heads), with K_s, V_s the sequence's logical rows 0..ctx-1:
  *     z_t = scale * <q[s,j,:], K_s[t,:]>,  out[s,j,:] = sum_t softmax(z)_t V_s[t,:]
- * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]).
+ * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]), 4-bit pools as
+ * code * s * k_scale[h] (tables of at most 2^30 tokens a sequence; an element
+ * of q below 2^-14 of its row's largest is rounded by at most 2^-25 of it).
  * The softmax is the max-subtracted one, accumulated online in fp32.
  *
  *   out       : device bf16 [num_seqs][num_heads][head_dim] (written when
@@ -412,41 +414,6 @@ int pkv_paged_attention_window(void* out, const void* q, const void* k_cache,
                                int max_context, float scale, int window, int sinks,
                                int partition_size, void* workspace, size_t workspace_bytes,
                                const int32_t* seq_order, void* stream);
-
-/* ------------------------------------------------------------------------ *
- * paged_attention_fp4: the decode attention of one step over 4-bit pools (the
- * pages have no counterpart). The result is pkv_paged_attention's over what the
- * codes stand for, code * s * k_scale[h] (v_scale[h]). The batch's work is cut
- * into equal shares whatever the lengths are, so there is no partition size and
- * no order to choose; where the cuts fall, and with them the last bits of a
- * sequence's result, depends on the lengths of the whole batch. The same call
- * gives the same bits.
- *
- *   workspace, workspace_bytes : device scratch of at least
- *               pkv_fp4_workspace_bytes(...) bytes (at most 31 MB and 4 bytes a
- *               sequence); its contents do not matter before or after; calls
- *               whose kernels may overlap need one each
- *   max_context : host upper bound of context_lens (a longer context is
- *               reported, PKV_DEVERR_CONTEXT, and cut)
- *   cache       : of dtype PKV_DTYPE_FP4_E2M1
- *   other args  : as for pkv_paged_attention_decode. A context of 0 yields
- *               zeros. `out` may not overlap `q`. Slots that hold no token of
- *               the context may hold anything, NaN scales included.
- * An element of q below 2^-14 of its row's largest is rounded by at most 2^-25
- * of that largest; softmax weights are rounded to 11 bits before they meet V,
- * with at most 2^-40 of the largest weight lost to underflow each; sums are
- * fp32.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA; PKV_ERR_UNSUPPORTED also for
- * tables of more than 2^30 tokens a sequence, pools of 2^31 pages or rows and
- * bounds of 2^31 or more runs of 8192 / head_dim tokens.
- * ------------------------------------------------------------------------ */
-size_t pkv_fp4_workspace_bytes(pkv_cache_desc cache, int num_seqs, int max_context);
-int pkv_paged_attention_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
-                            pkv_cache_desc cache, const float* k_scale, const float* v_scale,
-                            const int32_t* block_tables, int max_blocks_per_seq,
-                            const int32_t* context_lens, int num_seqs, int num_heads,
-                            int max_context, float scale, void* workspace,
-                            size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * block_bounds: for blocks of a K pool, the lowest and the highest cached value

@@ -100,9 +100,6 @@ SIGNATURES = {
     "pkv_paged_attention_window": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _I, _I,
                                         _I, ctypes.c_float, _I, _I, _I, _P, ctypes.c_size_t, _P,
                                         _P]),
-    "pkv_fp4_workspace_bytes": (ctypes.c_size_t, [CacheDesc, _I, _I]),
-    "pkv_paged_attention_fp4": (_I, [_P, _P, _P, _P, CacheDesc, _P, _P, _P, _I, _P, _I, _I, _I,
-                                     ctypes.c_float, _P, ctypes.c_size_t, _P]),
     "pkv_block_bounds": (_I, [_P, _P, CacheDesc, _P, _P, _P, _I, _P, _P, _I, _I, _P]),
     "pkv_select_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "pkv_select_blocks": (_I, [_P, _P, _P, _P, CacheDesc, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P,
@@ -377,18 +374,17 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, scale, max_
     """Decode attention in one C call: the one-pass decode, or the split
     decode followed by the merge of its partitions. Returns out [S, Hq, D]
     bf16. partition_size: 0 = one pass, None = the library's choice
-    (decode_partition_size). seq_order as for paged_attention_decode.
-    4-bit pools (pkv_paged_attention_fp4) have no partitions to choose and no
-    order: partition_size is 0 or None, seq_order makes no difference."""
+    (decode_partition_size). seq_order as for paged_attention_decode."""
     desc = cache_desc(k_cache)
-    if desc.dtype == PKV_DTYPE_FP4_E2M1:
-        if partition_size:
-            raise ValueError("4-bit pools: partition_size must be 0 or None")
-        return _paged_attention_fp4(q, k_cache, v_cache, block_tables, context_lens, scale,
-                                    max_context, k_scale, v_scale, out, workspace, stream)
     if partition_size is None:
-        partition_size = decode_partition_size(q.shape[0], desc.num_kv_heads, desc.head_dim,
-                                               desc.block_size, max_context, desc.dtype)
+        partition_size = _decode_partition(desc.num_blocks, desc.num_kv_heads, desc.head_dim,
+                                           desc.block_size, desc.dtype, q.shape[0], max_context)
+        if partition_size < 0:
+            _check(partition_size, "decode_partition_size")
+    if desc.dtype == PKV_DTYPE_FP4_E2M1:
+        return _paged_attention_fp4(q, k_cache, v_cache, block_tables, context_lens, scale,
+                                    max_context, partition_size, k_scale, v_scale, out, workspace,
+                                    stream, seq_order)
     S, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -711,26 +707,23 @@ def decode_partition_size(num_seqs, num_kv_heads, head_dim, block_size, max_cont
     return int(rc)
 
 
-def fp4_workspace_bytes(k_cache, num_seqs, max_context) -> int:
-    return int(lib().pkv_fp4_workspace_bytes(cache_desc(k_cache), num_seqs, max_context))
-
-
 def _paged_attention_fp4(q, k_cache, v_cache, block_tables, context_lens, scale, max_context,
-                         k_scale, v_scale, out, workspace, stream):
+                         partition_size, k_scale, v_scale, out, workspace, stream, seq_order):
     """paged_attention over 4-bit pools."""
     L = _lib or lib()
     desc, shape, dev, S, op, qp, kp, vp, ks, vs, tables, lens = _attention_args(
         q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, True, out)
+    order = _ptr(seq_order, "seq_order", dev, _I32, (S,))
     with _at(dev, stream) as raw:
         if out is None:
             out = torch.empty_like(q)
             op = out.data_ptr()
-        need = _fp4_need(desc.num_kv_heads, desc.head_dim, desc.block_size, S,
-                         max_context) if workspace is None else 0
+        need = 0 if partition_size == 0 or workspace is not None else _decode_need(
+            S, shape[1], desc.head_dim, max_context, partition_size)
         with _Scratch(workspace, need, dev, raw) as (ws, wsb):
-            rc = L.pkv_paged_attention_fp4(
+            rc = L.pkv_paged_attention(
                 op, qp, kp, vp, desc, ks, vs, tables, block_tables.shape[1], lens, S, shape[1],
-                max_context, scale, ws, wsb, raw)
+                max_context, scale, partition_size, ws, wsb, order, raw)
     if rc:
         _check(rc, "paged_attention")
     return out
@@ -850,9 +843,11 @@ def paged_attention_sparse(q, k_cache, v_cache, block_tables, context_lens, bloc
 
 # Functions of their sizes alone, asked for at every call (a call into the
 # library is 1 us).
-_fp4_need = functools.lru_cache(1024)(
-    lambda hk, d, b, *rest: lib().pkv_fp4_workspace_bytes(
-        CacheDesc(1, b, hk, d, PKV_DTYPE_FP4_E2M1), *rest))
+_decode_partition = functools.lru_cache(1024)(
+    lambda nb, hk, d, b, dtype, *rest: lib().pkv_decode_partition_size(
+        CacheDesc(nb, b, hk, d, dtype), *rest))
+_decode_need = functools.lru_cache(1024)(
+    lambda *sizes: lib().pkv_decode_workspace_bytes(*sizes))
 _select_need = functools.lru_cache(1024)(
     lambda *sizes: lib().pkv_select_workspace_bytes(*sizes))
 _sparse_need = functools.lru_cache(1024)(

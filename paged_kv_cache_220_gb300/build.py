@@ -25,7 +25,7 @@ CUFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
            "--expt-relaxed-constexpr", "-I" + INCLUDE]
 SOURCES = ["api.cu", "kv_cache_write.cu", "copy_blocks.cu", "swap_blocks.cu", "decode.cu", "decode_tc.cu", "decode_prefix.cu", "reduce.cu",
            "decode_noalloc.cu", "decode_tree.cu", "decode_window.cu", "kv_cache_accept.cu",
-           "decode_fp4.cu", "attention_simple.cu", "decode_sparse.cu", "kv_cache_read.cu", "block_bounds.cu", "select_blocks.cu", "allocator.cpp", "scheduler.cpp"]
+           "decode_fp4.cu", "decode_sparse.cu", "kv_cache_read.cu", "block_bounds.cu", "select_blocks.cu", "allocator.cpp", "scheduler.cpp"]
 
 
 def nvcc() -> str:

@@ -35,8 +35,15 @@ extern "C" size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int he
 
 extern "C" int pkv_decode_partition_size(pkv_cache_desc cache, int num_seqs, int max_context) {
   using namespace pkv;
-  const int rc = check_cache_desc(cache);
+  const int rc = check_cache_desc(cache, true);
   if (rc != PKV_OK) return rc;
+  if (cache.dtype == PKV_DTYPE_FP4_E2M1) {
+    if (num_seqs < 0 || max_context < 0) return PKV_ERR_INVALID_ARG;
+    const int unit = fp4_unit(cache.head_dim);
+    const Fp4Split f = fp4_split(static_cast<int64_t>(num_seqs) * cache.num_kv_heads,
+                                 (static_cast<int64_t>(max_context) + unit - 1) / unit);
+    return static_cast<int>(std::min<int64_t>(f.per * unit, INT32_MAX / 64 * 32));
+  }
   // a window as wide as the context
   return pkv_window_partition_size(num_seqs, cache.num_kv_heads, cache.head_dim,
                                    cache.block_size, max_context, std::max(1, max_context), 0);
@@ -75,7 +82,7 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
                                           size_t workspace_bytes, const int32_t* seq_order,
                                           void* stream) {
   using namespace pkv;
-  int rc = check_cache_desc(cache);
+  int rc = check_cache_desc(cache, true);
   if (rc != PKV_OK) return rc;
   if (num_seqs < 0 || num_heads <= 0 || max_context < 0 || max_blocks_per_seq <= 0 ||
       partition_size < 0)
@@ -90,7 +97,11 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
   if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
   const bool fp8 = cache.dtype == PKV_DTYPE_FP8_E4M3;
-  if (fp8 && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+  const bool fp4 = cache.dtype == PKV_DTYPE_FP4_E2M1;
+  if ((fp8 || fp4) && (!k_scale || !v_scale)) return PKV_ERR_INVALID_ARG;
+  // positions are 32-bit numbers in the 4-bit kernel
+  if (fp4 && static_cast<int64_t>(max_blocks_per_seq) * cache.block_size > (1 << 30))
+    return PKV_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
 
   DecodeParams p{};
@@ -121,6 +132,11 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
     while (c < 8 && static_cast<int64_t>(c) * 4 * cache.block_size < max_context) c <<= 1;
     while (c > 1 && static_cast<int64_t>(num_seqs) * cache.num_kv_heads * c > 1024) c >>= 1;
     p.cluster = c;
+    if (fp4) {
+      const int unit = fp4_unit(cache.head_dim);
+      p.cluster = fp4_split(static_cast<int64_t>(num_seqs) * cache.num_kv_heads,
+                            (static_cast<int64_t>(max_context) + unit - 1) / unit).cluster;
+    }
   } else {
     if (partition_size % cache.block_size != 0) return PKV_ERR_INVALID_ARG;
     if (max_context == 0) return PKV_OK;  // nothing to store; the reduce writes zeros
@@ -139,6 +155,7 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
     grid.x = np;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (fp4) return launch_decode_fp4(p, cache.head_dim, cache.block_size, grid, st);
   if (static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads * cache.block_size >=
       (int64_t{1} << 31))
     return PKV_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit

@@ -78,7 +78,7 @@ struct WindowBlocks {
   }
 };
 
-// Tensor-core decode (decode_tc.cu) for bf16 or E4M3 pools. Returns a pkv_status.
+// Tensor-core decode (decode_tc_kernel.cuh) for bf16 or E4M3 pools. Returns a pkv_status.
 int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_cache,
                      int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
 
@@ -86,15 +86,27 @@ int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_c
 int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
                          int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
 
-// 4-bit pools (decode_fp4.cu), the listed form (p.list) too; the result goes to p.out.
-// fp4_workspace_bytes: `blocks` the most blocks of a (sequence, KV head) pair.
-int launch_decode_fp4(const DecodeParams& p, const pkv_cache_desc& cache, int num_seqs,
-                      int max_context, void* workspace, cudaStream_t st);
-size_t fp4_workspace_bytes(const pkv_cache_desc& cache, int num_seqs, int64_t blocks,
-                           bool listed);
+// How the windowed and the listed form's work is cut: blocks to a partition, 0 =
+// one pass over clusters of *cluster CTAs. (decode_window.cu)
+int64_t parts_split(int64_t pairs, int64_t blocks, int head_dim, int* cluster);
 
-int launch_attention_simple(const DecodeParams& p, const pkv_cache_desc& cache, dim3 grid,
-                            cudaStream_t st);
+// 4-bit pools (decode_fp4.cu), the listed form too.
+int launch_decode_fp4(const DecodeParams& p, int head_dim, int block_size, dim3 grid,
+                      cudaStream_t st);
+
+// Tokens of a unit of the 4-bit kernel: what a warp takes at a time, four of them
+// in a CTA.
+__host__ __device__ constexpr int fp4_unit(int head_dim) { return head_dim == 256 ? 32 : 64; }
+constexpr int kFp4Warps = 4;
+
+// How the 4-bit kernel's work is cut: `pairs` of up to `units` units each. per: units
+// of a partition, 0 = one pass; cluster: CTAs of a pair's cluster in one pass.
+// (decode_fp4.cu)
+struct Fp4Split {
+  int cluster;
+  int64_t per;
+};
+Fp4Split fp4_split(int64_t pairs, int64_t units);
 
 // Merge of split partials (reduce.cu). With prefix_blocks == NULL the slots of
 // sequence s are [0, ceil(ctx/P)); otherwise [0, npre) and [slot_split,
@@ -111,5 +123,11 @@ int launch_reduce_window(void* out, const float* tmp, const float* ml, const flo
                          const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
                          int np_max, int partition_size, int block_size, int window, int sinks,
                          cudaStream_t st);
+
+// The merge of the listed form: a row has ceil(counts[pair] / partition_blocks) slots,
+// some of which may hold no token.
+int launch_reduce_listed(void* out, const float* tmp, const float* ml, const float* es,
+                         const int32_t* counts, int num_seqs, int num_heads, int num_kv_heads,
+                         int head_dim, int np_max, int partition_blocks, cudaStream_t st);
 
 }  // namespace pkv

@@ -1,10 +1,35 @@
 // paged_attention_sparse: the C entry points of decode attention over listed
-// blocks.
+// blocks, each (sequence, KV head) pair its own list. The kernels are the decode's
+// in their listed forms (decode_tc_kernel.cuh for bf16 and E4M3 pools, decode_fp4.cu
+// for 4-bit ones) and the merge is its merge (reduce.cu): what a list changes is
+// which blocks are walked, each with the two look-ups (entry, table) of a batch of
+// entries made ahead of its copies.
 #include <algorithm>
 
-#include "common.cuh"
-#include "decode_params.h"
-#include "host_util.h"
+#include "decode_tc_kernel.cuh"
+
+namespace pkv {
+
+static int launch_decode_listed(const DecodeParams& p, const void* k_cache, const void* v_cache,
+                                int head_dim, int block_size, bool fp8, dim3 grid,
+                                cudaStream_t st) {
+  return fp8 ? dispatch_tc<true, kListed>(p, k_cache, v_cache, head_dim, block_size, grid, st)
+             : dispatch_tc<false, kListed>(p, k_cache, v_cache, head_dim, block_size, grid, st);
+}
+
+// Entries to a partition of lists of up to max_selected, 0 = one pass.
+static int64_t listed_split(const pkv_cache_desc& cache, int num_seqs, int max_selected,
+                            int* cluster) {
+  const int64_t pairs = static_cast<int64_t>(num_seqs) * cache.num_kv_heads;
+  if (cache.dtype != PKV_DTYPE_FP4_E2M1)
+    return parts_split(pairs, max_selected, cache.head_dim, cluster);
+  const int64_t ub = fp4_unit(cache.head_dim) / cache.block_size;
+  const Fp4Split f = fp4_split(pairs, (max_selected + ub - 1) / ub);
+  *cluster = f.cluster;
+  return f.per * ub;
+}
+
+}  // namespace pkv
 
 extern "C" size_t pkv_sparse_workspace_bytes(pkv_cache_desc cache, int num_seqs, int num_heads,
                                              int max_selected) {
@@ -12,9 +37,11 @@ extern "C" size_t pkv_sparse_workspace_bytes(pkv_cache_desc cache, int num_seqs,
   if (check_cache_desc(cache, true) != PKV_OK || num_seqs <= 0 || num_heads <= 0 ||
       max_selected <= 0)
     return 0;
-  if (cache.dtype == PKV_DTYPE_FP4_E2M1)
-    return fp4_workspace_bytes(cache, num_seqs, max_selected, true);
-  return 0;
+  int cluster = 1;
+  const int64_t per = listed_split(cache, num_seqs, max_selected, &cluster);
+  if (per == 0) return 0;
+  return static_cast<size_t>(num_seqs) * num_heads * ((max_selected + per - 1) / per) *
+         (cache.head_dim + 2) * sizeof(float);
 }
 
 extern "C" int pkv_paged_attention_sparse(
@@ -57,8 +84,26 @@ extern "C" int pkv_paged_attention_sparse(
   p.list = blocks;
   p.counts = counts;
   p.max_selected = max_selected;
-  if (cache.dtype == PKV_DTYPE_FP4_E2M1)
-    return launch_decode_fp4(p, cache, num_seqs, max_blocks_per_seq * cache.block_size, workspace,
-                             static_cast<cudaStream_t>(stream));
-  return launch_attention_simple(p, cache, dim3(1, 1, num_seqs), static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t per = listed_split(cache, num_seqs, max_selected, &p.cluster);
+  dim3 grid(1, cache.num_kv_heads, num_seqs);
+  int np = 0;
+  if (per > 0) {
+    np = static_cast<int>((max_selected + per - 1) / per);
+    const int64_t rows = static_cast<int64_t>(num_seqs) * num_heads * np;
+    p.partition_blocks = static_cast<int>(per);
+    p.np_max = np;
+    p.tmp_out = static_cast<float*>(workspace);
+    p.max_logits = p.tmp_out + rows * cache.head_dim;
+    p.exp_sums = p.max_logits + rows;
+    grid.x = np;
+  }
+  rc = cache.dtype == PKV_DTYPE_FP4_E2M1
+           ? launch_decode_fp4(p, cache.head_dim, cache.block_size, grid, st)
+           : launch_decode_listed(p, k_cache, v_cache, cache.head_dim, cache.block_size,
+                                  cache.dtype == PKV_DTYPE_FP8_E4M3, grid, st);
+  if (rc != PKV_OK || per == 0) return rc;
+  return launch_reduce_listed(out, p.tmp_out, p.max_logits, p.exp_sums, counts, num_seqs,
+                              num_heads, cache.num_kv_heads, cache.head_dim, np,
+                              static_cast<int>(per), st);
 }

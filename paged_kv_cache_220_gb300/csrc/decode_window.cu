@@ -1,12 +1,11 @@
 // paged_attention_window: the C entry points of decode attention through a
-// sliding window with sink tokens. The kernel is the decode's (decode_tc.cu,
-// its windowed form) and the merge is its merge (reduce.cu): what a window
-// changes is which blocks are walked and which of their rows are masked.
+// sliding window with sink tokens. The kernel is the decode's
+// (decode_tc_kernel.cuh, its windowed form) and the merge is its merge
+// (reduce.cu): what a window changes is which blocks are walked and which of
+// their rows are masked.
 #include <algorithm>
 
-#include "common.cuh"
-#include "decode_params.h"
-#include "host_util.h"
+#include "decode_tc_kernel.cuh"
 
 namespace pkv {
 
@@ -41,6 +40,35 @@ static int64_t window_cluster(int64_t pairs, int64_t blocks, int64_t wave) {
   return c;
 }
 
+int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
+                         int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st) {
+  return fp8 ? dispatch_tc<true, kWindowed>(p, k_cache, v_cache, head_dim, block_size, grid, st)
+             : dispatch_tc<false, kWindowed>(p, k_cache, v_cache, head_dim, block_size, grid, st);
+}
+
+// Blocks to a partition for `pairs` of up to `blocks` blocks each, 0 = one pass; *cluster:
+// CTAs of a pair's cluster in one pass.
+int64_t parts_split(int64_t pairs, int64_t blocks, int head_dim, int* cluster) {
+  // One pass, a cluster of CTAs to a pair, saves the merge (64 pairs of 40
+  // blocks, bf16, d = 256, B = 16: 12.3 us against 16.6 in 8 partitions), as
+  // long as its CTAs have little to do each or fill most of a wave (64 pairs of
+  // 520 blocks: 85 against 90). Few pairs of many blocks are cut into as many
+  // partitions as a wave holds (4 pairs of 520 blocks: 17 us in 130, 46 in one
+  // pass; 8: 20 us in 58, 29 in 87, which do not fit one wave). Where one CTA
+  // to a pair leaves much of a wave empty or spills into the next one, about
+  // three waves even it out (256 pairs of 160 blocks, d = 128: 85 us in 5
+  // partitions, 101 in one pass; 512 pairs, 1.2 waves: 161 in 4, 225; but
+  // 1024 pairs of up to 34 blocks, d = 256, 1.7 waves: 103 in 2, 99).
+  const int64_t wave = window_wave(head_dim), c = window_cluster(pairs, blocks, wave);
+  *cluster = static_cast<int>(c);
+  const int64_t waves = (pairs * c + wave - 1) / wave;
+  if (blocks <= 12 * c || 10 * pairs * c >= (waves == 1 ? 6 : 7 * waves) * wave) return 0;
+  const int64_t np = 2 * pairs <= wave
+                         ? std::min(wave / pairs, blocks / 2)
+                         : std::min((3 * wave + pairs / 2) / pairs, blocks / 4);
+  return np <= 1 ? 0 : (blocks + np - 1) / np;
+}
+
 }  // namespace pkv
 
 extern "C" int pkv_window_partition_size(int num_seqs, int num_kv_heads, int head_dim,
@@ -53,24 +81,8 @@ extern "C" int pkv_window_partition_size(int num_seqs, int num_kv_heads, int hea
   const int64_t blocks = window_blocks_bound(block_size, max_context, window, sinks);
   const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
   if (pairs == 0) return 0;
-  // One pass, a cluster of CTAs to a pair, saves the merge (64 pairs of 40
-  // blocks, bf16, d = 256, B = 16: 12.3 us against 16.6 in 8 partitions), as
-  // long as its CTAs have little to do each or fill most of a wave (64 pairs of
-  // 520 blocks: 85 against 90). Few pairs of many blocks are cut into as many
-  // partitions as a wave holds (4 pairs of 520 blocks: 17 us in 130, 46 in one
-  // pass; 8: 20 us in 58, 29 in 87, which do not fit one wave). Where one CTA
-  // to a pair leaves much of a wave empty or spills into the next one, about
-  // three waves even it out (256 pairs of 160 blocks, d = 128: 85 us in 5
-  // partitions, 101 in one pass; 512 pairs, 1.2 waves: 161 in 4, 225; but
-  // 1024 pairs of up to 34 blocks, d = 256, 1.7 waves: 103 in 2, 99).
-  const int64_t wave = window_wave(head_dim), c = window_cluster(pairs, blocks, wave);
-  const int64_t waves = (pairs * c + wave - 1) / wave;
-  if (blocks <= 12 * c || 10 * pairs * c >= (waves == 1 ? 6 : 7 * waves) * wave) return 0;
-  const int64_t np = 2 * pairs <= wave
-                         ? std::min(wave / pairs, blocks / 2)
-                         : std::min((3 * wave + pairs / 2) / pairs, blocks / 4);
-  if (np <= 1) return 0;
-  const int64_t per = (blocks + np - 1) / np;
+  int cluster = 1;
+  const int64_t per = parts_split(pairs, blocks, head_dim, &cluster);
   return static_cast<int>(std::min<int64_t>(per, (INT32_MAX - 64) / block_size) * block_size);
 }
 

@@ -44,19 +44,29 @@ __device__ __forceinline__ void row_slots(const int32_t* context_lens, const int
   }
 }
 
-// The slots of a row: of the plain and the shared-prefix form (row_slots), or
-// of the windowed one, whose slots are partitions of the visible blocks.
+// The slots of a row: of the plain and the shared-prefix form (row_slots), of
+// the windowed one, whose slots are partitions of the visible blocks, or of the
+// listed one, partitions of the row's list (context_lens is then the lists' counts).
 struct SlotArgs {
   const int32_t* prefix_blocks;
   int partition_size, block_size, slot_split, prefix_partition;
   int window, sinks;
+  int num_kv_heads;
 };
 
-template <bool WIN>
+constexpr int kPlainSlots = 0, kWindowSlots = 1, kListSlots = 2;  // MODE
+
+template <int MODE>
 __device__ __forceinline__ void slots_of_row(const int32_t* context_lens, const SlotArgs& a, int s,
-                                             int np_max, int* err, bool report, int& npre,
-                                             int& nsuf) {
-  if constexpr (WIN) {
+                                             int j, int num_heads, int np_max, int* err,
+                                             bool report, int& npre, int& nsuf) {
+  if constexpr (MODE == kListSlots) {
+    // (a count outside its range has been reported by the decode)
+    const int n = context_lens[s * a.num_kv_heads + j / (num_heads / a.num_kv_heads)];
+    npre = 0;
+    nsuf = n <= 0 ? 0 : n > np_max * a.partition_size ? np_max
+                                                      : (n + a.partition_size - 1) / a.partition_size;
+  } else if constexpr (MODE == kWindowSlots) {
     const int ctx = min(max(0, context_lens[s]), 0x7FFFFF00);
     const int per = a.partition_size / a.block_size;
     npre = 0;
@@ -71,7 +81,7 @@ __device__ __forceinline__ void slots_of_row(const int32_t* context_lens, const 
   }
 }
 
-template <int D, int kReduceWarps, bool WIN>
+template <int D, int kReduceWarps, int MODE>
 __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
     uint16_t* __restrict__ out, const float* __restrict__ tmp_out,
     const float* __restrict__ max_logits, const float* __restrict__ exp_sums,
@@ -90,7 +100,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   int npre, nsuf;
-  slots_of_row<WIN>(context_lens, slots, s, np_max, err, tid == 0, npre, nsuf);
+  slots_of_row<MODE>(context_lens, slots, s, j, num_heads, np_max, err, tid == 0, npre, nsuf);
   const int np = npre + nsuf;
   const int64_t row = static_cast<int64_t>(s) * num_heads + j;
   if (np == 0) {
@@ -115,7 +125,8 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
   // W = sum_p w_p (fixed tree: lanes by xor, then warps in order)
   float W = 0.f;
   for (int i = tid; i < np; i += kReduceThreads) {
-    const float w = es[slot_of(i)] * fast_exp2((ml[slot_of(i)] - M) * kLog2eR);
+    float w = es[slot_of(i)] * fast_exp2((ml[slot_of(i)] - M) * kLog2eR);
+    if (MODE == kListSlots && M == -INFINITY) w = 0.f;  // no token in any slot
     wsh[i] = w;
     W += w;
   }
@@ -126,6 +137,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
   W = 0.f;
 #pragma unroll
   for (int w = 0; w < kReduceWarps; ++w) W += red[w];
+  if (MODE == kListSlots && W == 0.f) W = 1.f;
   for (int i = tid; i < np; i += kReduceThreads) wsh[i] = wsh[i] / W;
   __syncthreads();
 
@@ -179,7 +191,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
 
 constexpr int kRowWarps = 8;  // rows (warps) per CTA of the narrow merge
 
-template <int D, bool WIN>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
     uint16_t* __restrict__ out, const float* __restrict__ tmp_out,
     const float* __restrict__ max_logits, const float* __restrict__ exp_sums,
@@ -208,7 +220,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
       x[u][v] = u < np_max ? src[static_cast<int64_t>(u) * (D / 4) + lane + 32 * v]
                            : make_float4(0.f, 0.f, 0.f, 0.f);
   int npre, nsuf;
-  slots_of_row<WIN>(context_lens, slots, s, np_max, err, lane == 0, npre, nsuf);
+  slots_of_row<MODE>(context_lens, slots, s, static_cast<int>(row % num_heads), num_heads, np_max,
+                     err, lane == 0, npre, nsuf);
   const int np = npre + nsuf;  // <= np_max <= 32
   uint2* dst = reinterpret_cast<uint2*>(out + row * D);
   if (np == 0) {
@@ -226,11 +239,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
   float M = m;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float w = lane < np ? l * fast_exp2((m - M) * kLog2eR) : 0.f;
+  float w = lane < np ? l * fast_exp2((m - M) * kLog2eR) : 0.f;
+  if (MODE == kListSlots && M == -INFINITY) w = 0.f;  // no token in any slot
   float W = w;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
-  const float r = w / W;
+  const float r = MODE == kListSlots && W == 0.f ? 0.f : w / W;
 
   float4 acc[V4];
 #pragma unroll
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
 
 namespace pkv {
 
-template <int D, bool WIN>
+template <int D, int MODE>
 static int launch_reduce_t(uint16_t* o, const float* tmp, const float* ml, const float* es,
                            const int32_t* context_lens, int num_seqs, int num_heads, int np_max,
                            const SlotArgs& slots, cudaStream_t st) {
@@ -292,7 +306,7 @@ static int launch_reduce_t(uint16_t* o, const float* tmp, const float* ml, const
     // one warp per (sequence, query head) row
     const int rows = num_seqs * num_heads;
     const dim3 grid((rows + kRowWarps - 1) / kRowWarps);
-    return launch_dependent(reduce_rows_kernel<D, WIN>, grid, dim3(kRowWarps * 32), 0, st, o, tmp,
+    return launch_dependent(reduce_rows_kernel<D, MODE>, grid, dim3(kRowWarps * 32), 0, st, o, tmp,
                             ml, es, context_lens, rows, num_heads, np_max, slots, err);
   }
   // one 16-warp CTA per row and 128 columns
@@ -301,9 +315,9 @@ static int launch_reduce_t(uint16_t* o, const float* tmp, const float* ml, const
   if (smem > kMaxSmem) return PKV_ERR_UNSUPPORTED;
   const dim3 grid(num_heads, num_seqs, D / 128);
   static DeviceFlags done;
-  int rc = ensure_smem(reduce_kernel<D, 16, WIN>, kMaxSmem, done);
+  int rc = ensure_smem(reduce_kernel<D, 16, MODE>, kMaxSmem, done);
   if (rc != PKV_OK) return rc;
-  return launch_dependent(reduce_kernel<D, 16, WIN>, grid, dim3(16 * 32), smem, st, o, tmp, ml, es,
+  return launch_dependent(reduce_kernel<D, 16, MODE>, grid, dim3(16 * 32), smem, st, o, tmp, ml, es,
                           context_lens, num_heads, np_max, slots, err);
 }
 
@@ -312,11 +326,11 @@ int launch_reduce(void* out, const float* tmp, const float* ml, const float* es,
                   int np_max, int partition_size, const int32_t* prefix_blocks, int block_size,
                   int slot_split, int prefix_partition, cudaStream_t st) {
   const SlotArgs a{prefix_blocks, partition_size, block_size, slot_split,
-                   prefix_partition > 0 ? prefix_partition : partition_size, 0, 0};
+                   prefix_partition > 0 ? prefix_partition : partition_size, 0, 0, 0};
   uint16_t* o = static_cast<uint16_t*>(out);
-  return head_dim == 128 ? launch_reduce_t<128, false>(o, tmp, ml, es, context_lens, num_seqs,
+  return head_dim == 128 ? launch_reduce_t<128, kPlainSlots>(o, tmp, ml, es, context_lens, num_seqs,
                                                        num_heads, np_max, a, st)
-                         : launch_reduce_t<256, false>(o, tmp, ml, es, context_lens, num_seqs,
+                         : launch_reduce_t<256, kPlainSlots>(o, tmp, ml, es, context_lens, num_seqs,
                                                        num_heads, np_max, a, st);
 }
 
@@ -324,12 +338,23 @@ int launch_reduce_window(void* out, const float* tmp, const float* ml, const flo
                          const int32_t* context_lens, int num_seqs, int num_heads, int head_dim,
                          int np_max, int partition_size, int block_size, int window, int sinks,
                          cudaStream_t st) {
-  const SlotArgs a{nullptr, partition_size, block_size, 0, partition_size, window, sinks};
+  const SlotArgs a{nullptr, partition_size, block_size, 0, partition_size, window, sinks, 0};
   uint16_t* o = static_cast<uint16_t*>(out);
-  return head_dim == 128 ? launch_reduce_t<128, true>(o, tmp, ml, es, context_lens, num_seqs,
+  return head_dim == 128 ? launch_reduce_t<128, kWindowSlots>(o, tmp, ml, es, context_lens, num_seqs,
                                                       num_heads, np_max, a, st)
-                         : launch_reduce_t<256, true>(o, tmp, ml, es, context_lens, num_seqs,
+                         : launch_reduce_t<256, kWindowSlots>(o, tmp, ml, es, context_lens, num_seqs,
                                                       num_heads, np_max, a, st);
+}
+
+int launch_reduce_listed(void* out, const float* tmp, const float* ml, const float* es,
+                         const int32_t* counts, int num_seqs, int num_heads, int num_kv_heads,
+                         int head_dim, int np_max, int partition_blocks, cudaStream_t st) {
+  const SlotArgs a{nullptr, partition_blocks, 1, 0, partition_blocks, 0, 0, num_kv_heads};
+  uint16_t* o = static_cast<uint16_t*>(out);
+  return head_dim == 128 ? launch_reduce_t<128, kListSlots>(o, tmp, ml, es, counts, num_seqs,
+                                                            num_heads, np_max, a, st)
+                         : launch_reduce_t<256, kListSlots>(o, tmp, ml, es, counts, num_seqs,
+                                                            num_heads, np_max, a, st);
 }
 
 }  // namespace pkv
