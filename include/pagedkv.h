@@ -129,7 +129,7 @@ typedef struct {
  *   slot_mapping : device int64 [num_tokens]; -1 skips the token
  *   k_cache, v_cache : device pools described by `cache`
  *   k_scale, v_scale : device fp32 [num_kv_heads], FP8 and 4-bit pools only
- *     (else NULL).
+ *     (else NULL), not zero.
  *     FP8 code = round-to-nearest-even, saturating to +-448, of the fp32
  *     quotient x / scale[h] (IEEE division), OCP E4M3.
  *     4-bit pools: with y = x / scale[h] and a = the largest |y| of the 16
@@ -140,7 +140,8 @@ typedef struct {
  *     the 16 makes s NaN and the codes +0. Nothing saturates with a scale[h] of
  *     1/2688 of the head's largest |x| or more; s has its full precision where
  *     a >= 6 * 2^-6.
- * For bf16 pools the copy is bit-exact.
+ * For bf16 pools the copy is bit-exact. 4-bit pools: PKV_ERR_UNSUPPORTED also for
+ * 2^32 and more runs of 8 channels in the call.
  * Errors: PKV_ERR_INVALID_ARG (null pointers, num_tokens < 0, misaligned),
  * PKV_ERR_UNSUPPORTED (shape), PKV_ERR_CUDA. num_tokens == 0 is a no-op.
  * ------------------------------------------------------------------------ */
@@ -163,7 +164,7 @@ int pkv_kv_cache_write(const void* k, const void* v, const int64_t* slot_mapping
  *     row is zeros; a slot outside the pool is reported (PKV_DEVERR_SLOT), its
  *     row is zeros
  *   other args   : as for pkv_kv_cache_write
- * Errors: as for pkv_kv_cache_write.
+ * Errors: as for pkv_kv_cache_write (2^32 runs of 8 channels: any pool).
  * ------------------------------------------------------------------------ */
 int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tokens,
                       const void* k_cache, const void* v_cache, pkv_cache_desc cache,

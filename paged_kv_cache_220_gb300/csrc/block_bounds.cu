@@ -3,10 +3,13 @@
 //
 // One warp per (block, head) page: lane l has D/32 consecutive channels and
 // keeps their running minimum and maximum over the page's cached rows, the rows'
-// loads (16 at a time) in flight together; a row of a page is one coalesced
-// access. floor and ceil of a quotient by a positive step grow with the value,
-// so only the two extremes are divided. Bound by HBM over whole prompts, by
-// latency at one block per sequence.
+// loads (up to 64 words a lane) in flight together; a row of a page is one coalesced
+// access. The extremes are taken two channels at a time of what is stored, bf16
+// pairs, or f16 pairs that hold a code times its 16 channels' scale exactly: the
+// head's scale, floor and ceil of a quotient by a positive step grow with the value
+// (or all fall, for a negative scale), so only the extremes go through them. A
+// third running value, a maximum that keeps NaN, says where a zero has to join.
+// Bound by HBM over whole prompts, by latency at one block per sequence.
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,7 +34,7 @@ struct BoundsParams {
   int64_t items;    // num_seqs * per_seq * num_kv_heads
 };
 
-// Row r's channels [C*lane, C*lane + C) of a page, as loaded.
+// Row r's channels [C*lane, C*lane + C) of a page, as loaded, and as pairs.
 template <int DTYPE, int D>
 struct BoundsRow {
   static constexpr int C = D / 32;
@@ -67,29 +70,57 @@ struct BoundsRow {
     }
   }
 
-  // the values (fp32, a NaN as 0)
-  __device__ __forceinline__ void values(float scale, float (&x)[C]) const {
+  __device__ __forceinline__ void pairs(uint32_t (&x)[C / 2]) const {
     if constexpr (DTYPE == PKV_DTYPE_BF16) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) x[i] = (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+      for (int i = 0; i < C / 2; ++i) x[i] = w[i];
     } else if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        x[i] = e4m3_f32(static_cast<uint8_t>(w[i / 4] >> (8 * (i & 3)))) * scale;
+      for (int i = 0; i < C / 2; ++i) x[i] = e4m3x2_f16x2_lo(w[i / 2] >> (16 * (i & 1)));
     } else {
       uint32_t f[4];
       e2m1x8_f16x2(w[0], f);
-      const float sf = e4m3_f32(s);
+      const uint32_t by = e4m3x2_f16x2_lo(s | (static_cast<uint32_t>(s) << 8));
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[i / 2]));
-        x[i] = ((i & 1) ? y.y : y.x) * sf * scale;
-      }
+      for (int i = 0; i < C / 2; ++i)
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[i]) : "r"(f[i]), "r"(by));
     }
-#pragma unroll
-    for (int i = 0; i < C; ++i) x[i] = x[i] == x[i] ? x[i] : 0.f;
   }
 };
+
+// Extremes of pairs: bf16 pairs if BF, else f16 ones.
+template <bool BF>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF)
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF>
+__device__ __forceinline__ float2 to_f32(uint32_t a) {
+  if constexpr (BF) return make_float2(bf16lo(a), bf16hi(a));
+  return __half22float2(*reinterpret_cast<const __half2*>(&a));
+}
 
 template <int DTYPE, int D, int BS>
 __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsParams p) {
@@ -120,35 +151,65 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
   constexpr int kPage = DTYPE == PKV_DTYPE_BF16       ? BS * D * 2
                         : DTYPE == PKV_DTYPE_FP8_E4M3 ? BS * D
                                                       : BS * D / 16 * 9;
+  constexpr bool BF = DTYPE == PKV_DTYPE_BF16;
   const uint8_t* page = p.k_cache + (static_cast<int64_t>(pb) * p.num_kv_heads + h) * kPage;
-  const float scale = DTYPE == PKV_DTYPE_BF16 ? 1.f : p.k_scale[h];
   using Row = BoundsRow<DTYPE, D>;
   constexpr int C = Row::C;
-  float lo[C], hi[C];
+  constexpr int kTogether = Row::kWords * BS <= 64 ? BS : 64 / Row::kWords;  // rows
+  constexpr uint32_t kPlus = BF ? 0x7F807F80u : 0x7C007C00u;                 // +inf twice
+  uint32_t lo[C / 2], hi[C / 2], any[C / 2];
 #pragma unroll
-  for (int i = 0; i < C; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
+  for (int i = 0; i < C / 2; ++i) {
+    lo[i] = kPlus;
+    hi[i] = any[i] = kPlus | 0x80008000u;
+  }
 #pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += 16) {
-    Row row[16];
+  for (int r0 = 0; r0 < rows; r0 += kTogether) {
+    Row row[kTogether];
     // rows behind the last cached one are read as that one once more
 #pragma unroll
-    for (int r = 0; r < 16; ++r) row[r].load(page, min(r0 + r, rows - 1), lane);
+    for (int r = 0; r < kTogether; ++r) row[r].load(page, min(r0 + r, rows - 1), lane);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float x[C];
-      row[r].values(scale, x);
+    for (int r = 0; r < kTogether; ++r) {
+      uint32_t x[C / 2];
+      row[r].pairs(x);
 #pragma unroll
-      for (int i = 0; i < C; ++i) lo[i] = fminf(lo[i], x[i]), hi[i] = fmaxf(hi[i], x[i]);
+      for (int i = 0; i < C / 2; ++i) {
+        lo[i] = min2<BF>(lo[i], x[i]);
+        hi[i] = max2<BF>(hi[i], x[i]);
+        any[i] = max2_nan<BF>(any[i], x[i]);
+      }
     }
   }
+  const float scale = BF ? 1.f : p.k_scale[h];
   const float step = p.step[h];
   uint32_t wl[(C + 3) / 4] = {}, wh[(C + 3) / 4] = {};
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const float a = fminf(fmaxf(floorf(__fdiv_rn(lo[i], step)), -127.f), 127.f);
-    const float b = fminf(fmaxf(ceilf(__fdiv_rn(hi[i], step)), -127.f), 127.f);
-    wl[i / 4] |= (static_cast<uint32_t>(static_cast<int>(a)) & 0xFFu) << (8 * (i & 3));
-    wh[i / 4] |= (static_cast<uint32_t>(static_cast<int>(b)) & 0xFFu) << (8 * (i & 3));
+    const float2 l2 = to_f32<BF>(lo[i / 2]), h2 = to_f32<BF>(hi[i / 2]);
+    const float2 a2 = to_f32<BF>(any[i / 2]);
+    float l = (i & 1) ? l2.y : l2.x, u = (i & 1) ? h2.y : h2.x;
+    const float a = (i & 1) ? a2.y : a2.x;
+    if (a != a) {  // a NaN counts as 0
+      l = fminf(l, 0.f);
+      u = fmaxf(u, 0.f);
+    }
+    if (!BF) {
+      // (infinities times a scale of 0 are NaN, which count as 0)
+      l *= scale;
+      u *= scale;
+      l = l == l ? l : 0.f;
+      u = u == u ? u : 0.f;
+      if (scale < 0.f) {
+        const float t = l;
+        l = u;
+        u = t;
+      }
+    }
+    const float x = fminf(fmaxf(floorf(__fdiv_rn(l, step)), -127.f), 127.f);
+    const float y = fminf(fmaxf(ceilf(__fdiv_rn(u, step)), -127.f), 127.f);
+    wl[i / 4] |= (static_cast<uint32_t>(static_cast<int>(x)) & 0xFFu) << (8 * (i & 3));
+    wh[i / 4] |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xFFu) << (8 * (i & 3));
   }
   int8_t* out = p.bounds + (static_cast<int64_t>(pb) * p.num_kv_heads + h) * (2 * D) + C * lane;
   if constexpr (C == 8) {

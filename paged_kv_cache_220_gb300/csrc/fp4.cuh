@@ -47,6 +47,13 @@ __device__ __forceinline__ uint32_t e2m1x2_of(float lo, float hi) {
   return d;
 }
 
+// The two E4M3 codes in the low 16 bits of w as f16x2 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_lo(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+  return h;
+}
+
 // One E4M3 code as fp32 (exact; NaN stays NaN).
 __device__ __forceinline__ float e4m3_f32(uint8_t x) {
   uint32_t h;

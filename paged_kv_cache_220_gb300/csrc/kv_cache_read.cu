@@ -1,9 +1,11 @@
 // kv_cache_read: the rows that given slots of a cache hold, as bf16.
 //
-// Thread (h, c8) of a token's threads reads channels [8*c8, 8*c8+8) of head h
-// from both pools (16, 8 or 4 bytes) and writes 16 bytes each: the reads and
-// writes of a warp are whole rows. Bound by HBM where there are many tokens, by
-// latency at a step's few.
+// Item i is channels [8 c8, 8 c8 + 8) of head h of a token, c8 fastest: 16, 8 or 4
+// bytes of each pool, 16 bytes of each result; a warp's are whole rows. Bound by HBM
+// where there are many tokens (U items to a thread, their loads in flight
+// together), by latency at a step's few.
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4.cuh"
 #include "host_util.h"
@@ -15,60 +17,103 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Channels [8*c8, 8*c8+8) of token `off` of a page.
+// Channels [8*c8, 8*c8+8) of token `off` of a page, as stored.
 template <int DTYPE, int D>
-__device__ __forceinline__ uint4 read8(const uint8_t* page, int off, int c8, float scale) {
-  if constexpr (DTYPE == PKV_DTYPE_BF16) {
-    return *reinterpret_cast<const uint4*>(page + (off * D + 8 * c8) * 2);
-  } else {
-    float x[8];
-    if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
-      const uint2 w = *reinterpret_cast<const uint2*>(page + off * D + 8 * c8);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = e4m3_f32(static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)))) * scale;
+struct Eight {
+  uint4 w;
+  uint8_t s;
+
+  __device__ __forceinline__ void load(const uint8_t* page, int off, int c8) {
+    if constexpr (DTYPE == PKV_DTYPE_BF16) {
+      w = *reinterpret_cast<const uint4*>(page + (off * D + 8 * c8) * 2);
+    } else if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
+      const uint2 x = *reinterpret_cast<const uint2*>(page + off * D + 8 * c8);
+      w = make_uint4(x.x, x.y, 0, 0);
     } else {
-      const uint32_t w =
-          *reinterpret_cast<const uint32_t*>(page + fp4_codes_at<D>(off) + 4 * c8);
-      const float s = e4m3_f32(page[fp4_scales_at<D>(off) + c8 / 2]);
+      w.x = *reinterpret_cast<const uint32_t*>(page + fp4_codes_at<D>(off) + 4 * c8);
+      s = page[fp4_scales_at<D>(off) + c8 / 2];
+    }
+  }
+
+  __device__ __forceinline__ uint4 values(float scale) const {
+    if constexpr (DTYPE == PKV_DTYPE_BF16) {
+      return w;
+    } else {
+      float x[8];
       uint32_t f[4];
-      e2m1x8_f16x2(w, f);
+      float by = 1.f;
+      if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
+        f[0] = e4m3x2_f16x2_lo(w.x), f[1] = e4m3x2_f16x2_lo(w.x >> 16);
+        f[2] = e4m3x2_f16x2_lo(w.y), f[3] = e4m3x2_f16x2_lo(w.y >> 16);
+      } else {
+        e2m1x8_f16x2(w.x, f);
+        by = e4m3_f32(s);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-        x[2 * i] = y.x * s * scale;  // y * s is exact
-        x[2 * i + 1] = y.y * s * scale;
+        x[2 * i] = y.x * by * scale;  // y * by is exact
+        x[2 * i + 1] = y.y * by * scale;
       }
+      return make_uint4(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]), bf16x2_of(x[4], x[5]),
+                        bf16x2_of(x[6], x[7]));
     }
-    return make_uint4(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]), bf16x2_of(x[4], x[5]),
-                      bf16x2_of(x[6], x[7]));
+  }
+};
+
+constexpr int kReadThreads = 256;
+
+template <int DTYPE, int D, int U>
+__global__ void __launch_bounds__(kReadThreads) kv_cache_read_kernel(
+    uint4* __restrict__ k, uint4* __restrict__ v, const int64_t* __restrict__ slot_mapping,
+    const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache, int64_t num_slots,
+    int log_block, int num_kv_heads, int64_t page_bytes, uint32_t items,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale, int* err) {
+  wait_prerequisite();
+  const uint32_t per_token = num_kv_heads * (D / 8);
+  const uint32_t first = blockIdx.x * (U * kReadThreads) + threadIdx.x;
+  Eight<DTYPE, D> ke[U], ve[U];
+  int rest[U];
+  bool live[U], some[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = first + u * kReadThreads;
+    live[u] = i < items;
+    const uint32_t token = live[u] ? i / per_token : 0;
+    rest[u] = live[u] ? static_cast<int>(i - token * per_token) : 0;
+    const int64_t slot = live[u] ? slot_mapping[token] : -1;
+    if (slot >= num_slots && rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
+    some[u] = slot >= 0 && slot < num_slots;
+    if (some[u]) {
+      const int64_t blk = slot >> log_block;
+      const int64_t page = (blk * num_kv_heads + rest[u] / (D / 8)) * page_bytes;
+      const int off = static_cast<int>(slot - (blk << log_block));
+      ke[u].load(k_cache + page, off, rest[u] % (D / 8));
+      ve[u].load(v_cache + page, off, rest[u] % (D / 8));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!live[u]) continue;
+    const int h = rest[u] / (D / 8);
+    const bool coded = DTYPE != PKV_DTYPE_BF16;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint32_t i = first + u * kReadThreads;
+    k[i] = some[u] ? ke[u].values(coded ? k_scale[h] : 1.f) : zero;
+    v[i] = some[u] ? ve[u].values(coded ? v_scale[h] : 1.f) : zero;
   }
 }
 
-template <int DTYPE, int D>
-__global__ void __launch_bounds__(1024) kv_cache_read_kernel(
-    uint4* __restrict__ k, uint4* __restrict__ v, const int64_t* __restrict__ slot_mapping,
-    const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache, int num_blocks,
-    int block_size, int num_kv_heads, int64_t page_bytes, const float* __restrict__ k_scale,
-    const float* __restrict__ v_scale, int* err) {
-  wait_prerequisite();
-  const int token = blockIdx.x;
-  const int h = threadIdx.x / (D / 8);
-  const int c8 = threadIdx.x % (D / 8);
-  const int64_t slot = slot_mapping[token];
-  const int64_t at = (static_cast<int64_t>(token) * num_kv_heads + h) * (D / 8) + c8;
-  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
-  if (slot >= static_cast<int64_t>(num_blocks) * block_size) {
-    if (threadIdx.x == 0) report_error(err, PKV_DEVERR_SLOT);
-  } else if (slot >= 0) {
-    const int64_t page = (slot / block_size * num_kv_heads + h) * page_bytes;
-    const int off = static_cast<int>(slot % block_size);
-    const bool coded = DTYPE != PKV_DTYPE_BF16;
-    kr = read8<DTYPE, D>(k_cache + page, off, c8, coded ? k_scale[h] : 1.f);
-    vr = read8<DTYPE, D>(v_cache + page, off, c8, coded ? v_scale[h] : 1.f);
-  }
-  k[at] = kr;
-  v[at] = vr;
+template <int DTYPE, int D, typename... Args>
+static int launch_read(int64_t items, cudaStream_t st, Args... args) {
+  auto go = [&](auto kern, int u) {
+    const int64_t per = static_cast<int64_t>(u) * kReadThreads;
+    return launch_dependent(kern, dim3(static_cast<unsigned>((items + per - 1) / per)),
+                            dim3(kReadThreads), 0, st, args...);
+  };
+  // four items to a thread once they fill the SMs (8 CTAs each)
+  return items >= 4 * 8 * 152 * kReadThreads ? go(kv_cache_read_kernel<DTYPE, D, 4>, 4)
+                                             : go(kv_cache_read_kernel<DTYPE, D, 1>, 1);
 }
 
 }  // namespace pkv
@@ -96,25 +141,26 @@ extern "C" int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, 
         overlap(w, rows, slot_mapping, slots))
       return PKV_ERR_INVALID_ARG;
   if (overlap(k, rows, v, rows)) return PKV_ERR_INVALID_ARG;
-  auto go = [&](auto kern) {
-    return launch_dependent(kern, dim3(num_tokens), dim3(threads), 0,
-                            static_cast<cudaStream_t>(stream), static_cast<uint4*>(k),
-                            static_cast<uint4*>(v), slot_mapping,
-                            static_cast<const uint8_t*>(k_cache),
-                            static_cast<const uint8_t*>(v_cache), cache.num_blocks,
-                            cache.block_size, cache.num_kv_heads, page_bytes(cache), k_scale,
-                            v_scale, device_error_ptr());
+  const int64_t items = static_cast<int64_t>(num_tokens) * threads;
+  if (items >= (int64_t{1} << 32) - 4 * kReadThreads) return PKV_ERR_UNSUPPORTED;
+  auto go = [&](auto launch) {
+    return launch(items, static_cast<cudaStream_t>(stream), static_cast<uint4*>(k),
+                  static_cast<uint4*>(v), slot_mapping, static_cast<const uint8_t*>(k_cache),
+                  static_cast<const uint8_t*>(v_cache),
+                  static_cast<int64_t>(cache.num_blocks) * cache.block_size,
+                  cache.block_size == 16 ? 4 : 5, cache.num_kv_heads, page_bytes(cache),
+                  static_cast<uint32_t>(items), k_scale, v_scale,
+                  device_error_ptr());
   };
   const bool wide = cache.head_dim == 256;
+  auto at = [&](auto dtype) {
+    constexpr int kType = decltype(dtype)::value;
+    return wide ? go([](auto... a) { return launch_read<kType, 256>(a...); })
+                : go([](auto... a) { return launch_read<kType, 128>(a...); });
+  };
   switch (cache.dtype) {
-    case PKV_DTYPE_BF16:
-      return wide ? go(kv_cache_read_kernel<PKV_DTYPE_BF16, 256>)
-                  : go(kv_cache_read_kernel<PKV_DTYPE_BF16, 128>);
-    case PKV_DTYPE_FP8_E4M3:
-      return wide ? go(kv_cache_read_kernel<PKV_DTYPE_FP8_E4M3, 256>)
-                  : go(kv_cache_read_kernel<PKV_DTYPE_FP8_E4M3, 128>);
-    default:
-      return wide ? go(kv_cache_read_kernel<PKV_DTYPE_FP4_E2M1, 256>)
-                  : go(kv_cache_read_kernel<PKV_DTYPE_FP4_E2M1, 128>);
+    case PKV_DTYPE_BF16: return at(std::integral_constant<int, PKV_DTYPE_BF16>{});
+    case PKV_DTYPE_FP8_E4M3: return at(std::integral_constant<int, PKV_DTYPE_FP8_E4M3>{});
+    default: return at(std::integral_constant<int, PKV_DTYPE_FP4_E2M1>{});
   }
 }

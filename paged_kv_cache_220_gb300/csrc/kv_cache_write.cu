@@ -77,69 +77,116 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// a / b rounded to nearest from r = 1/b rounded to nearest, by two corrections with
+// the exact remainder (Markstein, IBM J. Res. Dev. 34, 1990): the first leaves at most
+// one unit in the last place, the second none. Holds while b, r, the quotient and
+// the remainder's last bit are normal numbers.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  float q = a * r;
+  q = fmaf(fmaf(-b, q, a), r, q);
+  return fmaf(fmaf(-b, q, a), r, q);
+}
+
 // Eight channels of a row -> their codes (a word) and the scale of their 16; the
-// lane next to this one has the group's other eight.
-__device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, uint8_t& s_code) {
+// lane next to this one has the group's other eight. inv: 1 / scale; plain: scale is
+// in 2^-40 .. 2^40.
+//
+// 17 divisions to 8 channels are what this costs, so they are made from the
+// divisors' reciprocals where that is exact: with a scale as above and the group's
+// largest |x| in 2^-40 .. 2^60 all that count are far inside the normal numbers.
+// Channels that are smaller by 2^20 get the code 0 however y is rounded.
+__device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, float inv,
+                                                 bool plain, uint8_t& s_code) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float y[8];
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y[i] = __fdiv_rn((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale);
-    a = max_nan(a, fabsf(y[i]));
-  }
-  a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  s_code = static_cast<uint8_t>(
-      __nv_cvt_float_to_fp8(__fdiv_rn(a, 6.f), __NV_SATFINITE, __NV_E4M3));
-  const float s = e4m3_f32(s_code);
-  if (!(s > 0.f)) return 0;  // zero or NaN
-  uint32_t codes = 0;
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    codes |= e2m1x2_of(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * i);
+    top = max_nan(top, max_nan(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  float y[8], z[8];
+  if (plain && top >= 0x1p-40f && top <= 0x1p60f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] = quotient((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale, inv);
+    // rounded quotients grow with their numerators: the largest is the largest's
+    const float a = quotient(top, scale, inv);
+    s_code = static_cast<uint8_t>(
+        __nv_cvt_float_to_fp8(quotient(a, 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3));
+    const float s = e4m3_f32(s_code);
+    if (!(s > 0.f)) return 0;
+    const float inv_s = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = quotient(y[i], s, inv_s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] = __fdiv_rn((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale);
+    const float a = fabsf(__fdiv_rn(top, scale));
+    s_code = static_cast<uint8_t>(
+        __nv_cvt_float_to_fp8(__fdiv_rn(a, 6.f), __NV_SATFINITE, __NV_E4M3));
+    const float s = e4m3_f32(s_code);
+    if (!(s > 0.f)) return 0;  // zero or NaN
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __fdiv_rn(y[i], s);
+  }
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) codes |= e2m1x2_of(z[2 * i], z[2 * i + 1]) << (8 * i);
   return codes;
 }
 
-// 4-bit pools: thread (h, c8) has channels [8*c8, 8*c8+8) of a row; two threads
-// share a scale. Every warp has a whole row of a head (D = 256) or two (128).
-template <int D>
-__global__ void __launch_bounds__(1024) kv_cache_write_fp4_kernel(
+// 4-bit pools. Item i is channels [8 c8, 8 c8 + 8) of head h of a token, c8 fastest:
+// rows of k and v are read straight through, a thread U items THREADS apart with
+// their loads in flight together. Two lanes share a scale.
+constexpr int kFp4WriteThreads = 256;
+
+template <int D, int U>
+__global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
     const uint4* __restrict__ k, const uint4* __restrict__ v,
     const int64_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_cache,
-    uint8_t* __restrict__ v_cache, int num_blocks, int block_size, int num_kv_heads,
-    const float* __restrict__ k_scale, const float* __restrict__ v_scale, int* err) {
+    uint8_t* __restrict__ v_cache, int64_t num_slots, int log_block, int num_kv_heads,
+    uint32_t items, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+    int* err) {
   allow_dependents();
-  const int token = blockIdx.x;
-  const int64_t slot = slot_mapping[token];
-  if (slot < 0) return;
-  if (slot >= static_cast<int64_t>(num_blocks) * block_size) {
-    if (threadIdx.x == 0) report_error(err, PKV_DEVERR_SLOT);
-    return;
+  wait_prerequisite();
+  const uint32_t per_token = num_kv_heads * (D / 8);
+  const uint32_t first = blockIdx.x * (U * kFp4WriteThreads) + threadIdx.x;
+  int64_t slot[U];
+  int rest[U];
+  uint4 kv[U], vv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = first + u * kFp4WriteThreads;
+    const bool live = i < items;
+    const uint32_t token = live ? i / per_token : 0;
+    rest[u] = live ? static_cast<int>(i - token * per_token) : 0;
+    slot[u] = live ? slot_mapping[token] : -1;
+    kv[u] = live ? k[i] : make_uint4(0, 0, 0, 0);
+    vv[u] = live ? v[i] : make_uint4(0, 0, 0, 0);
   }
-  // blockDim.x is a multiple of a row's threads; whole rows fall out, so the
-  // two lanes of a group stay together (a warp's idle half at D = 128 takes
-  // part in the shuffle with zeros)
-  const int h = threadIdx.x / (D / 8);
-  const int c8 = threadIdx.x % (D / 8);
-  const bool live = h < num_kv_heads;
-  const int64_t blk = slot / block_size;
-  const int off = static_cast<int>(slot % block_size);
-  const int64_t page = (blk * num_kv_heads + h) * (block_size * (D / 16 * 9));
-  const int64_t src = (static_cast<int64_t>(token) * num_kv_heads + h) * (D / 8) + c8;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 kv = live ? k[src] : zero;
-  const uint4 vv = live ? v[src] : zero;
-  uint8_t ks, vs;
-  const uint32_t kc = quantize_fp4(kv, live ? k_scale[h] : 1.f, ks);
-  const uint32_t vc = quantize_fp4(vv, live ? v_scale[h] : 1.f, vs);
-  if (!live) return;
-  const int64_t codes = page + fp4_codes_at<D>(off) + 4 * c8;
-  *reinterpret_cast<uint32_t*>(k_cache + codes) = kc;
-  *reinterpret_cast<uint32_t*>(v_cache + codes) = vc;
-  if ((c8 & 1) == 0) {
-    const int64_t scales = page + fp4_scales_at<D>(off) + c8 / 2;
-    k_cache[scales] = ks;
-    v_cache[scales] = vs;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = rest[u] / (D / 8), c8 = rest[u] % (D / 8);
+    const float ks = k_scale[h], vs = v_scale[h];
+    uint8_t k8, v8;
+    const uint32_t kc = quantize_fp4(kv[u], ks, __frcp_rn(ks), ks >= 0x1p-40f && ks <= 0x1p40f, k8);
+    const uint32_t vc = quantize_fp4(vv[u], vs, __frcp_rn(vs), vs >= 0x1p-40f && vs <= 0x1p40f, v8);
+    if (slot[u] < 0) continue;
+    if (slot[u] >= num_slots) {
+      if (rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
+      continue;
+    }
+    const int64_t blk = slot[u] >> log_block;
+    const int off = static_cast<int>(slot[u] - (blk << log_block));
+    const int64_t page = ((blk * num_kv_heads + h) << log_block) * (D / 16 * 9);
+    const int64_t codes = page + fp4_codes_at<D>(off) + 4 * c8;
+    *reinterpret_cast<uint32_t*>(k_cache + codes) = kc;
+    *reinterpret_cast<uint32_t*>(v_cache + codes) = vc;
+    if ((c8 & 1) == 0) {
+      const int64_t scales = page + fp4_scales_at<D>(off) + c8 / 2;
+      k_cache[scales] = k8;
+      v_cache[scales] = v8;
+    }
   }
 }
 
@@ -168,10 +215,23 @@ extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* s
   auto* kc = static_cast<uint8_t*>(k_cache);
   auto* vc = static_cast<uint8_t*>(v_cache);
   if (fp4) {
-    auto kern = hd == 256 ? kv_cache_write_fp4_kernel<256> : kv_cache_write_fp4_kernel<128>;
-    kern<<<num_tokens, (threads + 31) / 32 * 32, 0, st>>>(
-        static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, kc, vc, nb, bs,
-        hk, k_scale, v_scale, device_error_ptr());
+    const int64_t items = static_cast<int64_t>(num_tokens) * threads;
+    if (items >= (int64_t{1} << 32) - 4 * kFp4WriteThreads) return PKV_ERR_UNSUPPORTED;
+    auto go = [&](auto kern, int u) {
+      const int64_t per = static_cast<int64_t>(u) * kFp4WriteThreads;
+      return launch_dependent(kern, dim3(static_cast<unsigned>((items + per - 1) / per)),
+                              dim3(kFp4WriteThreads), 0, st, static_cast<const uint4*>(k),
+                              static_cast<const uint4*>(v), slot_mapping, kc, vc,
+                              static_cast<int64_t>(nb) * bs, bs == 16 ? 4 : 5, hk,
+                              static_cast<uint32_t>(items), k_scale, v_scale,
+                              device_error_ptr());
+    };
+    // two items to a thread once they fill the SMs (8 CTAs each)
+    if (items >= 2 * 8 * 152 * kFp4WriteThreads)
+      return hd == 256 ? go(kv_cache_write_fp4_kernel<256, 2>, 2)
+                       : go(kv_cache_write_fp4_kernel<128, 2>, 2);
+    return hd == 256 ? go(kv_cache_write_fp4_kernel<256, 1>, 1)
+                     : go(kv_cache_write_fp4_kernel<128, 1>, 1);
   } else if (fp8)
     kv_cache_write_kernel<true><<<num_tokens, threads, 0, st>>>(
         static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, kc, vc, nb,
