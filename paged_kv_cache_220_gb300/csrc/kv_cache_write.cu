@@ -70,68 +70,103 @@ __global__ void __launch_bounds__(1024) kv_cache_write_kernel(
   }
 }
 
-// The larger of two, NaN if one is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+// The larger of each of two bf16 pairs, NaN if one is.
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// a / b rounded to nearest from r = 1/b rounded to nearest, by two corrections with
-// the exact remainder (Markstein, IBM J. Res. Dev. 34, 1990): the first leaves at most
-// one unit in the last place, the second none. Holds while b, r, the quotient and
-// the remainder's last bit are normal numbers.
-__device__ __forceinline__ float quotient(float a, float b, float r) {
-  float q = a * r;
-  q = fmaf(fmaf(-b, q, a), r, q);
-  return fmaf(fmaf(-b, q, a), r, q);
+// Two fp32 in one register pair, and their products and sums (each rounded as by
+// itself) in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// a / b from r = 1/b and minus_b = -b, by STEPS corrections with the exact remainder
+// (Markstein, IBM J. Res. Dev. 34, 1990). With r rounded to nearest the first leaves
+// less than a unit in the last place and the second nothing: the quotient is
+// rounded to nearest. Holds while b, r, the quotient and the remainder's last bit
+// are normal numbers.
+template <int STEPS>
+__device__ __forceinline__ uint64_t quotients(uint64_t a, uint64_t minus_b, uint64_t r) {
+  uint64_t q = mul_pair(a, r);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) q = fma_pair(fma_pair(minus_b, q, a), r, q);
+  return q;
 }
 
 // Eight channels of a row -> their codes (a word) and the scale of their 16; the
-// lane next to this one has the group's other eight. inv: 1 / scale; plain: scale is
-// in 2^-40 .. 2^40.
+// lane next to this one has the group's other eight. inv: 1 / scale to nearest;
+// plain: scale is in 2^-40 .. 2^40.
 //
-// 17 divisions to 8 channels are what this costs, so they are made from the
-// divisors' reciprocals where that is exact: with a scale as above and the group's
-// largest |x| in 2^-40 .. 2^60 all that count are far inside the normal numbers.
-// Channels that are smaller by 2^20 get the code 0 however y is rounded.
+// 17 divisions to 8 channels are what this costs, so they are made in pairs from
+// the divisors' reciprocals where that gives the same: with a scale as above and
+// the group's largest |x| in 2^-40 .. 2^60 all that count are far inside the normal
+// numbers. Channels smaller than that by 2^20 get the code 0 however y is rounded.
+// Of y / s only the side of a midpoint between two codes counts. s has 4
+// significant bits and a midpoint m 3, so m s is an fp32 number: y / s rounds to m only
+// if y = m s, the next y is off by at least 1.6 % of a unit in the last place more than
+// half a unit, and one correction of an approximate reciprocal's quotient, off by
+// 2^-20 of a unit before it is rounded, decides the same.
 __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, float inv,
                                                  bool plain, uint8_t& s_code) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    top = max_nan(top, max_nan(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
-  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  float y[8], z[8];
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t t2 = max2_nan(max2_nan(w[0] & kAbs, w[1] & kAbs), max2_nan(w[2] & kAbs, w[3] & kAbs));
+  t2 = max2_nan(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
+  const float top = bf16lo(max2_nan(t2, t2 >> 16));
+  uint32_t codes = 0;
   if (plain && top >= 0x1p-40f && top <= 0x1p60f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] = quotient((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale, inv);
+    const uint64_t r = pair_of(inv, inv), b = pair_of(-scale, -scale);
     // rounded quotients grow with their numerators: the largest is the largest's
-    const float a = quotient(top, scale, inv);
-    s_code = static_cast<uint8_t>(
-        __nv_cvt_float_to_fp8(quotient(a, 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3));
+    const float a = of_pair(quotients<2>(pair_of(top, top), b, r)).x;
+    constexpr float kSixth = 1.f / 6.f;
+    const float a6 = of_pair(quotients<2>(pair_of(a, a), pair_of(-6.f, -6.f),
+                                          pair_of(kSixth, kSixth))).x;
+    s_code = static_cast<uint8_t>(__nv_cvt_float_to_fp8(a6, __NV_SATFINITE, __NV_E4M3));
     const float s = e4m3_f32(s_code);
     if (!(s > 0.f)) return 0;
-    const float inv_s = __frcp_rn(s);
+    float inv_s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(s));
+    const uint64_t rs = pair_of(inv_s, inv_s), bs = pair_of(-s, -s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = quotient(y[i], s, inv_s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] = __fdiv_rn((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale);
-    const float a = fabsf(__fdiv_rn(top, scale));
-    s_code = static_cast<uint8_t>(
-        __nv_cvt_float_to_fp8(__fdiv_rn(a, 6.f), __NV_SATFINITE, __NV_E4M3));
-    const float s = e4m3_f32(s_code);
-    if (!(s > 0.f)) return 0;  // zero or NaN
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = __fdiv_rn(y[i], s);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t y = quotients<2>(pair_of(bf16lo(w[i]), bf16hi(w[i])), b, r);
+      const float2 z = of_pair(quotients<1>(y, bs, rs));
+      // (a correction turns -0 into 0; the quotient has x's sign)
+      const float lo = __uint_as_float(__float_as_uint(z.x) | ((w[i] << 16) & 0x80000000u));
+      const float hi = __uint_as_float(__float_as_uint(z.y) | (w[i] & 0x80000000u));
+      codes |= e2m1x2_of(lo, hi) << (8 * i);
+    }
+    return codes;
   }
-  uint32_t codes = 0;
+  s_code = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
+      __fdiv_rn(fabsf(__fdiv_rn(top, scale)), 6.f), __NV_SATFINITE, __NV_E4M3));
+  const float s = e4m3_f32(s_code);
+  if (!(s > 0.f)) return 0;  // zero or NaN
 #pragma unroll
-  for (int i = 0; i < 4; ++i) codes |= e2m1x2_of(z[2 * i], z[2 * i + 1]) << (8 * i);
+  for (int i = 0; i < 4; ++i)
+    codes |= e2m1x2_of(__fdiv_rn(__fdiv_rn(bf16lo(w[i]), scale), s),
+                       __fdiv_rn(__fdiv_rn(bf16hi(w[i]), scale), s))
+             << (8 * i);
   return codes;
 }
 
@@ -147,8 +182,15 @@ __global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
     uint8_t* __restrict__ v_cache, int64_t num_slots, int log_block, int num_kv_heads,
     uint32_t items, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
     int* err) {
+  // the heads' scales and their reciprocals
+  __shared__ float2 by[2][32];
   allow_dependents();
   wait_prerequisite();
+  if (threadIdx.x < 2 * num_kv_heads) {
+    const int h = threadIdx.x >> 1;
+    const float x = (threadIdx.x & 1) ? v_scale[h] : k_scale[h];
+    by[threadIdx.x & 1][h] = make_float2(x, __frcp_rn(x));
+  }
   const uint32_t per_token = num_kv_heads * (D / 8);
   const uint32_t first = blockIdx.x * (U * kFp4WriteThreads) + threadIdx.x;
   int64_t slot[U];
@@ -164,13 +206,16 @@ __global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
     kv[u] = live ? k[i] : make_uint4(0, 0, 0, 0);
     vv[u] = live ? v[i] : make_uint4(0, 0, 0, 0);
   }
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = rest[u] / (D / 8), c8 = rest[u] % (D / 8);
-    const float ks = k_scale[h], vs = v_scale[h];
+    const float2 kb = by[0][h], vb = by[1][h];
     uint8_t k8, v8;
-    const uint32_t kc = quantize_fp4(kv[u], ks, __frcp_rn(ks), ks >= 0x1p-40f && ks <= 0x1p40f, k8);
-    const uint32_t vc = quantize_fp4(vv[u], vs, __frcp_rn(vs), vs >= 0x1p-40f && vs <= 0x1p40f, v8);
+    const uint32_t kc =
+        quantize_fp4(kv[u], kb.x, kb.y, kb.x >= 0x1p-40f && kb.x <= 0x1p40f, k8);
+    const uint32_t vc =
+        quantize_fp4(vv[u], vb.x, vb.y, vb.x >= 0x1p-40f && vb.x <= 0x1p40f, v8);
     if (slot[u] < 0) continue;
     if (slot[u] >= num_slots) {
       if (rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);

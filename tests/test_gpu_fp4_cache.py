@@ -64,6 +64,37 @@ def test_write_is_the_definition(d, block, hk, n, _lib):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("scale", [1.0, 1 / 64, 0.0123, 3e-13, 9e11, 2e-38, 3e37, -0.37])
+def test_every_size_of_row(scale, _lib):
+    """Rows of every exponent, in groups whose largest is any bf16 and the others
+    anything below it, zeros of both signs among them; scales on both sides of
+    what the quick division takes."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    n, d = 4096, 128
+    bits = torch.randint(0, 1 << 15, (n, 8, d // 16, 16), device="cuda", generator=g)
+    bits = torch.where(bits >= 0x7F80, bits - 0x7F80, bits)  # finite
+    top = bits[..., :1]
+    near = top - torch.randint(0, 900, bits.shape, device="cuda", generator=g)
+    bits = torch.where(torch.rand(bits.shape, device="cuda", generator=g) < 0.8, near, bits % (
+        top + 1)).clamp(min=0)
+    bits = torch.where(torch.rand(bits.shape, device="cuda", generator=g) < 0.05, 0, bits)
+    bits = bits | torch.randint(0, 2, bits.shape, device="cuda", generator=g) << 15
+    x = bits.to(torch.int32).to(torch.int16).view(torch.bfloat16).view(n, 8, d)
+    ks = scale * (1 + torch.rand(8, device="cuda", generator=g))
+    ks[0], ks[1] = scale, scale * 0.5
+    kc = pkv.fp4_cache(n // 32, 8, 32, d)
+    vc = torch.zeros_like(kc)
+    slots = torch.randperm(n, device="cuda", generator=g)
+    pkv.kv_cache_write(x, -x, slots, kc, vc, ks, ks)
+    for pool, y in ((kc, x), (vc, -x)):
+        codes, scales = at_slots(pool, slots, d)
+        want_c, want_s = quantize(y, ks)
+        assert torch.equal(scales, want_s)
+        assert torch.equal(codes, want_c)
+    assert int(_lib.item()) == 0
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_write_of_special_values(d, _lib):
     """Zeros, groups too small for a scale, infinities, NaN, largest values and
