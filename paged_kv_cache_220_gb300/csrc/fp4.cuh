@@ -35,15 +35,18 @@ __device__ __forceinline__ void e2m1x8_f16x2(uint32_t w, uint32_t (&o)[4]) {
       : "r"(w));
 }
 
-// Two fp32 -> a byte of two E2M1 codes, `lo` in its low half (nearest, ties to
-// the even code, saturating).
-__device__ __forceinline__ uint32_t e2m1x2_of(float lo, float hi) {
+// Eight fp32 -> a word of E2M1 codes, the first in its lowest four bits (nearest, ties
+// to the even code, saturating).
+__device__ __forceinline__ uint32_t e2m1x8_of(const float (&x)[8]) {
   uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, e;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 e, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, e};\n\t}"
       : "=r"(d)
-      : "f"(lo), "f"(hi));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return d;
 }
 
@@ -60,5 +63,27 @@ __device__ __forceinline__ float e4m3_f32(uint8_t x) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(x)));
   return __low2float(*reinterpret_cast<__half2*>(&h));
 }
+
+// The token of item i of rows with `per` items each and the item in its row, for i
+// = first, first + step, ..: one division to start with.
+struct RowItems {
+  uint32_t per, step_token, step_rest, token, rest;
+
+  __device__ __forceinline__ RowItems(uint32_t first, uint32_t step, uint32_t per_row) {
+    per = per_row;
+    step_token = step / per;
+    step_rest = step - step_token * per;
+    token = first / per;
+    rest = first - token * per;
+  }
+  __device__ __forceinline__ void next() {
+    token += step_token;
+    rest += step_rest;
+    if (rest >= per) {
+      rest -= per;
+      ++token;
+    }
+  }
+};
 
 }  // namespace pkv

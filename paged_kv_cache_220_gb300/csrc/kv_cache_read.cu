@@ -39,24 +39,23 @@ struct Eight {
     if constexpr (DTYPE == PKV_DTYPE_BF16) {
       return w;
     } else {
-      float x[8];
-      uint32_t f[4];
-      float by = 1.f;
+      uint32_t f[4], out[4];
       if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
         f[0] = e4m3x2_f16x2_lo(w.x), f[1] = e4m3x2_f16x2_lo(w.x >> 16);
         f[2] = e4m3x2_f16x2_lo(w.y), f[3] = e4m3x2_f16x2_lo(w.y >> 16);
       } else {
+        // code * s is an f16 number
         e2m1x8_f16x2(w.x, f);
-        by = e4m3_f32(s);
+        const uint32_t by = e4m3x2_f16x2_lo(s | (static_cast<uint32_t>(s) << 8));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(f[i]) : "r"(by));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-        x[2 * i] = y.x * by * scale;  // y * by is exact
-        x[2 * i + 1] = y.y * by * scale;
+        out[i] = bf16x2_of(y.x * scale, y.y * scale);
       }
-      return make_uint4(bf16x2_of(x[0], x[1]), bf16x2_of(x[2], x[3]), bf16x2_of(x[4], x[5]),
-                        bf16x2_of(x[6], x[7]));
+      return make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 };
@@ -70,8 +69,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_cache_read_kernel(
     int log_block, int num_kv_heads, int64_t page_bytes, uint32_t items,
     const float* __restrict__ k_scale, const float* __restrict__ v_scale, int* err) {
   wait_prerequisite();
-  const uint32_t per_token = num_kv_heads * (D / 8);
   const uint32_t first = blockIdx.x * (U * kReadThreads) + threadIdx.x;
+  RowItems at(first, kReadThreads, num_kv_heads * (D / 8));
   Eight<DTYPE, D> ke[U], ve[U];
   int rest[U];
   bool live[U], some[U];
@@ -79,9 +78,9 @@ __global__ void __launch_bounds__(kReadThreads) kv_cache_read_kernel(
   for (int u = 0; u < U; ++u) {
     const uint32_t i = first + u * kReadThreads;
     live[u] = i < items;
-    const uint32_t token = live[u] ? i / per_token : 0;
-    rest[u] = live[u] ? static_cast<int>(i - token * per_token) : 0;
-    const int64_t slot = live[u] ? slot_mapping[token] : -1;
+    rest[u] = at.rest;
+    const int64_t slot = live[u] ? slot_mapping[at.token] : -1;
+    at.next();
     if (slot >= num_slots && rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
     some[u] = slot >= 0 && slot < num_slots;
     if (some[u]) {

@@ -133,7 +133,7 @@ __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, fl
   uint32_t t2 = max2_nan(max2_nan(w[0] & kAbs, w[1] & kAbs), max2_nan(w[2] & kAbs, w[3] & kAbs));
   t2 = max2_nan(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
   const float top = bf16lo(max2_nan(t2, t2 >> 16));
-  uint32_t codes = 0;
+  float z8[8];
   if (plain && top >= 0x1p-40f && top <= 0x1p60f) {
     const uint64_t r = pair_of(inv, inv), b = pair_of(-scale, -scale);
     // rounded quotients grow with their numerators: the largest is the largest's
@@ -152,22 +152,19 @@ __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, fl
       const uint64_t y = quotients<2>(pair_of(bf16lo(w[i]), bf16hi(w[i])), b, r);
       const float2 z = of_pair(quotients<1>(y, bs, rs));
       // (a correction turns -0 into 0; the quotient has x's sign)
-      const float lo = __uint_as_float(__float_as_uint(z.x) | ((w[i] << 16) & 0x80000000u));
-      const float hi = __uint_as_float(__float_as_uint(z.y) | (w[i] & 0x80000000u));
-      codes |= e2m1x2_of(lo, hi) << (8 * i);
+      z8[2 * i] = __uint_as_float(__float_as_uint(z.x) | ((w[i] << 16) & 0x80000000u));
+      z8[2 * i + 1] = __uint_as_float(__float_as_uint(z.y) | (w[i] & 0x80000000u));
     }
-    return codes;
+    return e2m1x8_of(z8);
   }
   s_code = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
       __fdiv_rn(fabsf(__fdiv_rn(top, scale)), 6.f), __NV_SATFINITE, __NV_E4M3));
   const float s = e4m3_f32(s_code);
   if (!(s > 0.f)) return 0;  // zero or NaN
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    codes |= e2m1x2_of(__fdiv_rn(__fdiv_rn(bf16lo(w[i]), scale), s),
-                       __fdiv_rn(__fdiv_rn(bf16hi(w[i]), scale), s))
-             << (8 * i);
-  return codes;
+  for (int i = 0; i < 8; ++i)
+    z8[i] = __fdiv_rn(__fdiv_rn((i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]), scale), s);
+  return e2m1x8_of(z8);
 }
 
 // 4-bit pools. Item i is channels [8 c8, 8 c8 + 8) of head h of a token, c8 fastest:
@@ -191,8 +188,8 @@ __global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
     const float x = (threadIdx.x & 1) ? v_scale[h] : k_scale[h];
     by[threadIdx.x & 1][h] = make_float2(x, __frcp_rn(x));
   }
-  const uint32_t per_token = num_kv_heads * (D / 8);
   const uint32_t first = blockIdx.x * (U * kFp4WriteThreads) + threadIdx.x;
+  RowItems at(first, kFp4WriteThreads, num_kv_heads * (D / 8));
   int64_t slot[U];
   int rest[U];
   uint4 kv[U], vv[U];
@@ -200,9 +197,9 @@ __global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
   for (int u = 0; u < U; ++u) {
     const uint32_t i = first + u * kFp4WriteThreads;
     const bool live = i < items;
-    const uint32_t token = live ? i / per_token : 0;
-    rest[u] = live ? static_cast<int>(i - token * per_token) : 0;
-    slot[u] = live ? slot_mapping[token] : -1;
+    rest[u] = at.rest;
+    slot[u] = live ? slot_mapping[at.token] : -1;
+    at.next();
     kv[u] = live ? k[i] : make_uint4(0, 0, 0, 0);
     vv[u] = live ? v[i] : make_uint4(0, 0, 0, 0);
   }
