@@ -14,6 +14,12 @@
 // them. The second takes one CTA per (sequence, KV head): the scores go to shared
 // memory, a histogram over the range that is left finds the lowest chosen score
 // in two or three rounds, and ballots over runs of blocks write the list in order.
+//
+// Measured: 64 x 8192 tokens (B = 16, 4 heads, d = 256) 20.4 us, 8 x 131072 (B = 32)
+// 22.4 us, of which HBM has 10 us and the second kernel 5 to 7; the rest is the chain
+// of a CTA's loads (length, table, bounds) at the start of the first. Four heads to
+// a CTA, whose bounds of a block are one run, took longer (25, 27 us): 128
+// registers, and the queries' sums of four heads before the first product.
 #include <algorithm>
 
 #include "common.cuh"
@@ -49,121 +55,151 @@ constexpr int kScoreThreads = 128;
 constexpr int kScoreLanes = 8;                            // lanes to a block
 constexpr int kScoreStep = kScoreThreads / kScoreLanes;   // blocks of a CTA at a time
 
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads)
-    block_scores_kernel(const SelectParams p, int chunk) {
+// STEPS * kScoreStep blocks of one pair to a CTA. The table's entries are asked for
+// first, then the first bounds, and the query is made into whole numbers while
+// those are on their way.
+template <int D, int STEPS>
+__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectParams p) {
   constexpr int NV = D / (16 * kScoreLanes);  // 16-byte pieces of lo (and of hi) to a lane
   constexpr int CT = D / kScoreThreads;       // channels of a thread in the query's sums
+  constexpr int U = STEPS < 2 ? STEPS : 2;    // blocks of a lane whose loads are in flight
   __shared__ float red[kScoreThreads / 32];
-  __shared__ int16_t up[D], down[D];
+  __shared__ __align__(16) int16_t up[D], down[D];
   wait_prerequisite();
   const int h = blockIdx.x % p.num_kv_heads;
   const int s = blockIdx.y;
   const int tid = threadIdx.x;
   const int n = context_blocks(p, s, tid == 0 && blockIdx.x == 0);
-  const int b0 = blockIdx.x / p.num_kv_heads * chunk;
+  const int b0 = blockIdx.x / p.num_kv_heads * (STEPS * kScoreStep);
   if (n <= p.max_selected || b0 >= n) return;  // all of them are chosen, or none is here
-  const int b1 = min(n, b0 + chunk);
+  const int g8 = tid % kScoreLanes;
+  const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
+  const int mine = b0 + tid / kScoreLanes;  // this lane's first block
+  int id[STEPS];
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const int i = mine + k * kScoreStep;
+    id[k] = i < n ? table[i] : 0;
+  }
+  // the queries' channels of this thread, a head after another
+  const uint16_t* q =
+      p.q + (static_cast<int64_t>(s) * p.num_kv_heads + h) * p.group * D + tid * CT;
+  float x[8][CT];
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      x[j][i] = j < p.group ? bf16lo(q[j * D + i]) : 0.f;
+      top = fmaxf(top, fabsf(x[j][i]));
+    }
+  uint4 lo[U][NV], hi[U][NV];
+  auto load = [&](int k) {
+    const bool ok = id[k] >= 0 && id[k] < p.num_blocks;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.bounds + (static_cast<int64_t>(ok ? id[k] : 0) * p.num_kv_heads + h) * (2 * D));
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      lo[k % U][v] = __ldg(src + v * kScoreLanes + g8);
+      hi[k % U][v] = __ldg(src + D / 16 + v * kScoreLanes + g8);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < U; ++k) load(k);
 
   // ---- the group's queries as whole numbers, summed by sign
-  const uint16_t* q = p.q + (static_cast<int64_t>(s) * p.num_kv_heads + h) * p.group * D;
-  float top = 0.f;
-  for (int j = 0; j < p.group; ++j)
-#pragma unroll
-    for (int i = 0; i < CT; ++i)
-      top = fmaxf(top, fabsf(bf16lo(q[j * D + tid * CT + i])));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   if ((tid & 31) == 0) red[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kScoreThreads / 32; ++w) top = fmaxf(top, red[w]);
-  int u[CT] = {}, w[CT] = {};
-  if (top > 0.f)
-    for (int j = 0; j < p.group; ++j)
-#pragma unroll
-      for (int i = 0; i < CT; ++i) {
-        // x * 127 is exact, the quotient rounded once: an exact tie stays one
-        const float c = rintf(__fdiv_rn(bf16lo(q[j * D + tid * CT + i]) * 127.f, top));
-        const int k = c == c ? static_cast<int>(fminf(fmaxf(c, -127.f), 127.f)) : 0;
-        u[i] += max(k, 0);
-        w[i] += min(k, 0);
-      }
 #pragma unroll
   for (int i = 0; i < CT; ++i) {
-    up[tid * CT + i] = static_cast<int16_t>(u[i]);
-    down[tid * CT + i] = static_cast<int16_t>(w[i]);
+    int u = 0, w = 0;
+    if (top > 0.f)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= p.group) break;
+        // x * 127 is exact, the quotient rounded once: an exact tie stays one
+        const float c = rintf(__fdiv_rn(x[j][i] * 127.f, top));
+        const int k = c == c ? static_cast<int>(fminf(fmaxf(c, -127.f), 127.f)) : 0;
+        u += max(k, 0);
+        w += min(k, 0);
+      }
+    up[tid * CT + i] = static_cast<int16_t>(u);
+    down[tid * CT + i] = static_cast<int16_t>(w);
   }
   __syncthreads();
 
   // ---- this lane's channels: pieces g8, g8 + 8, .. of 16 channels
-  const int g8 = tid % kScoreLanes;
   int cu[NV][8], cw[NV][8];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * kScoreLanes + g8) * 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = (v * kScoreLanes + g8) * 16 + 2 * i;
-      cu[v][i] = *reinterpret_cast<const int*>(&up[c]);
-      cw[v][i] = *reinterpret_cast<const int*>(&down[c]);
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<int4*>(&cu[v][4 * i]) = *reinterpret_cast<const int4*>(&up[c + 8 * i]);
+      *reinterpret_cast<int4*>(&cw[v][4 * i]) = *reinterpret_cast<const int4*>(&down[c + 8 * i]);
     }
-  const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
+  }
   int32_t* scores = p.scores + (static_cast<int64_t>(s) * p.num_kv_heads + h) * p.blocks_max;
-  constexpr int U = 2;  // blocks of a lane whose loads are in flight together
-  for (int i0 = b0 + tid / kScoreLanes; i0 < b0 + chunk; i0 += U * kScoreStep) {
-    uint4 lo[U][NV], hi[U][NV];
-    bool ok[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + k * kScoreStep;
-      const int32_t pb = i < b1 ? table[i] : -1;
-      ok[k] = pb >= 0 && pb < p.num_blocks;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.bounds + (static_cast<int64_t>(ok[k] ? pb : 0) * p.num_kv_heads + h) * (2 * D));
+  for (int k = 0; k < STEPS; ++k) {
+    int sum = 0;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        lo[k][v] = __ldg(src + v * kScoreLanes + g8);
-        hi[k][v] = __ldg(src + D / 16 + v * kScoreLanes + g8);
+    for (int v = 0; v < NV; ++v) {
+      const uint4 l = lo[k % U][v], u = hi[k % U][v];
+      const int wl[4] = {static_cast<int>(l.x), static_cast<int>(l.y), static_cast<int>(l.z),
+                         static_cast<int>(l.w)};
+      const int wh[4] = {static_cast<int>(u.x), static_cast<int>(u.y), static_cast<int>(u.z),
+                         static_cast<int>(u.w)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum = __dp2a_lo(cu[v][2 * i], wh[i], sum);
+        sum = __dp2a_hi(cu[v][2 * i + 1], wh[i], sum);
+        sum = __dp2a_lo(cw[v][2 * i], wl[i], sum);
+        sum = __dp2a_hi(cw[v][2 * i + 1], wl[i], sum);
       }
     }
+    if (k + U < STEPS) load(k + U);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      int sum = 0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int wl[4] = {static_cast<int>(lo[k][v].x), static_cast<int>(lo[k][v].y),
-                           static_cast<int>(lo[k][v].z), static_cast<int>(lo[k][v].w)};
-        const int wh[4] = {static_cast<int>(hi[k][v].x), static_cast<int>(hi[k][v].y),
-                           static_cast<int>(hi[k][v].z), static_cast<int>(hi[k][v].w)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum = __dp2a_lo(cu[v][2 * i], wh[i], sum);
-          sum = __dp2a_hi(cu[v][2 * i + 1], wh[i], sum);
-          sum = __dp2a_lo(cw[v][2 * i], wl[i], sum);
-          sum = __dp2a_hi(cw[v][2 * i + 1], wl[i], sum);
-        }
-      }
-#pragma unroll
-      for (int off = 1; off < kScoreLanes; off <<= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const int i = i0 + k * kScoreStep;
-      if (g8 == 0 && i < b1) {
-        if (!ok[k]) report_error(p.err, PKV_DEVERR_BLOCK_ID);
-        scores[i] = ok[k] ? sum : INT32_MIN;
-      }
+    for (int off = 1; off < kScoreLanes; off <<= 1)
+      sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const int i = mine + k * kScoreStep;
+    if (g8 == 0 && i < n) {
+      const bool ok = id[k] >= 0 && id[k] < p.num_blocks;
+      if (!ok) report_error(p.err, PKV_DEVERR_BLOCK_ID);
+      scores[i] = ok ? sum : INT32_MIN;
     }
   }
   allow_dependents();
 }
 
-constexpr int kSelectBins = 1024;
+template <int D>
+static int launch_scores(const SelectParams& p, int num_seqs, cudaStream_t st) {
+  // 128 blocks to a CTA, or 32 where that gives fewer than three CTAs to an SM (1 x 32768
+  // tokens, 2 heads: 7.8 us; 64 x 8192, 4 heads: 20.4 us with 128, 22.0 with 32)
+  const int64_t pairs = static_cast<int64_t>(num_seqs) * p.num_kv_heads;
+  const bool large = (p.blocks_max + 127) / 128 * pairs >= 456;
+  const int64_t blocks = large ? 128 : 32;
+  const int64_t gx = (p.blocks_max + blocks - 1) / blocks * p.num_kv_heads;
+  const dim3 grid(static_cast<unsigned>(gx), num_seqs);
+  return large ? launch_dependent(block_scores_kernel<D, 8>, grid, dim3(kScoreThreads), 0, st, p)
+               : launch_dependent(block_scores_kernel<D, 2>, grid, dim3(kScoreThreads), 0, st, p);
+}
+
+// Bins of a round: two rounds for the 2^22 different scores that a context has at most
+// in practice (their range is below 2^27, three rounds)
+constexpr int kSelectBins = 2048;
 constexpr int kSelectSmem = 192 * 1024;  // scores of up to 49152 blocks
 
 template <int T>
 __global__ void __launch_bounds__(T) select_kernel(const SelectParams p, bool staged) {
   constexpr int W = T / 32;
+  constexpr int BT = kSelectBins / T;  // bins of a thread
   extern __shared__ uint32_t keys_sh[];
-  __shared__ int hist[kSelectBins];
+  __shared__ __align__(16) int hist[kSelectBins];
   __shared__ uint32_t red_lo[W], red_hi[W];
   __shared__ int seg_over[W], seg_equal[W];
   __shared__ int found_bin, found_need, found_in;
@@ -186,6 +222,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p, bool st
   };
   const int c0 = p.first, c1 = n - p.last;  // [c0, c1): by their score
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll 4
   for (int i = tid; i < n; i += T) {
     const uint32_t k = static_cast<uint32_t>(scores[i]) ^ 0x80000000u;
     if (staged) keys_sh[i] = k;
@@ -194,6 +231,8 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p, bool st
       hi = max(hi, k);
     }
   }
+#pragma unroll
+  for (int i = 0; i < BT; ++i) hist[tid * BT + i] = 0;
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
@@ -212,33 +251,47 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p, bool st
   int equal = 0;
   while (need > 0) {
     const int bits = 32 - __clz(hi - lo);
-    const int shift = bits > 10 ? bits - 10 : 0;
-    for (int i = tid; i < kSelectBins; i += T) hist[i] = 0;
-    __syncthreads();
+    const int shift = bits > 11 ? bits - 11 : 0;
     for (int i = c0 + tid; i < c1; i += T) {
       const uint32_t k = key(i);
       if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
     }
     __syncthreads();
-    if (warp == 0) {
-      // lane l has bins [32 l, 32 l + 32); from the top
-      int sum = 0;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) sum += hist[lane * 32 + ((i + lane) & 31)];
-      int above = sum;  // of this lane's bins and those above
+    // from the top: thread t has bins [BT t, BT t + BT); how many keys lie above them
+    int mine[BT], sum = 0;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_down_sync(0xffffffffu, above, off);
-        if (lane + off < 32) above += x;
-      }
-      if (above >= need && above - sum < need) {
-        int left = need - (above - sum);
-        int b = lane * 32 + 31;
-        while (hist[b] < left) left -= hist[b--];
-        found_bin = b;
-        found_need = left;
-        found_in = hist[b];
-      }
+    for (int i = 0; i < BT; ++i) {
+      mine[i] = hist[tid * BT + i];
+      sum += mine[i];
+    }
+    int above = sum;  // of this thread's bins and those above, in the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_down_sync(0xffffffffu, above, off);
+      if (lane + off < 32) above += x;
+    }
+    if (lane == 0) seg_over[warp] = above;
+    __syncthreads();
+    // the bins are read: ready for the next round
+#pragma unroll
+    for (int i = 0; i < BT; ++i) hist[tid * BT + i] = 0;
+    for (int w = warp + 1; w < W; ++w) above += seg_over[w];
+    above -= sum;
+    if (above < need && above + sum >= need) {
+      int left = need - above;
+      int b = BT - 1;
+#pragma unroll
+      for (int i = BT - 1; i > 0; --i)
+        if (b == i && mine[i] < left) {
+          left -= mine[i];
+          b = i - 1;
+        }
+      int in = mine[0];
+#pragma unroll
+      for (int i = 1; i < BT; ++i) in = b == i ? mine[i] : in;
+      found_bin = tid * BT + b;
+      found_need = left;
+      found_in = in;
     }
     __syncthreads();
     lo += static_cast<uint32_t>(found_bin) << shift;
@@ -363,22 +416,17 @@ extern "C" int pkv_select_blocks(int32_t* blocks, int32_t* counts, const void* q
   p.block_size = cache.block_size;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p.blocks_max > max_selected) {
-    const int64_t chunk = 128;
-    const int64_t gx = (p.blocks_max + chunk - 1) / chunk * cache.num_kv_heads;
-    const dim3 grid(static_cast<unsigned>(gx), num_seqs);
-    rc = cache.head_dim == 256
-             ? launch_dependent(block_scores_kernel<256>, grid, dim3(kScoreThreads), 0, st, p,
-                                static_cast<int>(chunk))
-             : launch_dependent(block_scores_kernel<128>, grid, dim3(kScoreThreads), 0, st, p,
-                                static_cast<int>(chunk));
+    rc = cache.head_dim == 256 ? launch_scores<256>(p, num_seqs, st)
+                               : launch_scores<128>(p, num_seqs, st);
     if (rc != PKV_OK) return rc;
   }
   const size_t smem = static_cast<size_t>(p.blocks_max) * 4;
   const bool staged = smem <= kSelectSmem;
   const dim3 grid(cache.num_kv_heads, num_seqs);
-  if (p.blocks_max <= 4096) {
+  // few warps pass a barrier sooner, more have fewer blocks each (8 x 4096 blocks, 4
+  // heads, with the scores: 24.5 us with 256 threads, 22.4 with 1024; 64 x 512: 20.4, 22)
+  if (p.blocks_max <= 1024)
     return launch_dependent(select_kernel<256>, grid, dim3(256), smem, st, p, staged);
-  }
   static DeviceFlags done;
   rc = ensure_smem(select_kernel<1024>, kSelectSmem, done);
   if (rc != PKV_OK) return rc;
