@@ -15,8 +15,8 @@
 // memory, a histogram over the range that is left finds the lowest chosen score
 // in two or three rounds, and ballots over runs of blocks write the list in order.
 //
-// Measured: 64 x 8192 tokens (B = 16, 4 heads, d = 256) 20.4 us, 8 x 131072 (B = 32)
-// 22.4 us, of which HBM has 10 us and the second kernel 5 to 7; the rest is the chain
+// Measured: 64 x 8192 tokens (B = 16, 4 heads, d = 256) 19.5 us, 8 x 131072 (B = 32)
+// 21.2 us, of which HBM has 10 us and the second kernel 5 to 7; the rest is the chain
 // of a CTA's loads (length, table, bounds) at the start of the first. Four heads to
 // a CTA, whose bounds of a block are one run, took longer (25, 27 us): 128
 // registers, and the queries' sums of four heads before the first product.
@@ -55,11 +55,12 @@ constexpr int kScoreThreads = 128;
 constexpr int kScoreLanes = 8;                            // lanes to a block
 constexpr int kScoreStep = kScoreThreads / kScoreLanes;   // blocks of a CTA at a time
 
-// STEPS * kScoreStep blocks of one pair to a CTA. The table's entries are asked for
-// first, then the first bounds, and the query is made into whole numbers while
-// those are on their way.
+// `rounds` rounds of STEPS * kScoreStep blocks of one pair to a CTA. The table's entries
+// are asked for first, then the first bounds, and the query is made into whole
+// numbers while those are on their way; later entries come a round ahead.
 template <int D, int STEPS>
-__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads)
+    block_scores_kernel(const SelectParams p, int rounds) {
   constexpr int NV = D / (16 * kScoreLanes);  // 16-byte pieces of lo (and of hi) to a lane
   constexpr int CT = D / kScoreThreads;       // channels of a thread in the query's sums
   constexpr int U = STEPS < 2 ? STEPS : 2;    // blocks of a lane whose loads are in flight
@@ -70,17 +71,20 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
   const int s = blockIdx.y;
   const int tid = threadIdx.x;
   const int n = context_blocks(p, s, tid == 0 && blockIdx.x == 0);
-  const int b0 = blockIdx.x / p.num_kv_heads * (STEPS * kScoreStep);
+  const int b0 = blockIdx.x / p.num_kv_heads * (rounds * STEPS * kScoreStep);
   if (n <= p.max_selected || b0 >= n) return;  // all of them are chosen, or none is here
   const int g8 = tid % kScoreLanes;
   const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
-  const int mine = b0 + tid / kScoreLanes;  // this lane's first block
-  int id[STEPS];
+  int mine = b0 + tid / kScoreLanes;  // this lane's first block of the round
+  int id[STEPS], id_next[STEPS];
+  auto ask = [&](int (&x)[STEPS], int from) {
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    const int i = mine + k * kScoreStep;
-    id[k] = i < n ? table[i] : 0;
-  }
+    for (int k = 0; k < STEPS; ++k) {
+      const int i = from + k * kScoreStep;
+      x[k] = i < n ? table[i] : 0;
+    }
+  };
+  ask(id, mine);
   // the queries' channels of this thread, a head after another
   const uint16_t* q =
       p.q + (static_cast<int64_t>(s) * p.num_kv_heads + h) * p.group * D + tid * CT;
@@ -94,10 +98,10 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
       top = fmaxf(top, fabsf(x[j][i]));
     }
   uint4 lo[U][NV], hi[U][NV];
-  auto load = [&](int k) {
-    const bool ok = id[k] >= 0 && id[k] < p.num_blocks;
+  auto load = [&](int k, int block) {
+    const bool ok = block >= 0 && block < p.num_blocks;
     const uint4* src = reinterpret_cast<const uint4*>(
-        p.bounds + (static_cast<int64_t>(ok ? id[k] : 0) * p.num_kv_heads + h) * (2 * D));
+        p.bounds + (static_cast<int64_t>(ok ? block : 0) * p.num_kv_heads + h) * (2 * D));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       lo[k % U][v] = __ldg(src + v * kScoreLanes + g8);
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
     }
   };
 #pragma unroll
-  for (int k = 0; k < U; ++k) load(k);
+  for (int k = 0; k < U; ++k) load(k, id[k]);
 
   // ---- the group's queries as whole numbers, summed by sign
 #pragma unroll
@@ -144,34 +148,44 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
     }
   }
   int32_t* scores = p.scores + (static_cast<int64_t>(s) * p.num_kv_heads + h) * p.blocks_max;
+#pragma unroll 1
+  for (int round = 0; round < rounds && b0 + round * STEPS * kScoreStep < n; ++round) {
+    if (round + 1 < rounds) ask(id_next, mine + STEPS * kScoreStep);
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    int sum = 0;
+    for (int k = 0; k < STEPS; ++k) {
+      int sum = 0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const uint4 l = lo[k % U][v], u = hi[k % U][v];
-      const int wl[4] = {static_cast<int>(l.x), static_cast<int>(l.y), static_cast<int>(l.z),
-                         static_cast<int>(l.w)};
-      const int wh[4] = {static_cast<int>(u.x), static_cast<int>(u.y), static_cast<int>(u.z),
-                         static_cast<int>(u.w)};
+      for (int v = 0; v < NV; ++v) {
+        const uint4 l = lo[k % U][v], u = hi[k % U][v];
+        const int wl[4] = {static_cast<int>(l.x), static_cast<int>(l.y), static_cast<int>(l.z),
+                           static_cast<int>(l.w)};
+        const int wh[4] = {static_cast<int>(u.x), static_cast<int>(u.y), static_cast<int>(u.z),
+                           static_cast<int>(u.w)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum = __dp2a_lo(cu[v][2 * i], wh[i], sum);
-        sum = __dp2a_hi(cu[v][2 * i + 1], wh[i], sum);
-        sum = __dp2a_lo(cw[v][2 * i], wl[i], sum);
-        sum = __dp2a_hi(cw[v][2 * i + 1], wl[i], sum);
+        for (int i = 0; i < 4; ++i) {
+          sum = __dp2a_lo(cu[v][2 * i], wh[i], sum);
+          sum = __dp2a_hi(cu[v][2 * i + 1], wh[i], sum);
+          sum = __dp2a_lo(cw[v][2 * i], wl[i], sum);
+          sum = __dp2a_hi(cw[v][2 * i + 1], wl[i], sum);
+        }
+      }
+      if (k + U < STEPS)
+        load(k + U, id[k + U]);
+      else if (round + 1 < rounds)
+        load(k + U, id_next[k + U - STEPS]);
+#pragma unroll
+      for (int off = 1; off < kScoreLanes; off <<= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      const int i = mine + k * kScoreStep;
+      if (g8 == 0 && i < n) {
+        const bool ok = id[k] >= 0 && id[k] < p.num_blocks;
+        if (!ok) report_error(p.err, PKV_DEVERR_BLOCK_ID);
+        scores[i] = ok ? sum : INT32_MIN;
       }
     }
-    if (k + U < STEPS) load(k + U);
+    mine += STEPS * kScoreStep;
 #pragma unroll
-    for (int off = 1; off < kScoreLanes; off <<= 1)
-      sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const int i = mine + k * kScoreStep;
-    if (g8 == 0 && i < n) {
-      const bool ok = id[k] >= 0 && id[k] < p.num_blocks;
-      if (!ok) report_error(p.err, PKV_DEVERR_BLOCK_ID);
-      scores[i] = ok ? sum : INT32_MIN;
-    }
+    for (int k = 0; k < STEPS; ++k) id[k] = id_next[k];
   }
   allow_dependents();
 }
@@ -179,14 +193,22 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Selec
 template <int D>
 static int launch_scores(const SelectParams& p, int num_seqs, cudaStream_t st) {
   // 128 blocks to a CTA, or 32 where that gives fewer than three CTAs to an SM (1 x 32768
-  // tokens, 2 heads: 7.8 us; 64 x 8192, 4 heads: 20.4 us with 128, 22.0 with 32)
+  // tokens, 2 heads: 7.8 us; 64 x 8192, 4 heads: 20.4 us with 128, 22.0 with 32); a
+  // CTA's start is 2 us, so rounds of 128 where there are still about three CTAs to an
+  // SM (six at d = 128: half the bytes in flight): 64 x 8192, d = 256 20.4 -> 19.5 us,
+  // 16 x 65536, 8 heads, d = 128 34.0 -> 32.7 in 4 rounds, 42.6 in 9
   const int64_t pairs = static_cast<int64_t>(num_seqs) * p.num_kv_heads;
-  const bool large = (p.blocks_max + 127) / 128 * pairs >= 456;
-  const int64_t blocks = large ? 128 : 32;
+  const int64_t all = (p.blocks_max + 127) / 128 * pairs;
+  const bool large = all >= 456;
+  const int rounds = large ? static_cast<int>(std::max<int64_t>(
+                                 1, std::min<int64_t>(all / (D == 256 ? 450 : 900),
+                                                         (p.blocks_max + 127) / 128)))
+                           : 1;
+  const int64_t blocks = large ? 128 * rounds : 32;
   const int64_t gx = (p.blocks_max + blocks - 1) / blocks * p.num_kv_heads;
-  const dim3 grid(static_cast<unsigned>(gx), num_seqs);
-  return large ? launch_dependent(block_scores_kernel<D, 8>, grid, dim3(kScoreThreads), 0, st, p)
-               : launch_dependent(block_scores_kernel<D, 2>, grid, dim3(kScoreThreads), 0, st, p);
+  const dim3 grid(static_cast<unsigned>(gx), num_seqs), block(kScoreThreads);
+  return large ? launch_dependent(block_scores_kernel<D, 8>, grid, block, 0, st, p, rounds)
+               : launch_dependent(block_scores_kernel<D, 2>, grid, block, 0, st, p, rounds);
 }
 
 // Bins of a round: two rounds for the 2^22 different scores that a context has at most
