@@ -41,7 +41,7 @@ extern "C" int pkv_decode_partition_size(pkv_cache_desc cache, int num_seqs, int
     if (num_seqs < 0 || max_context < 0) return PKV_ERR_INVALID_ARG;
     const int unit = fp4_unit(cache.head_dim);
     const Fp4Split f = fp4_split(static_cast<int64_t>(num_seqs) * cache.num_kv_heads,
-                                 (static_cast<int64_t>(max_context) + unit - 1) / unit);
+                                 (static_cast<int64_t>(max_context) + unit - 1) / unit, unit);
     return static_cast<int>(std::min<int64_t>(f.per * unit, INT32_MAX / 64 * 32));
   }
   // a window as wide as the context
@@ -135,7 +135,8 @@ extern "C" int pkv_paged_attention_decode(void* out, const void* q, const void* 
     if (fp4) {
       const int unit = fp4_unit(cache.head_dim);
       p.cluster = fp4_split(static_cast<int64_t>(num_seqs) * cache.num_kv_heads,
-                            (static_cast<int64_t>(max_context) + unit - 1) / unit).cluster;
+                            (static_cast<int64_t>(max_context) + unit - 1) / unit, unit)
+                      .cluster;
     }
   } else {
     if (partition_size % cache.block_size != 0) return PKV_ERR_INVALID_ARG;

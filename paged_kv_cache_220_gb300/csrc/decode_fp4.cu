@@ -622,9 +622,11 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
 //   more: partitions of 8 units (4 where one CTA to an SM does: 1 x 8192, d = 128:
 //   9.7 us, 10.2 with 8).
 // - Else somewhat over two waves, whose end is short (256 pairs of 8192, d = 256: 112 us
-//   in 4, 118 in 3, 117 in 8), in partitions of at most 64 units, as contexts may
-//   differ (768 pairs of 16 to 16384, d = 128: 66 us; longest first 56).
-Fp4Split fp4_split(int64_t pairs, int64_t units) {
+//   in 4, 118 in 3, 117 in 8), in partitions of at most 2048 tokens, as contexts may
+//   differ (768 pairs of 16 to 16384, d = 128: 66 us, 70 in partitions of 4096; with
+//   the sequences longest first 61 and 56. Ranking them in every CTA cost more than
+//   it gave from about 100 sequences on).
+Fp4Split fp4_split(int64_t pairs, int64_t units, int unit) {
   constexpr int64_t kWave = 456, kSms = 152;
   if (pairs <= 0 || units <= 0) return {1, 0};
   int c = 1;
@@ -633,7 +635,7 @@ Fp4Split fp4_split(int64_t pairs, int64_t units) {
   int64_t np = std::min(kWave / pairs, units / 8);
   if (pairs * (units / 4) <= kSms) np = units / 4;
   if (np * pairs < kWave * 7 / 8 && np < units / 8)
-    np = std::max((11 * kWave / 5 + pairs - 1) / pairs, (units + 63) / 64);
+    np = std::max((11 * kWave / 5 + pairs - 1) / pairs, (units * unit + 2047) / 2048);
   np = std::min<int64_t>(np, 8192);  // the merge takes 32767
   if (np <= 1) return {c, 0};
   return {c, (units + np - 1) / np};

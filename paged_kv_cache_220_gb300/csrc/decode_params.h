@@ -99,14 +99,14 @@ int launch_decode_fp4(const DecodeParams& p, int head_dim, int block_size, dim3 
 __host__ __device__ constexpr int fp4_unit(int head_dim) { return head_dim == 256 ? 32 : 64; }
 constexpr int kFp4Warps = 4;
 
-// How the 4-bit kernel's work is cut: `pairs` of up to `units` units each. per: units
+// How the 4-bit kernel's work is cut: `pairs` of up to `units` units of `unit` tokens. per: units
 // of a partition, 0 = one pass; cluster: CTAs of a pair's cluster in one pass.
 // (decode_fp4.cu)
 struct Fp4Split {
   int cluster;
   int64_t per;
 };
-Fp4Split fp4_split(int64_t pairs, int64_t units);
+Fp4Split fp4_split(int64_t pairs, int64_t units, int unit);
 
 // Merge of split partials (reduce.cu). With prefix_blocks == NULL the slots of
 // sequence s are [0, ceil(ctx/P)); otherwise [0, npre) and [slot_split,

@@ -23,8 +23,9 @@ static int64_t listed_split(const pkv_cache_desc& cache, int num_seqs, int max_s
   const int64_t pairs = static_cast<int64_t>(num_seqs) * cache.num_kv_heads;
   if (cache.dtype != PKV_DTYPE_FP4_E2M1)
     return parts_split(pairs, max_selected, cache.head_dim, cluster);
-  const int64_t ub = fp4_unit(cache.head_dim) / cache.block_size;
-  const Fp4Split f = fp4_split(pairs, (max_selected + ub - 1) / ub);
+  const int unit = fp4_unit(cache.head_dim);
+  const int64_t ub = unit / cache.block_size;
+  const Fp4Split f = fp4_split(pairs, (max_selected + ub - 1) / ub, unit);
   *cluster = f.cluster;
   return f.per * ub;
 }
