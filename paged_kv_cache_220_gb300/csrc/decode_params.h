@@ -86,9 +86,10 @@ int launch_decode_tc(const DecodeParams& p, const void* k_cache, const void* v_c
 int launch_decode_window(const DecodeParams& p, const void* k_cache, const void* v_cache,
                          int head_dim, int block_size, bool fp8, dim3 grid, cudaStream_t st);
 
-// How the windowed and the listed form's work is cut: blocks to a partition, 0 =
-// one pass over clusters of *cluster CTAs. (decode_window.cu)
-int64_t parts_split(int64_t pairs, int64_t blocks, int head_dim, int* cluster);
+// How the windowed and the listed form's work is cut, `wave` CTAs running at once:
+// blocks to a partition, 0 = one pass over clusters of *cluster CTAs.
+// (decode_window.cu)
+int64_t parts_split(int64_t pairs, int64_t blocks, int64_t wave, int* cluster);
 
 // 4-bit pools (decode_fp4.cu), the listed form too.
 int launch_decode_fp4(const DecodeParams& p, int head_dim, int block_size, dim3 grid,

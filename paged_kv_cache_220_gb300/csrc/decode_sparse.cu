@@ -17,12 +17,15 @@ static int launch_decode_listed(const DecodeParams& p, const void* k_cache, cons
              : dispatch_tc<false, kListed>(p, k_cache, v_cache, head_dim, block_size, grid, st);
 }
 
+// CTAs that run at once on 152 SMs: four to an SM at d = 256, eight at d = 128.
+static int64_t listed_wave(int head_dim) { return head_dim == 256 ? 600 : 1200; }
+
 // Entries to a partition of lists of up to max_selected, 0 = one pass.
 static int64_t listed_split(const pkv_cache_desc& cache, int num_seqs, int max_selected,
                             int* cluster) {
   const int64_t pairs = static_cast<int64_t>(num_seqs) * cache.num_kv_heads;
   if (cache.dtype != PKV_DTYPE_FP4_E2M1)
-    return parts_split(pairs, max_selected, cache.head_dim, cluster);
+    return parts_split(pairs, max_selected, listed_wave(cache.head_dim), cluster);
   const int unit = fp4_unit(cache.head_dim);
   const int64_t ub = unit / cache.block_size;
   const Fp4Split f = fp4_split(pairs, (max_selected + ub - 1) / ub, unit);

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
     if (threadIdx.x == 0 && part == 0 && h == 0) report_error(p.err, PKV_DEVERR_CONTEXT);
     ctx = ctx < 0 ? 0 : cap;
   }
-  // BPP == 1: ring pages [blk_begin, blk_end); BPP > 1 (split form only):
+  // BPP == 1: ring pages [blk_begin, blk_end); BPP > 1:
   // pool blocks [blk_begin, blk_end), BPP of them to a ring page
   int blk_begin = 0, blk_end = 0, nblk = 0;
   int tok0 = 0;  // first token of this CTA's pages
@@ -212,9 +212,16 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
     tok0 = blk_begin * BS;
   } else {
     blk_end = WIN ? wb.count : LIST ? listed : (ctx + PB - 1) / PB;
-    blk_begin = part * p.partition_blocks + (p.block_offset ? p.block_offset[s] : 0);
-    if (blk_begin >= blk_end) return;  // partition past the end: nothing to store
-    blk_end = min(blk_end, blk_begin + p.partition_blocks);
+    if (LIST && p.partition_blocks == 0) {
+      // one pass: rank r of the cluster takes an equal share of whole pages
+      const int share = (blk_end + BPP * p.cluster - 1) / (BPP * p.cluster) * BPP;
+      blk_begin = min(blk_end, part * share);
+      blk_end = min(blk_end, blk_begin + share);
+    } else {
+      blk_begin = part * p.partition_blocks + (p.block_offset ? p.block_offset[s] : 0);
+      if (blk_begin >= blk_end) return;  // partition past the end: nothing to store
+      blk_end = min(blk_end, blk_begin + p.partition_blocks);
+    }
     nblk = (blk_end - blk_begin + BPP - 1) / BPP;
     tok0 = blk_begin * PB;
   }
@@ -890,7 +897,8 @@ static int dispatch_tc(const DecodeParams& p, const void* k_cache, const void* v
     // (GB300, same box: long-context shapes at B = 16 0.3338 -> 0.3227 ms per
     // decode, copy-on-write rollouts over an E4M3 cache 0.1533 -> 0.1460 ms)
     if constexpr (FP8)
-      if (p.partition_blocks > 0) return launch_tc<MODE, 256, 32, FP8, 2, 2, 1, 2>(p, k_cache, v_cache, grid, st);
+      if (MODE == kListed || p.partition_blocks > 0)
+        return launch_tc<MODE, 256, 32, FP8, 2, 2, 1, 2>(p, k_cache, v_cache, grid, st);
     if (p.partition_blocks > 0 && p.partition_blocks <= 48)
       return launch_tc<MODE, 256, 16, FP8, 2, 3>(p, k_cache, v_cache, grid, st);
     return launch_tc<MODE, 256, 16, FP8, 2, 2>(p, k_cache, v_cache, grid, st);
@@ -904,6 +912,25 @@ static int dispatch_tc(const DecodeParams& p, const void* k_cache, const void* v
       if (p.partition_blocks > 0 && 2 * p.partition_blocks <= 48)
         return launch_tc<MODE, 256, 16, FP8, 2, 3, 2>(p, k_cache, v_cache, grid, st);
       return launch_tc<MODE, 256, 16, FP8, 2, 2, 2>(p, k_cache, v_cache, grid, st);
+    }
+  }
+  // Lists at d = 128: two consumer warps and three stages of 16-row pages, or two of 32
+  // rows on E4M3 pools (two 16-token blocks to a page in one pass too), so that eight
+  // CTAs and more run on an SM instead of three (256 pairs of 256 blocks of 16: bf16
+  // 117.0 -> 89.0 us, E4M3 82.9 -> 49.2; 1024 pairs of 64 blocks: bf16 135.2 -> 84.6, E4M3 86.4
+  // -> 46.9; blocks of 32: bf16 273.3 -> 162.4, E4M3 111.4 -> 85.2; d = 256, 256 pairs of
+  // 128 blocks of 16, E4M3: 61.8 -> 50.7)
+  if constexpr (MODE == kListed) {
+    if constexpr (FP8) {
+      if (head_dim == 128 && block_size == 16)
+        return launch_tc<MODE, 128, 32, FP8, 2, 2, 1, 2>(p, k_cache, v_cache, grid, st);
+      if (head_dim == 128)
+        return launch_tc<MODE, 128, 32, FP8, 2, 2>(p, k_cache, v_cache, grid, st);
+    } else {
+      if (head_dim == 128 && block_size == 16)
+        return launch_tc<MODE, 128, 16, FP8, 2, 3>(p, k_cache, v_cache, grid, st);
+      if (head_dim == 128)
+        return launch_tc<MODE, 128, 16, FP8, 2, 3, 2>(p, k_cache, v_cache, grid, st);
     }
   }
   if (head_dim == 128 && block_size == 16)

@@ -46,9 +46,9 @@ int launch_decode_window(const DecodeParams& p, const void* k_cache, const void*
              : dispatch_tc<false, kWindowed>(p, k_cache, v_cache, head_dim, block_size, grid, st);
 }
 
-// Blocks to a partition for `pairs` of up to `blocks` blocks each, 0 = one pass; *cluster:
-// CTAs of a pair's cluster in one pass.
-int64_t parts_split(int64_t pairs, int64_t blocks, int head_dim, int* cluster) {
+// Blocks to a partition for `pairs` of up to `blocks` blocks each, 0 = one pass; wave: CTAs
+// that run at once; *cluster: CTAs of a pair's cluster in one pass.
+int64_t parts_split(int64_t pairs, int64_t blocks, int64_t wave, int* cluster) {
   // One pass, a cluster of CTAs to a pair, saves the merge (64 pairs of 40
   // blocks, bf16, d = 256, B = 16: 12.3 us against 16.6 in 8 partitions), as
   // long as its CTAs have little to do each or fill most of a wave (64 pairs of
@@ -59,7 +59,7 @@ int64_t parts_split(int64_t pairs, int64_t blocks, int head_dim, int* cluster) {
   // three waves even it out (256 pairs of 160 blocks, d = 128: 85 us in 5
   // partitions, 101 in one pass; 512 pairs, 1.2 waves: 161 in 4, 225; but
   // 1024 pairs of up to 34 blocks, d = 256, 1.7 waves: 103 in 2, 99).
-  const int64_t wave = window_wave(head_dim), c = window_cluster(pairs, blocks, wave);
+  const int64_t c = window_cluster(pairs, blocks, wave);
   *cluster = static_cast<int>(c);
   const int64_t waves = (pairs * c + wave - 1) / wave;
   if (blocks <= 12 * c || 10 * pairs * c >= (waves == 1 ? 6 : 7 * waves) * wave) return 0;
@@ -82,7 +82,7 @@ extern "C" int pkv_window_partition_size(int num_seqs, int num_kv_heads, int hea
   const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
   if (pairs == 0) return 0;
   int cluster = 1;
-  const int64_t per = parts_split(pairs, blocks, head_dim, &cluster);
+  const int64_t per = parts_split(pairs, blocks, window_wave(head_dim), &cluster);
   return static_cast<int>(std::min<int64_t>(per, (INT32_MAX - 64) / block_size) * block_size);
 }
 
