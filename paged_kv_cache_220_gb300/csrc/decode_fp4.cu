@@ -616,7 +616,9 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
 // 456 CTAs run at once on 152 SMs, and a CTA costs 5 to 6 us besides its units
 // (start, first loads, merge), which the SM's other two hide in part.
 // - One pass, a cluster of CTAs to a pair, where a warp then has two units or fewer
-//   (1 x 1033, d = 128: 6.3 us, 7.5 in partitions; 1 x 8192, 8 units a warp: 11.5, 8.0).
+//   (1 x 1033, d = 128: 6.3 us, 7.5 in partitions; 1 x 8192, 8 units a warp: 11.5, 8.0),
+//   or where the pairs fill half a wave by themselves and have 64 units or fewer (256
+//   pairs of 64, d = 256: 39.6 us, 44.1 in 4 partitions; of 256: 128, 117).
 // - One wave of partitions where the pairs fill it (32 pairs of 131072 tokens, d =
 //   256: 191 us in 14 partitions each, 207 in 56), or where there is not enough for
 //   more: partitions of 8 units (4 where one CTA to an SM does: 1 x 8192, d = 128:
@@ -631,7 +633,7 @@ Fp4Split fp4_split(int64_t pairs, int64_t units, int unit) {
   if (pairs <= 0 || units <= 0) return {1, 0};
   int c = 1;
   while (c < 8 && kFp4Warps * c < units && 2 * c * pairs <= kWave) c <<= 1;
-  if (units <= 2 * kFp4Warps * c) return {c, 0};
+  if (units <= 2 * kFp4Warps * c || (2 * pairs >= kWave && units <= 64)) return {c, 0};
   int64_t np = std::min(kWave / pairs, units / 8);
   if (pairs * (units / 4) <= kSms) np = units / 4;
   if (np * pairs < kWave * 7 / 8 && np < units / 8)
