@@ -61,6 +61,27 @@ def test_the_definition(d, block, hk, kind, _lib):
     assert int(_lib.item()) == 0
 
 
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+def test_scales_below_zero_and_nan_codes(kind, _lib):
+    c = AnyCache([70, 33], 2, 256, 32, kind, seed=9)
+    c.ks[1] = -c.ks[1]
+    for s in range(2):
+        c.K[s][:, 1] = -c.K[s][:, 1]
+    # one token of NaN (a scale of 16 channels, or all channels) and a whole block
+    c.poison(0, 5, 6)
+    c.K[0][5] = float("nan")
+    c.poison(1, 0, 32)
+    c.K[1][:32] = float("nan")
+    step = torch.full((2,), 1 / 40, device="cuda")
+    out = fresh(c)
+    pkv.block_bounds(out, c.k, c.tables, c.context_lens, step, 100, k_scale=c.ks)
+    for s, n in enumerate(c.lens):
+        for b in range(-(-n // 32)):
+            assert torch.equal(out[int(c.tables[s, b])], bounds_of(c, step, s, b)), (s, b)
+    assert float(out[int(c.tables[1, 0])].abs().max()) == 0
+    assert int(_lib.item()) == 0
+
+
 def test_nan_counts_as_zero(_lib):
     c = AnyCache([40], 2, 128, 16, "bf16", seed=1)
     c.k[int(c.tables[0, 1]), 1, 3, 7] = float("nan")

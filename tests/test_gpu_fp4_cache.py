@@ -95,6 +95,23 @@ def test_every_size_of_row(scale, _lib):
     assert int(_lib.item()) == 0
 
 
+@pytest.mark.parametrize("hk,d,n", [(32, 256, 3), (32, 128, 700), (5, 128, 9001), (7, 256, 1)])
+def test_many_heads_and_many_rows(hk, d, n, _lib):
+    """Rows and heads on both sides of what a CTA takes, the read back included."""
+    b = 32
+    nb = -(-n // b) + 1
+    k, v = rows(n, hk, d, 5), rows(n, hk, d, 6)
+    ks, vs = torch.rand(hk, device="cuda") + 0.1, torch.rand(hk, device="cuda") + 0.1
+    kc, vc = pkv.fp4_cache(nb, hk, b, d), pkv.fp4_cache(nb, hk, b, d)
+    slots = torch.randperm(nb * b, device="cuda")[:n]
+    pkv.kv_cache_write(k, v, slots, kc, vc, ks, vs)
+    got = pkv.kv_cache_read(slots, kc, vc, ks, vs)
+    for x, y, scale in ((k, got[0], ks), (v, got[1], vs)):
+        want = (values(*quantize(x, scale)) * scale.double()[:, None]).float().to(torch.bfloat16)
+        assert torch.equal(y, want)
+    assert int(_lib.item()) == 0
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_write_of_special_values(d, _lib):
     """Zeros, groups too small for a scale, infinities, NaN, largest values and

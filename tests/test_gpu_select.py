@@ -124,6 +124,25 @@ def test_long_contexts(_lib):
     assert int(_lib.item()) == 0
 
 
+@pytest.mark.parametrize("hk,g,d,lens,take", [
+    (32, 8, 128, [3000, 40], 50), (32, 1, 256, [900] * 3, 10), (8, 4, 128, [4096] * 260, 40),
+    (4, 6, 256, [70000] * 3, 900), (1, 2, 128, [100] * 400, 6), (2, 4, 128, [5000], 100000)])
+def test_many_heads_blocks_and_sequences(hk, g, d, lens, take, _lib):
+    c = Case(lens, hk, g, d, 16, seed=take)
+    got = c.call(take, 1, 1)
+    c.verify(got, take, 1, 1, skip=[s for s in range(len(lens)) if len(lens) > 100 and s % 41])
+    # the lists of sequences that were skipped above: ascending, the ends among them
+    n = (c.context_lens.long() + 15) // 16
+    m = n.clamp(max=take)
+    blocks = got[0].long()
+    i = torch.arange(take, device="cuda")
+    inside = i < m[:, None, None]
+    assert torch.equal(blocks >= 0, inside.expand_as(blocks))
+    step = blocks[..., 1:] - blocks[..., :-1]
+    assert bool(((step > 0) | ~inside[..., 1:]).all())
+    assert int(_lib.item()) == 0
+
+
 def test_queries_of_any_size(_lib):
     """Zero, tiny and huge queries; elements that are exact halves of a step."""
     c = Case([2000] * 5, 2, 4, 128, 16, seed=6)
