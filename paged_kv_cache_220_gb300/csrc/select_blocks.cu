@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kScoreThreads)
   const int h = blockIdx.x % p.num_kv_heads;
   const int s = blockIdx.y;
   const int tid = threadIdx.x;
-  const int n = context_blocks(p, s, tid == 0 && blockIdx.x == 0);
+  const int n = context_blocks(p, s, false);  // (the second kernel reports)
   const int b0 = blockIdx.x / p.num_kv_heads * (rounds * STEPS * kScoreStep);
   if (n <= p.max_selected || b0 >= n) return;  // all of them are chosen, or none is here
   const int g8 = tid % kScoreLanes;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p, bool st
   const int h = blockIdx.x, s = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = static_cast<int64_t>(s) * p.num_kv_heads + h;
-  const int n = context_blocks(p, s, false);
+  const int n = context_blocks(p, s, tid == 0 && h == 0);
   const int K = p.max_selected;
   int32_t* out = p.blocks + row * K;
   if (tid == 0) p.counts[row] = min(n, K);

@@ -188,6 +188,17 @@ def test_bad_blocks_and_contexts_are_reported(_lib):
     c.verify(c.call(20, 1, 1), 20, 1, 1)
 
 
+def test_bad_contexts_are_reported_where_all_blocks_are_chosen(_lib):
+    c = Case([1600, 1500], 2, 4, 128, 16, seed=12)
+    for bad in (-1, 1601):
+        c.context_lens[1] = bad
+        got = c.call(100, 1, 1)
+        torch.cuda.synchronize()
+        assert int(_lib.item()) == pkv.DEVERR_CONTEXT
+        _lib.zero_()
+        assert got[1].tolist() == [[100, 100], [0, 0] if bad < 0 else [100, 100]]
+
+
 def test_streams_graphs_and_given_buffers(_lib):
     c = Case([4000, 70, 900], 2, 4, 256, 16, seed=9)
     blocks = torch.full((3, 2, 30), 7, dtype=torch.int32, device="cuda")
