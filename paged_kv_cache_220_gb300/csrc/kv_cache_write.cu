@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "host_util.h"
+#include "quotients.cuh"
 
 namespace pkv {
 
@@ -77,57 +78,26 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Two fp32 in one register pair, and their products and sums (each rounded as by
-// itself) in one instruction.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 of_pair(uint64_t a) {
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
-// a / b from r = 1/b and minus_b = -b, by STEPS corrections with the exact remainder
-// (Markstein, IBM J. Res. Dev. 34, 1990). With r rounded to nearest the first leaves
-// less than a unit in the last place and the second nothing: the quotient is
-// rounded to nearest. Holds while b, r, the quotient and the remainder's last bit
-// are normal numbers.
-template <int STEPS>
-__device__ __forceinline__ uint64_t quotients(uint64_t a, uint64_t minus_b, uint64_t r) {
-  uint64_t q = mul_pair(a, r);
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) q = fma_pair(fma_pair(minus_b, q, a), r, q);
-  return q;
-}
-
 // Eight channels of a row -> their codes (a word) and the scale of their 16; the
 // lane next to this one has the group's other eight. inv: 1 / scale to nearest;
 // plain: scale is in 2^-40 .. 2^40.
 //
-// 17 divisions to 8 channels are what this costs, so they are made in pairs from
-// the divisors' reciprocals where that gives the same: with a scale as above and
-// the group's largest |x| in 2^-40 .. 2^60 all that count are far inside the normal
-// numbers. Channels smaller than that by 2^20 get the code 0 however y is rounded.
-// Of y / s only the side of a midpoint between two codes counts. s has 4
-// significant bits and a midpoint m 3, so m s is an fp32 number: y / s rounds to m only
-// if y = m s, the next y is off by at least 1.6 % of a unit in the last place more than
-// half a unit, and one correction of an approximate reciprocal's quotient, off by
-// 2^-20 of a unit before it is rounded, decides the same.
+// 17 divisions to 8 channels are what this would cost. With a scale as above and the
+// group's largest |x| in 2^-40 .. 2^60 all that count are far inside the normal
+// numbers (channels smaller than that by 2^20 get the code 0 however they are
+// rounded), and a product with reciprocals is off by less than 2^-21 of the rounded
+// quotient of the rounded quotient: the same product 2^-20 lower and 2^-20 higher
+// have it between them, and rounding to a code keeps the order. Where both get the
+// same code, that is the one (8192 tokens, 8 heads, d = 128: 12.1 us, 14.1 without).
+// Elsewhere, near a midpoint between two codes, the quotients are made exact, in
+// pairs. Of y / s only the side of a midpoint counts. s has 4 significant bits and a
+// midpoint m 3, so m s is an fp32 number: y / s rounds to m only if y = m s, the next y
+// is off by at least 1.6 % of a unit in the last place more than half a unit, and one
+// correction of an approximate reciprocal's quotient, off by 2^-20 of a unit before
+// it is rounded, decides the same.
 __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, float inv,
                                                  bool plain, uint8_t& s_code) {
+  constexpr float kLess = 1.f - 0x1p-20f, kMore = 1.f + 0x1p-20f, kSixth = 1.f / 6.f;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   constexpr uint32_t kAbs = 0x7FFF7FFFu;
   uint32_t t2 = max2_nan(max2_nan(w[0] & kAbs, w[1] & kAbs), max2_nan(w[2] & kAbs, w[3] & kAbs));
@@ -136,16 +106,36 @@ __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, fl
   float z8[8];
   if (plain && top >= 0x1p-40f && top <= 0x1p60f) {
     const uint64_t r = pair_of(inv, inv), b = pair_of(-scale, -scale);
-    // rounded quotients grow with their numerators: the largest is the largest's
-    const float a = of_pair(quotients<2>(pair_of(top, top), b, r)).x;
-    constexpr float kSixth = 1.f / 6.f;
-    const float a6 = of_pair(quotients<2>(pair_of(a, a), pair_of(-6.f, -6.f),
-                                          pair_of(kSixth, kSixth))).x;
-    s_code = static_cast<uint8_t>(__nv_cvt_float_to_fp8(a6, __NV_SATFINITE, __NV_E4M3));
+    const float t6 = top * inv * kSixth;
+    const uint32_t both = __nv_cvt_float2_to_fp8x2(make_float2(t6 * kLess, t6 * kMore),
+                                                   __NV_SATFINITE, __NV_E4M3);
+    s_code = static_cast<uint8_t>(both);
+    if (s_code != both >> 8) {
+      // rounded quotients grow with their numerators: the largest is the largest's
+      const float a = of_pair(quotients<2>(pair_of(top, top), b, r)).x;
+      const float a6 = of_pair(quotients<2>(pair_of(a, a), pair_of(-6.f, -6.f),
+                                            pair_of(kSixth, kSixth))).x;
+      s_code = static_cast<uint8_t>(__nv_cvt_float_to_fp8(a6, __NV_SATFINITE, __NV_E4M3));
+    }
     const float s = e4m3_f32(s_code);
     if (!(s > 0.f)) return 0;
     float inv_s;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(s));
+    // (with a scale that is a power of two x meets midpoints exactly all the time)
+    if ((__float_as_uint(scale) & 0x007FFFFFu) != 0) {
+      const float f = inv * inv_s, less = f * kLess, more = f * kMore;
+      const uint64_t f_less = pair_of(less, less), f_more = pair_of(more, more);
+      float y8[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t xs = pair_of(bf16lo(w[i]), bf16hi(w[i]));
+        const float2 y = of_pair(mul_pair(xs, f_less)), z = of_pair(mul_pair(xs, f_more));
+        y8[2 * i] = y.x, y8[2 * i + 1] = y.y;
+        z8[2 * i] = z.x, z8[2 * i + 1] = z.y;
+      }
+      const uint32_t codes = e2m1x8_of(y8);
+      if (codes == e2m1x8_of(z8)) return codes;
+    }
     const uint64_t rs = pair_of(inv_s, inv_s), bs = pair_of(-s, -s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
