@@ -1,20 +1,27 @@
 // block_bounds: the lowest and highest K of every channel of a block, as whole
 // multiples of a step per head.
 //
-// One warp per (block, head) page: lane l has D/32 consecutive channels and
-// keeps their running minimum and maximum over the page's cached rows, the rows'
-// loads (up to 64 words a lane) in flight together; a row of a page is one coalesced
-// access. The extremes are taken two channels at a time of what is stored, bf16
-// pairs, or f16 pairs that hold a code times its 16 channels' scale exactly: the
-// head's scale, floor and ceil of a quotient by a positive step grow with the value
-// (or all fall, for a negative scale), so only the extremes go through them. A
-// third running value, a maximum that keeps NaN, says where a zero has to join.
-// Bound by HBM over whole prompts, by latency at one block per sequence.
+// One warp per (block, head) page, in lines of 256 values (one token at d = 256, two
+// at d = 128): a lane has 8 channels of one token of every line, a line is one
+// coalesced access, and up to 32 words a lane are in flight together. The extremes
+// are taken two channels at a time of what is stored, bf16 pairs, or f16 pairs that
+// hold a code times its 16 channels' scale exactly: the head's scale, floor and ceil of a
+// quotient by a positive step grow with the value (or all fall, for a negative
+// scale), so only the extremes go through them. Extremes that keep a NaN say which
+// lanes have to take theirs once more, value by value.
+//
+// Bound by HBM on bf16 pools (8 x 16384 tokens, 4 heads, d = 256, B = 16: 45 us, 93 % of
+// the copy rate), by latency and the instructions of the extremes and conversions on
+// coded ones (E4M3 27.4 us, 81 %; 4-bit 29 us, 47 %), and by latency alone at one block
+// per sequence (2.7 us). Two to eight pages to a warp, with their blocks looked up
+// together, took longer (E4M3, d = 128: 25 us with one, 34 to 63), and so did a grid
+// without the 64-bit divisions (21.1, 24.6).
 #include <algorithm>
 
 #include "common.cuh"
 #include "fp4.cuh"
 #include "host_util.h"
+#include "quotients.cuh"
 
 namespace pkv {
 
@@ -34,77 +41,57 @@ struct BoundsParams {
   int64_t items;    // num_seqs * per_seq * num_kv_heads
 };
 
-// Row r's channels [C*lane, C*lane + C) of a page, as loaded, and as pairs.
+// Eight channels of a token, as loaded from a line of a page, and as pairs.
 template <int DTYPE, int D>
-struct BoundsRow {
-  static constexpr int C = D / 32;
-  static constexpr int kWords = DTYPE == PKV_DTYPE_BF16 ? C / 2 : (C + 3) / 4;
+struct BoundsEight {
+  static constexpr int kWords = DTYPE == PKV_DTYPE_BF16 ? 4 : DTYPE == PKV_DTYPE_FP8_E4M3 ? 2 : 1;
+  static constexpr int kLine = DTYPE == PKV_DTYPE_FP4_E2M1 ? kFp4Line : 64 * 2 * kWords;
   uint32_t w[kWords];
-  uint8_t s;
+  uint32_t s;
 
-  __device__ __forceinline__ void load(const uint8_t* page, int r, int lane) {
-    if constexpr (DTYPE == PKV_DTYPE_BF16) {
-      const uint8_t* p = page + (r * D + C * lane) * 2;
-      if constexpr (C == 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
-      }
-    } else if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
-      const uint8_t* p = page + r * D + C * lane;
-      if constexpr (C == 8) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      }
+  // piece: which 8 of the line's 256 values. Loads stay in program order, so that a
+  // batch of them is issued before the first is used (left to the compiler, few
+  // registers: 8 x 8192 tokens, 8 heads, d = 128, bf16 27.5 us, 24.2 so)
+  __device__ __forceinline__ void load(const uint8_t* line, int piece) {
+    const uint8_t* p = line + 4 * kWords * piece;
+    if constexpr (kWords == 4) {
+      asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
+    } else if constexpr (kWords == 2) {
+      asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
     } else {
-      const uint8_t* p = page + fp4_codes_at<D>(r) + C / 2 * lane;
-      if constexpr (C == 8)
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      else
-        w[0] = *reinterpret_cast<const uint16_t*>(p);
-      s = page[fp4_scales_at<D>(r) + C * lane / kFp4Group];
+      asm volatile("ld.global.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+      asm volatile("ld.global.u8 %0, [%1];" : "=r"(s) : "l"(line + 128 + piece / 2));
     }
   }
 
-  __device__ __forceinline__ void pairs(uint32_t (&x)[C / 2]) const {
+  __device__ __forceinline__ void pairs(uint32_t (&x)[4]) const {
     if constexpr (DTYPE == PKV_DTYPE_BF16) {
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) x[i] = w[i];
+      for (int i = 0; i < 4; ++i) x[i] = w[i];
     } else if constexpr (DTYPE == PKV_DTYPE_FP8_E4M3) {
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) x[i] = e4m3x2_f16x2_lo(w[i / 2] >> (16 * (i & 1)));
+      for (int i = 0; i < 4; ++i) x[i] = e4m3x2_f16x2_lo(w[i / 2] >> (16 * (i & 1)));
     } else {
       uint32_t f[4];
       e2m1x8_f16x2(w[0], f);
-      const uint32_t by = e4m3x2_f16x2_lo(s | (static_cast<uint32_t>(s) << 8));
+      const uint32_t by = e4m3x2_f16x2_lo(s * 0x0101u);
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i)
+      for (int i = 0; i < 4; ++i)
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(x[i]) : "r"(f[i]), "r"(by));
     }
   }
 };
 
-// Extremes of pairs: bf16 pairs if BF, else f16 ones.
+// Extremes of pairs, NaN where one is: bf16 pairs if BF, else f16 ones.
 template <bool BF>
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   uint32_t d;
   if constexpr (BF)
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   else
-    asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  if constexpr (BF)
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 template <bool BF>
@@ -122,8 +109,23 @@ __device__ __forceinline__ float2 to_f32(uint32_t a) {
   return __half22float2(*reinterpret_cast<const __half2*>(&a));
 }
 
+// The two numbers' whole steps below and above, clamped. plain: step in 2^-40 .. 2^16
+// and l, u within a factor of 2^60 of it, whose quotients by it inv gives to nearest.
+__device__ __forceinline__ void whole_steps(float l, float u, float step, float inv, bool plain,
+                                            uint32_t& lo, uint32_t& hi) {
+  float2 q;
+  if (plain)
+    q = of_pair(quotients<2>(pair_of(l, u), pair_of(-step, -step), pair_of(inv, inv)));
+  else
+    q = make_float2(__fdiv_rn(l, step), __fdiv_rn(u, step));
+  // added to 1.5 * 2^23 a number below 2^22 leaves its whole part in the low bits
+  constexpr float kWhole = 12582912.f;
+  lo = __float_as_uint(__fadd_rd(fminf(fmaxf(q.x, -127.f), 127.f), kWhole)) & 0xFFu;
+  hi = __float_as_uint(__fadd_ru(fminf(fmaxf(q.y, -127.f), 127.f), kWhole)) & 0xFFu;
+}
+
 template <int DTYPE, int D, int BS>
-__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kBoundsWarps * 32, 8) block_bounds_kernel(const BoundsParams p) {
   wait_prerequisite();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5);
@@ -148,53 +150,96 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
     if (lane == 0 && h == 0) report_error(p.err, PKV_DEVERR_BLOCK_ID);
     return;
   }
-  constexpr int kPage = DTYPE == PKV_DTYPE_BF16       ? BS * D * 2
-                        : DTYPE == PKV_DTYPE_FP8_E4M3 ? BS * D
-                                                      : BS * D / 16 * 9;
+  using Eight = BoundsEight<DTYPE, D>;
+  constexpr int R = 256 / D;        // tokens of a line
+  constexpr int NL = BS / R;        // lines of a page
+  constexpr int P = 32 / R;         // lanes to a token
+  constexpr int kTogether = Eight::kWords * NL <= 32 ? NL : 32 / Eight::kWords;
   constexpr bool BF = DTYPE == PKV_DTYPE_BF16;
-  const uint8_t* page = p.k_cache + (static_cast<int64_t>(pb) * p.num_kv_heads + h) * kPage;
-  using Row = BoundsRow<DTYPE, D>;
-  constexpr int C = Row::C;
-  constexpr int kTogether = Row::kWords * BS <= 64 ? BS : 64 / Row::kWords;  // rows
-  constexpr uint32_t kPlus = BF ? 0x7F807F80u : 0x7C007C00u;                 // +inf twice
-  uint32_t lo[C / 2], hi[C / 2], any[C / 2];
-#pragma unroll
-  for (int i = 0; i < C / 2; ++i) {
-    lo[i] = kPlus;
-    hi[i] = any[i] = kPlus | 0x80008000u;
-  }
-#pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += kTogether) {
-    Row row[kTogether];
-    // rows behind the last cached one are read as that one once more
-#pragma unroll
-    for (int r = 0; r < kTogether; ++r) row[r].load(page, min(r0 + r, rows - 1), lane);
-#pragma unroll
-    for (int r = 0; r < kTogether; ++r) {
-      uint32_t x[C / 2];
-      row[r].pairs(x);
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        lo[i] = min2<BF>(lo[i], x[i]);
-        hi[i] = max2<BF>(hi[i], x[i]);
-        any[i] = max2_nan<BF>(any[i], x[i]);
-      }
-    }
-  }
+  const int64_t at = static_cast<int64_t>(pb) * p.num_kv_heads + h;
+  const uint8_t* page = p.k_cache + at * (NL * Eight::kLine);
   const float scale = BF ? 1.f : p.k_scale[h];
   const float step = p.step[h];
-  uint32_t wl[(C + 3) / 4] = {}, wh[(C + 3) / 4] = {};
+  const int off = lane / P;  // this lane's token of a line
+  uint32_t lo[4], hi[4];
+  auto take = [&](const Eight& e, bool first) {
+    uint32_t x[4];
+    e.pairs(x);
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const float2 l2 = to_f32<BF>(lo[i / 2]), h2 = to_f32<BF>(hi[i / 2]);
-    const float2 a2 = to_f32<BF>(any[i / 2]);
-    float l = (i & 1) ? l2.y : l2.x, u = (i & 1) ? h2.y : h2.x;
-    const float a = (i & 1) ? a2.y : a2.x;
-    if (a != a) {  // a NaN counts as 0
-      l = fminf(l, 0.f);
-      u = fmaxf(u, 0.f);
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = first ? x[i] : min2_nan<BF>(lo[i], x[i]);
+      hi[i] = first ? x[i] : max2_nan<BF>(hi[i], x[i]);
     }
-    if (!BF) {
+  };
+  if (rows == BS) {
+#pragma unroll
+    for (int l0 = 0; l0 < NL; l0 += kTogether) {
+      Eight e[kTogether];
+#pragma unroll
+      for (int l = 0; l < kTogether; ++l) e[l].load(page + (l0 + l) * Eight::kLine, lane);
+#pragma unroll
+      for (int l = 0; l < kTogether; ++l) take(e[l], l0 + l == 0);
+    }
+  } else {
+    // tokens behind the last cached one are read as that one once more
+    constexpr int kSome = kTogether < 8 ? kTogether : 8;
+#pragma unroll 1
+    for (int t0 = 0; t0 < rows; t0 += kSome * R) {
+      Eight e[kSome];
+#pragma unroll
+      for (int l = 0; l < kSome; ++l) {
+        const int t = min(t0 + l * R + off, rows - 1);
+        e[l].load(page + t / R * Eight::kLine, t % R * P + lane % P);
+      }
+#pragma unroll
+      for (int l = 0; l < kSome; ++l) take(e[l], t0 == 0 && l == 0);
+    }
+  }
+  // ---- the tokens of a line are joined; a lane goes on with 8 / R channels
+  constexpr int NP = 4 / R;
+  if constexpr (R == 2) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t l = __shfl_xor_sync(0xffffffffu, off ? lo[i] : lo[NP + i], P);
+      const uint32_t u = __shfl_xor_sync(0xffffffffu, off ? hi[i] : hi[NP + i], P);
+      lo[i] = min2_nan<BF>(off ? lo[NP + i] : lo[i], l);
+      hi[i] = max2_nan<BF>(off ? hi[NP + i] : hi[i], u);
+    }
+  }
+  const int c0 = lane % P * 8 + off * (2 * NP);
+  const float inv = __frcp_rn(step);
+  // a code times its scale is 0 or in 2^-10 .. 2688
+  const bool plain = step >= 0x1p-40f && step <= 0x1p16f &&
+                     (BF || (scale >= 0x1p-20f && scale <= 0x1p20f));
+  uint32_t wl[(NP + 1) / 2] = {}, wh[(NP + 1) / 2] = {};
+#pragma unroll
+  for (int i = 0; i < 2 * NP; ++i) {
+    const float2 l2 = to_f32<BF>(lo[i / 2]), h2 = to_f32<BF>(hi[i / 2]);
+    float l = (i & 1) ? l2.y : l2.x, u = (i & 1) ? h2.y : h2.x;
+    if (l != l) {
+      // a NaN counts as 0
+      l = INFINITY;
+      u = -INFINITY;
+#pragma unroll 1
+      for (int t = 0; t < rows; ++t) {
+        Eight e;
+        uint32_t x[4];
+        e.load(page + t / R * Eight::kLine, t % R * P + lane % P);
+        e.pairs(x);
+        const float2 v2 = to_f32<BF>(R == 2 && off ? x[(NP + i / 2) & 3] : x[i / 2]);
+        float v = (i & 1) ? v2.y : v2.x;
+        v = v == v ? v : 0.f;
+        l = fminf(l, v);
+        u = fmaxf(u, v);
+      }
+    }
+    if (BF) {
+      if (plain) {
+        // far outside the bounds' range before, far outside after
+        l = fminf(fmaxf(l, -512.f * step), 512.f * step);
+        u = fminf(fmaxf(u, -512.f * step), 512.f * step);
+      }
+    } else {
       // (infinities times a scale of 0 are NaN, which count as 0)
       l *= scale;
       u *= scale;
@@ -206,13 +251,13 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
         u = t;
       }
     }
-    const float x = fminf(fmaxf(floorf(__fdiv_rn(l, step)), -127.f), 127.f);
-    const float y = fminf(fmaxf(ceilf(__fdiv_rn(u, step)), -127.f), 127.f);
-    wl[i / 4] |= (static_cast<uint32_t>(static_cast<int>(x)) & 0xFFu) << (8 * (i & 3));
-    wh[i / 4] |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xFFu) << (8 * (i & 3));
+    uint32_t bl, bh;
+    whole_steps(l, u, step, inv, plain, bl, bh);
+    wl[i / 4] |= bl << (8 * (i & 3));
+    wh[i / 4] |= bh << (8 * (i & 3));
   }
-  int8_t* out = p.bounds + (static_cast<int64_t>(pb) * p.num_kv_heads + h) * (2 * D) + C * lane;
-  if constexpr (C == 8) {
+  int8_t* out = p.bounds + at * (2 * D) + c0;
+  if constexpr (R == 1) {
     *reinterpret_cast<uint2*>(out) = make_uint2(wl[0], wl[1]);
     *reinterpret_cast<uint2*>(out + D) = make_uint2(wh[0], wh[1]);
   } else {

@@ -153,3 +153,56 @@ def test_large_pool_stream_and_graph(_lib):
     graph.replay()
     verify()
     assert int(_lib.item()) == 0
+
+
+@pytest.mark.parametrize("d,block", [(128, 16), (256, 32)])
+def test_values_and_steps_of_any_size(d, block, _lib):
+    c = AnyCache([5 * block, 3 * block - 1], 8, d, block, "bf16", seed=6)
+    r = torch.Generator(device="cuda")
+    r.manual_seed(8)
+    for s, n in enumerate(c.lens):
+        for b in range(-(-n // block)):
+            # every exponent, zeros, infinities, or few exponents
+            bits = torch.randint(0, 1 << 16, (8, block, d), device="cuda", generator=r)
+            if b == 1:
+                bits = bits & 0x81FF | 0x3F00
+            if b == 2:
+                bits = bits & 0x807F  # below the normal numbers
+            x = bits.to(torch.int32).to(torch.int16).view(torch.bfloat16)
+            x = torch.where(x.isnan(), 0.0, x.float()).to(torch.bfloat16)
+            c.k[int(c.tables[s, b])] = x
+            lo, hi = b * block, min(n, (b + 1) * block)
+            c.K[s][lo:hi] = x.transpose(0, 1)[:hi - lo].to(c.K[s].dtype)
+    for steps in ([1e-30, 2.0 ** -41, 2.0 ** -40, 1e-7, 0.0123, 0.5, 1.0, 3.0],
+                  [700.0, 2.0 ** 16, 2.0 ** 17, 1e9, 1e30, 1.9999999, 1e-38, 3e38]):
+        step = torch.tensor(steps, device="cuda")
+        out = fresh(c)
+        pkv.block_bounds(out, c.k, c.tables, c.context_lens, step, 5 * block)
+        for s, n in enumerate(c.lens):
+            for b in range(-(-n // block)):
+                assert torch.equal(out[int(c.tables[s, b])], bounds_of(c, step, s, b)), (s, b)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("d", [128, 256])
+def test_scales_of_any_size(d, kind, _lib):
+    c = AnyCache([50, 64], 4, d, 16, kind, seed=7)
+    keep = c.ks.clone()
+    for by, step in ((1e-9, 1e-10), (1e9, 1e8), (1e-35, 1e-36), (1e-3, 1e-38), (1.0, 2.0 ** -5),
+                     (1e20, 1e18)):
+        c.ks.copy_(keep * by)
+        steps = torch.full((4,), step, device="cuda")
+        out = fresh(c)
+        pkv.block_bounds(out, c.k, c.tables, c.context_lens, steps, 64, k_scale=c.ks)
+        kv = pkv.kv_cache_read  # the codes' values without the scale are bf16 numbers
+        one = torch.ones_like(c.ks)
+        for s, n in enumerate(c.lens):
+            slots = (c.tables[s].long().repeat_interleave(16)[:n] * 16
+                     + torch.arange(n, device="cuda") % 16)
+            x = kv(slots, c.k, c.k, one, one)[0].float() * c.ks[:, None]
+            x = x / steps[:, None]
+            for b in range(-(-n // 16)):
+                y = x[16 * b:16 * b + 16]
+                want = torch.stack([y.floor().clamp(-127, 127).amin(0),
+                                    y.ceil().clamp(-127, 127).amax(0)], 1).to(torch.int8)
+                assert torch.equal(out[int(c.tables[s, b])], want), (by, s, b)
