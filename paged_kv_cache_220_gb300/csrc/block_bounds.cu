@@ -12,10 +12,9 @@
 //
 // Bound by HBM on bf16 pools (8 x 16384 tokens, 4 heads, d = 256, B = 16: 45 us, 93 % of
 // the copy rate), by latency and the instructions of the extremes and conversions on
-// coded ones (E4M3 27.4 us, 81 %; 4-bit 29 us, 47 %), and by latency alone at one block
-// per sequence (2.7 us). Two to eight pages to a warp, with their blocks looked up
-// together, took longer (E4M3, d = 128: 25 us with one, 34 to 63), and so did a grid
-// without the 64-bit divisions (21.1, 24.6).
+// coded ones (E4M3 26.3 us, 85 %; 4-bit 27.9 us, 49 %), and by latency alone at one block
+// per sequence (2.5 us). Two to eight pages to a warp, with their blocks looked up
+// together, took longer (E4M3, d = 128: 25 us with one, 34 to 63).
 #include <algorithm>
 
 #include "common.cuh"
@@ -38,7 +37,6 @@ struct BoundsParams {
   int* err;
   int num_blocks, num_kv_heads, max_blocks_per_seq, max_new;
   int per_seq;      // most blocks of a sequence that its newest tokens touch
-  int64_t items;    // num_seqs * per_seq * num_kv_heads
 };
 
 // Eight channels of a token, as loaded from a line of a page, and as pairs.
@@ -128,12 +126,11 @@ template <int DTYPE, int D, int BS>
 __global__ void __launch_bounds__(kBoundsWarps * 32, 8) block_bounds_kernel(const BoundsParams p) {
   wait_prerequisite();
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5);
-  if (item >= p.items) return;
-  const int h = static_cast<int>(item % p.num_kv_heads);
-  const int64_t sj = item / p.num_kv_heads;
-  const int j = static_cast<int>(sj % p.per_seq);
-  const int s = static_cast<int>(sj / p.per_seq);
+  const uint32_t jh = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
+  const uint32_t heads = p.num_kv_heads;
+  const int s = blockIdx.y;
+  if (jh >= p.per_seq * heads) return;
+  const int h = jh % heads, j = jh / heads;
   const int ctx = p.context_lens[s];
   int n = p.num_new != nullptr ? p.num_new[s] : p.max_new;
   if (ctx < 0 || ctx > static_cast<int64_t>(p.max_blocks_per_seq) * BS || n < 0 ||
@@ -267,8 +264,9 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, 8) block_bounds_kernel(cons
 }
 
 template <int DTYPE>
-static int launch_bounds(const BoundsParams& p, int head_dim, int block_size, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((p.items + kBoundsWarps - 1) / kBoundsWarps));
+static int launch_bounds(const BoundsParams& p, int num_seqs, int head_dim, int block_size, cudaStream_t st) {
+  const int64_t pages = static_cast<int64_t>(p.per_seq) * p.num_kv_heads;  // up to 2^31
+  const dim3 grid(static_cast<unsigned>((pages + kBoundsWarps - 1) / kBoundsWarps), num_seqs);
   const dim3 block(kBoundsWarps * 32);
   if (head_dim == 256)
     return block_size == 16
@@ -291,7 +289,7 @@ extern "C" int pkv_block_bounds(int8_t* bounds, const void* k_cache, pkv_cache_d
   if (rc != PKV_OK) return rc;
   if (num_seqs < 0 || max_new < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
   const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * cache.block_size;
-  if (cap > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+  if (cap > (1 << 30) || num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0 || max_new == 0) return PKV_OK;
   if (!bounds || !k_cache || !step || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
   if (!aligned16(bounds) || !aligned16(k_cache)) return PKV_ERR_INVALID_ARG;
@@ -322,15 +320,13 @@ extern "C" int pkv_block_bounds(int8_t* bounds, const void* k_cache, pkv_cache_d
   p.per_seq = static_cast<int>(std::min<int64_t>(
       max_blocks_per_seq, (static_cast<int64_t>(max_new) + cache.block_size - 2) /
                               cache.block_size + 1));
-  p.items = static_cast<int64_t>(num_seqs) * p.per_seq * cache.num_kv_heads;
-  if ((p.items + kBoundsWarps - 1) / kBoundsWarps > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (cache.dtype) {
     case PKV_DTYPE_BF16:
-      return launch_bounds<PKV_DTYPE_BF16>(p, cache.head_dim, cache.block_size, st);
+      return launch_bounds<PKV_DTYPE_BF16>(p, num_seqs, cache.head_dim, cache.block_size, st);
     case PKV_DTYPE_FP8_E4M3:
-      return launch_bounds<PKV_DTYPE_FP8_E4M3>(p, cache.head_dim, cache.block_size, st);
+      return launch_bounds<PKV_DTYPE_FP8_E4M3>(p, num_seqs, cache.head_dim, cache.block_size, st);
     default:
-      return launch_bounds<PKV_DTYPE_FP4_E2M1>(p, cache.head_dim, cache.block_size, st);
+      return launch_bounds<PKV_DTYPE_FP4_E2M1>(p, num_seqs, cache.head_dim, cache.block_size, st);
   }
 }

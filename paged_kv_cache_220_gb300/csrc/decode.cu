@@ -1,5 +1,5 @@
 // paged_attention_decode: C entry points (validation, workspace layout) for
-// the decode kernel in decode_tc.cu.
+// the decode kernels in decode_tc.cu and decode_fp4.cu.
 //
 // One query token per sequence, grouped-query attention over a paged KV
 // cache: the kernel walks the sequence's block table and gathers K/V from the

@@ -129,7 +129,7 @@ def test_bounds(lib):
                 dict(desc=_desc(dt=1), out=C)):
         assert call(**bad) == INV, bad
     for bad in (dict(desc=_desc(bs=8)), dict(desc=_desc(d=64)), dict(mb=(1 << 26) + 1),
-                dict(desc=_desc(hk=33)), dict(S=1 << 30, mb=1 << 20, new=1 << 28)):
+                dict(desc=_desc(hk=33)), dict(S=1 << 30, mb=1 << 20, new=1 << 28), dict(S=65536)):
         assert call(**bad) == UNS, bad
 
 
