@@ -141,7 +141,8 @@ typedef struct {
  *     1/2688 of the head's largest |x| or more; s has its full precision where
  *     a >= 6 * 2^-6.
  * For bf16 pools the copy is bit-exact. 4-bit pools: PKV_ERR_UNSUPPORTED also for
- * 2^32 and more runs of 8 channels in the call.
+ * 2^32 and more runs of 8 channels in the call. Two tokens of a call with the
+ * same slot leave parts of either there.
  * Errors: PKV_ERR_INVALID_ARG (null pointers, num_tokens < 0, misaligned),
  * PKV_ERR_UNSUPPORTED (shape), PKV_ERR_CUDA. num_tokens == 0 is a no-op.
  * ------------------------------------------------------------------------ */
@@ -181,7 +182,9 @@ int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tok
  *     z_t = scale * <q[s,j,:], K_s[t,:]>,  out[s,j,:] = sum_t softmax(z)_t V_s[t,:]
  * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]), 4-bit pools as
  * code * s * k_scale[h] (tables of at most 2^30 tokens a sequence; an element
- * of q below 2^-14 of its row's largest is rounded by at most 2^-25 of it).
+ * of q below 2^-14 of its row's largest is rounded by at most 2^-25 of it; the
+ * softmax's weights meet V rounded to 11 bits, those below 2^-40 of the largest
+ * as zero).
  * The softmax is the max-subtracted one, accumulated online in fp32.
  *
  *   out       : device bf16 [num_seqs][num_heads][head_dim] (written when
@@ -689,8 +692,9 @@ int pkv_paged_attention_decode_noalloc(void* out, const void* q, const void* k_c
  *   blocks  : int32 [n] block ids, readable by the device (device memory or
  *             pinned host memory)
  *   k_buf, v_buf : [n][num_kv_heads*page bytes] (a page is block_size*head_dim
- *             elements of 2, 1 or 9/16 bytes), block i of the list at row i; device memory or pinned host memory the device
- *             can address (the kernel reads/writes it directly)
+ *             elements of 2, 1 or 9/16 bytes), block i of the list at row i;
+ *             device memory or pinned host memory the device can address (the
+ *             kernel reads/writes it directly)
  * swap_out: buf[i] = pool[blocks[i]]; swap_in: pool[blocks[i]] = buf[i]
  * (byte for byte). The allocator side (freeing a sequence, re-creating it
  * with fresh blocks on the way back) is the caller's.

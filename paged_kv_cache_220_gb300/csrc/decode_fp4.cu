@@ -29,6 +29,11 @@
 //   largest and not 2^-25. Both factors leave exactly.
 // - A hidden token (behind the context, of a skipped block) gets the logit -inf and
 //   V's scale 0: codes are always finite, only a scale can be NaN.
+//
+// Bound by HBM in whole waves (8 x 131072 tokens, 4 heads, d = 256 191 us with the merge,
+// 6.3 TB/s of codes and scales, 93 % of the copy rate); 64 x 8192 117 us (5.2 TB/s):
+// 2.25 waves, whose starts, ends and uneven last part three warps to a scheduler
+// (168 registers, 56 % of the issue slots) do not hide.
 #include <algorithm>
 
 #include "common.cuh"

@@ -159,7 +159,9 @@ __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, fl
 
 // 4-bit pools. Item i is channels [8 c8, 8 c8 + 8) of head h of a token, c8 fastest:
 // rows of k and v are read straight through, a thread U items THREADS apart with
-// their loads in flight together. Two lanes share a scale.
+// their loads in flight together. Two lanes share a scale. Bound by the integer pipe
+// (conversions, packing, addresses; 73 % busy): 8192 tokens, 8 heads, d = 128 12.1 us,
+// 3.5 TB/s, 14.8 with scales that are powers of two; 64 tokens 1.7 us.
 constexpr int kFp4WriteThreads = 256;
 
 template <int D, int U>
