@@ -117,6 +117,14 @@ __device__ __forceinline__ __half2 scales_of(uint32_t w, int hi) {
   return *reinterpret_cast<const __half2*>(&d);
 }
 
+// The bits of a where mask has ones, those of b elsewhere (written as an expression it
+// became two instructions)
+__device__ __forceinline__ uint32_t bits_of(uint32_t mask, uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(mask), "r"(a), "r"(b));
+  return d;
+}
+
 template <int D, int BS, bool LIST, int TU, int W, int NST, int CTAS>
 __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodeParams p) {
   using G = Fp4Geom<D, TU, W, NST>;
@@ -476,10 +484,10 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
         const __half2 s23 = scales_of(__byte_perm(e8[2], e8[3], sel), 0);
         constexpr uint32_t kLow = 0x0F0F0F0Fu;
         uint32_t ev01[4], od01[4], ev23[4], od23[4];
-        e2m1x8_f16x2((w[0][x] & kLow) | ((w[1][x] << 4) & ~kLow), ev01);
-        e2m1x8_f16x2(((w[0][x] >> 4) & kLow) | (w[1][x] & ~kLow), od01);
-        e2m1x8_f16x2((w[2][x] & kLow) | ((w[3][x] << 4) & ~kLow), ev23);
-        e2m1x8_f16x2(((w[2][x] >> 4) & kLow) | (w[3][x] & ~kLow), od23);
+        e2m1x8_f16x2(bits_of(kLow, w[0][x], w[1][x] << 4), ev01);
+        e2m1x8_f16x2(bits_of(kLow, w[0][x] >> 4, w[1][x]), od01);
+        e2m1x8_f16x2(bits_of(kLow, w[2][x], w[3][x] << 4), ev23);
+        e2m1x8_f16x2(bits_of(kLow, w[2][x] >> 4, w[3][x]), od23);
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           mma_f16(o[4 * x + y], mul_f16x2(ev01[y], s01), mul_f16x2(od01[y], s01),
