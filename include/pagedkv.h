@@ -141,7 +141,7 @@ typedef struct {
  *     1/2688 of the head's largest |x| or more; s has its full precision where
  *     a >= 6 * 2^-6.
  * For bf16 pools the copy is bit-exact. 4-bit pools: PKV_ERR_UNSUPPORTED also for
- * 2^32 and more runs of 8 channels in the call. Two tokens of a call with the
+ * 2^32 and more runs of 8 channels in the call or pages in the pool. Two tokens of a call with the
  * same slot leave parts of either there.
  * Errors: PKV_ERR_INVALID_ARG (null pointers, num_tokens < 0, misaligned),
  * PKV_ERR_UNSUPPORTED (shape), PKV_ERR_CUDA. num_tokens == 0 is a no-op.
@@ -165,7 +165,7 @@ int pkv_kv_cache_write(const void* k, const void* v, const int64_t* slot_mapping
  *     row is zeros; a slot outside the pool is reported (PKV_DEVERR_SLOT), its
  *     row is zeros
  *   other args   : as for pkv_kv_cache_write
- * Errors: as for pkv_kv_cache_write (2^32 runs of 8 channels: any pool).
+ * Errors: as for pkv_kv_cache_write (2^32 runs of 8 channels, pages: any pool).
  * ------------------------------------------------------------------------ */
 int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tokens,
                       const void* k_cache, const void* v_cache, pkv_cache_desc cache,

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "host_util.h"
+#include "quotients.cuh"
 
 namespace pkv {
 
@@ -54,7 +55,8 @@ struct Eight {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-        out[i] = bf16x2_of(y.x * scale, y.y * scale);
+        const float2 z = of_pair(mul_pair(pair_of(y.x, y.y), pair_of(scale, scale)));
+        out[i] = bf16x2_of(z.x, z.y);
       }
       return make_uint4(out[0], out[1], out[2], out[3]);
     }
@@ -67,7 +69,7 @@ template <int DTYPE, int D, int U>
 __global__ void __launch_bounds__(kReadThreads) kv_cache_read_kernel(
     uint4* __restrict__ k, uint4* __restrict__ v, const int64_t* __restrict__ slot_mapping,
     const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache, int64_t num_slots,
-    int log_block, int num_kv_heads, int64_t page_bytes, uint32_t items,
+    int log_block, int num_kv_heads, uint32_t page_bytes, uint32_t items,
     const float* __restrict__ k_scale, const float* __restrict__ v_scale, int* err) {
   wait_prerequisite();
   const uint32_t first = blockIdx.x * (U * kReadThreads) + threadIdx.x;
@@ -85,9 +87,10 @@ __global__ void __launch_bounds__(kReadThreads) kv_cache_read_kernel(
     if (slot >= num_slots && rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
     some[u] = slot >= 0 && slot < num_slots;
     if (some[u]) {
-      const int64_t blk = slot >> log_block;
-      const int64_t page = (blk * num_kv_heads + rest[u] / (D / 8)) * page_bytes;
-      const int off = static_cast<int>(slot - (blk << log_block));
+      const uint32_t blk = static_cast<uint32_t>(slot >> log_block);
+      const uint64_t page =
+          static_cast<uint64_t>(blk * num_kv_heads + rest[u] / (D / 8)) * page_bytes;
+      const int off = static_cast<int>(slot) & ((1 << log_block) - 1);
       ke[u].load(k_cache + page, off, rest[u] % (D / 8));
       ve[u].load(v_cache + page, off, rest[u] % (D / 8));
     }
@@ -142,13 +145,16 @@ extern "C" int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, 
       return PKV_ERR_INVALID_ARG;
   if (overlap(k, rows, v, rows)) return PKV_ERR_INVALID_ARG;
   const int64_t items = static_cast<int64_t>(num_tokens) * threads;
-  if (items >= (int64_t{1} << 32) - 4 * kReadThreads) return PKV_ERR_UNSUPPORTED;
+  if (items >= (int64_t{1} << 32) - 4 * kReadThreads ||
+      static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads >= int64_t{1} << 32)
+    return PKV_ERR_UNSUPPORTED;
   auto go = [&](auto launch) {
     return launch(items, static_cast<cudaStream_t>(stream), static_cast<uint4*>(k),
                   static_cast<uint4*>(v), slot_mapping, static_cast<const uint8_t*>(k_cache),
                   static_cast<const uint8_t*>(v_cache),
                   static_cast<int64_t>(cache.num_blocks) * cache.block_size,
-                  cache.block_size == 16 ? 4 : 5, cache.num_kv_heads, page_bytes(cache),
+                  cache.block_size == 16 ? 4 : 5, cache.num_kv_heads,
+                  static_cast<uint32_t>(page_bytes(cache)),
                   static_cast<uint32_t>(items), k_scale, v_scale,
                   device_error_ptr());
   };

@@ -71,10 +71,10 @@ __global__ void __launch_bounds__(1024) kv_cache_write_kernel(
   }
 }
 
-// The larger of each of two bf16 pairs, NaN if one is.
-__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+// The larger magnitude of each of two bf16 pairs, NaN if one is; some sign.
+__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -99,10 +99,9 @@ __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, fl
                                                  bool plain, uint8_t& s_code) {
   constexpr float kLess = 1.f - 0x1p-20f, kMore = 1.f + 0x1p-20f, kSixth = 1.f / 6.f;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  constexpr uint32_t kAbs = 0x7FFF7FFFu;
-  uint32_t t2 = max2_nan(max2_nan(w[0] & kAbs, w[1] & kAbs), max2_nan(w[2] & kAbs, w[3] & kAbs));
-  t2 = max2_nan(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
-  const float top = bf16lo(max2_nan(t2, t2 >> 16));
+  uint32_t t2 = max2_abs(max2_abs(w[0], w[1]), max2_abs(w[2], w[3]));
+  t2 = max2_abs(t2, __shfl_xor_sync(0xffffffffu, t2, 1));
+  const float top = fabsf(bf16lo(max2_abs(t2, t2 >> 16)));
   float z8[8];
   if (plain && top >= 0x1p-40f && top <= 0x1p60f) {
     const uint64_t r = pair_of(inv, inv), b = pair_of(-scale, -scale);
@@ -210,9 +209,10 @@ __global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
       if (rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
       continue;
     }
-    const int64_t blk = slot[u] >> log_block;
-    const int off = static_cast<int>(slot[u] - (blk << log_block));
-    const int64_t page = ((blk * num_kv_heads + h) << log_block) * (D / 16 * 9);
+    const uint32_t blk = static_cast<uint32_t>(slot[u] >> log_block);
+    const int off = static_cast<int>(slot[u]) & ((1 << log_block) - 1);
+    const int64_t page = static_cast<uint64_t>(blk * num_kv_heads + h) *
+                         static_cast<uint32_t>((D / 16 * 9) << log_block);
     const int64_t codes = page + fp4_codes_at<D>(off) + 4 * c8;
     *reinterpret_cast<uint32_t*>(k_cache + codes) = kc;
     *reinterpret_cast<uint32_t*>(v_cache + codes) = vc;
@@ -250,7 +250,9 @@ extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* s
   auto* vc = static_cast<uint8_t*>(v_cache);
   if (fp4) {
     const int64_t items = static_cast<int64_t>(num_tokens) * threads;
-    if (items >= (int64_t{1} << 32) - 4 * kFp4WriteThreads) return PKV_ERR_UNSUPPORTED;
+    if (items >= (int64_t{1} << 32) - 4 * kFp4WriteThreads ||
+        static_cast<int64_t>(nb) * hk >= int64_t{1} << 32)
+      return PKV_ERR_UNSUPPORTED;
     auto go = [&](auto kern, int u) {
       const int64_t per = static_cast<int64_t>(u) * kFp4WriteThreads;
       return launch_dependent(kern, dim3(static_cast<unsigned>((items + per - 1) / per)),
