@@ -10,12 +10,15 @@ E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
 
 def quantize(x, scale):
     """x [..., heads, d] fp32, scale [heads] -> (codes 0..15 as uint8 [..., heads, d],
-    scale codes uint8 [..., heads, d/16]): the definition, division by division."""
-    y = (x.float() / scale.float()[:, None]).unflatten(-1, (-1, 16))
+    scale codes uint8 [..., heads, d/16]): the definition, division by division.
+    (A quotient in 64 bits rounded to 32 is the quotient rounded to 32: 53 bits are
+    more than 2 * 24 + 1. A tensor divided by a Python number on the GPU is a product
+    with 1/6 and not that.)"""
+    y = (x.double() / scale.double()[:, None]).float().unflatten(-1, (-1, 16))
     a = y.abs().amax(-1)  # a NaN stays one
-    s8 = torch.where(a.isnan(), a, (a / 6).clamp(max=448)).to(torch.float8_e4m3fn)
+    s8 = torch.where(a.isnan(), a, (a.double() / 6).float().clamp(max=448)).to(torch.float8_e4m3fn)
     s = s8.float()[..., None]
-    z = torch.where(s > 0, y / s, torch.zeros_like(y))
+    z = torch.where(s > 0, (y.double() / s.double()).float(), torch.zeros_like(y))
     m = z.abs()
     code = ((m > 0.25).int() + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5)
             + (m > 5)) + 8 * torch.signbit(z)
