@@ -64,25 +64,23 @@ __device__ __forceinline__ float e4m3_f32(uint8_t x) {
   return __low2float(*reinterpret_cast<__half2*>(&h));
 }
 
-// The token of item i of rows with `per` items each and the item in its row, for i
-// = first, first + step, ..: one division to start with.
-struct RowItems {
-  uint32_t per, step_token, step_rest, token, rest;
+// How rows of `per` 8-channel pieces are dealt to threads: a CTA has whole rows, `rows` of
+// them side by side, so that a thread's piece is the same in every one it has (its head,
+// its scales) and the row is found without a division.
+struct RowsOfCta {
+  uint32_t per, rows, inverse;  // inverse: of per, for a product in the place of a division
 
-  __device__ __forceinline__ RowItems(uint32_t first, uint32_t step, uint32_t per_row) {
-    per = per_row;
-    step_token = step / per;
-    step_rest = step - step_token * per;
-    token = first / per;
-    rest = first - token * per;
-  }
-  __device__ __forceinline__ void next() {
-    token += step_token;
-    rest += step_rest;
-    if (rest >= per) {
-      rest -= per;
-      ++token;
-    }
+  static constexpr int kThreads = 256;  // or one row, up to 1024
+
+  explicit RowsOfCta(int per_row)
+      : per(per_row), rows(per_row < kThreads ? kThreads / per_row : 1),
+        inverse((1u << 16) / per_row + 1) {}
+  int threads() const { return static_cast<int>((rows * per + 31) / 32 * 32); }
+
+  // The row of the CTA's that thread tid has a piece of, `rows` or more for none. (Below
+  // 256 threads tid * per is below 2^16, so that the rounded-up inverse is exact.)
+  __device__ __forceinline__ uint32_t row_of(uint32_t tid) const {
+    return rows == 1 ? (tid >= per ? 1 : 0) : (tid * inverse) >> 16;
   }
 };
 

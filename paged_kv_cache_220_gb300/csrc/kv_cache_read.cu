@@ -1,10 +1,10 @@
 // kv_cache_read: the rows that given slots of a cache hold, as bf16.
 //
-// Item i is channels [8 c8, 8 c8 + 8) of head h of a token, c8 fastest: 16, 8 or 4
-// bytes of each pool, 16 bytes of each result; a warp's are whole rows. Many tokens
-// (U items to a thread, their loads in flight together) are bound by HBM and, on 4-bit
-// pools, as much by the conversions' instructions: 8192 tokens, 8 heads, d = 128 8.1 us,
-// 5.3 TB/s. A step's few are bound by latency (64 tokens: 1.5 us).
+// A thread has channels [8 c8, 8 c8 + 8) of a head of U tokens, their loads in flight
+// together: 16, 8 or 4 bytes of each pool, 16 bytes of each result; a warp's are whole
+// rows. Many tokens are bound by HBM and, on 4-bit pools, as much by the conversions'
+// instructions: 32768 tokens, 8 heads, d = 128 30.4 us, 5.7 TB/s. A step's few are bound by
+// latency (64 tokens: 1.5 us).
 #include <type_traits>
 
 #include "common.cuh"
@@ -63,60 +63,59 @@ struct Eight {
   }
 };
 
-constexpr int kReadThreads = 256;
-
 template <int DTYPE, int D, int U>
-__global__ void __launch_bounds__(kReadThreads) kv_cache_read_kernel(
+__global__ void __launch_bounds__(1024) kv_cache_read_kernel(
     uint4* __restrict__ k, uint4* __restrict__ v, const int64_t* __restrict__ slot_mapping,
     const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache, int64_t num_slots,
-    int log_block, int num_kv_heads, uint32_t page_bytes, uint32_t items,
+    int log_block, int num_kv_heads, uint32_t page_bytes, uint32_t num_tokens, RowsOfCta deal,
     const float* __restrict__ k_scale, const float* __restrict__ v_scale, int* err) {
   wait_prerequisite();
-  const uint32_t first = blockIdx.x * (U * kReadThreads) + threadIdx.x;
-  RowItems at(first, kReadThreads, num_kv_heads * (D / 8));
+  const uint32_t row = deal.row_of(threadIdx.x);
+  if (row >= deal.rows) return;
+  const uint32_t rest = threadIdx.x - row * deal.per;
+  const int h = rest / (D / 8), c8 = rest % (D / 8);
+  const uint32_t first = blockIdx.x * (U * deal.rows) + row;
+  constexpr bool kCoded = DTYPE != PKV_DTYPE_BF16;
+  const float ks = kCoded ? k_scale[h] : 1.f, vs = kCoded ? v_scale[h] : 1.f;
   Eight<DTYPE, D> ke[U], ve[U];
-  int rest[U];
-  bool live[U], some[U];
+  bool some[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = first + u * kReadThreads;
-    live[u] = i < items;
-    rest[u] = at.rest;
-    const int64_t slot = live[u] ? slot_mapping[at.token] : -1;
-    at.next();
-    if (slot >= num_slots && rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
+    const uint32_t token = first + u * deal.rows;
+    const int64_t slot = token < num_tokens ? slot_mapping[token] : -1;
+    if (slot >= num_slots && rest == 0) report_error(err, PKV_DEVERR_SLOT);
     some[u] = slot >= 0 && slot < num_slots;
     if (some[u]) {
       const uint32_t blk = static_cast<uint32_t>(slot >> log_block);
-      const uint64_t page =
-          static_cast<uint64_t>(blk * num_kv_heads + rest[u] / (D / 8)) * page_bytes;
+      const uint64_t page = static_cast<uint64_t>(blk * num_kv_heads + h) * page_bytes;
       const int off = static_cast<int>(slot) & ((1 << log_block) - 1);
-      ke[u].load(k_cache + page, off, rest[u] % (D / 8));
-      ve[u].load(v_cache + page, off, rest[u] % (D / 8));
+      ke[u].load(k_cache + page, off, c8);
+      ve[u].load(v_cache + page, off, c8);
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (!live[u]) continue;
-    const int h = rest[u] / (D / 8);
-    const bool coded = DTYPE != PKV_DTYPE_BF16;
+    const uint32_t token = first + u * deal.rows;
+    if (token >= num_tokens) continue;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint32_t i = first + u * kReadThreads;
-    k[i] = some[u] ? ke[u].values(coded ? k_scale[h] : 1.f) : zero;
-    v[i] = some[u] ? ve[u].values(coded ? v_scale[h] : 1.f) : zero;
+    const uint32_t i = token * deal.per + rest;
+    k[i] = some[u] ? ke[u].values(ks) : zero;
+    v[i] = some[u] ? ve[u].values(vs) : zero;
   }
 }
 
 template <int DTYPE, int D, typename... Args>
-static int launch_read(int64_t items, cudaStream_t st, Args... args) {
+static int launch_read(int num_tokens, const RowsOfCta& deal, cudaStream_t st, Args... args) {
   auto go = [&](auto kern, int u) {
-    const int64_t per = static_cast<int64_t>(u) * kReadThreads;
-    return launch_dependent(kern, dim3(static_cast<unsigned>((items + per - 1) / per)),
-                            dim3(kReadThreads), 0, st, args...);
+    const int per = u * static_cast<int>(deal.rows);
+    return launch_dependent(kern, dim3((num_tokens + int64_t{per} - 1) / per),
+                            dim3(deal.threads()), 0, st, args...);
   };
-  // four items to a thread once they fill the SMs (8 CTAs each)
-  return items >= 4 * 8 * 152 * kReadThreads ? go(kv_cache_read_kernel<DTYPE, D, 4>, 4)
-                                             : go(kv_cache_read_kernel<DTYPE, D, 1>, 1);
+  // two tokens to a thread once they fill the SMs (2048 threads each): 32768 tokens right
+  // after they were written, 4-bit, 8 heads, d = 128 32 us; one 39, four 34
+  return int64_t{num_tokens} * deal.per >= 2 * 2048 * 152
+             ? go(kv_cache_read_kernel<DTYPE, D, 2>, 2)
+             : go(kv_cache_read_kernel<DTYPE, D, 1>, 1);
 }
 
 }  // namespace pkv
@@ -144,18 +143,18 @@ extern "C" int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, 
         overlap(w, rows, slot_mapping, slots))
       return PKV_ERR_INVALID_ARG;
   if (overlap(k, rows, v, rows)) return PKV_ERR_INVALID_ARG;
-  const int64_t items = static_cast<int64_t>(num_tokens) * threads;
-  if (items >= (int64_t{1} << 32) - 4 * kReadThreads ||
+  const RowsOfCta deal(threads);
+  if (static_cast<int64_t>(num_tokens) * threads >= (int64_t{1} << 32) - 4096 ||
       static_cast<int64_t>(cache.num_blocks) * cache.num_kv_heads >= int64_t{1} << 32)
     return PKV_ERR_UNSUPPORTED;
   auto go = [&](auto launch) {
-    return launch(items, static_cast<cudaStream_t>(stream), static_cast<uint4*>(k),
+    return launch(num_tokens, deal, static_cast<cudaStream_t>(stream), static_cast<uint4*>(k),
                   static_cast<uint4*>(v), slot_mapping, static_cast<const uint8_t*>(k_cache),
                   static_cast<const uint8_t*>(v_cache),
                   static_cast<int64_t>(cache.num_blocks) * cache.block_size,
                   cache.block_size == 16 ? 4 : 5, cache.num_kv_heads,
                   static_cast<uint32_t>(page_bytes(cache)),
-                  static_cast<uint32_t>(items), k_scale, v_scale,
+                  static_cast<uint32_t>(num_tokens), deal, k_scale, v_scale,
                   device_error_ptr());
   };
   const bool wide = cache.head_dim == 256;

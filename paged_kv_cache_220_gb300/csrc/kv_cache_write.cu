@@ -88,7 +88,7 @@ __device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
 // rounded), and a product with reciprocals is off by less than 2^-21 of the rounded
 // quotient of the rounded quotient: the same product 2^-20 lower and 2^-20 higher
 // have it between them, and rounding to a code keeps the order. Where both get the
-// same code, that is the one (8192 tokens, 8 heads, d = 128: 12.1 us, 14.1 without).
+// same code, that is the one (8192 tokens, 8 heads, d = 128: 14.1 -> 12.1 us).
 // Elsewhere, near a midpoint between two codes, the quotients are made exact, in
 // pairs. Of y / s only the side of a midpoint counts. s has 4 significant bits and a
 // midpoint m 3, so m s is an fp32 number: y / s rounds to m only if y = m s, the next y
@@ -156,57 +156,48 @@ __device__ __forceinline__ uint32_t quantize_fp4(const uint4& x, float scale, fl
   return e2m1x8_of(z8);
 }
 
-// 4-bit pools. Item i is channels [8 c8, 8 c8 + 8) of head h of a token, c8 fastest:
-// rows of k and v are read straight through, a thread U items THREADS apart with
-// their loads in flight together. Two lanes share a scale. Bound by the integer pipe
-// (conversions, packing, addresses; 73 % busy): 8192 tokens, 8 heads, d = 128 12.1 us,
-// 3.5 TB/s, 14.8 with scales that are powers of two; 64 tokens 1.7 us.
-constexpr int kFp4WriteThreads = 256;
-
+// 4-bit pools. A thread has channels [8 c8, 8 c8 + 8) of a head of U tokens, their loads
+// in flight together; rows of k and v are read straight through. Two lanes share a
+// scale. Bound by the integer pipe (conversions, packing, addresses): 32768 tokens, 8
+// heads, d = 128 38.0 us, 4.5 TB/s, 47.5 with scales that are powers of two; 64 tokens 1.5
+// us. (One token to a thread: 8192 tokens 11.6 us, two 11.2, three 12.0, four 13.5.)
 template <int D, int U>
-__global__ void __launch_bounds__(kFp4WriteThreads) kv_cache_write_fp4_kernel(
+__global__ void __launch_bounds__(1024) kv_cache_write_fp4_kernel(
     const uint4* __restrict__ k, const uint4* __restrict__ v,
     const int64_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_cache,
     uint8_t* __restrict__ v_cache, int64_t num_slots, int log_block, int num_kv_heads,
-    uint32_t items, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-    int* err) {
-  // the heads' scales and their reciprocals
-  __shared__ float2 by[2][32];
+    uint32_t num_tokens, RowsOfCta deal, const float* __restrict__ k_scale,
+    const float* __restrict__ v_scale, int* err) {
   allow_dependents();
   wait_prerequisite();
-  if (threadIdx.x < 2 * num_kv_heads) {
-    const int h = threadIdx.x >> 1;
-    const float x = (threadIdx.x & 1) ? v_scale[h] : k_scale[h];
-    by[threadIdx.x & 1][h] = make_float2(x, __frcp_rn(x));
-  }
-  const uint32_t first = blockIdx.x * (U * kFp4WriteThreads) + threadIdx.x;
-  RowItems at(first, kFp4WriteThreads, num_kv_heads * (D / 8));
+  const uint32_t row = deal.row_of(threadIdx.x);
+  const bool some = row < deal.rows;
+  const uint32_t rest = some ? threadIdx.x - row * deal.per : 0;
+  const int h = rest / (D / 8), c8 = rest % (D / 8);
+  const uint32_t first = blockIdx.x * (U * deal.rows) + row;
   int64_t slot[U];
-  int rest[U];
   uint4 kv[U], vv[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = first + u * kFp4WriteThreads;
-    const bool live = i < items;
-    rest[u] = at.rest;
-    slot[u] = live ? slot_mapping[at.token] : -1;
-    at.next();
+    const uint32_t token = first + u * deal.rows;
+    const bool live = some && token < num_tokens;
+    const uint32_t i = token * deal.per + rest;
+    slot[u] = live ? slot_mapping[token] : -1;
     kv[u] = live ? k[i] : make_uint4(0, 0, 0, 0);
     vv[u] = live ? v[i] : make_uint4(0, 0, 0, 0);
   }
-  __syncthreads();
+  const float ks = k_scale[h], vs = v_scale[h];
+  const float k_inv = __frcp_rn(ks), v_inv = __frcp_rn(vs);
+  const bool k_plain = ks >= 0x1p-40f && ks <= 0x1p40f;
+  const bool v_plain = vs >= 0x1p-40f && vs <= 0x1p40f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = rest[u] / (D / 8), c8 = rest[u] % (D / 8);
-    const float2 kb = by[0][h], vb = by[1][h];
     uint8_t k8, v8;
-    const uint32_t kc =
-        quantize_fp4(kv[u], kb.x, kb.y, kb.x >= 0x1p-40f && kb.x <= 0x1p40f, k8);
-    const uint32_t vc =
-        quantize_fp4(vv[u], vb.x, vb.y, vb.x >= 0x1p-40f && vb.x <= 0x1p40f, v8);
+    const uint32_t kc = quantize_fp4(kv[u], ks, k_inv, k_plain, k8);
+    const uint32_t vc = quantize_fp4(vv[u], vs, v_inv, v_plain, v8);
     if (slot[u] < 0) continue;
     if (slot[u] >= num_slots) {
-      if (rest[u] == 0) report_error(err, PKV_DEVERR_SLOT);
+      if (rest == 0) report_error(err, PKV_DEVERR_SLOT);
       continue;
     }
     const uint32_t blk = static_cast<uint32_t>(slot[u] >> log_block);
@@ -249,21 +240,22 @@ extern "C" int pkv_kv_cache_write(const void* k, const void* v, const int64_t* s
   auto* kc = static_cast<uint8_t*>(k_cache);
   auto* vc = static_cast<uint8_t*>(v_cache);
   if (fp4) {
-    const int64_t items = static_cast<int64_t>(num_tokens) * threads;
-    if (items >= (int64_t{1} << 32) - 4 * kFp4WriteThreads ||
+    const int64_t pieces = static_cast<int64_t>(num_tokens) * threads;
+    if (pieces >= (int64_t{1} << 32) - 4096 ||
         static_cast<int64_t>(nb) * hk >= int64_t{1} << 32)
       return PKV_ERR_UNSUPPORTED;
+    const RowsOfCta deal(threads);
     auto go = [&](auto kern, int u) {
-      const int64_t per = static_cast<int64_t>(u) * kFp4WriteThreads;
-      return launch_dependent(kern, dim3(static_cast<unsigned>((items + per - 1) / per)),
-                              dim3(kFp4WriteThreads), 0, st, static_cast<const uint4*>(k),
+      const int per = u * static_cast<int>(deal.rows);
+      return launch_dependent(kern, dim3((num_tokens + int64_t{per} - 1) / per),
+                              dim3(deal.threads()), 0, st, static_cast<const uint4*>(k),
                               static_cast<const uint4*>(v), slot_mapping, kc, vc,
                               static_cast<int64_t>(nb) * bs, bs == 16 ? 4 : 5, hk,
-                              static_cast<uint32_t>(items), k_scale, v_scale,
+                              static_cast<uint32_t>(num_tokens), deal, k_scale, v_scale,
                               device_error_ptr());
     };
-    // two items to a thread once they fill the SMs (8 CTAs each)
-    if (items >= 2 * 8 * 152 * kFp4WriteThreads)
+    // two tokens to a thread once they fill the SMs (2048 threads each)
+    if (pieces >= 2 * 2048 * 152)
       return hd == 256 ? go(kv_cache_write_fp4_kernel<256, 2>, 2)
                        : go(kv_cache_write_fp4_kernel<128, 2>, 2);
     return hd == 256 ? go(kv_cache_write_fp4_kernel<256, 1>, 1)

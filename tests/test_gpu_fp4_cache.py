@@ -235,3 +235,36 @@ def test_copies_and_swaps(d, block, _lib):
     pkv.swap_in(kc, vc, back, kb, vb)
     k0[[5, 6, 8]], v0[[5, 6, 8]] = kb, vb
     assert torch.equal(kc, k0) and torch.equal(vc, v0) and int(_lib.item()) == 0
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("hk", [1, 3, 9, 15, 16, 17, 31])
+def test_rows_that_do_not_fill_a_cta(hk, d, _lib):
+    """Numbers of rows around multiples of what a CTA takes, up to two rows to a thread."""
+    per = hk * d // 8
+    many = 2 * 2048 * 152 // per + 1
+    nb = -(-many // 16) + 1
+    ks, vs = torch.rand(hk, device="cuda") + 0.1, torch.rand(hk, device="cuda") + 0.1
+    for n in (1, 256 // per + 1, 5, many):
+        k, v = rows(n, hk, d, n), rows(n, hk, d, n + 1)
+        kc, vc = pkv.fp4_cache(nb, hk, 16, d), pkv.fp4_cache(nb, hk, 16, d)
+        slots = torch.randperm(nb * 16, device="cuda")[:n]
+        pkv.kv_cache_write(k, v, slots, kc, vc, ks, vs)
+        got = pkv.kv_cache_read(slots, kc, vc, ks, vs)
+        for x, y, pool, scale in ((k, got[0], kc, ks), (v, got[1], vc, vs)):
+            codes, scales = quantize(x, scale)
+            want = (values(codes, scales) * scale.double()[:, None]).float().to(torch.bfloat16)
+            assert torch.equal(y, want), n
+            # nothing else was written
+            have = at_slots(pool, slots, d)
+            assert torch.equal(have[0], codes) and torch.equal(have[1], scales), n
+            for b in range(0, nb, max(1, nb // 3)):
+                used = slots[slots // 16 == b] % 16
+                free = torch.ones(16, dtype=torch.bool, device="cuda")
+                free[used] = False
+                lines = pool[b].view(hk, -1, 144)
+                per_line = 256 // d
+                for t in free.nonzero().flatten().tolist():
+                    r, i = t // per_line, t % per_line
+                    assert int(lines[:, r, i * d // 2:(i + 1) * d // 2].max()) == 0
+    assert int(_lib.item()) == 0
