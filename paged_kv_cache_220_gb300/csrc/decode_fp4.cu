@@ -30,10 +30,11 @@
 // - A hidden token (behind the context, of a skipped block) gets the logit -inf and
 //   V's scale 0: codes are always finite, only a scale can be NaN.
 //
-// Bound by HBM in whole waves (8 x 131072 tokens, 4 heads, d = 256 191 us with the merge,
-// 6.3 TB/s of codes and scales, 93 % of the copy rate); 64 x 8192 117 us (5.2 TB/s):
+// Bound by HBM in whole waves (8 x 131072 tokens, 4 heads, d = 256 186 us with the merge,
+// 6.5 TB/s of codes and scales, 96 % of the copy rate); 64 x 8192 112 us (5.4 TB/s):
 // 2.25 waves, whose starts, ends and uneven last part three warps to a scheduler
-// (168 registers, 56 % of the issue slots) do not hide.
+// (168 registers, 55 % of the issue slots) do not hide. About 1040 instructions to a
+// warp's unit, 750 of them conversions, products by scales and the mma.
 #include <algorithm>
 
 #include "common.cuh"
@@ -642,15 +643,15 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
 // - One pass, a cluster of CTAs to a pair, where a warp then has two units or fewer
 //   (1 x 1033, d = 128: 6.3 us, 7.5 in partitions; 1 x 8192, 8 units a warp: 11.5, 8.0),
 //   or where the pairs fill half a wave by themselves and have 64 units or fewer (256
-//   pairs of 64, d = 256: 39.6 us, 44.1 in 4 partitions; of 256: 128, 117).
+//   pairs of 64, d = 256: 39.6 us, 44.1 in 4 partitions; of 128: 126, 113).
 // - One wave of partitions where the pairs fill it (32 pairs of 131072 tokens, d =
-//   256: 191 us in 14 partitions each, 207 in 56), or where there is not enough for
+//   256: 186 us in 14 partitions each, 207 in 56), or where there is not enough for
 //   more: partitions of 8 units (4 where one CTA to an SM does: 1 x 8192, d = 128:
 //   9.7 us, 10.2 with 8).
 // - Else somewhat over two waves, whose end is short (256 pairs of 8192, d = 256: 112 us
 //   in 4, 118 in 3, 117 in 8), in partitions of at most 2048 tokens, as contexts may
-//   differ (768 pairs of 16 to 16384, d = 128: 66 us, 70 in partitions of 4096; with
-//   the sequences longest first 61 and 56. Ranking them in every CTA cost more than
+//   differ (768 pairs of 16 to 16384, d = 128: 65 us, 70 in partitions of 4096; with
+//   the sequences longest first 60 and 56. Ranking them in every CTA cost more than
 //   it gave from about 100 sequences on).
 Fp4Split fp4_split(int64_t pairs, int64_t units, int unit) {
   constexpr int64_t kWave = 456, kSms = 152;

@@ -8,7 +8,7 @@
 // Measured: bf16, d = 256, 256 pairs of 128 blocks of 16 85.5 to 86.7 us (92 % of the copy
 // rate); d = 128, 256 pairs of 256 blocks 89 us (89 %), 1024 of 64 blocks of 32 162 (98 %);
 // E4M3 d = 128 49 us (81 %) and 85 (93 %); 4-bit, 32 pairs of 512 blocks of 32, d = 256,
-// 37.7 us (59 %: one wave of short shares and the merge).
+// 36.8 us (61 %: one wave of short shares and the merge).
 #include <algorithm>
 
 #include "decode_tc_kernel.cuh"
