@@ -83,6 +83,17 @@ __device__ __forceinline__ bool elected() {
   return e != 0;
 }
 
+// 16 bytes of the cluster's CTA `rank`, at this CTA's address a
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t a, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at));
+  return v;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -619,21 +630,38 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
   // ---- the CTAs of the cluster: rank k has channels [k D/C, (k + 1) D/C) of the
   // result, from every rank's state in rank order
   cluster_sync_all();
-  const int C = p.cluster, SL = D / C;
+  const int C = p.cluster, SL = D / C;  // up to 8 ranks
   const uint32_t o_addr = smem_addr(cs_o), m_addr = smem_addr(cs_m), l_addr = smem_addr(cs_l);
-  for (int idx = threadIdx.x; idx < g * SL; idx += G::kThreads) {
-    const int j = idx / SL, col = part * SL + idx % SL;
-    float M = -INFINITY;
-    for (int k = 0; k < C; ++k) M = fmaxf(M, ld_dsmem(m_addr + 4 * j, k));
-    float L = 0.f, O = 0.f;
+  for (int idx = threadIdx.x; idx < g * SL / 4; idx += G::kThreads) {
+    const int j = idx / (SL / 4), col = part * SL + idx % (SL / 4) * 4;
+    // all ranks' loads in flight together; -inf and zeros for ranks that there are not
+    float m[8], l[8];
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m[k] = k < C ? ld_dsmem(m_addr + 4 * j, k) : -INFINITY;
+      l[k] = k < C ? ld_dsmem(l_addr + 4 * j, k) : 0.f;
+      x[k] = k < C ? ld_dsmem4(o_addr + 4 * (j * D + col), k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float M = m[0], L = 0.f;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) M = fmaxf(M, m[k]);
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     if (M != -INFINITY) {
-      for (int k = 0; k < C; ++k) {
-        const float a = fast_exp2(ld_dsmem(m_addr + 4 * j, k) - M);
-        L = fmaf(ld_dsmem(l_addr + 4 * j, k), a, L);
-        O = fmaf(ld_dsmem(o_addr + 4 * (j * D + col), k), a, O);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float a = fast_exp2(m[k] - M);
+        L = fmaf(l[k], a, L);
+        O.x = fmaf(x[k].x, a, O.x);
+        O.y = fmaf(x[k].y, a, O.y);
+        O.z = fmaf(x[k].z, a, O.z);
+        O.w = fmaf(x[k].w, a, O.w);
       }
     }
-    p.out[(hq0 + j) * D + col] = float_to_bf16_bits(L != 0.f ? O / L * vsc : 0.f);
+    const bool any = L != 0.f;
+    *reinterpret_cast<uint2*>(p.out + (hq0 + j) * D + col) = make_uint2(
+        pack_bf16(any ? O.x / L * vsc : 0.f, any ? O.y / L * vsc : 0.f),
+        pack_bf16(any ? O.z / L * vsc : 0.f, any ? O.w / L * vsc : 0.f));
   }
   cluster_sync_all();  // this CTA's state lives until every rank has read it
 }
