@@ -667,33 +667,49 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
 }
 
 // 456 CTAs run at once on 152 SMs, and a CTA costs 5 to 6 us besides its units
-// (start, first loads, merge), which the SM's other two hide in part.
-// - One pass, a cluster of CTAs to a pair, where a warp then has two units or fewer
-//   (1 x 1033, d = 128: 6.3 us, 7.5 in partitions; 1 x 8192, 8 units a warp: 11.5, 8.0),
-//   or where the pairs fill half a wave by themselves and have 64 units or fewer (256
-//   pairs of 64, d = 256: 39.6 us, 44.1 in 4 partitions; of 128: 126, 113).
-// - One wave of partitions where the pairs fill it (32 pairs of 131072 tokens, d =
-//   256: 186 us in 14 partitions each, 207 in 56), or where there is not enough for
-//   more: partitions of 8 units (4 where one CTA to an SM does: 1 x 8192, d = 128:
-//   9.7 us, 10.2 with 8).
-// - Else somewhat over two waves, whose end is short (256 pairs of 8192, d = 256: 112 us
-//   in 4, 118 in 3, 117 in 8), in partitions of at most 2048 tokens, as contexts may
-//   differ (768 pairs of 16 to 16384, d = 128: 65 us, 70 in partitions of 4096; with
-//   the sequences longest first 60 and 56. Ranking them in every CTA cost more than
-//   it gave from about 100 sequences on).
+// (start, first loads, merge), which the SM's other two hide in part. Figures are d =
+// 256, "u units" are those of a pair, of 32 tokens.
+// - One pass where a warp has four units or fewer, with a cluster of CTAs to a pair as long
+//   as there is one CTA to an SM or less (32 pairs of 64 units: 11.8 us with 4 CTAs, 13.5
+//   with 8, 12.3 in 8 partitions; 120 of 16: 11.4 with 1, 13.2 with 2), none up to 8 units
+//   (100 pairs: 7.7, with two CTAs 9.3); and where the pairs fill half a wave by
+//   themselves and have 64 units or fewer (256 pairs of 64: 36.6 us, 42.6 in 2 partitions).
+//   Pairs that leave no room for two CTAs each get four if a warp then has two units or
+//   fewer (96 of 17 units of 64 tokens, d = 128: 9.3 us, 11.6 in 2 partitions).
+// - Else partitions: of 8 units up to two CTAs to an SM, of 16 up to a wave (64 pairs of 64:
+//   16.9 us in 4, 18.7 in 7, 22 in 8; 160 of 32: 20.6 in 2, 29.4 in 7; 32 pairs of 131072
+//   tokens: 186 us in 14, 207 in 56); 16 or fewer are made a multiple of the four warps.
+// - Where whole partitions leave more than a quarter of a wave empty and the pairs are long,
+//   somewhat over two waves, whose end is short (256 pairs of 256: 112 us in 4, 118 in 3,
+//   117 in 8, 123 in one pass; 160 of 256: 82 in 7, 88 in 2, but 160 of 128: 52.6, 49.7),
+//   in partitions of at most 2048 tokens, as contexts may differ (768 pairs of 16 to
+//   16384 tokens, d = 128: 65 us, 70 in partitions of 4096; with the sequences longest
+//   first 60 and 56. Ranking them in every CTA cost more than it gave from about 100
+//   sequences on).
+// A pass that the caller asks for has a cluster as long as that fits a wave (100 pairs of
+// 256: 51 us with 4 CTAs, 93 with 1).
 Fp4Split fp4_split(int64_t pairs, int64_t units, int unit) {
   constexpr int64_t kWave = 456, kSms = 152;
   if (pairs <= 0 || units <= 0) return {1, 0};
-  int c = 1;
-  while (c < 8 && kFp4Warps * c < units && 2 * c * pairs <= kWave) c <<= 1;
-  if (units <= 2 * kFp4Warps * c || (2 * pairs >= kWave && units <= 64)) return {c, 0};
-  int64_t np = std::min(kWave / pairs, units / 8);
-  if (pairs * (units / 4) <= kSms) np = units / 4;
-  if (np * pairs < kWave * 7 / 8 && np < units / 8)
+  auto cluster = [&](int64_t ctas) {
+    int c = 1;
+    while (c < 8 && kFp4Warps * c < units && 2 * c * pairs <= ctas) c <<= 1;
+    return c;
+  };
+  const int c = units <= 2 * kFp4Warps ? 1 : cluster(kSms);
+  if (units <= std::min(4 * kFp4Warps * c, 64) || (2 * pairs >= kWave && units <= 64))
+    return {c, 0};
+  const int wide = cluster(kWave);
+  if (c == 1 && wide >= 4 && units <= 2 * kFp4Warps * wide) return {wide, 0};
+  const int64_t one = kWave / pairs;
+  int64_t np = std::max(std::min(units / 8, 2 * kSms / pairs), std::min(units / 16, one));
+  if (one * pairs < kWave * 3 / 4 && one <= units / 16 && (units > 128 || one == 0))
     np = std::max((11 * kWave / 5 + pairs - 1) / pairs, (units * unit + 2047) / 2048);
   np = std::min<int64_t>(np, 8192);  // the merge takes 32767
   if (np <= 1) return {c, 0};
-  return {c, (units + np - 1) / np};
+  int64_t per = (units + np - 1) / np;
+  if (per <= 16) per = (per + kFp4Warps - 1) / kFp4Warps * kFp4Warps;
+  return {wide, per};
 }
 
 template <int D, int BS, bool LIST>
