@@ -29,6 +29,9 @@
 //   largest and not 2^-25. Both factors leave exactly.
 // - A hidden token (behind the context, of a skipped block) gets the logit -inf and
 //   V's scale 0: codes are always finite, only a scale can be NaN.
+// - A logit that is NaN passes the maxima by and reaches the sums: a query whose logits
+//   are all NaN has the maximum -inf of one without a token, a sum of NaN in the place
+//   of 0, and every merge multiplies and adds them as any other state's.
 //
 // Bound by HBM in whole waves (8 x 131072 tokens, 4 heads, d = 256 186 us with the merge,
 // 6.5 TB/s of codes and scales, 96 % of the copy rate); 64 x 8192 112 us (5.4 TB/s):
@@ -565,9 +568,9 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
     float M = sm_m[j], L = 0.f;
 #pragma unroll
     for (int w = 1; w < W; ++w) M = fmaxf(M, sm_m[w * 8 + j]);
-    if (M != -INFINITY)
+    const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-      for (int w = 0; w < W; ++w) L = fmaf(sm_l[w * 8 + j], fast_exp2(sm_m[w * 8 + j] - M), L);
+    for (int w = 0; w < W; ++w) L = fmaf(sm_l[w * 8 + j], fast_exp2(sm_m[w * 8 + j] - ref), L);
     cs_m[j] = M;
     cs_l[j] = L;
     cs_f[j] = L != 0.f ? vsc / L : 0.f;
@@ -646,17 +649,16 @@ __global__ void __launch_bounds__(W * 32, CTAS) decode_fp4_kernel(const DecodePa
     float M = m[0], L = 0.f;
 #pragma unroll
     for (int k = 1; k < 8; ++k) M = fmaxf(M, m[k]);
+    const float ref = M == -INFINITY ? 0.f : M;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float a = fast_exp2(m[k] - M);
-        L = fmaf(l[k], a, L);
-        O.x = fmaf(x[k].x, a, O.x);
-        O.y = fmaf(x[k].y, a, O.y);
-        O.z = fmaf(x[k].z, a, O.z);
-        O.w = fmaf(x[k].w, a, O.w);
-      }
+    for (int k = 0; k < 8; ++k) {
+      const float a = fast_exp2(m[k] - ref);
+      L = fmaf(l[k], a, L);
+      O.x = fmaf(x[k].x, a, O.x);
+      O.y = fmaf(x[k].y, a, O.y);
+      O.z = fmaf(x[k].z, a, O.z);
+      O.w = fmaf(x[k].w, a, O.w);
     }
     const bool any = L != 0.f;
     *reinterpret_cast<uint2*>(p.out + (hq0 + j) * D + col) = make_uint2(
