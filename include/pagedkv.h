@@ -185,9 +185,10 @@ int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tok
  * of q below 2^-14 of its row's largest is rounded by at most 2^-25 of it; the
  * softmax's weights meet V rounded to 11 bits, those below 2^-40 of the largest
  * as zero).
- * The softmax is the max-subtracted one, accumulated online in fp32. 4-bit
- * pools: a NaN in a row of q, or in a cached row of K of the context, makes the
- * output rows it meets NaN however the context is cut.
+ * The softmax is the max-subtracted one, accumulated online in fp32. A NaN in a
+ * row of q, or in a cached row of K that is seen, makes the output rows it meets
+ * NaN however the work is cut, here and in the windowed and the sparse call; a
+ * row without a token is zeros.
  *
  *   out       : device bf16 [num_seqs][num_heads][head_dim] (written when
  *               partition_size == 0; untouched otherwise)

@@ -754,14 +754,14 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
       float M = -INFINITY;
       for (int r = 0; r < C; ++r) M = fmaxf(M, ld_dsmem(m_addr + 4 * j, r));
       float L = 0.f, O = 0.f;
-      if (M != -INFINITY) {
-        for (int r = 0; r < C; ++r) {
-          const float a = fast_exp2(ld_dsmem(m_addr + 4 * j, r) - M);
-          L = fmaf(ld_dsmem(l_addr + 4 * j, r), a, L);
-          O = fmaf(ld_dsmem(o_addr + 4 * (j * D + c), r), a, O);
-        }
+      // -inf: no token, or logits that are all NaN, which the sums have
+      const float ref = M == -INFINITY ? 0.f : M;
+      for (int r = 0; r < C; ++r) {
+        const float a = fast_exp2(ld_dsmem(m_addr + 4 * j, r) - ref);
+        L = fmaf(ld_dsmem(l_addr + 4 * j, r), a, L);
+        O = fmaf(ld_dsmem(o_addr + 4 * (j * D + c), r), a, O);
       }
-      const float res = L > 0.f ? (O / L) * vsc : 0.f;
+      const float res = L != 0.f ? (O / L) * vsc : 0.f;
       const int64_t hq = static_cast<int64_t>(s) * p.num_heads + h * g + j;
       p.out[hq * D + c] = float_to_bf16_bits(res);
     }
@@ -780,8 +780,8 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
     const int64_t hq = static_cast<int64_t>(s) * p.num_heads + h * g + j;
 #pragma unroll
     for (int kk = 0; kk < KW; ++kk) {
-      const float lo = L > 0.f ? (o[kk][e] / L) * vsc : 0.f;
-      const float hi = L > 0.f ? (o[kk][2 + e] / L) * vsc : 0.f;
+      const float lo = L != 0.f ? (o[kk][e] / L) * vsc : 0.f;
+      const float hi = L != 0.f ? (o[kk][2 + e] / L) * vsc : 0.f;
       if (p.partition_blocks == 0) {
         p.out[hq * D + col(kk, 0)] = float_to_bf16_bits(lo);
         p.out[hq * D + col(kk, 1)] = float_to_bf16_bits(hi);

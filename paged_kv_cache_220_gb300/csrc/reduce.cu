@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kReduceWarps * 32) reduce_kernel(
   float W = 0.f;
   for (int i = tid; i < np; i += kReduceThreads) {
     float w = es[slot_of(i)] * fast_exp2((ml[slot_of(i)] - M) * kLog2eR);
-    if (MODE == kListSlots && M == -INFINITY) w = 0.f;  // no token in any slot
+    // no token in any slot: 0, or NaN where the logits are
+    if (MODE == kListSlots && M == -INFINITY) w = es[slot_of(i)];
     wsh[i] = w;
     W += w;
   }
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) reduce_rows_kernel(
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float w = lane < np ? l * fast_exp2((m - M) * kLog2eR) : 0.f;
-  if (MODE == kListSlots && M == -INFINITY) w = 0.f;  // no token in any slot
+  if (MODE == kListSlots && M == -INFINITY) w = l;  // no token: 0, or NaN
   float W = w;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);

@@ -1,6 +1,8 @@
 """A NaN in a query, or in a cached row that is seen, makes NaN of the outputs it
 enters however the call is cut (clusters, single CTAs, partitions), and of no
 other one. Rows without a token are zeros whatever their query holds."""
+import functools
+
 import pytest
 import torch
 
@@ -23,11 +25,34 @@ def _lib():
     pkv.set_device_check(flag)
     yield flag
     pkv.set_device_check(None)
+    cache_of.cache_clear()
+    cache_with_bad_rows.cache_clear()
+
+
+@functools.lru_cache(None)
+def cache_of(lens, kind, d):
+    return AnyCache(lens, 2, d, 16, kind, seed=len(lens))
+
+
+@functools.lru_cache(None)
+def cache_with_bad_rows(lens, kind):
+    """A NaN row in the middle of the first context, and one of NaN rows alone."""
+    c = AnyCache(lens, 2, 128, 16, kind, seed=len(lens))
+    c.poison(0, lens[0] // 2, lens[0] // 2 + 1)
+    if len(lens) > 1:
+        c.poison(1, 0, lens[1])
+    return c
 
 
 def whole(c, q, scale, partition):
     return pkv.paged_attention(q, c.k, c.v, c.tables, c.context_lens, scale, c.max_context,
                                partition, **c.kw())
+
+
+def window(c, q, scale, partition):
+    """A window behind which nothing lies."""
+    return pkv.paged_attention_window(q, c.k, c.v, c.tables, c.context_lens, scale,
+                                      c.max_context, c.max_context + 1, 3, partition, **c.kw())
 
 
 def is_nan(out):
@@ -46,17 +71,18 @@ def verify(c, q, out, scale, bad, rows):
 
 # (lengths, how a pass or the partitions are cut): one sequence takes a cluster to
 # a pair, hundreds one CTA each
-BATCHES = [[1000], [1000] + [130] * 3, [200] * 130, [40] * 600, [1] * 3, [3000] + [700] * 300]
+BATCHES = [[1000], [1000] + [130] * 3, [200] * 130, [40] * 600, [1] * 3]
 
 
 @pytest.mark.parametrize("partition", [0, 32, 512, None])
 @pytest.mark.parametrize("d", [128, 256])
-@pytest.mark.parametrize("call,kind", [(whole, "fp4")])
+@pytest.mark.parametrize("call,kind", [(whole, "fp4"), (whole, "bf16"), (whole, "fp8"),
+                                       (window, "bf16"), (window, "fp8")])
 def test_queries(call, kind, d, partition, _lib):
     scale, hk, g = d ** -0.5, 2, 3
     for lens in BATCHES:
         n = len(lens)
-        c = AnyCache(lens + [0], hk, d, 16, kind, seed=n)
+        c = cache_of(tuple(lens + [0]), kind, d)
         q = queries(n + 1, hk * g, d, seed=n)
         q[0, 1, 5] = NAN          # one element of a row
         q[0, 4] = NAN             # a whole row
@@ -75,16 +101,13 @@ def test_queries(call, kind, d, partition, _lib):
 
 
 @pytest.mark.parametrize("partition", [0, 32, 512, None])
-@pytest.mark.parametrize("call,kind", [(whole, "fp4")])
+@pytest.mark.parametrize("call,kind", [(whole, "fp4"), (whole, "bf16"), (whole, "fp8"),
+                                       (window, "bf16"), (window, "fp8")])
 def test_cached_rows(call, kind, partition, _lib):
-    """A NaN row in the middle of a context, and one that is all there is."""
     for lens in BATCHES:
         n = len(lens)
-        c = AnyCache(lens, 2, 128, 16, kind, seed=n)
+        c = cache_with_bad_rows(tuple(lens), kind)
         q = queries(n, 6, 128, seed=n)
-        c.poison(0, lens[0] // 2, lens[0] // 2 + 1)
-        if n > 1:
-            c.poison(1, 0, lens[1])
         out = call(c, q, 0.09, partition)
         bad = {(s, j) for s in range(min(n, 2)) for j in range(6)}
         verify(c, q, out, 0.09, bad, sorted({0, min(1, n - 1), n - 1}))
@@ -98,7 +121,7 @@ LISTS = [([1000], 40), ([700] * 130, 30), ([40] * 600, 2), ([20000, 9], 1200),
          ([30000] + [3000] * 11, 180)]
 
 
-@pytest.mark.parametrize("kind", ["fp4"])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("d", [128, 256])
 def test_listed_blocks(d, kind, _lib):
     hk, g, cut = 2, 3, set()
