@@ -180,7 +180,8 @@ int pkv_kv_cache_read(void* k, void* v, const int64_t* slot_mapping, int num_tok
  * For sequence s and query head j (KV head h = j / g, g = num_heads /
  * num_kv_heads), with K_s, V_s the sequence's logical rows 0..ctx-1:
  *     z_t = scale * <q[s,j,:], K_s[t,:]>,  out[s,j,:] = sum_t softmax(z)_t V_s[t,:]
- * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]), 4-bit pools as
+ * FP8 pools dequantise as code * k_scale[h] (resp. v_scale[h]; an element of q
+ * below 2^-16 of its row's largest is rounded by at most 2^-24 of it), 4-bit pools as
  * code * s * k_scale[h] (tables of at most 2^30 tokens a sequence; an element
  * of q below 2^-14 of its row's largest is rounded by at most 2^-25 of it; the
  * softmax's weights meet V rounded to 11 bits, those below 2^-40 of the largest
@@ -357,7 +358,8 @@ int pkv_paged_attention(void* out, const void* q, const void* k_cache,
  * Per group, KV head and row tile, a kernel computes partials of the members'
  * query heads over the shared pages (the members' queries form the rows of
  * one tensor-core product; for E4M3 pools the codes are turned into exact f16
- * operands in shared memory and P is one f16 part); each member's own blocks
+ * operands in shared memory, q, below 65520 in magnitude, becomes f16 too and P
+ * is one f16 part); each member's own blocks
  * go through the split decode; the merge combines both.
  * ------------------------------------------------------------------------ */
 size_t pkv_shared_prefix_workspace_bytes(int num_seqs, int num_heads, int head_dim,

@@ -98,6 +98,13 @@ struct TcGeom {
   static constexpr bool kSplitKV = kPage >= 8192;
 };
 
+// The larger magnitude of each of two bf16 pairs (a NaN is passed by); some sign.
+__device__ __forceinline__ uint32_t larger2_abs(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 constexpr int kWhole = 0, kWindowed = 1, kListed = 2;  // MODE
 constexpr int kNoToken = 0x7F000000;  // first "token" of a block that is not there
 
@@ -421,7 +428,11 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
     // FP8 (f16 operands): the contraction index of k-step k is permuted so that
     // plain ldmatrix rows of the FP8 page line up with it: b0 = Q[n][16k +
     // 4(lane%4) + {0,1}], b1 = Q[n][16k + 4(lane%4) + {2,3}].
+    // A row whose largest element is not in [1/2, 2^15) is scaled by a power of two to
+    // [1, 2) before it becomes f16 (it would end as infinities, or lose bits), the factor
+    // of its logits by the inverse. Both leave exactly.
     uint32_t bq[KW][2];
+    float qs0 = p.qscale, qs1 = qs0;  // logit factors of queries q0, q1
     {
       const int n = lane >> 2;
       const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
@@ -433,17 +444,42 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
           bq[kk][0] = n < g ? __ldg(qrow + (k * 16 + (lane & 3) * 2) / 2) : 0u;
           bq[kk][1] = n < g ? __ldg(qrow + (k * 16 + 8 + (lane & 3) * 2) / 2) : 0u;
         } else {
-          const uint32_t w0 = n < g ? __ldg(qrow + (k * 16 + (lane & 3) * 4) / 2) : 0u;
-          const uint32_t w1 = n < g ? __ldg(qrow + (k * 16 + (lane & 3) * 4 + 2) / 2) : 0u;
-          bq[kk][0] = pack_f16(bf16lo(w0), bf16hi(w0));
-          bq[kk][1] = pack_f16(bf16lo(w1), bf16hi(w1));
+          bq[kk][0] = n < g ? __ldg(qrow + (k * 16 + (lane & 3) * 4) / 2) : 0u;
+          bq[kk][1] = n < g ? __ldg(qrow + (k * 16 + (lane & 3) * 4 + 2) / 2) : 0u;
         }
+      }
+      if constexpr (FP8) {
+        uint32_t pair = 0;  // largest magnitudes of this warp's part of row n
+#pragma unroll
+        for (int kk = 0; kk < KW; ++kk)
+          pair = larger2_abs(pair, larger2_abs(bq[kk][0], bq[kk][1]));
+        pair = larger2_abs(pair, __shfl_xor_sync(0xffffffffu, pair, 1));
+        pair = larger2_abs(pair, __shfl_xor_sync(0xffffffffu, pair, 2));
+        // the parts meet in the second exchange buffer, which is written to only after
+        // every warp has stored a slice to the first
+        float* tops = reinterpret_cast<float*>(xs + NW * G::kNH * 32);  // [NW][8]
+        if ((lane & 3) == 0) tops[warp * 8 + n] = fmaxf(fabsf(bf16lo(pair)), fabsf(bf16hi(pair)));
+        asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
+        float top = tops[n];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, tops[w * 8 + n]);
+        const int e = top == 0.f || (top >= 0.5f && top < 32768.f)
+                          ? 127
+                          : min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < KW; ++kk)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            bq[kk][i] = pack_f16(bf16lo(bq[kk][i]) * down, bf16hi(bq[kk][i]) * down);
+        const float qs = p.qscale * p.k_scale[h];
+        qs0 = qs * __shfl_sync(0xffffffffu, up, 8 * (lane & 3));
+        qs1 = qs * __shfl_sync(0xffffffffu, up, 8 * (lane & 3) + 4);
       }
     }
 #pragma unroll
     for (int kk = 0; kk < KW; ++kk) o[kk][0] = o[kk][1] = o[kk][2] = o[kk][3] = 0.f;
-    float qs = p.qscale;
-    if constexpr (FP8) qs *= p.k_scale[h];
 
     // slots past the context hold whatever was there: zero this warp's
     // columns of their V rows so the zero probabilities cannot meet a NaN
@@ -581,10 +617,10 @@ __global__ void __launch_bounds__(TcGeom<D, BS, FP8, NW, NST>::kThreads)
           const int t0 = r0 + 16 * hh + (lane >> 2), t1 = t0 + 8;
           const bool see0 = SOME ? whole || sees(tok(t0)) : t0 < ntok;
           const bool see1 = SOME ? whole || sees(tok(t1)) : t1 < ntok;
-          sc[hh][0] = see0 ? sv[0] * qs : -INFINITY;
-          sc[hh][1] = see0 ? sv[1] * qs : -INFINITY;
-          sc[hh][2] = see1 ? sv[2] * qs : -INFINITY;
-          sc[hh][3] = see1 ? sv[3] * qs : -INFINITY;
+          sc[hh][0] = see0 ? sv[0] * qs0 : -INFINITY;
+          sc[hh][1] = see0 ? sv[1] * qs1 : -INFINITY;
+          sc[hh][2] = see1 ? sv[2] * qs0 : -INFINITY;
+          sc[hh][3] = see1 ? sv[3] * qs1 : -INFINITY;
           mx0 = fmaxf(mx0, fmaxf(sc[hh][0], sc[hh][2]));
           mx1 = fmaxf(mx1, fmaxf(sc[hh][1], sc[hh][3]));
         }
