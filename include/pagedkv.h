@@ -487,8 +487,8 @@ int pkv_block_bounds(int8_t* bounds, const void* k_cache, pkv_cache_desc cache,
  * A bad block id is reported (PKV_DEVERR_BLOCK_ID); the block then comes after
  * all others. blocks, counts and workspace may not overlap each other or an
  * input. Errors: PKV_ERR_INVALID_ARG (max_selected < 1 among them),
- * PKV_ERR_UNSUPPORTED (tables of more than 2^30 tokens a sequence among them),
- * PKV_ERR_CUDA. num_seqs == 0 is a no-op.
+ * PKV_ERR_UNSUPPORTED (tables of more than 2^30 tokens a sequence and
+ * max_selected above 2^30 among them), PKV_ERR_CUDA. num_seqs == 0 is a no-op.
  * ------------------------------------------------------------------------ */
 size_t pkv_select_workspace_bytes(int num_seqs, int num_kv_heads, int block_size,
                                   int max_context);

@@ -390,7 +390,9 @@ extern "C" int pkv_select_blocks(int32_t* blocks, int32_t* counts, const void* q
   const int group = num_heads / cache.num_kv_heads;
   const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * cache.block_size;
   if (max_context > cap) return PKV_ERR_INVALID_ARG;
-  if (group > 8 || num_seqs > 65535 || cap > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+  // positions in a context and in a list, a CTA's stride behind the last, are 32-bit numbers
+  if (group > 8 || num_seqs > 65535 || cap > (1 << 30) || max_selected > (1 << 30))
+    return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   if (!blocks || !counts || !q || !bounds || !block_tables || !context_lens)
     return PKV_ERR_INVALID_ARG;
