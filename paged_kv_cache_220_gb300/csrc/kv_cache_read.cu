@@ -3,8 +3,9 @@
 // A thread has channels [8 c8, 8 c8 + 8) of a head of U tokens, their loads in flight
 // together: 16, 8 or 4 bytes of each pool, 16 bytes of each result; a warp's are whole
 // rows. Many tokens are bound by HBM and, on 4-bit pools, as much by the conversions'
-// instructions: 32768 tokens, 8 heads, d = 128 30.4 us, 5.7 TB/s. A step's few are bound by
-// latency (64 tokens: 1.5 us).
+// instructions: 32768 tokens, 8 heads, d = 128, from HBM, bf16 42.4 us, 94 % of the copy
+// rate, E4M3 32.6 (91 %), 4-bit 32.1 (80 %; 30.4 right after they were written). A step's
+// few are bound by latency (64 tokens: 2.4 us, 1.5 right behind a write).
 #include <type_traits>
 
 #include "common.cuh"
